@@ -212,21 +212,23 @@ def run(s):
 
 
 def _run_own(s):
+    # check_status=False, as a training or serving loop has it: reading the status word of packed input would wait for the GPU
     gdn, op, c = _gdn(), s["op"], s["case"]
     if op == "conv_fwd":
-        y, state = gdn.conv_forward(s["x"], s["w"], s["bias"], s["state"], cu_seqlens=s["cu"], silu=c["silu"])
+        y, state = gdn.conv_forward(s["x"], s["w"], s["bias"], s["state"], cu_seqlens=s["cu"], silu=c["silu"], check_status=False)
         return dict(y=y, state=state)
     if op == "conv_bwd":
-        return gdn.conv_backward(s["x"], s["w"], s["bias"], s["state"], s["dy"], s["dstate"], cu_seqlens=s["cu"], silu=c["silu"])
+        return gdn.conv_backward(s["x"], s["w"], s["bias"], s["state"], s["dy"], s["dstate"], cu_seqlens=s["cu"], silu=c["silu"], check_status=False)
     if op == "conv_step":
         y, state = gdn.conv_step(s["x"], s["w"], s["bias"], s["state"], out_state=s["out_state"], silu=c["silu"])
         return dict(y=y, state=state)
     if op == "scan_fwd":
-        y, hT = gdn.scan_forward(*_scan_args(s), h0=s["h0"], cu_seqlens=s["cu"])
+        y, hT = gdn.scan_forward(*_scan_args(s), h0=s["h0"], cu_seqlens=s["cu"], check_status=False)
         return dict(y=y, state=hT)
     if op == "scan_train":
-        y, hT, saved = gdn.scan_forward(*_scan_args(s), h0=s["h0"], cu_seqlens=s["cu"], save=True)
-        grads = gdn.scan_backward(*_scan_args(s), h0=s["h0"], dy=s["dy"], dhT=s["dhT"], saved=saved, cu_seqlens=s["cu"])
+        y, hT, saved = gdn.scan_forward(*_scan_args(s), h0=s["h0"], cu_seqlens=s["cu"], save=True, check_status=False)
+        grads = gdn.scan_backward(*_scan_args(s), h0=s["h0"], dy=s["dy"], dhT=s["dhT"], saved=saved, cu_seqlens=s["cu"],
+                                  check_status=False)
         return dict(grads, y=y, state=hT)
     if op == "scan_step":
         y, state = gdn.scan_step(*_scan_args(s), state=s["h0"], out_state=s["out_state"])
