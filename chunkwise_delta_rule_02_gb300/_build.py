@@ -13,7 +13,7 @@ LIB = os.path.join(PKG, "libgdn_gb300.so")
 ROOT = os.path.dirname(PKG)
 
 SOURCES = ["api.cu", "general.cu", "fast.cu", "coop.cu", "decode.cu", "affine.cu", "bwd_tc.cu",
-           "bscan_tc.cu"]
+           "bscan_tc.cu", "layers_api.cu", "conv.cu", "norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-extended-lambda", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-Wall", "-I" + os.path.join(ROOT, "include")]
@@ -39,7 +39,7 @@ def _newer(dst, srcs):
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    headers.append(os.path.join(ROOT, "include", "gdn.h"))
+    headers += [os.path.join(ROOT, "include", f) for f in ("gdn.h", "gdn_layers.h")]
     objs, jobs = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)

@@ -1,0 +1,267 @@
+// C ABI of the layer operators: argument checks, workspace layout, dispatch; and
+// the two kernels they share (packed offsets, sums of partial results).
+#include <string.h>
+
+#include "layers.h"
+
+namespace gdn {
+namespace lay {
+
+namespace {
+
+// One block: copies the offsets, or zeros and the status flag if they are malformed.
+__global__ void __launch_bounds__(256) k_offsets(const int32_t *cu, int N, int T, int32_t *out, uint32_t *status)
+{
+    int bad = 0;
+    for (int i = threadIdx.x; i <= N; i += blockDim.x) {
+        const int v = cu[i];
+        if (i == 0 ? v != 0 : cu[i - 1] > v) bad = 1;
+        if (i == N && v != T) bad = 1;
+    }
+    bad = __syncthreads_or(bad);
+    for (int i = threadIdx.x; i <= N; i += blockDim.x) out[i] = bad ? 0 : cu[i];
+    if (bad && threadIdx.x == 0) raise_status(status, kStatusBadOffsets);
+}
+
+constexpr int kSumX = 32, kSumY = 32;
+
+__global__ void __launch_bounds__(kSumX *kSumY) k_col_sum(const float *__restrict__ part, long long P, ColSum c)
+{
+    __shared__ float sm[kSumY][kSumX + 1];
+    const long long n = c.C * c.kinds, col = blockIdx.x * (long long)kSumX + threadIdx.x;
+    float a = 0.f;
+    if (col < n) {
+#pragma unroll 4
+        for (long long p = threadIdx.y; p < P; p += kSumY) a += part[p * n + col];
+    }
+    sm[threadIdx.y][threadIdx.x] = a;
+    __syncthreads();
+    if (threadIdx.y == 0 && col < n) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSumY; ++i) s += sm[i][threadIdx.x];
+        const int k = (int)(col / c.C);
+        if (c.dst[k]) c.dst[k][(col - k * c.C) * c.step[k]] = s;
+    }
+}
+
+}  // namespace
+
+cudaError_t check_offsets(const int32_t *cu, int N, int T, int32_t *out, uint32_t *status, cudaStream_t st)
+{
+    k_offsets<<<1, 256, 0, st>>>(cu, N, T, out, status);
+    return cudaPeekAtLastError();
+}
+
+cudaError_t col_sum(const float *part, long long P, const ColSum &c, cudaStream_t st)
+{
+    const long long n = c.C * c.kinds;
+    if (n == 0) return cudaSuccess;
+    k_col_sum<<<(unsigned)((n + kSumX - 1) / kSumX), dim3(kSumX, kSumY), 0, st>>>(part, P, c);
+    return cudaPeekAtLastError();
+}
+
+int sm_count()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+    return n;
+}
+
+namespace {
+
+bool aligned(const void *p, size_t n) { return ((uintptr_t)p % n) == 0; }
+bool has(const dn_view *v) { return v && v->data; }
+dn_status status_of(cudaError_t e) { return e == cudaSuccess ? DN_OK : DN_ERR_CUDA; }
+
+constexpr int kMaxT = 1 << 30;   // token indices plus a tile stay in 32 bits
+
+dn_status check_packed(const int32_t *cu, int B, int num_seqs)
+{
+    if (!cu) return DN_OK;
+    if (B != 1 || num_seqs < 0 || num_seqs == INT32_MAX || !aligned(cu, 4)) return DN_ERR_INVALID_ARG;
+    return DN_OK;
+}
+
+// ------------------------------------------------------------------ convolution
+dn_status conv_shape_ok(const dn_conv_shape *s)
+{
+    if (!s || s->B < 1 || s->H < 1 || s->T < 0 || s->d < 1) return DN_ERR_INVALID_ARG;
+    if (s->dtype != DN_F32 && s->dtype != DN_BF16) return DN_ERR_INVALID_ARG;
+    if ((long long)s->H * s->d > (1 << 24) || s->T > kMaxT) return DN_ERR_UNSUPPORTED;
+    if (s->width < 2 || s->width > 4) return DN_ERR_UNSUPPORTED;
+    return check_packed(s->cu_seqlens, s->B, s->num_seqs);
+}
+
+struct ConvWs {
+    size_t cu, part, total;
+};
+
+ConvWs conv_ws(const dn_conv_shape *s, bool bwd)
+{
+    ConvWs w;
+    w.cu = 256;
+    w.part = w.cu + (s->cu_seqlens ? align256(sizeof(int32_t) * ((size_t)s->num_seqs + 1)) : 0);
+    w.total = w.part;
+    if (bwd) w.total += align256(sizeof(float) * (size_t)conv_part_rows(s) * (s->width + 1) * s->H * s->d);
+    return w;
+}
+
+dn_status conv_begin(ConvCall &c, const dn_conv_shape *s, bool bwd, void *ws, size_t ws_bytes, cudaStream_t st)
+{
+    const ConvWs l = conv_ws(s, bwd);
+    if (!ws || !aligned(ws, 16) || ws_bytes < l.total) return DN_ERR_WORKSPACE;
+    char *base = (char *)ws;
+    c.s = s;
+    c.N = s->cu_seqlens ? s->num_seqs : s->B;
+    c.part = (float *)(base + l.part);
+    if (s->cu_seqlens) {
+        if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return DN_ERR_CUDA;
+        c.cu = (const int32_t *)(base + l.cu);
+        return status_of(check_offsets(s->cu_seqlens, s->num_seqs, s->T, (int32_t *)(base + l.cu), (uint32_t *)ws, st));
+    }
+    return DN_OK;
+}
+
+// ------------------------------------------------------------------ norm
+dn_status norm_shape_ok(const dn_norm_shape *s)
+{
+    if (!s || s->B < 1 || s->H < 1 || s->T < 0 || s->d < 1) return DN_ERR_INVALID_ARG;
+    if (s->dtype != DN_F32 && s->dtype != DN_BF16) return DN_ERR_INVALID_ARG;
+    if (!(s->eps >= 0.f)) return DN_ERR_INVALID_ARG;
+    if (s->d > 16384) return DN_ERR_UNSUPPORTED;
+    if ((double)s->B * s->H * s->T > 2147483647.0 || (s->w_per_head && s->H > 65535)) return DN_ERR_UNSUPPORTED;
+    return DN_OK;
+}
+
+}  // namespace
+}  // namespace lay
+}  // namespace gdn
+
+using namespace gdn;
+using namespace gdn::lay;
+
+extern "C" {
+
+size_t dn_conv_workspace_size(const dn_conv_shape *shape, int for_backward)
+{
+    return conv_shape_ok(shape) == DN_OK ? conv_ws(shape, for_backward != 0).total : 0;
+}
+
+dn_status dn_conv_fwd(const dn_conv_shape *shape, const dn_view *x, const float *w, const float *bias, const void *s0,
+                      const dn_view *y, void *sT, void *ws, size_t ws_bytes, void *stream)
+{
+    dn_status rc = conv_shape_ok(shape);
+    if (rc != DN_OK) return rc;
+    const size_t e = shape->dtype == DN_F32 ? 4 : 2;
+    if (!w || !aligned(w, 4) || !aligned(bias, 4) || !aligned(s0, e) || !aligned(sT, e)) return DN_ERR_INVALID_ARG;
+    if (shape->T > 0 && (!has(x) || !has(y))) return DN_ERR_INVALID_ARG;
+    if ((has(x) && !aligned(x->data, e)) || (has(y) && !aligned(y->data, e))) return DN_ERR_INVALID_ARG;
+    ConvCall c;
+    memset(&c, 0, sizeof(c));
+    if ((rc = conv_begin(c, shape, false, ws, ws_bytes, (cudaStream_t)stream)) != DN_OK) return rc;
+    c.x = x; c.y = y; c.w = w; c.bias = bias; c.s0 = s0; c.sT = sT;
+    return status_of(conv_fwd(c, (cudaStream_t)stream));
+}
+
+dn_status dn_conv_bwd(const dn_conv_shape *shape, const dn_view *x, const float *w, const float *bias, const void *s0,
+                      const dn_view *dy, const void *dsT, const dn_view *dx, float *dw, float *dbias, void *ds0,
+                      void *ws, size_t ws_bytes, void *stream)
+{
+    dn_status rc = conv_shape_ok(shape);
+    if (rc != DN_OK) return rc;
+    const size_t e = shape->dtype == DN_F32 ? 4 : 2;
+    if (!w || !dw || !aligned(w, 4) || !aligned(bias, 4) || !aligned(dw, 4) || !aligned(dbias, 4)) return DN_ERR_INVALID_ARG;
+    if (!aligned(s0, e) || !aligned(dsT, e) || !aligned(ds0, e)) return DN_ERR_INVALID_ARG;
+    if (shape->T > 0 && (!has(x) || !has(dy) || !has(dx))) return DN_ERR_INVALID_ARG;
+    const dn_view *views[] = {x, dy, dx};
+    for (const dn_view *v : views)
+        if (has(v) && !aligned(v->data, e)) return DN_ERR_INVALID_ARG;
+    ConvCall c;
+    memset(&c, 0, sizeof(c));
+    if ((rc = conv_begin(c, shape, true, ws, ws_bytes, (cudaStream_t)stream)) != DN_OK) return rc;
+    c.x = x; c.dy = dy; c.dx = dx; c.w = w; c.bias = bias; c.s0 = s0; c.dsT = dsT; c.ds0 = ds0;
+    c.dw = dw; c.dbias = dbias;
+    return status_of(conv_bwd(c, (cudaStream_t)stream));
+}
+
+dn_status dn_conv_step(const dn_conv_shape *shape, const dn_view *x, const float *w, const float *bias,
+                       const void *state_in, void *state_out, const dn_view *y, void *stream)
+{
+    dn_status rc = conv_shape_ok(shape);
+    if (rc != DN_OK) return rc;
+    const size_t e = shape->dtype == DN_F32 ? 4 : 2;
+    if (shape->T != 1 || shape->cu_seqlens || !w || !has(x) || !has(y)) return DN_ERR_INVALID_ARG;
+    if (!aligned(w, 4) || !aligned(bias, 4) || !aligned(state_in, e) || !aligned(state_out, e) || !aligned(x->data, e) ||
+        !aligned(y->data, e))
+        return DN_ERR_INVALID_ARG;
+    ConvCall c;
+    memset(&c, 0, sizeof(c));
+    c.s = shape; c.N = shape->B;
+    c.x = x; c.y = y; c.w = w; c.bias = bias; c.s0 = state_in; c.sT = state_out;
+    return status_of(conv_step(c, (cudaStream_t)stream));
+}
+
+dn_status dn_norm_fwd(const dn_norm_shape *shape, const dn_view *x, const float *w, const dn_view *z,
+                      const dn_view *residual, const float *res_scale, const dn_view *y, const dn_view *sum,
+                      void *stream)
+{
+    dn_status rc = norm_shape_ok(shape);
+    if (rc != DN_OK) return rc;
+    const size_t e = shape->dtype == DN_F32 ? 4 : 2;
+    if (!w || !aligned(w, 4) || !aligned(res_scale, 4)) return DN_ERR_INVALID_ARG;
+    if ((has(sum) || res_scale) && !has(residual)) return DN_ERR_INVALID_ARG;
+    if (shape->T == 0) return DN_OK;
+    if (!has(x) || !has(y)) return DN_ERR_INVALID_ARG;
+    const dn_view *views[] = {x, z, residual, y, sum};
+    for (const dn_view *v : views)
+        if (has(v) && !aligned(v->data, e)) return DN_ERR_INVALID_ARG;
+    NormCall c;
+    memset(&c, 0, sizeof(c));
+    c.s = shape; c.x = x; c.z = z; c.residual = residual; c.res_scale = res_scale; c.y = y; c.sum = sum; c.w = w;
+    return status_of(norm_fwd(c, (cudaStream_t)stream));
+}
+
+size_t dn_norm_workspace_size(const dn_norm_shape *shape)
+{
+    if (norm_shape_ok(shape) != DN_OK) return 0;
+    return align256(2 * sizeof(float) * (size_t)norm_part_rows(shape) * shape->d);
+}
+
+dn_status dn_norm_bwd(const dn_norm_shape *shape, const dn_view *x, const float *w, const dn_view *z,
+                      const float *res_scale, const dn_view *sum, const dn_view *dy, const dn_view *dsum,
+                      const dn_view *dx, float *dw, const dn_view *dz, const dn_view *dresidual, float *dres_scale,
+                      void *ws, size_t ws_bytes, void *stream)
+{
+    dn_status rc = norm_shape_ok(shape);
+    if (rc != DN_OK) return rc;
+    const size_t e = shape->dtype == DN_F32 ? 4 : 2;
+    if (!w || !dw || !aligned(w, 4) || !aligned(dw, 4) || !aligned(res_scale, 4) || !aligned(dres_scale, 4))
+        return DN_ERR_INVALID_ARG;
+    const bool res = has(sum);
+    if (!res && (res_scale || dres_scale || has(dsum) || has(dresidual))) return DN_ERR_INVALID_ARG;
+    if (has(dz) && !has(z)) return DN_ERR_INVALID_ARG;
+    if (shape->T > 0) {
+        if (!has(dy) || (!has(dx) && !has(dresidual))) return DN_ERR_INVALID_ARG;
+        if (!has(x) && (!res || dres_scale)) return DN_ERR_INVALID_ARG;
+    }
+    const dn_view *views[] = {x, z, sum, dy, dsum, dx, dz, dresidual};
+    for (const dn_view *v : views)
+        if (has(v) && !aligned(v->data, e)) return DN_ERR_INVALID_ARG;
+    if (!ws || !aligned(ws, 16) || ws_bytes < dn_norm_workspace_size(shape)) return DN_ERR_WORKSPACE;
+    NormCall c;
+    memset(&c, 0, sizeof(c));
+    c.s = shape; c.x = x; c.z = z; c.sum = sum; c.dy = dy; c.dsum = dsum; c.dx = dx; c.dz = dz; c.dresidual = dresidual;
+    c.w = w; c.res_scale = res_scale; c.dw = dw; c.dres_scale = dres_scale; c.part = (float *)ws;
+    if (shape->T == 0) {   // no rows: the sums are zero
+        const size_t nw = (size_t)(shape->w_per_head ? shape->H : 1) * shape->d;
+        if (cudaMemsetAsync(dw, 0, nw * 4, (cudaStream_t)stream) != cudaSuccess) return DN_ERR_CUDA;
+        if (dres_scale && cudaMemsetAsync(dres_scale, 0, (size_t)shape->d * 4, (cudaStream_t)stream) != cudaSuccess)
+            return DN_ERR_CUDA;
+        return DN_OK;
+    }
+    return status_of(norm_bwd(c, (cudaStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,349 @@
+"""The layer operators around the delta rule (include/gdn_layers.h): short causal
+convolution, selective state space scan, RMS norm with gate or residual sum.
+
+As in ``binding``: argument checks and marshalling only, every step of the
+computation runs in the library's CUDA kernels on the current torch stream, and a
+call that cannot run raises (TypeError, ValueError, or GdnError with the library's
+status).  The ``dn_*`` functions take caller-owned buffers and carry the C names;
+``conv_*``, ``scan_*`` and ``norm_*`` allocate the results (and workspaces) with
+torch and call them.
+
+Token arrays may have any strides as long as the feature axis is contiguous, so
+slices and transposed views of a projection go in, and come out (``out=``), without
+a copy.  They are float32 or bfloat16, all of one type in a call; parameters (weights,
+A, D, biases), scan states and their gradients are float32.
+
+Packed sequences: B = 1 and ``cu_seqlens``, int32 offsets on the device, as in
+``binding.forward``.  The kernels check the offsets; with ``check_status`` (the
+default) a packed call reads the status word afterwards, which waits for the
+stream, and raises if they were malformed.  Other calls never wait.
+"""
+from __future__ import annotations
+
+import struct
+from typing import Optional
+
+import torch
+
+from . import binding
+from .binding import DN_BF16, DN_ERR_INVALID_ARG, DN_F32, GdnError, _check, dn_device_status
+
+EXPORTS = ["dn_conv_workspace_size", "dn_conv_fwd", "dn_conv_bwd", "dn_conv_step", "dn_norm_fwd",
+           "dn_norm_workspace_size", "dn_norm_bwd"]
+
+_DTYPES = {torch.float32: DN_F32, torch.bfloat16: DN_BF16}
+_CONV_SHAPE = struct.Struct("8iq")        # dn_conv_shape
+_NORM_SHAPE = struct.Struct("6ifi")       # dn_norm_shape
+_VIEW = struct.Struct("4q")               # dn_view
+_NO_VIEW = _VIEW.pack(0, 0, 0, 0)
+
+_lib = None
+
+
+def _L():
+    """The library, with this module's entry points declared."""
+    global _lib
+    if _lib is None:
+        import ctypes
+        L = binding.lib()
+        P, S, I, R = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_char_p   # R: a packed record
+        for name, args, res in (
+                ("dn_conv_workspace_size", [R, I], S),
+                ("dn_conv_fwd", [R, R, P, P, P, R, P, P, S, P], I),
+                ("dn_conv_bwd", [R, R, P, P, P, R, P, R, P, P, P, P, S, P], I),
+                ("dn_conv_step", [R, R, P, P, P, P, R, P], I),
+                ("dn_norm_fwd", [R, R, P, R, R, P, R, R, P], I),
+                ("dn_norm_workspace_size", [R], S),
+                ("dn_norm_bwd", [R, R, P, R, P, R, R, R, R, P, R, R, P, P, S, P], I)):
+            f = getattr(L, name)
+            f.argtypes, f.restype = args, res
+        _lib = L
+    return _lib
+
+
+# ------------------------------------------------------------------ checks
+
+def _tokens(t: torch.Tensor, name: str, shape, dtype) -> torch.Tensor:
+    """A token array: CUDA, the call's dtype and shape, contiguous features."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s like the call's other token arrays, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError("%s: the feature axis must be contiguous (stride 1), got strides %s" % (name, t.stride()))
+    if not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    return t
+
+
+def _dense(t: Optional[torch.Tensor], name: str, shape, dtype=torch.float32):
+    """A dense array (parameter, state) or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    return t
+
+
+def _dtype_code(t: torch.Tensor, name: str) -> int:
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise TypeError("%s must be float32 or bfloat16, got %s" % (name, t.dtype)) from None
+
+
+def _result(t: Optional[torch.Tensor], name: str, like: torch.Tensor) -> torch.Tensor:
+    """A result like `like`: new and contiguous, or the caller's, whose elements must be distinct."""
+    if t is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    _tokens(t, name, like.shape, like.dtype)
+    if t.device != like.device:
+        raise ValueError("%s is on %s, the inputs are on %s" % (name, t.device, like.device))
+    if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
+        raise ValueError("%s must not repeat memory along an axis (stride 0)" % name)
+    return t
+
+
+def _same_device(first: torch.Tensor, *rest):
+    """All arguments on one device, and that device current (its stream is the one used)."""
+    dev = first.device
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors on different devices: %s and %s" % (dev, t.device))
+    if torch.cuda.current_device() != dev.index:
+        raise ValueError("%s is not the current CUDA device: call under torch.cuda.device(%d)" % (dev, dev.index))
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(stream):
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _view4(t: Optional[torch.Tensor]) -> Optional[bytes]:
+    """[B,H,T,d] as a dn_view record."""
+    if t is None:
+        return None
+    b, h, tm, _ = t.stride()
+    return _VIEW.pack(t.data_ptr(), b, h, tm)
+
+
+def _four(t: Optional[torch.Tensor]):
+    """[B,T,C] as [B,1,T,C]; [B,H,T,d] as it is."""
+    return t if t is None or t.dim() == 4 else t.unsqueeze(1)
+
+
+def _cu(cu_seqlens, B):
+    """(pointer, num_seqs) of packed offsets."""
+    if cu_seqlens is None:
+        return 0, 0
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise TypeError("cu_seqlens must be a one-dimensional int32 tensor of at least one offset")
+    if not cu_seqlens.is_cuda or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous CUDA tensor")
+    if B != 1:
+        raise ValueError("packed sequences need B = 1, got B = %d" % B)
+    return cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
+
+
+def _ws(nbytes: int, device, where: str) -> torch.Tensor:
+    if nbytes == 0:
+        raise GdnError(DN_ERR_INVALID_ARG, where)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+# ------------------------------------------------------------------ convolution
+
+def conv_shape(x: torch.Tensor, width: int, silu: bool = True, cu_seqlens=None) -> bytes:
+    """dn_conv_shape record of x [B,H,T,d]."""
+    B, H, T, d = x.shape
+    cu, n = _cu(cu_seqlens, B)
+    return _CONV_SHAPE.pack(B, H, T, d, width, _dtype_code(x, "x"), 1 if silu else 0, n, cu)
+
+
+def dn_conv_workspace_size(shape: bytes, for_backward: bool = False) -> int:
+    return int(_L().dn_conv_workspace_size(shape, int(for_backward)))
+
+
+def dn_conv_fwd(shape, x, w, bias, s0, y, sT, ws, stream=None):
+    _check(_L().dn_conv_fwd(shape, _view4(x), _p(w), _p(bias), _p(s0), _view4(y), _p(sT), _p(ws),
+                            ws.numel() * ws.element_size(), _stream(stream)), "dn_conv_fwd")
+
+
+def dn_conv_bwd(shape, x, w, bias, s0, dy, dsT, dx, dw, dbias, ds0, ws, stream=None):
+    _check(_L().dn_conv_bwd(shape, _view4(x), _p(w), _p(bias), _p(s0), _view4(dy), _p(dsT), _view4(dx),
+                            _p(dw), _p(dbias), _p(ds0), _p(ws), ws.numel() * ws.element_size(),
+                            _stream(stream)), "dn_conv_bwd")
+
+
+def dn_conv_step(shape, x, w, bias, state_in, state_out, y, stream=None):
+    _check(_L().dn_conv_step(shape, _view4(x), _p(w), _p(bias), _p(state_in), _p(state_out), _view4(y),
+                             _stream(stream)), "dn_conv_step")
+
+
+def _conv_args(x, w, bias, state, cu_seqlens):
+    if x.dim() not in (3, 4):
+        raise ValueError("x must be [B,H,T,d] or [B,T,C], got %d axes" % x.dim())
+    x4 = _four(x)
+    B, H, T, d = x4.shape
+    _tokens(x4, "x", x4.shape, x.dtype)
+    if w.dim() != 2:
+        raise ValueError("w must be [channels, width]")
+    width = w.shape[1]
+    _dense(w, "w", (H * d, width))
+    _dense(bias, "bias", (H * d,))
+    n = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    _dense(state, "state", (n, width - 1, H * d), x.dtype)
+    _same_device(x, w, bias, state, cu_seqlens)
+    return x4, n, width
+
+
+def conv_forward(x, w, bias=None, state=None, cu_seqlens=None, silu=True, out=None, want_state=True, ws=None,
+                 check_status=True):
+    """Short causal convolution.  x [B,H,T,d] or [B,T,C] (any strides, contiguous features),
+    w [C,width] and bias [C] float32 with C = H d, width 2..4; state [N,width-1,C] in x's dtype:
+    the inputs before each sequence (None: zero).  Returns (y, final state or None); y is a new
+    contiguous tensor of x's shape, or ``out``."""
+    x4, n, width = _conv_args(x, w, bias, state, cu_seqlens)
+    y = _result(out, "out", x)
+    sT = torch.empty((n, width - 1, w.shape[0]), dtype=x.dtype, device=x.device) if want_state else None
+    shape = conv_shape(x4, width, silu, cu_seqlens)
+    if ws is None:
+        ws = _ws(dn_conv_workspace_size(shape, False), x.device, "dn_conv_fwd")
+    dn_conv_fwd(shape, x4, w, bias, state, _four(y), sT, ws)
+    if check_status and cu_seqlens is not None:
+        _check(dn_device_status(ws), "dn_conv_fwd (device status)")
+    return y, sT
+
+
+def conv_backward(x, w, bias, state, dy, dstate=None, cu_seqlens=None, silu=True, out=None, ws=None, check_status=True):
+    """Gradients of <y, dy> + <final state, dstate>: dict dx (x's shape; contiguous, or ``out``), dw, dbias
+    (None without bias), dstate (of the initial state, None without one)."""
+    x4, n, width = _conv_args(x, w, bias, state, cu_seqlens)
+    _tokens(dy, "dy", x.shape, x.dtype)
+    _dense(dstate, "dstate", (n, width - 1, w.shape[0]), x.dtype)
+    _same_device(x, dy, dstate)
+    dx = _result(out, "out", x)
+    g = dict(dx=dx, dw=torch.empty_like(w), dbias=None if bias is None else torch.empty_like(bias),
+             dstate=None if state is None else torch.empty_like(state))
+    shape = conv_shape(x4, width, silu, cu_seqlens)
+    if ws is None:
+        ws = _ws(dn_conv_workspace_size(shape, True), x.device, "dn_conv_bwd")
+    dn_conv_bwd(shape, x4, w, bias, state, _four(dy), dstate, _four(dx), g["dw"], g["dbias"], g["dstate"], ws)
+    if check_status and cu_seqlens is not None:
+        _check(dn_device_status(ws), "dn_conv_bwd (device status)")
+    return g
+
+
+def conv_step(x, w, bias=None, state=None, out_state=None, silu=True, out=None):
+    """One token per sequence: x [N,C], state [N,width-1,C] (None: zero).  Returns (y, new state); pass
+    out_state=state to update the state in place."""
+    if x.dim() != 2:
+        raise ValueError("x must be [N,C], got %d axes" % x.dim())
+    N, C = x.shape
+    _tokens(x, "x", x.shape, x.dtype)
+    width = w.shape[1]
+    _dense(w, "w", (C, width))
+    _dense(bias, "bias", (C,))
+    sshape = (N, width - 1, C)
+    _dense(state, "state", sshape, x.dtype)
+    _same_device(x, w, bias, state, out_state)
+    y = _result(out, "out", x)
+    if out_state is None:
+        out_state = torch.empty(sshape, dtype=x.dtype, device=x.device)
+    else:
+        _dense(out_state, "out_state", sshape, x.dtype)
+    shape = _CONV_SHAPE.pack(N, 1, 1, C, width, _dtype_code(x, "x"), 1 if silu else 0, 0, 0)
+    _check(_L().dn_conv_step(shape, _VIEW.pack(x.data_ptr(), x.stride(0), 0, 0), _p(w), _p(bias), _p(state),
+                             _p(out_state), _VIEW.pack(y.data_ptr(), y.stride(0), 0, 0), _stream(None)), "dn_conv_step")
+    return y, out_state
+
+
+# ------------------------------------------------------------------ norm
+
+def norm_shape(x4: torch.Tensor, w: torch.Tensor, eps: float) -> bytes:
+    """dn_norm_shape record of x [B,H,T,d] and w [d] or [H,d]."""
+    B, H, T, d = x4.shape
+    return _NORM_SHAPE.pack(B, H, T, d, _dtype_code(x4, "x"), 1 if w.dim() == 2 else 0, eps, 0)
+
+
+def dn_norm_workspace_size(shape: bytes) -> int:
+    return int(_L().dn_norm_workspace_size(shape))
+
+
+def dn_norm_fwd(shape, x, w, z, residual, res_scale, y, sum, stream=None):
+    _check(_L().dn_norm_fwd(shape, _view4(x), _p(w), _view4(z), _view4(residual), _p(res_scale), _view4(y),
+                            _view4(sum), _stream(stream)), "dn_norm_fwd")
+
+
+def dn_norm_bwd(shape, x, w, z, res_scale, sum, dy, dsum, dx, dw, dz, dresidual, dres_scale, ws, stream=None):
+    _check(_L().dn_norm_bwd(shape, _view4(x), _p(w), _view4(z), _p(res_scale), _view4(sum), _view4(dy),
+                            _view4(dsum), _view4(dx), _p(dw), _view4(dz), _view4(dresidual), _p(dres_scale),
+                            _p(ws), ws.numel() * ws.element_size(), _stream(stream)), "dn_norm_bwd")
+
+
+def _rows(t, name, x):
+    """x [..., d] of 2, 3 or 4 axes as [B,H,T,d]: [R,d] -> [1,1,R,d], [B,T,d] -> [B,1,T,d]."""
+    if t is None:
+        return None
+    _tokens(t, name, x.shape, x.dtype)
+    return t[None, None] if t.dim() == 2 else _four(t)
+
+
+def _norm_args(x, w):
+    if x.dim() not in (2, 3, 4):
+        raise ValueError("x must be [R,d], [B,T,d] or [B,H,T,d], got %d axes" % x.dim())
+    x4 = _rows(x, "x", x)
+    H, d = x4.shape[1], x4.shape[3]
+    _dense(w, "w", (H, d) if w.dim() == 2 else (d,))
+    return x4, d
+
+
+def norm_forward(x, w, z=None, residual=None, res_scale=None, eps=1e-6, out=None, out_sum=None):
+    """RMS norm over the last axis.  x [R,d], [B,T,d] or [B,H,T,d]; w [d], or [H,d] for a weight per head.
+    z: gate, y = rms(r) w silu(z).  residual: r = residual + res_scale x (res_scale [d] float32 or
+    None: 1), otherwise r = x.  Returns y, or (y, r) with a residual."""
+    x4, d = _norm_args(x, w)
+    _dense(res_scale, "res_scale", (d,))
+    if residual is None and (res_scale is not None or out_sum is not None):
+        raise ValueError("res_scale and out_sum need a residual")
+    _same_device(x, w, z, residual, res_scale)
+    y = _result(out, "out", x)
+    r = None if residual is None else _result(out_sum, "out_sum", x)
+    dn_norm_fwd(norm_shape(x4, w, eps), x4, w, _rows(z, "z", x), _rows(residual, "residual", x), res_scale,
+                _rows(y, "out", x), _rows(r, "out_sum", x))
+    return y if residual is None else (y, r)
+
+
+def norm_backward(x, w, dy, z=None, sum=None, dsum=None, res_scale=None, eps=1e-6, ws=None):
+    """Gradients of <y, dy> + <r, dsum>.  Without a residual r = x; with one pass ``sum`` = r as norm_forward
+    returned it, and x.  Returns dict dx, dw, dz (with z), dresidual (with sum), dres_scale (with
+    res_scale); the others are None."""
+    x4, d = _norm_args(x, w)
+    _dense(res_scale, "res_scale", (d,))
+    if sum is None and (res_scale is not None or dsum is not None):
+        raise ValueError("res_scale and dsum need sum (the residual sum of the forward pass)")
+    _same_device(x, w, dy, z, sum, dsum, res_scale)
+    new = lambda: torch.empty(x.shape, dtype=x.dtype, device=x.device)  # noqa: E731
+    dres = None if sum is None else new()
+    # without a scale dx and dresidual are the same gradient: one tensor
+    dx = new() if sum is None or res_scale is not None else None
+    g = dict(dx=dres if dx is None else dx, dw=torch.empty_like(w), dz=None if z is None else new(), dresidual=dres,
+             dres_scale=None if res_scale is None else torch.empty_like(res_scale))
+    shape = norm_shape(x4, w, eps)
+    if ws is None:
+        ws = _ws(dn_norm_workspace_size(shape), x.device, "dn_norm_bwd")
+    v = lambda t, name: _rows(t, name, x)  # noqa: E731
+    dn_norm_bwd(shape, x4, w, v(z, "z"), res_scale, v(sum, "sum"), v(dy, "dy"), v(dsum, "dsum"), v(dx, "dx"), g["dw"],
+                v(g["dz"], "dz"), v(dres, "dresidual"), g["dres_scale"], ws)
+    return g
