@@ -13,5 +13,6 @@ from .binding import (  # noqa: F401
     make_shape, saved_supported,
 )
 from .layers import (  # noqa: F401
-    conv_backward, conv_forward, conv_step, norm_backward, norm_forward,
+    conv_backward, conv_forward, conv_step, norm_backward, norm_forward, scan_backward, scan_forward,
+    scan_step,
 )

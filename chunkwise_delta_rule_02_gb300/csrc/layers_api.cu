@@ -3,6 +3,7 @@
 #include <string.h>
 
 #include "layers.h"
+#include "scan.cuh"
 
 namespace gdn {
 namespace lay {
@@ -135,6 +136,62 @@ dn_status norm_shape_ok(const dn_norm_shape *s)
     return DN_OK;
 }
 
+// ------------------------------------------------------------------ scan
+constexpr int kMaxStates = 128;
+
+dn_status scan_shape_ok(const dn_scan_shape *s)
+{
+    if (!s || s->B < 1 || s->T < 0 || s->D < 1 || s->N < 1 || s->G < 1 || s->D % s->G) return DN_ERR_INVALID_ARG;
+    if (s->dtype != DN_F32 && s->dtype != DN_BF16) return DN_ERR_INVALID_ARG;
+    if (s->N > kMaxStates || s->D > (1 << 24) || s->T > kMaxT) return DN_ERR_UNSUPPORTED;
+    return check_packed(s->cu_seqlens, s->B, s->num_seqs);
+}
+
+size_t scan_offsets(const dn_scan_shape *s)
+{
+    return 256 + (s->cu_seqlens ? align256(sizeof(int32_t) * ((size_t)s->num_seqs + 1)) : 0);
+}
+
+size_t scan_saved(const dn_scan_shape *s)
+{
+    const size_t n = (size_t)s->B * ((s->T + kScanKeep - 1) / kScanKeep) * s->D * scan_padded(s->N) * sizeof(float);
+    return n ? n : 256;
+}
+
+dn_status scan_io_ok(const dn_scan_shape *s, const dn_scan_io *io, bool need_y)
+{
+    if (!io || !io->A) return DN_ERR_INVALID_ARG;
+    const size_t e = s->dtype == DN_F32 ? 4 : 2;
+    const float *params[] = {io->A, io->D, io->dt_bias, io->h0, io->hT};
+    for (const float *p : params)
+        if (!aligned(p, 4)) return DN_ERR_INVALID_ARG;
+    if (s->T > 0 && (!io->x.data || !io->dt.data || !io->b.data || !io->c.data || (need_y && !io->y.data)))
+        return DN_ERR_INVALID_ARG;
+    const dn_view *views[] = {&io->x, &io->dt, &io->b, &io->c, &io->z, &io->y};
+    for (const dn_view *v : views)
+        if (v->data && !aligned(v->data, e)) return DN_ERR_INVALID_ARG;
+    return DN_OK;
+}
+
+dn_status scan_begin(ScanCall &c, const dn_scan_shape *s, const dn_scan_io *io, size_t need, void *ws, size_t ws_bytes,
+                     cudaStream_t st)
+{
+    const size_t head = scan_offsets(s);
+    if (!ws || !aligned(ws, 16) || ws_bytes < head + need) return DN_ERR_WORKSPACE;
+    memset(&c, 0, sizeof(c));
+    c.s = s;
+    c.io = io;
+    c.Nseq = s->cu_seqlens ? s->num_seqs : s->B;
+    c.ws = (char *)ws + head;
+    if (s->cu_seqlens) {
+        if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return DN_ERR_CUDA;
+        int32_t *cu = (int32_t *)((char *)ws + 256);
+        c.cu = cu;
+        return status_of(check_offsets(s->cu_seqlens, s->num_seqs, s->T, cu, (uint32_t *)ws, st));
+    }
+    return DN_OK;
+}
+
 }  // namespace
 }  // namespace lay
 }  // namespace gdn
@@ -201,6 +258,66 @@ dn_status dn_conv_step(const dn_conv_shape *shape, const dn_view *x, const float
     c.s = shape; c.N = shape->B;
     c.x = x; c.y = y; c.w = w; c.bias = bias; c.s0 = state_in; c.sT = state_out;
     return status_of(conv_step(c, (cudaStream_t)stream));
+}
+
+size_t dn_scan_workspace_size(const dn_scan_shape *shape, int for_backward)
+{
+    if (scan_shape_ok(shape) != DN_OK) return 0;
+    return scan_offsets(shape) + (for_backward ? scan_bwd_bytes(shape) : scan_fwd_bytes(shape));
+}
+
+size_t dn_scan_saved_size(const dn_scan_shape *shape) { return scan_shape_ok(shape) == DN_OK ? scan_saved(shape) : 0; }
+
+dn_status dn_scan_fwd(const dn_scan_shape *shape, const dn_scan_io *io, void *saved, size_t saved_bytes, void *ws,
+                      size_t ws_bytes, void *stream)
+{
+    dn_status rc = scan_shape_ok(shape);
+    if (rc != DN_OK) return rc;
+    if ((rc = scan_io_ok(shape, io, true)) != DN_OK) return rc;
+    if (saved && (!aligned(saved, 16) || saved_bytes < scan_saved(shape))) return DN_ERR_WORKSPACE;
+    ScanCall c;
+    if ((rc = scan_begin(c, shape, io, scan_fwd_bytes(shape), ws, ws_bytes, (cudaStream_t)stream)) != DN_OK) return rc;
+    c.keep = (float *)saved;
+    return status_of(scan_fwd(c, (cudaStream_t)stream));
+}
+
+dn_status dn_scan_bwd(const dn_scan_shape *shape, const dn_scan_io *io, const dn_scan_grads *grads, const void *saved,
+                      size_t saved_bytes, void *ws, size_t ws_bytes, void *stream)
+{
+    dn_status rc = scan_shape_ok(shape);
+    if (rc != DN_OK) return rc;
+    if ((rc = scan_io_ok(shape, io, false)) != DN_OK) return rc;
+    const size_t e = shape->dtype == DN_F32 ? 4 : 2;
+    if (!grads || !grads->dA) return DN_ERR_INVALID_ARG;
+    const float *params[] = {grads->dhT, grads->dA, grads->dD, grads->ddt_bias, grads->dh0};
+    for (const float *p : params)
+        if (!aligned(p, 4)) return DN_ERR_INVALID_ARG;
+    if (shape->T > 0 && (!grads->dy.data || !grads->dx.data || !grads->ddt.data || !grads->db.data || !grads->dc.data ||
+                         (io->z.data && !grads->dz.data)))
+        return DN_ERR_INVALID_ARG;
+    const dn_view *views[] = {&grads->dy, &grads->dx, &grads->ddt, &grads->db, &grads->dc, &grads->dz};
+    for (const dn_view *v : views)
+        if (v->data && !aligned(v->data, e)) return DN_ERR_INVALID_ARG;
+    if (!saved || !aligned(saved, 16) || saved_bytes < scan_saved(shape)) return DN_ERR_WORKSPACE;
+    ScanCall c;
+    if ((rc = scan_begin(c, shape, io, scan_bwd_bytes(shape), ws, ws_bytes, (cudaStream_t)stream)) != DN_OK) return rc;
+    c.gr = grads;
+    c.keep = (float *)saved;
+    return status_of(scan_bwd(c, (cudaStream_t)stream));
+}
+
+dn_status dn_scan_step(const dn_scan_shape *shape, const dn_scan_io *io, void *stream)
+{
+    dn_status rc = scan_shape_ok(shape);
+    if (rc != DN_OK) return rc;
+    if (shape->T != 1 || shape->cu_seqlens) return DN_ERR_INVALID_ARG;
+    if ((rc = scan_io_ok(shape, io, true)) != DN_OK) return rc;
+    ScanCall c;
+    memset(&c, 0, sizeof(c));
+    c.s = shape;
+    c.io = io;
+    c.Nseq = shape->B;
+    return status_of(scan_step(c, (cudaStream_t)stream));
 }
 
 dn_status dn_norm_fwd(const dn_norm_shape *shape, const dn_view *x, const float *w, const dn_view *z,

@@ -29,13 +29,15 @@ from . import binding
 from .binding import DN_BF16, DN_ERR_INVALID_ARG, DN_F32, GdnError, _check, dn_device_status
 
 EXPORTS = ["dn_conv_workspace_size", "dn_conv_fwd", "dn_conv_bwd", "dn_conv_step", "dn_norm_fwd",
-           "dn_norm_workspace_size", "dn_norm_bwd"]
+           "dn_norm_workspace_size", "dn_norm_bwd", "dn_scan_workspace_size", "dn_scan_saved_size",
+           "dn_scan_fwd", "dn_scan_bwd", "dn_scan_step"]
 
 _DTYPES = {torch.float32: DN_F32, torch.bfloat16: DN_BF16}
 _CONV_SHAPE = struct.Struct("8iq")        # dn_conv_shape
 _NORM_SHAPE = struct.Struct("6ifi")       # dn_norm_shape
+_SCAN_SHAPE = struct.Struct("8iq")        # dn_scan_shape
+_SCAN_IO = struct.Struct("29q")           # dn_scan_io, dn_scan_grads: six views, five pointers
 _VIEW = struct.Struct("4q")               # dn_view
-_NO_VIEW = _VIEW.pack(0, 0, 0, 0)
 
 _lib = None
 
@@ -54,6 +56,11 @@ def _L():
                 ("dn_conv_step", [R, R, P, P, P, P, R, P], I),
                 ("dn_norm_fwd", [R, R, P, R, R, P, R, R, P], I),
                 ("dn_norm_workspace_size", [R], S),
+                ("dn_scan_workspace_size", [R, I], S),
+                ("dn_scan_saved_size", [R], S),
+                ("dn_scan_fwd", [R, R, P, S, P, S, P], I),
+                ("dn_scan_bwd", [R, R, R, P, S, P, S, P], I),
+                ("dn_scan_step", [R, R, P], I),
                 ("dn_norm_bwd", [R, R, P, R, P, R, R, R, R, P, R, R, P, P, S, P], I)):
             f = getattr(L, name)
             f.argtypes, f.restype = args, res
@@ -266,6 +273,159 @@ def conv_step(x, w, bias=None, state=None, out_state=None, silu=True, out=None):
     shape = _CONV_SHAPE.pack(N, 1, 1, C, width, _dtype_code(x, "x"), 1 if silu else 0, 0, 0)
     _check(_L().dn_conv_step(shape, _VIEW.pack(x.data_ptr(), x.stride(0), 0, 0), _p(w), _p(bias), _p(state),
                              _p(out_state), _VIEW.pack(y.data_ptr(), y.stride(0), 0, 0), _stream(None)), "dn_conv_step")
+    return y, out_state
+
+
+# ------------------------------------------------------------------ selective scan
+
+def _flat(t: Optional[torch.Tensor]):
+    """[B,T,D] as the four numbers of a dn_view."""
+    if t is None:
+        return 0, 0, 0, 0
+    b, tm, _ = t.stride()
+    return t.data_ptr(), b, 0, tm
+
+
+def _grouped(t: torch.Tensor):
+    """[B,T,G,N] likewise (head = group)."""
+    b, tm, g, _ = t.stride()
+    return t.data_ptr(), b, g, tm
+
+
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def scan_shape(x: torch.Tensor, Bm: torch.Tensor, dt_softplus: bool = True, cu_seqlens=None) -> bytes:
+    """dn_scan_shape record of x [B,T,D] and Bm [B,T,G,N]."""
+    B, T, D = x.shape
+    cu, n = _cu(cu_seqlens, B)
+    return _SCAN_SHAPE.pack(B, T, D, Bm.shape[3], Bm.shape[2], _dtype_code(x, "x"), 1 if dt_softplus else 0, n, cu)
+
+
+def scan_io(x, dt, A, B, C, D, z, dt_bias, h0, y, hT) -> bytes:
+    """dn_scan_io record; x, dt, z, y [B,T,D], B, C [B,T,G,N]."""
+    return _SCAN_IO.pack(*_flat(x), *_flat(dt), *_grouped(B), *_grouped(C), *_flat(z), *_flat(y), A.data_ptr(),
+                         _ptr(D), _ptr(dt_bias), _ptr(h0), _ptr(hT))
+
+
+def scan_grads(dy, dx, ddt, dB, dC, dz, dhT, dA, dD, ddt_bias, dh0) -> bytes:
+    """dn_scan_grads record."""
+    return _SCAN_IO.pack(*_flat(dy), *_flat(dx), *_flat(ddt), *_grouped(dB), *_grouped(dC), *_flat(dz), _ptr(dhT),
+                         dA.data_ptr(), _ptr(dD), _ptr(ddt_bias), _ptr(dh0))
+
+
+def dn_scan_workspace_size(shape: bytes, for_backward: bool = False) -> int:
+    return int(_L().dn_scan_workspace_size(shape, int(for_backward)))
+
+
+def dn_scan_saved_size(shape: bytes) -> int:
+    return int(_L().dn_scan_saved_size(shape))
+
+
+def dn_scan_fwd(shape, io, saved, ws, stream=None):
+    _check(_L().dn_scan_fwd(shape, io, _p(saved), 0 if saved is None else saved.numel() * saved.element_size(), _p(ws),
+                            ws.numel() * ws.element_size(), _stream(stream)), "dn_scan_fwd")
+
+
+def dn_scan_bwd(shape, io, grads, saved, ws, stream=None):
+    _check(_L().dn_scan_bwd(shape, io, grads, _p(saved), saved.numel() * saved.element_size(), _p(ws),
+                            ws.numel() * ws.element_size(), _stream(stream)), "dn_scan_bwd")
+
+
+def dn_scan_step(shape, io, stream=None):
+    _check(_L().dn_scan_step(shape, io, _stream(stream)), "dn_scan_step")
+
+
+def _scan_args(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens):
+    if x.dim() != 3:
+        raise ValueError("x must be [B,T,D], got %d axes" % x.dim())
+    nb, T, Dc = x.shape
+    if A.dim() != 2:
+        raise ValueError("A must be [D,N]")
+    N = A.shape[1]
+    # one group: B and C may come without the group axis
+    B4 = B.unsqueeze(2) if B.dim() == 3 else B
+    C4 = C.unsqueeze(2) if C.dim() == 3 else C
+    if B4.dim() != 4 or B4.shape[2] < 1 or Dc % B4.shape[2]:
+        raise ValueError("B must be [B,T,G,N] (or [B,T,N]) with G dividing the %d channels" % Dc)
+    dtype = x.dtype
+    _dtype_code(x, "x")
+    _tokens(x, "x", x.shape, dtype)
+    _tokens(dt, "dt", x.shape, dtype)
+    if z is not None:
+        _tokens(z, "z", x.shape, dtype)
+    _tokens(B4, "B", (nb, T, B4.shape[2], N), dtype)
+    _tokens(C4, "C", B4.shape, dtype)
+    _dense(A, "A", (Dc, N))
+    _dense(D, "D", (Dc,))
+    _dense(dt_bias, "dt_bias", (Dc,))
+    n = nb if cu_seqlens is None else cu_seqlens.numel() - 1
+    _dense(h0, "h0", (n, Dc, N))
+    _same_device(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens)
+    return B4, C4, n
+
+
+def scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=None, dt_softplus=True, out=None,
+                 want_state=True, save=False, ws=None, check_status=True):
+    """Selective state space scan.  x, dt, z (gate, optional) [B,T,D]; B, C [B,T,G,N] or [B,T,N];
+    A [D,N], D, dt_bias [D] and the initial states h0 [N_seq,D,N] float32; 1 <= N <= 128.  The step is
+    softplus(dt + dt_bias) (dt + dt_bias with dt_softplus=False); A <= 0 and steps >= 0 decay.
+    Returns (y, hT), or (y, hT, saved) with save=True for scan_backward(saved=saved): the states
+    entering every 16th token, N / 4 bytes a token and channel."""
+    B4, C4, n = _scan_args(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens)
+    y = _result(out, "out", x)
+    hT = torch.empty((n,) + tuple(A.shape), dtype=torch.float32, device=x.device) if want_state else None
+    shape = scan_shape(x, B4, dt_softplus, cu_seqlens)
+    if ws is None:
+        ws = _ws(dn_scan_workspace_size(shape, False), x.device, "dn_scan_fwd")
+    saved = _ws(dn_scan_saved_size(shape), x.device, "dn_scan_fwd") if save else None
+    dn_scan_fwd(shape, scan_io(x, dt, A, B4, C4, D, z, dt_bias, h0, y, hT), saved, ws)
+    if check_status and cu_seqlens is not None:
+        _check(dn_device_status(ws), "dn_scan_fwd (device status)")
+    return (y, hT, saved) if save else (y, hT)
+
+
+def scan_backward(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, dy=None, dhT=None, saved=None, cu_seqlens=None,
+                  dt_softplus=True, ws=None, check_status=True):
+    """Gradients of <y, dy> + <hT, dhT>, from scan_forward's arguments and ``saved`` buffer.  Returns dict
+    dx, ddt, dA, dB, dC, and dD, dz, ddt_bias, dh0 (None for an argument that was not given)."""
+    B4, C4, n = _scan_args(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens)
+    if dy is None or saved is None:
+        raise ValueError("scan_backward needs dy and saved (scan_forward(save=True))")
+    _tokens(dy, "dy", x.shape, x.dtype)
+    _dense(dhT, "dhT", (n,) + tuple(A.shape))
+    _same_device(x, dy, dhT, saved)
+    new = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
+    g = dict(dx=new(x), ddt=new(x), dA=new(A), dB=new(B), dC=new(C), dD=new(D), dz=new(z), ddt_bias=new(dt_bias), dh0=new(h0))
+    shape = scan_shape(x, B4, dt_softplus, cu_seqlens)
+    if ws is None:
+        ws = _ws(dn_scan_workspace_size(shape, True), x.device, "dn_scan_bwd")
+    dB4 = g["dB"].view(B4.shape)
+    dC4 = g["dC"].view(C4.shape)
+    dn_scan_bwd(shape, scan_io(x, dt, A, B4, C4, D, z, dt_bias, h0, None, None),
+                scan_grads(dy, g["dx"], g["ddt"], dB4, dC4, g["dz"], dhT, g["dA"], g["dD"], g["ddt_bias"], g["dh0"]), saved, ws)
+    if check_status and cu_seqlens is not None:
+        _check(dn_device_status(ws), "dn_scan_bwd (device status)")
+    return g
+
+
+def scan_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, state=None, out_state=None, dt_softplus=True, out=None):
+    """One token per sequence: x, dt, z [n,D], B, C [n,G,N] or [n,N], state [n,D,N] float32 (None: zero).
+    Returns (y, new state); pass out_state=state to update the states in place."""
+    if x.dim() != 2:
+        raise ValueError("x must be [n,D], got %d axes" % x.dim())
+    one = lambda t: None if t is None else t.unsqueeze(1)  # noqa: E731
+    x3 = one(x)
+    B4, C4, n = _scan_args(x3, one(dt), A, one(B), one(C), D, one(z), dt_bias, state, None)
+    y = _result(out, "out", x)
+    sshape = (n,) + tuple(A.shape)
+    if out_state is None:
+        out_state = torch.empty(sshape, dtype=torch.float32, device=x.device)
+    else:
+        _dense(out_state, "out_state", sshape)
+        _same_device(x, out_state)
+    dn_scan_step(scan_shape(x3, B4, dt_softplus), scan_io(x3, one(dt), A, B4, C4, D, one(z), dt_bias, state, one(y), out_state))
     return y, out_state
 
 

@@ -1,7 +1,8 @@
 /*
  * gdn_layers.h — C ABI of the layer operators around the delta rule, in the same
  * library (libgdn_gb300.so, sm_103a): the short causal convolution ahead of
- * q, k, v, and the RMS norm with its output gate or its residual sum.
+ * q, k, v, the selective state space scan of the layers that hybrid stacks mix
+ * with the delta rule, and the RMS norm with its output gate or its residual sum.
  *
  * Token arrays are passed as dn_view: a base pointer and element strides of the
  * batch, head and time axes; the feature axis is contiguous.  So the projection's
@@ -76,6 +77,60 @@ dn_status dn_conv_bwd(const dn_conv_shape *shape, const dn_view *x, const float 
 dn_status dn_conv_step(const dn_conv_shape *shape, const dn_view *x, const float *w,
                        const float *bias, const void *state_in, void *state_out, const dn_view *y,
                        void *stream);
+
+/* ------------------------------------------------------- selective state space scan
+ * D channels with N states each; B and C are shared by the D / G channels of a group:
+ *     delta = dt_softplus ? softplus(dt + dt_bias) : dt + dt_bias
+ *     h_t[c][n] = exp(delta A[c][n]) h_{t-1}[c][n] + delta x_t[c] B_t[g][n]
+ *     o_t[c]    = sum_n C_t[g][n] h_t[c][n] + D[c] x_t[c]
+ *     y_t[c]    = z ? o_t[c] silu(z_t[c]) : o_t[c]
+ * A <= 0 and delta >= 0 in use (a decay); nothing checks either.                  */
+typedef struct {
+    int32_t B, T, D;              /* batch rows, tokens per row, channels          */
+    int32_t N, G;                 /* states per channel 1..128, groups (D % G == 0) */
+    int32_t dtype, dt_softplus;
+    int32_t num_seqs;
+    const int32_t *cu_seqlens;
+} dn_scan_shape;
+
+typedef struct {
+    dn_view x, dt, b, c;          /* [B][T][D] (no head axis), [B][G][T][N] (head = group) */
+    dn_view z, y;                 /* [B][T][D]; z.data == NULL: no gate             */
+    const float *A;               /* [D][N]                                        */
+    const float *D, *dt_bias;     /* [D] or NULL (zero)                            */
+    const float *h0;              /* [N_seq][D][N] initial states or NULL (zero)    */
+    float *hT;                    /* final states or NULL                          */
+} dn_scan_io;
+
+typedef struct {
+    dn_view dy;                   /* gradient of y                                 */
+    dn_view dx, ddt, db, dc;      /* all written                                   */
+    dn_view dz;                   /* written when io.z is given                     */
+    const float *dhT;             /* gradient of hT or NULL (zero)                 */
+    float *dA;                    /* [D][N]                                        */
+    float *dD, *ddt_bias;         /* [D] or NULL (not written)                     */
+    float *dh0;                   /* [N_seq][D][N] or NULL (not written)           */
+} dn_scan_grads;
+
+size_t dn_scan_workspace_size(const dn_scan_shape *shape, int for_backward);
+
+/* Bytes of the buffer that dn_scan_fwd fills for dn_scan_bwd: the state entering every 16th
+ * token, float32 (4 N bytes per 16 tokens and channel). */
+size_t dn_scan_saved_size(const dn_scan_shape *shape);
+
+/* saved may be NULL (nothing kept). */
+dn_status dn_scan_fwd(const dn_scan_shape *shape, const dn_scan_io *io, void *saved,
+                      size_t saved_bytes, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradients of <y, dy> + <hT, dhT>, from the buffer that dn_scan_fwd filled for the same
+ * arguments (the library does not check that they are the same). */
+dn_status dn_scan_bwd(const dn_scan_shape *shape, const dn_scan_io *io, const dn_scan_grads *grads,
+                      const void *saved, size_t saved_bytes, void *ws, size_t ws_bytes,
+                      void *stream);
+
+/* One token for each of B sequences (T must be 1, no packing), states io->h0 -> io->hT, which
+ * may be the same buffer.  No workspace. */
+dn_status dn_scan_step(const dn_scan_shape *shape, const dn_scan_io *io, void *stream);
 
 /* --------------------------------------------------------------------------- norm
  * Per row of d features:

@@ -2,8 +2,9 @@
 64-bit forms: types, widths, odd sizes, strides, packed sequences with empty and one-token members,
 initial and final taps, gradients (against the formula's and against differences), refusals.
 
-Bounds, relative Frobenius per tensor.  A bf16 result is a float32 one rounded once: at most 2^-9 an
-element, so at most 2^-9 in the norm.  float32 results: the sums of the longest case (some 1000 terms,
+Bounds, relative Frobenius per tensor.  A bf16 result is a float32 one rounded once to 8 significant bits:
+at most 2^-8 an element, 2^-8 / sqrt(3) / 1.4 = 1.7e-3 over many (errors uniform within half a unit in the
+last place, significands spread over [1, 2)); 2^-9 = 1.95e-3 is asked.  float32 results: the sums of the longest case (some 1000 terms,
 summed in runs of 64 and then pairwise-like) and the exponential and reciprocal of the sigmoid (a few
 2^-22, its argument's rounding included) stay below 5e-6."""
 import math
