@@ -57,10 +57,17 @@ struct Vec {
     }
     __device__ __forceinline__ void set(const float (&f)[V])
     {
-        T e[V];
+        if constexpr (sizeof(T) == 2 && V % 2 == 0) {   // two conversions an instruction
+            __nv_bfloat162 e[V / 2];
 #pragma unroll
-        for (int i = 0; i < V; ++i) st_out(&e[i], f[i]);
-        memcpy(&raw, e, sizeof(e));
+            for (int i = 0; i < V / 2; ++i) e[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            memcpy(&raw, e, sizeof(e));
+        } else {
+            T e[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) st_out(&e[i], f[i]);
+            memcpy(&raw, e, sizeof(e));
+        }
     }
 };
 
@@ -73,31 +80,87 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + ex2(-kLog2e * x)); }
+// 1 / x for x >= 1 (the plain division's care for denormal divisors is several instructions)
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
 
 // d/dx of x sigmoid(x)
 __device__ __forceinline__ float dsilu(float x, float s) { return s * fmaf(x, 1.f - s, 1.f); }
 
-// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1], and its derivative
-// sigmoid(x).  log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by the series
-// 2 (s + s^3/3 + s^5/5 + ...): lg2(1 + e) would lose the small e of small steps
-// (delta ~ 1e-3) to the rounding of 1 + e.  Terms to s^15: the first one left out
-// is below 2 (1/3)^17 / 17 = 1e-9 absolute, 1.3e-9 of log1p(1).
-__device__ __forceinline__ void softplus(float x, float &val, float &der)
+// Pairs of float32 in one instruction: these kernels run out of issue slots before
+// they run out of the float32 pipe.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
 {
-    const float e = ex2(-kLog2e * fabsf(x));
-    const float s = __fdividef(e, 2.f + e), q = s * s;
-    float p = fmaf(q, 1.f / 15.f, 1.f / 13.f);
-    p = fmaf(q, p, 1.f / 11.f);
-    p = fmaf(q, p, 1.f / 9.f);
-    p = fmaf(q, p, 1.f / 7.f);
-    p = fmaf(q, p, 1.f / 5.f);
-    p = fmaf(q, p, 1.f / 3.f);
-    p = fmaf(q, p, 1.f);
-    val = fmaf(2.f * s, p, fmaxf(x, 0.f));
-    const float r = __fdividef(1.f, 1.f + e);
-    der = x >= 0.f ? r : e * r;
-    if (x != x) val = x;   // fmaxf drops a NaN
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long &>(r))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return r;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<unsigned long long &>(r))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)),
+          "l"(reinterpret_cast<unsigned long long &>(c)));
+    return r;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long &>(r))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return r;
+}
+
+__device__ __forceinline__ float2 two(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 ex2_2(float2 a) { return make_float2(ex2(a.x), ex2(a.y)); }
+
+// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1], and its derivative
+// sigmoid(x).  log1p(e) = 2 atanh(s) = 2 s f(s^2), s = e / (2 + e) <= 1/3: lg2(1 + e)
+// would lose the small e of small steps (delta ~ 1e-3) to the rounding of 1 + e.
+// f(q) = atanh(sqrt q) / sqrt q = 1 + q/3 + q^2/5 + ... on [0, 1/9] by the polynomial of
+// degree 4 that is least off relative to f (fitted by reweighted least squares): 8e-9.
+// e is NaN where x is, so a NaN stays one although max drops it.
+__device__ __forceinline__ void softplus(float2 x, float2 &val, float2 &der)
+{
+    const float2 e = ex2_2(mul2(make_float2(fabsf(x.x), fabsf(x.y)), two(-kLog2e)));
+    const float2 u = add2(e, two(2.f));
+    const float2 s = mul2(e, make_float2(rcp(u.x), rcp(u.y))), q = mul2(s, s);
+    float2 p = fma2(q, two(0.14089517295360565f), two(0.13980233669281006f));
+    p = fma2(q, p, two(0.200124591588974f));
+    p = fma2(q, p, two(0.3333315849304199f));
+    p = fma2(q, p, two(1.f));
+    val = fma2(add2(s, s), p, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+    const float2 r = make_float2(rcp(1.f + e.x), rcp(1.f + e.y));
+    der = make_float2(x.x >= 0.f ? r.x : e.x * r.x, x.y >= 0.f ? r.y : e.y * r.y);
+}
+
+__device__ __forceinline__ float2 sigmoid2(float2 x)
+{
+    const float2 e = add2(ex2_2(mul2(x, two(-kLog2e))), two(1.f));
+    return make_float2(rcp(e.x), rcp(e.y));
+}
+
+// N floats as pairs (a single one is paired with itself)
+template <int N>
+__device__ __forceinline__ float2 pair_at(const float (&v)[N], int i)
+{
+    return N == 1 ? two(v[0]) : make_float2(v[i], v[N == 1 ? 0 : i + 1]);
+}
+
+template <int N>
+__device__ __forceinline__ void put_pair(float (&v)[N], int i, float2 a)
+{
+    v[i] = a.x;
+    if (N > 1) v[N == 1 ? 0 : i + 1] = a.y;
 }
 
 // The sequence that holds token t: the last s with cu[s] <= t (an empty sequence

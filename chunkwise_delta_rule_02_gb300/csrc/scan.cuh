@@ -5,12 +5,18 @@
 //     h_t[n] = exp(delta A[n]) h_{t-1}[n] + delta x B_t[n],  o_t = sum_n C_t[n] h_t[n] + D x
 //
 // Lane layout.  L lanes share a channel, S states each (L S = Np >= N, padded states
-// have A = B = C = 0 and stay 0); 256 threads hold CH = 256 / L channels.  Splitting a
-// channel's states over lanes gives L times the threads of one thread a channel, which
-// a few thousand channels need to fill the SMs, and keeps 16-byte reads of B_t and C_t;
-// the price, sums over the L lanes, is paid once for L tokens: the L partial sums of a
-// lane are exchanged in a halving butterfly (L - 1 shuffles) that leaves token l's sum
-// in lane l, instead of log2 L shuffles a token.
+// have A = B = C = 0 and stay 0), and a lane holds CT neighbouring channels; 256 threads
+// hold CH = 256 CT / L channels.  Splitting a channel's states over lanes gives the
+// threads that a few thousand channels need to fill the SMs; the price, sums over the L
+// lanes, is paid once for L tokens: the L partial sums of a lane are exchanged in a
+// halving butterfly (L - 1 shuffles) that leaves token l's sum in lane l, instead of
+// log2 L shuffles a token.
+//
+// What CT is for: B_t and C_t come from shared memory at 8 bytes a state, 2 cycles of the
+// SM's read port for 16 bytes a lane (measured: 2.1 where neighbouring lanes read the same
+// address, 4.0 where they do not, which is why a channel's lanes are 32 / L apart).  With one
+// channel a lane that port, at 1 cycle a state and warp for B and C alone, is what binds: the
+// exponentials and the multiply-adds take 1 cycle each.  Two channels halve it.
 #pragma once
 
 #include "layers.h"
@@ -39,46 +45,32 @@ struct ScanIo {
     float *segP, *segH;            // per segment: product of the decays, end state from zero [B][K][D][Np]
 };
 
-// ---- packed pairs: two float32 operations an instruction (issue slots, not the
-// arithmetic pipe, are what the scan runs out of first)
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    float2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long &>(r))
-        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
-    return r;
-}
-
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<unsigned long long &>(r))
-        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)),
-          "l"(reinterpret_cast<unsigned long long &>(c)));
-    return r;
-}
-
-__device__ __forceinline__ float2 two(float a) { return make_float2(a, a); }
-__device__ __forceinline__ float2 ex2_2(float2 a) { return make_float2(ex2(a.x), ex2(a.y)); }
-
-// S consecutive floats (16-byte aligned) as pairs
+// S consecutive floats (aligned to them) as pairs
 template <int S>
 __device__ __forceinline__ void load_pairs(float2 (&v)[S / 2], const float *p)
 {
+    if constexpr (S == 2) {
+        v[0] = *reinterpret_cast<const float2 *>(p);
+    } else {
 #pragma unroll
-    for (int i = 0; i < S / 4; ++i) {
-        const float4 q = reinterpret_cast<const float4 *>(p)[i];
-        v[2 * i] = make_float2(q.x, q.y);
-        v[2 * i + 1] = make_float2(q.z, q.w);
+        for (int i = 0; i < S / 4; ++i) {
+            const float4 q = reinterpret_cast<const float4 *>(p)[i];
+            v[2 * i] = make_float2(q.x, q.y);
+            v[2 * i + 1] = make_float2(q.z, q.w);
+        }
     }
 }
 
 template <int S>
 __device__ __forceinline__ void store_pairs(float *p, const float2 (&v)[S / 2])
 {
+    if constexpr (S == 2) {
+        *reinterpret_cast<float2 *>(p) = v[0];
+    } else {
 #pragma unroll
-    for (int i = 0; i < S / 4; ++i)
-        reinterpret_cast<float4 *>(p)[i] = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+        for (int i = 0; i < S / 4; ++i)
+            reinterpret_cast<float4 *>(p)[i] = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+    }
 }
 
 // A lane's states of [..][D][N] arrays (N need not be a multiple of anything)
@@ -102,26 +94,32 @@ __device__ __forceinline__ void store_states(float *p, const float2 (&v)[S / 2],
     }
 }
 
-// v[0 .. L-1] of each of L neighbouring lanes -> the sum over the lanes of v[l] in lane l
+// v[0 .. L-1] of each of a channel's L lanes (32 / L apart) -> the sum over them of v[l] in lane l
 template <int L>
 __device__ __forceinline__ float lane_sum(float (&v)[L], int lane)
 {
+    constexpr int M = 32 / L;
 #pragma unroll
     for (int m = L / 2; m > 0; m >>= 1) {
-        const bool up = lane & m;
+        const bool up = lane & (m * M);
 #pragma unroll
         for (int k = 0; k < m; ++k) {
             const float send = up ? v[k] : v[k + m], mine = up ? v[k + m] : v[k];
-            v[k] = mine + __shfl_xor_sync(0xffffffffu, send, m);
+            v[k] = mine + __shfl_xor_sync(0xffffffffu, send, m * M);
         }
     }
     return v[0];
 }
 
-// L and S by N; tokens of a tile; elements of a tile a thread moves
-template <int L_, int S_>
+// TT: tokens of a tile
+template <int L_, int S_, int CT_, int TT_ = kScanKeep>
 struct ScanCfg {
-    static constexpr int L = L_, S = S_, Np = L_ * S_, CH = kScanThreads / L_;
+    static constexpr int L = L_, S = S_, CT = CT_, TT = TT_, M = 32 / L_, Np = L_ * S_;
+    static constexpr int CH = kScanThreads / L_ * CT_;                   // channels of a block
+    static constexpr int EPT = TT * CH / kScanThreads;                // a tile's elements a thread moves
+    static constexpr int VEC = EPT < 4 ? EPT : 4;
+    static constexpr int NBC = (TT * Np + kScanThreads - 1) / kScanThreads;   // and of B (and C)
+    static constexpr int RS = CH + M * CT_;   // row of a padded [token][channel] array: L rows of M CT channels, no bank twice
 };
 
 // Sequence starts and ends among the tile's tokens t0 .. t0+n-1 (n <= 32): bit masks,
@@ -151,24 +149,77 @@ __device__ __forceinline__ void tile_edges(const ScanDims &g, int b, int t0, int
     }
 }
 
-// The state entering segment k: the segments before it, composed in order.  A product
-// of 0 is a sequence start inside the segment: nothing from before it, not even an
-// infinity, goes on.
-template <int S>
-__device__ __forceinline__ void carry_in(float2 (&h)[S / 2], const ScanDims &g, const float *segP, const float *segH, int b,
-                                         int k, long long c, int n0, int Np)
+// Composes the K segments of every (row, channel, state) in place: segH[k] becomes what
+// enters segment k, from the segments before it (FWD) or behind it.  A product of 0 is a
+// sequence start inside a segment: nothing from before it, not even an infinity, goes on.
+// Segment k of the last one in that order is never read.
+template <bool FWD>
+__global__ void __launch_bounds__(128) k_scan_carry(const float *__restrict__ segP, float *segH, int K, long long per, long long all)
 {
-    for (int j = 0; j < k; ++j) {
-        const size_t at = (((size_t)b * g.K + j) * g.D + c) * Np + n0;
-        float2 p[S / 2], e[S / 2];
-        load_pairs<S>(p, segP + at);
-        load_pairs<S>(e, segH + at);
+    const long long i = blockIdx.x * 128ll + threadIdx.x;   // (row, channel, state), per = channels x states of a row
+    if (i >= all) return;
+    const size_t at = (size_t)(i / per) * K * per + i % per;
+    float h = 0.f;
+    constexpr int U = 8;
+    for (int k0 = 0; k0 < K; k0 += U) {
+        float p[U], e[U];
 #pragma unroll
-        for (int i = 0; i < S / 2; ++i) {
-            h[i].x = p[i].x == 0.f ? e[i].x : fmaf(p[i].x, h[i].x, e[i].x);
-            h[i].y = p[i].y == 0.f ? e[i].y : fmaf(p[i].y, h[i].y, e[i].y);
+        for (int u = 0; u < U; ++u) {
+            const int k = FWD ? k0 + u : K - 1 - k0 - u;
+            if (k0 + u < K - 1) {
+                p[u] = segP[at + k * per];
+                e[u] = segH[at + k * per];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = FWD ? k0 + u : K - 1 - k0 - u;
+            if (k0 + u < K) {
+                segH[at + k * per] = h;
+                if (k0 + u < K - 1) h = p[u] == 0.f ? e[u] : fmaf(p[u], h, e[u]);
+            }
         }
     }
+}
+
+template <bool FWD>
+inline void scan_carry(const ScanDims &g, const float *segP, float *segH, int Np, cudaStream_t st)
+{
+    const long long per = (long long)g.D * Np, all = g.B * per;
+    k_scan_carry<FWD><<<(unsigned)((all + 127) / 128), 128, 0, st>>>(segP, segH, g.K, per, all);
+}
+
+// (delta, delta x) of CT neighbouring channels
+template <int CT>
+__device__ __forceinline__ void load_steps(float (&dl)[CT], float (&dx)[CT], const float2 *p)
+{
+    if constexpr (CT == 1) {
+        dl[0] = p->x;
+        dx[0] = p->y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < CT / 2; ++i) {
+            const float4 q = reinterpret_cast<const float4 *>(p)[i];
+            dl[2 * i] = q.x; dx[2 * i] = q.y; dl[2 * i + 1] = q.z; dx[2 * i + 1] = q.w;
+        }
+    }
+}
+
+// CT neighbouring floats
+template <int CT>
+__device__ __forceinline__ void load_ct(float (&v)[CT], const float *p)
+{
+    Vec<float, CT> q;
+    q.load(p);
+    q.get(v);
+}
+
+template <int CT>
+__device__ __forceinline__ void store_ct(float *p, const float (&v)[CT])
+{
+    Vec<float, CT> q;
+    q.set(v);
+    q.store(p);
 }
 
 struct ScanCall {
@@ -190,16 +241,26 @@ cudaError_t scan_step(const ScanCall &c, cudaStream_t st);
 
 ScanDims scan_dims(const ScanCall &c);
 
-// Calls f(ScanCfg<L, S>{}) for the layout of N states.
+// Calls f(ScanCfg<...>{}) for the layout of N states: the forward pass's, and the backward
+// pass's (the same Np).
 template <class F>
-cudaError_t scan_layout(int N, F f)
+cudaError_t fwd_layout(int N, F f)
 {
-    if (N <= 4) return f(ScanCfg<1, 4>{});
-    if (N <= 8) return f(ScanCfg<2, 4>{});
-    if (N <= 16) return f(ScanCfg<4, 4>{});
-    if (N <= 32) return f(ScanCfg<8, 4>{});
-    if (N <= 64) return f(ScanCfg<16, 4>{});
-    return f(ScanCfg<16, 8>{});
+    if (N <= 8) return f(ScanCfg<4, 2, 2>{});
+    if (N <= 16) return f(ScanCfg<4, 4, 2>{});
+    if (N <= 32) return f(ScanCfg<8, 4, 2>{});
+    if (N <= 64) return f(ScanCfg<16, 4, 1>{});
+    return f(ScanCfg<16, 8, 1>{});
+}
+
+template <class F>
+cudaError_t bwd_layout(int N, F f)
+{
+    if (N <= 8) return f(ScanCfg<4, 2, 2>{});
+    if (N <= 16) return f(ScanCfg<4, 4, 2>{});
+    if (N <= 32) return f(ScanCfg<8, 4, 2>{});
+    if (N <= 64) return f(ScanCfg<16, 4, 1>{});
+    return f(ScanCfg<16, 8, 1>{});
 }
 
 }  // namespace lay

@@ -8,9 +8,10 @@
 //     dA += delta e,  dB_t = sum_c delta x dh_t,  dC_t = sum_c g h_t,  dh0 = a_0 dh_0
 //
 // A block walks its channels' tokens backwards in tiles of 16.  The forward pass kept the
-// state entering every tile, so a tile's states are computed forward from it into
-// registers (S x 16 of them) and then used from the last one back; a_t is an exponential
-// each time, which costs less than registers for it would.
+// state entering every tile; from it the tile is run forward once for the states that
+// enter its groups of L tokens (shared memory), then, from the last group back, each
+// group once more with its states and decays left in registers, and back.  That is two
+// exponentials a (token, channel, state) less those of the last group's first run.
 //
 // Sums.  Over a channel's states (o, p, sum e A): the lanes' butterfly.  Over channels
 // (dB, dC): a butterfly over the warp's channels that leaves a share of the 2 S values in
@@ -44,85 +45,82 @@ struct BwdIo {
 };
 
 template <class Cfg>
-struct BwdTile {
-    static constexpr int EPT = kTile * Cfg::CH / kScanThreads;
-    static constexpr int NBC = (kTile * Cfg::Np + kScanThreads - 1) / kScanThreads;
-    static constexpr int RS = Cfg::CH + Cfg::CH / 8;
-    struct Shared {
-        float2 dd[kTile][Cfg::CH];                      // delta, delta x
-        float g[kTile][RS], x[kTile][RS], s[kTile][RS], gz[kTile][RS];   // the last three: results dx, ddt, dz
-        __align__(16) float b[kTile][Cfg::Np];
-        __align__(16) float c[kTile][Cfg::Np];
-        float bc[kTile][kWarps][2 * Cfg::Np];
-        int seq[32];
-        uint32_t edge[2];
-    };
+struct BwdShared {
+    float2 dd[kTile][Cfg::CH];                        // delta, delta x
+    float g[kTile][Cfg::RS];
+    float x[kTile][Cfg::RS], s[kTile][Cfg::RS], gz[kTile][Cfg::RS];   // x, softplus', dy silu'(z); then dx, ddt, dz
+    __align__(16) float b[kTile][Cfg::Np];
+    __align__(16) float c[kTile][Cfg::Np];
+    __align__(16) float st[(kTile / Cfg::L) * Cfg::CT * kScanThreads * Cfg::S];   // states entering the groups
+    float bc[kTile][kWarps][2 * Cfg::Np];
+    int seq[32];
+    uint32_t edge[2];
 };
 
 template <class T, class Cfg, int VEC, bool SUM>
-__global__ void __launch_bounds__(kScanThreads) k_scan_bwd(ScanDims g, BwdIo<T> io)
+__global__ void __launch_bounds__(kScanThreads, 2) k_scan_bwd(ScanDims g, BwdIo<T> io)
 {
-    constexpr int L = Cfg::L, S = Cfg::S, Np = Cfg::Np, CH = Cfg::CH, M = 32 / L;
-    using Tile = BwdTile<Cfg>;
-    constexpr int NV = Tile::EPT / VEC, NBC = Tile::NBC;
+    constexpr int L = Cfg::L, S = Cfg::S, CT = Cfg::CT, M = Cfg::M, Np = Cfg::Np, CH = Cfg::CH, P = S / 2;
+    constexpr int NV = Cfg::EPT / VEC, NBC = Cfg::NBC;
     extern __shared__ __align__(16) char smem_raw[];
-    typename Tile::Shared &sm = *reinterpret_cast<typename Tile::Shared *>(smem_raw);
+    BwdShared<Cfg> &sm = *reinterpret_cast<BwdShared<Cfg> *>(smem_raw);
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = tid & (L - 1), ch = tid / L, n0 = l * S;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = lane / M, n0 = l * S;
+    const int ch = (warp * M + lane % M) * CT;
     int id = blockIdx.x;
     const int tiles = g.G * g.tiles, tile = id % tiles;
     id /= tiles;
     const int nseg = SUM ? g.K - 1 : g.K, k = id % nseg + (SUM ? 1 : 0), b = id / nseg;
     const int grp = tile / g.tiles, cg0 = (tile - grp * g.tiles) * CH;
-    const bool live = cg0 + ch < g.Dg;
     const int c0 = grp * g.Dg + cg0;
-    const long long c = live ? c0 + ch : c0;
+    const long long c = c0 + ch;
+    bool live[CT];
+#pragma unroll
+    for (int e = 0; e < CT; ++e) live[e] = cg0 + ch + e < g.Dg;
     const int ts = k * g.seg, te = min(ts + g.seg, g.T);
     const bool gated = io.z.p != nullptr;
 
-    float2 a2[S / 2], dh[S / 2], dA[S / 2], prod[S / 2];
-    load_states<S>(a2, g.A + c * g.N, n0, g.N, live);
+    float2 a2[CT][P], dh[CT][P], dA[CT][P], prod[CT];
+    float Dc[CT], aD[CT], aBias[CT], total[CT];
 #pragma unroll
-    for (int i = 0; i < S / 2; ++i) {
-        a2[i] = mul2(a2[i], two(kLog2e));
-        dh[i] = dA[i] = two(0.f);
-        prod[i] = two(1.f);
-    }
-    const float Dc = !SUM && g.Dskip && live ? g.Dskip[c] : 0.f;
-    float aD = 0.f, aBias = 0.f;
-    if constexpr (!SUM) {
-        // the segments behind this one, composed from the last
-        for (int j = g.K - 1; j > k; --j) {
-            const size_t at = (((size_t)b * g.K + j) * g.D + c) * Np + n0;
-            float2 p[S / 2], e[S / 2];
-            load_pairs<S>(p, io.segP + at);
-            load_pairs<S>(e, io.segH + at);
+    for (int e = 0; e < CT; ++e) {
+        load_states<S>(a2[e], g.A + (c + e) * g.N, n0, g.N, live[e]);
 #pragma unroll
-            for (int i = 0; i < S / 2; ++i) {
-                dh[i].x = p[i].x == 0.f ? e[i].x : fmaf(p[i].x, dh[i].x, e[i].x);
-                dh[i].y = p[i].y == 0.f ? e[i].y : fmaf(p[i].y, dh[i].y, e[i].y);
-            }
+        for (int i = 0; i < P; ++i) {
+            a2[e][i] = mul2(a2[e][i], two(kLog2e));
+            dh[e][i] = dA[e][i] = two(0.f);
+        }
+        prod[e] = two(1.f);
+        Dc[e] = !SUM && g.Dskip && live[e] ? g.Dskip[c + e] : 0.f;
+        aD[e] = aBias[e] = total[e] = 0.f;
+        // what the segments behind this one send back
+        if constexpr (!SUM) {
+            if (k < g.K - 1 && live[e]) load_pairs<S>(dh[e], io.segH + (((size_t)b * g.K + k) * g.D + c + e) * Np + n0);
         }
     }
 
+    constexpr int RV = CH / VEC, ES = kScanThreads / RV;
+    const int vt = tid / RV, vc = tid % RV * VEC;
+    const bool col = cg0 + vc < g.Dg;
+    const int cv = c0 + (col ? vc : 0);
     Vec<T, VEC> xn[NV], dn[NV], zn[NV], gn[NV];
     T br[NBC], cr[NBC];
-    constexpr int RV = CH / VEC;
-    auto vt = [&](int e) { return (tid + e * kScanThreads) / RV; };
-    auto vc = [&](int e) { return (tid + e * kScanThreads) % RV * VEC; };
+    float bias[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) bias[i] = col && g.bias ? g.bias[cv + i] : 0.f;
     auto fetch = [&](int t0) {
 #pragma unroll
         for (int e = 0; e < NV; ++e) {
-            const int t = t0 + vt(e), q = vc(e);
+            const int t = t0 + vt + e * ES;
             xn[e].zero();
             dn[e].zero();
             zn[e].zero();
             gn[e].zero();
-            if (t >= ts && t < te && cg0 + q < g.Dg) {
-                if (!SUM) xn[e].load(io.x.at(b, 0, t) + c0 + q);
-                dn[e].load(io.dt.at(b, 0, t) + c0 + q);
-                gn[e].load(io.dy.at(b, 0, t) + c0 + q);
-                if (gated) zn[e].load(io.z.at(b, 0, t) + c0 + q);
+            if (col && t >= ts && t < te) {
+                if (!SUM) xn[e].load(io.x.at(b, 0, t) + cv);
+                dn[e].load(io.dt.at(b, 0, t) + cv);
+                gn[e].load(io.dy.at(b, 0, t) + cv);
+                if (gated) zn[e].load(io.z.at(b, 0, t) + cv);
             }
         }
 #pragma unroll
@@ -143,29 +141,35 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_bwd(ScanDims g, BwdIo<T> 
         // 1. the tile into shared memory
 #pragma unroll
         for (int e = 0; e < NV; ++e) {
-            float x[VEC], d[VEC], z[VEC], gy[VEC];
+            float x[VEC], d[VEC], z[VEC], gy[VEC], sp[VEC], gz[VEC];
             xn[e].get(x);
             dn[e].get(d);
             zn[e].get(z);
             gn[e].get(gy);
-            const int t = vt(e), q = vc(e);
-            const bool in = t0 + t < te && cg0 + q < g.Dg;
+            const int t = vt + e * ES;
+            const bool in = col && t0 + t < te;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                float v = d[i] + (in && g.bias ? g.bias[c0 + q + i] : 0.f), der = 1.f;
+            for (int i = 0; i < VEC; i += 2) {
+                float2 v = add2(pair_at(d, i), pair_at(bias, i)), der = two(1.f);
                 if (g.softplus) softplus(v, v, der);
-                sm.dd[t][q + i] = in ? make_float2(v, v * x[i]) : make_float2(0.f, 0.f);
-                float gate = 1.f;
+                if (!in) v = two(0.f);
+                const float2 w = in ? mul2(v, pair_at(x, i)) : two(0.f);
+                if constexpr (VEC > 1) *reinterpret_cast<float4 *>(&sm.dd[t][vc + i]) = make_float4(v.x, w.x, v.y, w.y);
+                else sm.dd[t][vc] = make_float2(v.x, w.x);
+                put_pair(sp, i, der);
+                float2 gg = pair_at(gy, i);
                 if (gated) {
-                    const float sg = sigmoid(z[i]);
-                    gate = z[i] * sg;
-                    if (!SUM) sm.gz[t][q + i] = gy[i] * dsilu(z[i], sg);
+                    const float2 zz = pair_at(z, i), sg = sigmoid2(zz);
+                    put_pair(gz, i, mul2(gg, make_float2(dsilu(zz.x, sg.x), dsilu(zz.y, sg.y))));
+                    gg = mul2(gg, mul2(zz, sg));
                 }
-                sm.g[t][q + i] = gy[i] * gate;
-                if (!SUM) {
-                    sm.x[t][q + i] = x[i];
-                    sm.s[t][q + i] = der;
-                }
+                put_pair(gy, i, gg);
+            }
+            store_ct<VEC>(&sm.g[t][vc], gy);
+            if constexpr (!SUM) {
+                store_ct<VEC>(&sm.x[t][vc], x);
+                store_ct<VEC>(&sm.s[t][vc], sp);
+                if (gated) store_ct<VEC>(&sm.gz[t][vc], gz);
             }
         }
 #pragma unroll
@@ -180,113 +184,160 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_bwd(ScanDims g, BwdIo<T> 
         __syncthreads();
         fetch(t0 - kTile);
         const uint32_t starts = sm.edge[0], ends = sm.edge[1];
+        auto steps = [&](int t, float (&dl)[CT], float (&dx)[CT]) { load_steps<CT>(dl, dx, &sm.dd[t][ch]); };
+        // gradients that arrive at a sequence's final state
+        auto end_of = [&](int t) {
+            if ((ends >> t & 1) && io.dhT) {
+#pragma unroll
+                for (int e = 0; e < CT; ++e) {
+                    float2 v[P];
+                    load_states<S>(v, io.dhT + ((size_t)sm.seq[t] * g.D + c + e) * g.N, n0, g.N, live[e]);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) dh[e][i] = add2(dh[e][i], v[i]);
+                }
+            }
+        };
 
         if constexpr (SUM) {
-#pragma unroll
+#pragma unroll 4
             for (int t = kTile - 1; t >= 0; --t) {
-                const float dl = sm.dd[t][ch].x, gg = sm.g[t][ch];
-                float2 cc[S / 2];
+                float dl[CT], dx[CT], gg[CT];
+                steps(t, dl, dx);
+                load_ct<CT>(gg, &sm.g[t][ch]);
+                float2 cc[P];
                 load_pairs<S>(cc, &sm.c[t][n0]);
-                if ((ends >> t & 1) && io.dhT) {
-                    float2 v[S / 2];
-                    load_states<S>(v, io.dhT + ((size_t)sm.seq[t] * g.D + c) * g.N, n0, g.N, live);
+                end_of(t);
 #pragma unroll
-                    for (int i = 0; i < S / 2; ++i) dh[i].x += v[i].x, dh[i].y += v[i].y;
-                }
+                for (int e = 0; e < CT; ++e) {
+                    total[e] += dl[e];
 #pragma unroll
-                for (int i = 0; i < S / 2; ++i) {
-                    const float2 a = ex2_2(mul2(two(dl), a2[i]));
-                    dh[i] = mul2(a, fma2(two(gg), cc[i], dh[i]));
-                    prod[i] = mul2(prod[i], a);
+                    for (int i = 0; i < P; ++i)
+                        dh[e][i] = mul2(ex2_2(mul2(two(dl[e]), a2[e][i])), fma2(two(gg[e]), cc[i], dh[e][i]));
                 }
                 if (starts >> t & 1) {
 #pragma unroll
-                    for (int i = 0; i < S / 2; ++i) dh[i] = prod[i] = two(0.f);
+                    for (int e = 0; e < CT; ++e) {
+                        prod[e] = two(0.f);
+                        total[e] = 0.f;
+#pragma unroll
+                        for (int i = 0; i < P; ++i) dh[e][i] = two(0.f);
+                    }
                 }
             }
             __syncthreads();
         } else {
-            // 2. the tile's states, forward from the kept one: hist[t] enters token t
-            float2 hist[kTile][S / 2], h[S / 2];
+            // 2. forward from the kept state: what enters each group of L tokens
+            float2 h[CT][P], tA[CT][P];
 #pragma unroll
-            for (int i = 0; i < S / 2; ++i) h[i] = two(0.f);
-            if (live)
-                load_pairs<S>(h, io.keep + (((size_t)b * ((g.T + kScanKeep - 1) / kScanKeep) + t0 / kScanKeep) * g.D + c) * Np + n0);
+            for (int e = 0; e < CT; ++e) {
 #pragma unroll
-            for (int t = 0; t < kTile; ++t) {
-                const float2 q = sm.dd[t][ch];
-                float2 bb[S / 2];
+                for (int i = 0; i < P; ++i) h[e][i] = tA[e][i] = two(0.f);
+                if (live[e])
+                    load_pairs<S>(h[e], io.keep + (((size_t)b * ((g.T + kScanKeep - 1) / kScanKeep) + t0 / kScanKeep) * g.D + c + e) * Np + n0);
+            }
+            // one token on: from h to the state behind it; `a`, and `before` the state that entered
+            auto forward = [&](int t, float2 (&a)[CT][P], float2 (&before)[CT][P]) {
+                float dl[CT], dx[CT];
+                steps(t, dl, dx);
+                float2 bb[P];
                 load_pairs<S>(bb, &sm.b[t][n0]);
-                if (starts >> t & 1)
-                    load_states<S>(h, g.h0 + ((size_t)sm.seq[t] * g.D + c) * g.N, n0, g.N, live && g.h0);
 #pragma unroll
-                for (int i = 0; i < S / 2; ++i) {
-                    hist[t][i] = h[i];
-                    h[i] = fma2(ex2_2(mul2(two(q.x), a2[i])), h[i], mul2(two(q.y), bb[i]));
+                for (int e = 0; e < CT; ++e) {
+                    if (starts >> t & 1)
+                        load_states<S>(h[e], g.h0 + ((size_t)sm.seq[t] * g.D + c + e) * g.N, n0, g.N, live[e] && g.h0);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        before[e][i] = h[e][i];
+                        a[e][i] = ex2_2(mul2(two(dl[e]), a2[e][i]));
+                        h[e][i] = fma2(a[e][i], h[e][i], mul2(two(dx[e]), bb[i]));
+                    }
+                }
+            };
+            auto group_state = [&](int gi, int e) { return &sm.st[((gi * CT + e) * kScanThreads + tid) * S]; };
+#pragma unroll 1
+            for (int gi = 0; gi < kTile / L - 1; ++gi) {
+#pragma unroll
+                for (int e = 0; e < CT; ++e) store_pairs<S>(group_state(gi, e), h[e]);
+#pragma unroll
+                for (int j = 0; j < L; ++j) {
+                    float2 a[CT][P], before[CT][P];
+                    forward(gi * L + j, a, before);
                 }
             }
-            // 3. back through the tile
+            // 3. back through the tile, a group at a time: its states again, now kept with the decays
+#pragma unroll 1
+            for (int gi = kTile / L - 1; gi >= 0; --gi) {
+                const int g0 = gi * L;
+                float2 a[L][CT][P], hist[L][CT][P];
+                if (gi < kTile / L - 1) {
 #pragma unroll
-            for (int g0 = kTile - L; g0 >= 0; g0 -= L) {
-                float po[L], pp[L], pe[L];
+                    for (int e = 0; e < CT; ++e) load_pairs<S>(h[e], group_state(gi, e));
+                }
+#pragma unroll
+                for (int j = 0; j < L; ++j) forward(g0 + j, a[j], hist[j]);
+                float po[CT][L], pp[CT][L], pe[CT][L];
 #pragma unroll
                 for (int j = L - 1; j >= 0; --j) {
                     const int t = g0 + j;
-                    const float2 q = sm.dd[t][ch];
-                    const float gg = sm.g[t][ch];
-                    float2 bb[S / 2], cc[S / 2];
+                    float dl[CT], dx[CT], gg[CT];
+                    steps(t, dl, dx);
+                    load_ct<CT>(gg, &sm.g[t][ch]);
+                    float2 bb[P], cc[P], vb[P], vc2[P];
                     load_pairs<S>(bb, &sm.b[t][n0]);
                     load_pairs<S>(cc, &sm.c[t][n0]);
-                    if ((ends >> t & 1) && io.dhT) {
-                        float2 v[S / 2];
-                        load_states<S>(v, io.dhT + ((size_t)sm.seq[t] * g.D + c) * g.N, n0, g.N, live);
+                    end_of(t);
 #pragma unroll
-                        for (int i = 0; i < S / 2; ++i) dh[i].x += v[i].x, dh[i].y += v[i].y;
-                    }
-                    float2 o = two(0.f), p = two(0.f), e2 = two(0.f);
-                    float v[2 * S];
+                    for (int e = 0; e < CT; ++e) {
+                        float2 o, p, e2;
 #pragma unroll
-                    for (int i = 0; i < S / 2; ++i) {
-                        const float2 a = ex2_2(mul2(two(q.x), a2[i])), ah = mul2(a, hist[t][i]);
-                        const float2 hn = fma2(two(q.y), bb[i], ah);
-                        o = fma2(cc[i], hn, o);
-                        dh[i] = fma2(two(gg), cc[i], dh[i]);
-                        const float2 e = mul2(dh[i], ah);
-                        p = fma2(dh[i], bb[i], p);
-                        e2 = fma2(e, a2[i], e2);
-                        dA[i] = fma2(two(q.x), e, dA[i]);
-                        const float2 vb = mul2(two(q.y), dh[i]), vcc = mul2(two(gg), hn);
-                        v[2 * i] = vb.x;
-                        v[2 * i + 1] = vb.y;
-                        v[S + 2 * i] = vcc.x;
-                        v[S + 2 * i + 1] = vcc.y;
-                        dh[i] = mul2(a, dh[i]);
+                        for (int i = 0; i < P; ++i) {
+                            const float2 ah = mul2(a[j][e][i], hist[j][e][i]), hn = fma2(two(dx[e]), bb[i], ah);
+                            dh[e][i] = fma2(two(gg[e]), cc[i], dh[e][i]);
+                            const float2 q = mul2(dh[e][i], ah);
+                            o = i == 0 ? mul2(cc[i], hn) : fma2(cc[i], hn, o);
+                            p = i == 0 ? mul2(dh[e][i], bb[i]) : fma2(dh[e][i], bb[i], p);
+                            e2 = i == 0 ? mul2(q, a2[e][i]) : fma2(q, a2[e][i], e2);
+                            tA[e][i] = fma2(two(dl[e]), q, tA[e][i]);
+                            vb[i] = e == 0 ? mul2(two(dx[e]), dh[e][i]) : fma2(two(dx[e]), dh[e][i], vb[i]);
+                            vc2[i] = e == 0 ? mul2(two(gg[e]), hn) : fma2(two(gg[e]), hn, vc2[i]);
+                            dh[e][i] = mul2(a[j][e][i], dh[e][i]);
+                        }
+                        po[e][j] = o.x + o.y;
+                        pp[e][j] = p.x + p.y;
+                        pe[e][j] = e2.x + e2.y;
                     }
-                    po[j] = o.x + o.y;
-                    pp[j] = p.x + p.y;
-                    pe[j] = e2.x + e2.y;
                     if (starts >> t & 1) {
-                        if (io.dh0) store_states<S>(io.dh0 + ((size_t)sm.seq[t] * g.D + c) * g.N, dh, n0, g.N, live);
 #pragma unroll
-                        for (int i = 0; i < S / 2; ++i) dh[i] = two(0.f);
+                        for (int e = 0; e < CT; ++e) {
+                            if (io.dh0) store_states<S>(io.dh0 + ((size_t)sm.seq[t] * g.D + c + e) * g.N, dh[e], n0, g.N, live[e]);
+#pragma unroll
+                            for (int i = 0; i < P; ++i) dh[e][i] = two(0.f);
+                        }
                     }
                     // dB, dC over the warp's channels
+                    float v[2 * S];
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        v[2 * i] = vb[i].x;
+                        v[2 * i + 1] = vb[i].y;
+                        v[S + 2 * i] = vc2[i].x;
+                        v[S + 2 * i + 1] = vc2[i].y;
+                    }
                     constexpr int left = 2 * S > M ? 2 * S / M : 1;   // values a lane ends with
-                    int off = 0;
-                    int cur = 2 * S;
+                    int off = 0, cur = 2 * S;
 #pragma unroll
                     for (int bit = M / 2; bit > 0; bit >>= 1) {
-                        const bool up = lane & (bit * L);
+                        const bool up = lane & bit;
                         if (cur > 1) {
                             cur >>= 1;
 #pragma unroll
                             for (int i = 0; i < cur; ++i) {
                                 const float send = up ? v[i] : v[i + cur], mine = up ? v[i + cur] : v[i];
-                                v[i] = mine + __shfl_xor_sync(0xffffffffu, send, bit * L);
+                                v[i] = mine + __shfl_xor_sync(0xffffffffu, send, bit);
                             }
                             off += up ? cur : 0;
                         } else {
-                            v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit * L);
+                            v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
                         }
                     }
 #pragma unroll
@@ -295,38 +346,51 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_bwd(ScanDims g, BwdIo<T> 
                         sm.bc[t][warp][(w >= S ? Np : 0) + n0 + (w & (S - 1))] = v[i];
                     }
                 }
-                const float o = lane_sum<L>(po, lane), p = lane_sum<L>(pp, lane), e = lane_sum<L>(pe, lane) * kLn2;
                 const int t = g0 + l;
-                const float x = sm.x[t][ch], gg = sm.g[t][ch];
-                const float ddt = fmaf(p, x, e) * sm.s[t][ch];
-                aD = fmaf(gg, x, aD);
-                aBias += ddt;
-                sm.x[t][ch] = fmaf(sm.dd[t][ch].x, p, Dc * gg);
-                sm.s[t][ch] = ddt;
-                if (gated) sm.gz[t][ch] *= fmaf(Dc, x, o);
+                float dl[CT], dx[CT], x[CT], gg[CT], sp[CT], gz[CT];
+                steps(t, dl, dx);
+                load_ct<CT>(x, &sm.x[t][ch]);
+                load_ct<CT>(gg, &sm.g[t][ch]);
+                load_ct<CT>(sp, &sm.s[t][ch]);
+                if (gated) load_ct<CT>(gz, &sm.gz[t][ch]);
+#pragma unroll
+                for (int e = 0; e < CT; ++e) {
+                    const float o = lane_sum<L>(po[e], lane), p = lane_sum<L>(pp[e], lane), q = lane_sum<L>(pe[e], lane) * kLn2;
+                    const float ddt = fmaf(p, x[e], q) * sp[e];
+                    aD[e] = fmaf(gg[e], x[e], aD[e]);
+                    aBias[e] += ddt;
+                    if (gated) gz[e] *= fmaf(Dc[e], x[e], o);
+                    x[e] = fmaf(dl[e], p, Dc[e] * gg[e]);
+                    sp[e] = ddt;
+                }
+                store_ct<CT>(&sm.x[t][ch], x);
+                store_ct<CT>(&sm.s[t][ch], sp);
+                if (gated) store_ct<CT>(&sm.gz[t][ch], gz);
             }
+            // a tile's sum first, then the total: fewer roundings on the long axis
+#pragma unroll
+            for (int e = 0; e < CT; ++e)
+#pragma unroll
+                for (int i = 0; i < P; ++i) dA[e][i] = add2(dA[e][i], tA[e][i]);
             __syncthreads();
 
             // 4. the tile's results
 #pragma unroll
             for (int e = 0; e < NV; ++e) {
-                const int t = vt(e), q = vc(e);
-                if (t0 + t < te && cg0 + q < g.Dg) {
+                const int t = vt + e * ES;
+                if (col && t0 + t < te) {
                     Vec<T, VEC> out;
                     float f[VEC];
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) f[i] = sm.x[t][q + i];
+                    load_ct<VEC>(f, &sm.x[t][vc]);
                     out.set(f);
-                    out.store(io.dx.at(b, 0, t0 + t) + c0 + q);
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) f[i] = sm.s[t][q + i];
+                    out.store(io.dx.at(b, 0, t0 + t) + cv);
+                    load_ct<VEC>(f, &sm.s[t][vc]);
                     out.set(f);
-                    out.store(io.ddt.at(b, 0, t0 + t) + c0 + q);
+                    out.store(io.ddt.at(b, 0, t0 + t) + cv);
                     if (gated) {
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) f[i] = sm.gz[t][q + i];
+                        load_ct<VEC>(f, &sm.gz[t][vc]);
                         out.set(f);
-                        out.store(io.dz.at(b, 0, t0 + t) + c0 + q);
+                        out.store(io.dz.at(b, 0, t0 + t) + cv);
                     }
                 }
             }
@@ -342,22 +406,30 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_bwd(ScanDims g, BwdIo<T> 
         }
     }
     if constexpr (SUM) {
-        if (live) {
-            const size_t at = (((size_t)b * g.K + k) * g.D + c) * Np + n0;
-            store_pairs<S>(io.segP + at, prod);
-            store_pairs<S>(io.segH + at, dh);
+#pragma unroll
+        for (int e = 0; e < CT; ++e) {
+            if (!live[e]) continue;
+            const size_t at = (((size_t)b * g.K + k) * g.D + c + e) * Np + n0;
+            float2 p[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) p[i] = mul2(prod[e], ex2_2(mul2(two(total[e]), a2[e][i])));
+            store_pairs<S>(io.segP + at, p);
+            store_pairs<S>(io.segH + at, dh[e]);
         }
     } else {
         const size_t row = (size_t)b * g.K + k;
-        store_states<S>(io.part_a + (row * g.D + c) * g.N, dA, n0, g.N, live);
 #pragma unroll
-        for (int o = L >> 1; o > 0; o >>= 1) {
-            aD += __shfl_xor_sync(0xffffffffu, aD, o);
-            aBias += __shfl_xor_sync(0xffffffffu, aBias, o);
-        }
-        if (live && l == 0) {
-            io.part_d[row * 2 * g.D + c] = aD;
-            io.part_d[(row * 2 + 1) * g.D + c] = aBias;
+        for (int e = 0; e < CT; ++e) {
+            store_states<S>(io.part_a + (row * g.D + c + e) * g.N, dA[e], n0, g.N, live[e]);
+#pragma unroll
+            for (int o = M; o < 32; o <<= 1) {
+                aD[e] += __shfl_xor_sync(0xffffffffu, aD[e], o);
+                aBias[e] += __shfl_xor_sync(0xffffffffu, aBias[e], o);
+            }
+            if (live[e] && l == 0) {
+                io.part_d[row * 2 * g.D + c + e] = aD[e];
+                io.part_d[(row * 2 + 1) * g.D + c + e] = aBias[e];
+            }
         }
     }
 }
@@ -399,7 +471,7 @@ Plan plan_of(const dn_scan_shape *s)
 {
     Plan p;
     int CH = 0;
-    scan_layout(s->N, [&](auto cfg) { CH = decltype(cfg)::CH; return cudaSuccess; });
+    bwd_layout(s->N, [&](auto cfg) { CH = decltype(cfg)::CH; return cudaSuccess; });
     const int Dg = s->D / s->G, Np = scan_padded(s->N);
     p.tiles = (Dg + CH - 1) / CH;
     const long long blocks = (long long)s->B * s->G * p.tiles, want = 2 * sm_count();
@@ -442,12 +514,13 @@ cudaError_t launch(const ScanCall &c, cudaStream_t st)
     io.part_a = F(p.part_a); io.part_d = F(p.part_d); io.part_bc = F(p.part_bc);
     const long long per = (long long)g.B * g.G * g.tiles;
     if (per * g.K > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const size_t smem = sizeof(typename BwdTile<Cfg>::Shared);
+    const size_t smem = sizeof(BwdShared<Cfg>);
     cudaError_t e;
     if (g.K > 1) {
         e = cudaFuncSetAttribute(k_scan_bwd<T, Cfg, VEC, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         k_scan_bwd<T, Cfg, VEC, true><<<(unsigned)(per * (g.K - 1)), kScanThreads, smem, st>>>(g, io);
+        scan_carry<false>(g, io.segP, io.segH, Cfg::Np, st);
     }
     e = cudaFuncSetAttribute(k_scan_bwd<T, Cfg, VEC, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -475,9 +548,9 @@ cudaError_t bwd_t(const ScanCall &c, cudaStream_t st)
     }
     const Plan p = plan_of(s);
     if (s->T > 0) {
-        const cudaError_t e = scan_layout(s->N, [&](auto cfg) {
+        const cudaError_t e = bwd_layout(s->N, [&](auto cfg) {
             using Cfg = decltype(cfg);
-            constexpr int VEC = BwdTile<Cfg>::EPT < 4 ? BwdTile<Cfg>::EPT : 4;
+            constexpr int VEC = Cfg::VEC;
             const dn_view *all[] = {&io->x, &io->dt, &io->z, &gr->dy, &gr->dx, &gr->ddt, &gr->dz};
             bool v = (s->D / s->G) % VEC == 0;
             for (const dn_view *q : all) v = v && can_vector(q, sizeof(T), VEC * sizeof(T));

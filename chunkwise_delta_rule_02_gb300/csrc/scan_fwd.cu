@@ -4,8 +4,8 @@
 // time segment of them) in tiles:
 //   1. every thread turns its part of the tile's x and dt into (delta, delta x), and
 //      its part of B, C into float32, in shared memory;
-//   2. the recurrence: per token a lane reads (delta, delta x) of its channel and S
-//      values of B and C, and does S exponentials and 4 S multiply-adds;
+//   2. the recurrence: per token a lane reads (delta, delta x) of its channels and S
+//      values of B and C, and does S exponentials and 4 S multiply-adds for each channel;
 //   3. y = (sum + D x) silu(z), stored with the tile's layout of x.
 // The loads of the next tile are in flight during step 2.
 //
@@ -22,109 +22,150 @@ namespace lay {
 
 namespace {
 
-template <class Cfg>
-struct FwdTile {
-    static constexpr int TT = Cfg::L <= 2 ? 16 : 32;                 // tokens
-    static constexpr int EPT = TT * Cfg::CH / kScanThreads;          // elements a thread
-    static constexpr int NBC = (TT * Cfg::Np + kScanThreads - 1) / kScanThreads;   // elements of B (and of C) a thread
-    static constexpr int YS = Cfg::CH + Cfg::CH / 8;                 // padded row of y: L rows x 32/L channels, no bank twice
-};
-
 template <class T, class Cfg, int VEC, bool SUM>
 __global__ void __launch_bounds__(kScanThreads) k_scan_fwd(ScanDims g, ScanIo<T> io)
 {
-    constexpr int L = Cfg::L, S = Cfg::S, Np = Cfg::Np, CH = Cfg::CH;
-    using F = FwdTile<Cfg>;
-    constexpr int TT = F::TT, NV = F::EPT / VEC, NBC = F::NBC;
-    __shared__ float2 dd[TT][CH];
+    constexpr int L = Cfg::L, S = Cfg::S, CT = Cfg::CT, M = Cfg::M, Np = Cfg::Np, CH = Cfg::CH, P = S / 2;
+    constexpr int TT = Cfg::TT, NV = Cfg::EPT / VEC, NBC = Cfg::NBC;
+    __shared__ __align__(16) float2 dd[TT][CH];   // delta, delta x
     __shared__ __align__(16) float sb[TT][Np], sc[SUM ? 1 : TT][Np];
-    __shared__ float sy[SUM ? 1 : TT][F::YS];
+    __shared__ __align__(16) float sy[SUM ? 1 : TT][Cfg::RS];
     __shared__ int seq[32];
     __shared__ uint32_t edge[2];
 
-    const int tid = threadIdx.x, lane = tid & 31, l = tid & (L - 1), ch = tid / L, n0 = l * S;
+    const int tid = threadIdx.x, lane = tid & 31, l = lane / M, n0 = l * S;
+    const int ch = ((tid >> 5) * M + lane % M) * CT;   // first of this lane's channels in the block
     // block -> (channel tile, segment, row)
     int id = blockIdx.x;
     const int tile = id % (g.G * g.tiles);
     id /= g.G * g.tiles;
     const int nseg = SUM ? g.K - 1 : g.K, k = id % nseg, b = id / nseg;
     const int grp = tile / g.tiles, cg0 = (tile - grp * g.tiles) * CH;   // first channel within the group
-    const bool live = cg0 + ch < g.Dg;
     const int c0 = grp * g.Dg + cg0;
-    const long long c = live ? c0 + ch : c0;
+    const long long c = c0 + ch;
+    bool live[CT];
+#pragma unroll
+    for (int e = 0; e < CT; ++e) live[e] = cg0 + ch + e < g.Dg;
     const int ts = k * g.seg, te = min(ts + g.seg, g.T);
+    float total[CT];   // SUM: of delta since the last sequence start
 
-    float2 a2[S / 2], h[S / 2], prod[S / 2];
-    load_states<S>(a2, g.A + c * g.N, n0, g.N, live);
+    float2 a2[CT][P], h[CT][P], prod[CT];   // prod: 1, 0 after a sequence start
 #pragma unroll
-    for (int i = 0; i < S / 2; ++i) {
-        a2[i] = mul2(a2[i], two(kLog2e));
-        h[i] = two(0.f);
-        prod[i] = two(1.f);
-    }
-    if constexpr (!SUM) {
-        if (k > 0) carry_in<S>(h, g, io.segP, io.segH, b, k, c, n0, Np);
+    for (int e = 0; e < CT; ++e) {
+        load_states<S>(a2[e], g.A + (c + e) * g.N, n0, g.N, live[e]);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            a2[e][i] = mul2(a2[e][i], two(kLog2e));
+            h[e][i] = two(0.f);
+        }
+        prod[e] = two(1.f);
+        total[e] = 0.f;
+        if constexpr (!SUM) {
+            if (k > 0 && live[e]) load_pairs<S>(h[e], io.segH + (((size_t)b * g.K + k) * g.D + c + e) * Np + n0);
+        }
     }
 
-    // this thread's vectors of a tile: token vt[e], channels vc[e] ..
-    Vec<T, VEC> xr[NV], dr[NV], zr[NV], xn[NV], dn[NV], zn[NV];
+    // This thread's vectors of a tile: tokens vt, vt + ES, ..., always channels vc .. vc + VEC - 1
+    // (a token's vectors divide the threads).
+    constexpr int RV = CH / VEC, ES = kScanThreads / RV;
+    const int vt = tid / RV, vc = tid % RV * VEC;
+    const bool col = cg0 + vc < g.Dg, gated = !SUM && io.z.p != nullptr;
+    const int cv = c0 + (col ? vc : 0);
+    Vec<T, VEC> xr[NV], zr[NV], xn[NV], dn[NV], zn[NV];
     T br[NBC], cr[NBC];
-    constexpr int RV = CH / VEC;   // vectors of a token
-    auto vt = [&](int e) { return (tid + e * kScanThreads) / RV; };
-    auto vc = [&](int e) { return (tid + e * kScanThreads) % RV * VEC; };
-    const bool gated = !SUM && io.z.p != nullptr;
+    const T *px = io.x.at(b, 0, ts + vt) + cv, *pd = io.dt.at(b, 0, ts + vt) + cv;
+    const T *pz = gated ? io.z.at(b, 0, ts + vt) + cv : nullptr;
+    T *py = SUM ? nullptr : io.y.at(b, 0, ts + vt) + cv;
+    float bias[VEC], skip[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        bias[i] = col && g.bias ? g.bias[cv + i] : 0.f;
+        skip[i] = !SUM && col && g.Dskip ? g.Dskip[cv + i] : 0.f;
+    }
+    // this thread's elements of B and C: state bn of tokens bt, bt + BS, ...
+    constexpr int BS = kScanThreads / Np;
+    const int bt = tid / Np, bn = tid % Np;
+    const bool bc_in = bn < g.N && (NBC * kScanThreads == TT * Np || tid < TT * Np);
+    const T *pb = io.b.at(b, grp, ts + bt) + bn, *pc = SUM ? nullptr : io.c.at(b, grp, ts + bt) + bn;
+    const bool whole = cg0 + CH <= g.Dg;   // no channel of the block is behind its group's end
+    // whole tiles (the same for every thread) take the loads without their checks
     auto fetch = [&](int t0) {
+        if (whole && t0 + TT <= te) {
 #pragma unroll
-        for (int e = 0; e < NV; ++e) {
-            const int t = t0 + vt(e), q = vc(e);
-            xn[e].zero();
-            dn[e].zero();
-            zn[e].zero();
-            if (t < te && cg0 + q < g.Dg) {
-                xn[e].load(io.x.at(b, 0, t) + c0 + q);
-                dn[e].load(io.dt.at(b, 0, t) + c0 + q);
-                if (gated) zn[e].load(io.z.at(b, 0, t) + c0 + q);
+            for (int e = 0; e < NV; ++e) {
+                xn[e].load(px + e * ES * io.x.t);
+                dn[e].load(pd + e * ES * io.dt.t);
+                if (gated) zn[e].load(pz + e * ES * io.z.t);
+            }
+#pragma unroll
+            for (int e = 0; e < NBC; ++e) {
+                if (bc_in) {
+                    br[e] = pb[e * BS * io.b.t];
+                    if (!SUM) cr[e] = pc[e * BS * io.c.t];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < NV; ++e) {
+                xn[e].zero();
+                dn[e].zero();
+                if (!SUM) zn[e].zero();
+                if (col && t0 + vt + e * ES < te) {
+                    xn[e].load(px + e * ES * io.x.t);
+                    dn[e].load(pd + e * ES * io.dt.t);
+                    if (gated) zn[e].load(pz + e * ES * io.z.t);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < NBC; ++e) {
+                st_out(&br[e], 0.f);
+                st_out(&cr[e], 0.f);
+                if (bc_in && t0 + bt + e * BS < te) {
+                    br[e] = pb[e * BS * io.b.t];
+                    if (!SUM) cr[e] = pc[e * BS * io.c.t];
+                }
             }
         }
-#pragma unroll
-        for (int e = 0; e < NBC; ++e) {
-            const int i = tid + e * kScanThreads, t = t0 + i / Np, n = i % Np;
-            st_out(&br[e], 0.f);
-            st_out(&cr[e], 0.f);
-            if (i < TT * Np && t < te && n < g.N) {
-                br[e] = io.b.at(b, grp, t)[n];
-                if (!SUM) cr[e] = io.c.at(b, grp, t)[n];
-            }
-        }
+        px += TT * io.x.t;
+        pd += TT * io.dt.t;
+        if (gated) pz += TT * io.z.t;
+        pb += TT * io.b.t;
+        if (!SUM) pc += TT * io.c.t;
     };
+#pragma unroll
+    for (int e = 0; e < NBC; ++e) {   // padded states stay zero
+        st_out(&br[e], 0.f);
+        st_out(&cr[e], 0.f);
+    }
     fetch(ts);
 
     for (int t0 = ts; t0 < te; t0 += TT) {
+        const bool full = whole && t0 + TT <= te;
         // 1. the tile into shared memory
 #pragma unroll
         for (int e = 0; e < NV; ++e) {
             float x[VEC], d[VEC];
             xr[e] = xn[e];
-            dr[e] = dn[e];
-            zr[e] = zn[e];
-            xr[e].get(x);
-            dr[e].get(d);
-            const int t = vt(e), q = vc(e);
-            const bool in = t0 + t < te && cg0 + q < g.Dg;
+            if (!SUM) zr[e] = zn[e];
+            xn[e].get(x);
+            dn[e].get(d);
+            // tokens behind the end (and channels behind the group's) change nothing: delta = 0
+            const bool in = full || (col && t0 + vt + e * ES < te);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                float v = d[i] + (in && g.bias ? g.bias[c0 + q + i] : 0.f), der;
+            for (int i = 0; i < VEC; i += 2) {
+                float2 v = add2(pair_at(d, i), pair_at(bias, i)), der;
                 if (g.softplus) softplus(v, v, der);
-                // tokens behind the end change nothing: delta = 0
-                dd[t][q + i] = in ? make_float2(v, v * x[i]) : make_float2(0.f, 0.f);
+                float2 w = mul2(v, pair_at(x, i));
+                if (!in) v = w = two(0.f);
+                if constexpr (VEC > 1) *reinterpret_cast<float4 *>(&dd[vt + e * ES][vc + i]) = make_float4(v.x, w.x, v.y, w.y);
+                else dd[vt + e * ES][vc] = make_float2(v.x, w.x);
             }
         }
 #pragma unroll
         for (int e = 0; e < NBC; ++e) {
-            const int i = tid + e * kScanThreads;
-            if (i < TT * Np) {
-                sb[i / Np][i % Np] = ld_in(&br[e]);
-                if constexpr (!SUM) sc[i / Np][i % Np] = ld_in(&cr[e]);
+            if (NBC * kScanThreads == TT * Np || tid < TT * Np) {
+                sb[bt + e * BS][bn] = ld_in(&br[e]);
+                if constexpr (!SUM) sc[bt + e * BS][bn] = ld_in(&cr[e]);
             }
         }
         if (tid < 32) tile_edges(g, b, t0, min(TT, te - t0), seq, edge);
@@ -133,38 +174,45 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_fwd(ScanDims g, ScanIo<T>
 
         // 2. the recurrence
         const uint32_t starts = edge[0], ends = edge[1];
+        if constexpr (!SUM) {
+            if (io.keep && t0 % kScanKeep == 0) {
+#pragma unroll
+                for (int e = 0; e < CT; ++e)
+                    if (live[e])
+                        store_pairs<S>(io.keep + (((size_t)b * ((g.T + kScanKeep - 1) / kScanKeep) + t0 / kScanKeep) * g.D + c + e) * Np + n0, h[e]);
+            }
+        }
 #pragma unroll 1
         for (int g0 = 0; g0 < TT; g0 += L) {
-            if constexpr (!SUM) {
-                if (io.keep && g0 % kScanKeep == 0 && t0 + g0 < te && live)
-                    store_pairs<S>(io.keep + (((size_t)b * ((g.T + kScanKeep - 1) / kScanKeep) + (t0 + g0) / kScanKeep) * g.D + c) * Np + n0, h);
-            }
             const uint32_t in_group = ((starts | ends) >> g0) & (uint32_t)((1ull << L) - 1);
-            float yp[L];
+            float yp[CT][L];
             auto token = [&](int j, bool edges) {
                 const int t = g0 + j;
-                const float2 q = dd[t][ch];
-                float2 bb[S / 2];
+                float dl[CT], dx[CT];
+                load_steps<CT>(dl, dx, &dd[t][ch]);
+                float2 bb[P], cc[P];
                 load_pairs<S>(bb, &sb[t][n0]);
-                if (edges && (starts >> t & 1)) {
-                    load_states<S>(h, g.h0 + ((size_t)seq[t] * g.D + c) * g.N, n0, g.N, live && g.h0);
-#pragma unroll
-                    for (int i = 0; i < S / 2; ++i) prod[i] = two(0.f);
-                }
-                float2 yy = two(0.f);
-                float2 cc[S / 2];
                 if constexpr (!SUM) load_pairs<S>(cc, &sc[t][n0]);
 #pragma unroll
-                for (int i = 0; i < S / 2; ++i) {
-                    const float2 a = ex2_2(mul2(two(q.x), a2[i]));
-                    h[i] = fma2(a, h[i], mul2(two(q.y), bb[i]));
-                    if constexpr (SUM) prod[i] = mul2(prod[i], a);
-                    else yy = fma2(cc[i], h[i], yy);
-                }
-                yp[j] = yy.x + yy.y;
-                if constexpr (!SUM) {
-                    if (edges && (ends >> t & 1) && io.hT)
-                        store_states<S>(io.hT + ((size_t)seq[t] * g.D + c) * g.N, h, n0, g.N, live);
+                for (int e = 0; e < CT; ++e) {
+                    if (edges && (starts >> t & 1)) {
+                        load_states<S>(h[e], g.h0 + ((size_t)seq[t] * g.D + c + e) * g.N, n0, g.N, live[e] && g.h0);
+                        prod[e] = two(0.f);
+                        total[e] = 0.f;
+                    }
+                    if constexpr (SUM) total[e] += dl[e];
+                    float2 yy = two(0.f);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        const float2 a = ex2_2(mul2(two(dl[e]), a2[e][i]));
+                        h[e][i] = fma2(a, h[e][i], mul2(two(dx[e]), bb[i]));
+                        if constexpr (!SUM) yy = i == 0 ? mul2(cc[i], h[e][i]) : fma2(cc[i], h[e][i], yy);
+                    }
+                    yp[e][j] = yy.x + yy.y;
+                    if constexpr (!SUM) {
+                        if (edges && (ends >> t & 1) && io.hT)
+                            store_states<S>(io.hT + ((size_t)seq[t] * g.D + c + e) * g.N, h[e], n0, g.N, live[e]);
+                    }
                 }
             };
             if (in_group == 0) {
@@ -174,7 +222,12 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_fwd(ScanDims g, ScanIo<T>
 #pragma unroll
                 for (int j = 0; j < L; ++j) token(j, true);
             }
-            if constexpr (!SUM) sy[g0 + l][ch] = lane_sum<L>(yp, lane);
+            if constexpr (!SUM) {
+                float y[CT];
+#pragma unroll
+                for (int e = 0; e < CT; ++e) y[e] = lane_sum<L>(yp[e], lane);
+                store_ct<CT>(&sy[g0 + l][ch], y);
+            }
         }
         __syncthreads();
 
@@ -182,28 +235,41 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_fwd(ScanDims g, ScanIo<T>
         if constexpr (!SUM) {
 #pragma unroll
             for (int e = 0; e < NV; ++e) {
-                const int t = vt(e), q = vc(e);
-                if (t0 + t < te && cg0 + q < g.Dg) {
+                if (full || (col && t0 + vt + e * ES < te)) {
                     float x[VEC], z[VEC], o[VEC];
                     xr[e].get(x);
                     zr[e].get(z);
+                    Vec<float, VEC> s4;
+                    s4.load(&sy[vt + e * ES][vc]);
+                    s4.get(o);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        o[i] = fmaf(g.Dskip ? g.Dskip[c0 + q + i] : 0.f, x[i], sy[t][q + i]);
-                        if (gated) o[i] *= z[i] * sigmoid(z[i]);
+                    for (int i = 0; i < VEC; i += 2) {
+                        float2 v = fma2(pair_at(skip, i), pair_at(x, i), pair_at(o, i));
+                        if (gated) {
+                            const float2 w = pair_at(z, i);
+                            v = mul2(v, mul2(w, sigmoid2(w)));
+                        }
+                        put_pair(o, i, v);
                     }
                     Vec<T, VEC> out;
                     out.set(o);
-                    out.store(io.y.at(b, 0, t0 + t) + c0 + q);
+                    out.store(py + e * ES * io.y.t);
                 }
             }
+            py += TT * io.y.t;
         }
     }
     if constexpr (SUM) {
-        if (live) {
-            const size_t at = (((size_t)b * g.K + k) * g.D + c) * Np + n0;
-            store_pairs<S>(io.segP + at, prod);
-            store_pairs<S>(io.segH + at, h);
+#pragma unroll
+        for (int e = 0; e < CT; ++e) {
+            if (!live[e]) continue;
+            const size_t at = (((size_t)b * g.K + k) * g.D + c + e) * Np + n0;
+            // the product of the decays is one exponential of the steps' sum
+            float2 p[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) p[i] = mul2(prod[e], ex2_2(mul2(two(total[e]), a2[e][i])));
+            store_pairs<S>(io.segP + at, p);
+            store_pairs<S>(io.segH + at, h[e]);
         }
     }
 }
@@ -229,8 +295,12 @@ __global__ void __launch_bounds__(256) k_scan_step(ScanDims g, ScanIo<T> io, int
     const long long j = live ? i : 0;
     const int b = (int)(j / g.D), c = (int)(j - (long long)b * g.D), grp = c / g.Dg;
     const float x = ld_in(io.x.at(b, 0, 0) + c);
-    float d = ld_in(io.dt.at(b, 0, 0) + c) + (g.bias ? g.bias[c] : 0.f), der;
-    if (g.softplus) softplus(d, d, der);
+    float d = ld_in(io.dt.at(b, 0, 0) + c) + (g.bias ? g.bias[c] : 0.f);
+    if (g.softplus) {
+        float2 v, der;
+        softplus(two(d), v, der);
+        d = v.x;
+    }
     const float dx = d * x;
     const T *bp = io.b.at(b, grp, 0), *cp = io.c.at(b, grp, 0);
     const float *hi = g.h0 ? g.h0 + j * g.N : nullptr;
@@ -288,7 +358,7 @@ int scan_blocks(const dn_scan_shape *s, int CH)
 int channels_of(int N)
 {
     int ch = 0;
-    scan_layout(N, [&](auto cfg) { ch = decltype(cfg)::CH; return cudaSuccess; });
+    fwd_layout(N, [&](auto cfg) { ch = decltype(cfg)::CH; return cudaSuccess; });
     return ch;
 }
 
@@ -310,8 +380,7 @@ cudaError_t launch(const ScanCall &c, cudaStream_t st)
     ScanDims g = scan_dims(c);
     g.tiles = (g.Dg + Cfg::CH - 1) / Cfg::CH;
     g.K = segments(c.s, scan_blocks(c.s, Cfg::CH));
-    const int TT = FwdTile<Cfg>::TT;
-    g.seg = ((g.T + g.K - 1) / g.K + TT - 1) / TT * TT;
+    g.seg = ((g.T + g.K - 1) / g.K + kScanKeep - 1) / kScanKeep * kScanKeep;
     g.K = (g.T + g.seg - 1) / g.seg;
     ScanIo<T> io = io_of<T>(c);
     const long long per = (long long)g.B * g.G * g.tiles;
@@ -320,6 +389,7 @@ cudaError_t launch(const ScanCall &c, cudaStream_t st)
         io.segP = (float *)c.ws;
         io.segH = io.segP + (size_t)g.B * g.K * g.D * Cfg::Np;
         k_scan_fwd<T, Cfg, VEC, true><<<(unsigned)(per * (g.K - 1)), kScanThreads, 0, st>>>(g, io);
+        scan_carry<true>(g, io.segP, io.segH, Cfg::Np, st);
     }
     k_scan_fwd<T, Cfg, VEC, false><<<(unsigned)(per * g.K), kScanThreads, 0, st>>>(g, io);
     return cudaPeekAtLastError();
@@ -339,13 +409,16 @@ cudaError_t fwd_t(const ScanCall &c, cudaStream_t st)
         }
     }
     if (s->T == 0) return cudaPeekAtLastError();
-    return scan_layout(s->N, [&](auto cfg) {
+    return fwd_layout(s->N, [&](auto cfg) {
         using Cfg = decltype(cfg);
-        constexpr int VEC = FwdTile<Cfg>::EPT < 4 ? FwdTile<Cfg>::EPT : 4;
+        constexpr int VEC = Cfg::VEC;
         const int bytes = VEC * sizeof(T);
         const bool v = (s->D / s->G) % VEC == 0 && can_vector(&io->x, sizeof(T), bytes) && can_vector(&io->dt, sizeof(T), bytes) &&
                        can_vector(&io->z, sizeof(T), bytes) && can_vector(&io->y, sizeof(T), bytes);
-        return v ? launch<T, Cfg, VEC>(c, st) : launch<T, Cfg, 1>(c, st);
+        if constexpr (VEC > 1) {
+            if (v) return launch<T, Cfg, VEC>(c, st);
+        }
+        return launch<T, Cfg, 1>(c, st);
     });
 }
 
@@ -371,7 +444,7 @@ cudaError_t step_t(const ScanCall &c, cudaStream_t st)
 int scan_padded(int N)
 {
     int np = 0;
-    scan_layout(N, [&](auto cfg) { np = decltype(cfg)::Np; return cudaSuccess; });
+    fwd_layout(N, [&](auto cfg) { np = decltype(cfg)::Np; return cudaSuccess; });
     return np;
 }
 
