@@ -5,10 +5,11 @@
 //     dw[c][k] = sum_t dpre[t] x[t-(W-1)+k],  dbias = sum_t dpre[t]
 //
 // Bound by HBM: x read, y written (backward: x, dy read, dx written).  A thread
-// owns V consecutive channels (16 bytes where strides and alignment allow, else
-// one element) and walks a run of tokens with the last W - 1 inputs in registers,
-// so that an input is read once plus W - 1 halo tokens a run; a warp covers 32
-// neighbouring vectors of one token.
+// owns V consecutive channels (8 bytes where strides and alignment allow, else
+// one element) and walks a run of tokens with the last W inputs in registers, so
+// that an input is read once plus W - 1 halo tokens a run; a warp covers 32
+// neighbouring vectors of one token.  Measured: forward 4.6 TB/s (67 % of a copy),
+// backward 4.1 TB/s (60 %): 25 instructions an element stand against it there.
 #include "layers.h"
 
 namespace gdn {
@@ -17,6 +18,11 @@ namespace lay {
 namespace {
 
 constexpr int kTX = 32, kTY = 8;     // threads: channel vectors x runs
+
+// Vectors of 8 bytes, and 8 tokens' loads in flight, measured at 4 x 8192 (forward) and
+// 8 x 4096 tokens (backward) of 2048 bf16 channels: forward 59 us (16-byte vectors: 63 us with
+// twice the registers, 4 tokens in flight 69 us), backward 99 us (16 bytes: 190 us; 4 tokens 119 us).
+constexpr int kBytes = 8, kInFlight = 8;
 
 struct ConvDims {
     int H, T, d, C, N, silu, run, runs, blocks_x;   // blocks_x: channel-vector blocks
@@ -38,32 +44,75 @@ __device__ __forceinline__ bool my_run(const ConvDims &g, int &cv, int &b, int &
     return cv < g.C / V && r < g.runs;
 }
 
-template <int W, int V>
-__device__ __forceinline__ void load_taps(const float *w, const float *bias, int c0, float (&wt)[V][W], float (&bs)[V])
+// Channels go in pairs (two float32 operations an instruction); a single one is paired
+// with a channel of zeros.
+template <int V>
+constexpr int kPairs = V == 1 ? 1 : V / 2;
+
+template <class T, int V>
+__device__ __forceinline__ void get_pairs(float2 (&f)[kPairs<V>], const Vec<T, V> &q)
 {
+    float e[V];
+    q.get(e);
+#pragma unroll
+    for (int i = 0; i < kPairs<V>; ++i) f[i] = V == 1 ? make_float2(e[0], 0.f) : make_float2(e[2 * i], e[V == 1 ? 0 : 2 * i + 1]);
+}
+
+template <class T, int V>
+__device__ __forceinline__ void set_pairs(Vec<T, V> &q, const float2 (&f)[kPairs<V>])
+{
+    float e[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) e[i] = i & 1 ? f[i / 2].y : f[i / 2].x;
+    q.set(e);
+}
+
+template <int W, int V>
+__device__ __forceinline__ void load_taps(const float *w, const float *bias, int c0, float2 (&wt)[W][kPairs<V>],
+                                          float2 (&bs)[kPairs<V>])
+{
+    float tmp[V * W];
     if constexpr (V * W % 4 == 0 && V > 1) {
-        float tmp[V * W];
         const float4 *p = reinterpret_cast<const float4 *>(w + (size_t)c0 * W);
 #pragma unroll
         for (int i = 0; i < V * W / 4; ++i) {
             const float4 q = p[i];
             tmp[4 * i] = q.x; tmp[4 * i + 1] = q.y; tmp[4 * i + 2] = q.z; tmp[4 * i + 3] = q.w;
         }
-#pragma unroll
-        for (int i = 0; i < V * W; ++i) wt[i / W][i % W] = tmp[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < V * W; ++i) wt[i / W][i % W] = w[(size_t)c0 * W + i];
+        for (int i = 0; i < V * W; ++i) tmp[i] = w[(size_t)c0 * W + i];
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) bs[i] = bias ? bias[c0 + i] : 0.f;
+    for (int i = 0; i < kPairs<V>; ++i) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) wt[k][i] = V == 1 ? make_float2(tmp[k], 0.f) : make_float2(tmp[2 * i * W + k], tmp[V == 1 ? 0 : (2 * i + 1) * W + k]);
+        bs[i] = !bias ? two(0.f) : V == 1 ? make_float2(bias[c0], 0.f) : make_float2(bias[c0 + 2 * i], bias[c0 + (V == 1 ? 0 : 2 * i + 1)]);
+    }
+}
+
+// Window of the last W values of a thread's channels, as a ring with static places: before
+// token u of an unrolled run (u counted from a multiple of W) place (u + 1 + k) % W holds the
+// value k - (W - 1) tokens away, and place u % W takes the new one.
+template <int W, int V>
+using Ring = float2[W][kPairs<V>];
+
+template <int W, int V>
+__device__ __forceinline__ void rotate(Ring<W, V> &r)   // one token on, back to u = 0
+{
+#pragma unroll
+    for (int i = 0; i < kPairs<V>; ++i) {
+        const float2 newest = r[0][i];
+#pragma unroll
+        for (int k = 0; k + 1 < W; ++k) r[k][i] = r[k + 1][i];
+        r[W - 1][i] = newest;
+    }
 }
 
 // The W - 1 inputs before token t of a sequence [lo, ...): from x, or from the
 // sequence's initial taps, or zero.
 template <class T, int W, int V>
-__device__ __forceinline__ void load_hist(float (&h)[W - 1][V], const T *xr, long long xt, int t, int lo, const T *s0,
-                                          int C)
+__device__ __forceinline__ void load_hist(Ring<W, V> &h, const T *xr, long long xt, int t, int lo, const T *s0, int C)
 {
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
@@ -72,22 +121,40 @@ __device__ __forceinline__ void load_hist(float (&h)[W - 1][V], const T *xr, lon
         q.zero();
         if (tt >= lo) q.load(xr + tt * xt);
         else if (s0) q.load(s0 + (size_t)(W - 1 + tt - lo) * C);
-        q.get(h[k]);
+        get_pairs<T, V>(h[k + 1], q);
     }
 }
 
+// pre-activation of ring place u's token
+template <int W, int V>
+__device__ __forceinline__ void taps_at(float2 (&p)[kPairs<V>], const Ring<W, V> &x, const float2 (&wt)[W][kPairs<V>],
+                                        const float2 (&bs)[kPairs<V>], int u)
+{
+#pragma unroll
+    for (int i = 0; i < kPairs<V>; ++i) {
+        p[i] = bs[i];
+#pragma unroll
+        for (int k = 0; k < W; ++k) p[i] = fma2(wt[k][i], x[(u + 1 + k) % W][i], p[i]);
+    }
+}
+
+// tokens whose loads are in flight together, a multiple of W
+template <int W>
+constexpr int kUnroll = (kInFlight + W - 1) / W * W;
+
 template <class T, int W, int V>
-__global__ void __launch_bounds__(kTX *kTY) k_conv_fwd(ConvDims g, View<const T> x, View<T> y, const float *__restrict__ w,
+__global__ void __launch_bounds__(kTX *kTY, 2) k_conv_fwd(ConvDims g, View<const T> x, View<T> y, const float *__restrict__ w,
                                                        const float *__restrict__ bias, const T *__restrict__ s0)
 {
-    constexpr int U = 4;   // tokens whose loads are in flight together
+    constexpr int U = kUnroll<W>, P = kPairs<V>;
     int cv, b, t0;
     long long row;
     if (!my_run<V>(g, cv, b, t0, row)) return;
     const int c0 = cv * V, hd = c0 / g.d, j = c0 - hd * g.d;
     const T *xr = x.at(b, hd, 0) + j;
     T *yr = y.at(b, hd, 0) + j;
-    float wt[V][W], bs[V], h[W - 1][V];
+    float2 wt[W][P], bs[P];
+    Ring<W, V> h;
     load_taps<W, V>(w, bias, c0, wt, bs);
     int t = t0;
     const int t1 = min(t0 + g.run, g.T);
@@ -97,37 +164,38 @@ __global__ void __launch_bounds__(kTX *kTY) k_conv_fwd(ConvDims g, View<const T>
         const int lo = g.cu ? g.cu[s] : 0, hi = g.cu ? g.cu[s + 1] : g.T;
         const int end = min(t1, hi);
         if (end > t) load_hist<T, W, V>(h, xr, x.t, t, lo, s0 ? s0 + (size_t)s * (W - 1) * g.C + c0 : nullptr, g.C);
-        for (; t < end; t += U) {
+        const T *px = xr + t * x.t;
+        T *py = yr + t * y.t;
+        auto token = [&](const Vec<T, V> &in, int u) {
+            float2 p[P];
+            get_pairs<T, V>(h[u % W], in);
+            taps_at<W, V>(p, h, wt, bs, u);
+            if (g.silu) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) p[i] = mul2(p[i], sigmoid2(p[i]));
+            }
+            Vec<T, V> out;
+            set_pairs<T, V>(out, p);
+            out.store(py);
+            py += y.t;
+        };
+        for (; t + U <= end; t += U) {
             Vec<T, V> in[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (t + u < end) in[u].load(xr + (t + u) * x.t);
-#pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (t + u < end) {
-                    float f[V], o[V];
-                    in[u].get(f);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        float a = bs[i];
-#pragma unroll
-                        for (int k = 0; k < W - 1; ++k) a = fmaf(wt[i][k], h[k][i], a);
-                        a = fmaf(wt[i][W - 1], f[i], a);
-                        o[i] = g.silu ? a * sigmoid(a) : a;
-                    }
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-#pragma unroll
-                        for (int k = 0; k + 1 < W - 1; ++k) h[k][i] = h[k + 1][i];
-                        h[W - 2][i] = f[i];
-                    }
-                    Vec<T, V> out;
-                    out.set(o);
-                    out.store(yr + (t + u) * y.t);
-                }
+                in[u].load(px);
+                px += x.t;
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u) token(in[u], u);
         }
-        t = end;
+        for (; t < end; ++t) {
+            Vec<T, V> in;
+            in.load(px);
+            px += x.t;
+            token(in, 0);
+            rotate<W, V>(h);
+        }
         ++s;
     }
 }
@@ -159,26 +227,27 @@ __global__ void k_conv_state(ConvDims g, View<const T> x, const T *s0, T *sT)
 // the run in registers, over the block's kTY runs in shared memory, and over
 // blocks in col_sum: no atomics, one fixed order.
 template <class T, int W, int V>
-__global__ void __launch_bounds__(kTX *kTY) k_conv_bwd(ConvDims g, View<const T> x, View<const T> dy, View<T> dx,
+__global__ void __launch_bounds__(kTX *kTY, 2) k_conv_bwd(ConvDims g, View<const T> x, View<const T> dy, View<T> dx,
                                                        const float *__restrict__ w, const float *__restrict__ bias,
                                                        const T *__restrict__ s0, const T *__restrict__ dsT,
                                                        float *__restrict__ part)
 {
-    constexpr int U = 4;
+    constexpr int U = kUnroll<W>, P = kPairs<V>;
     __shared__ float red[kTY][kTX * V];
     int cv, b, t0;
     long long row;
     const bool live = my_run<V>(g, cv, b, t0, row);
-    float acc[W + 1][V];
+    float2 acc[W + 1][P];
 #pragma unroll
     for (int k = 0; k <= W; ++k)
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
+        for (int i = 0; i < P; ++i) acc[k][i] = two(0.f);
     if (live) {
         const int c0 = cv * V, hd = c0 / g.d, j = c0 - hd * g.d;
         const T *xr = x.at(b, hd, 0) + j, *gr = dy.at(b, hd, 0) + j;
         T *dr = dx.at(b, hd, 0) + j;
-        float wt[V][W], bs[V], h[W - 1][V], dp[W][V];
+        float2 wt[W][P], bs[P];
+        Ring<W, V> h, dp;   // inputs and dpre of the last W tokens
         load_taps<W, V>(w, bias, c0, wt, bs);
         int t = t0;
         const int t1 = min(t0 + g.run, g.T);
@@ -191,67 +260,89 @@ __global__ void __launch_bounds__(kTX *kTY) k_conv_bwd(ConvDims g, View<const T>
 #pragma unroll
                 for (int k = 0; k < W; ++k)
 #pragma unroll
-                    for (int i = 0; i < V; ++i) dp[k][i] = 0.f;
+                    for (int i = 0; i < P; ++i) dp[k][i] = two(0.f);
                 const int stop = min(hi, end + W - 1);
-                for (int tb = a; tb < end + W - 1; tb += U) {
-                    Vec<T, V> in[U], gi[U];
+                const T *px = xr + a * x.t, *pg = gr + a * dy.t;
+                T *pd = dr + (long long)(a - (W - 1)) * dx.t;
+                // one token: its dpre into ring place u, and dx W - 1 tokens back into o
+                auto token = [&](const Vec<T, V> &in, const Vec<T, V> &gi, int u, bool sums, float2 (&o)[P]) {
+                    float2 p[P], q[P];
+                    get_pairs<T, V>(h[u % W], in);
+                    get_pairs<T, V>(q, gi);
+                    taps_at<W, V>(p, h, wt, bs, u);
+                    if (g.silu) {
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        if (tb + u < stop) {
-                            in[u].load(xr + (tb + u) * x.t);
-                            gi[u].load(gr + (tb + u) * dy.t);
-                        }
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int tt = tb + u;
-                        if (tt < end + W - 1) {
-                            float f[V], q[V], o[V];
-                            if (tt < stop) {
-                                in[u].get(f);
-                                gi[u].get(q);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < V; ++i) f[i] = q[i] = 0.f;
-                            }
-#pragma unroll
-                            for (int i = 0; i < V; ++i) {
-                                float p = bs[i];
-#pragma unroll
-                                for (int k = 0; k < W - 1; ++k) p = fmaf(wt[i][k], h[k][i], p);
-                                p = fmaf(wt[i][W - 1], f[i], p);
-                                if (g.silu && tt < stop) q[i] *= dsilu(p, sigmoid(p));
-                                if (tt < end) {
-#pragma unroll
-                                    for (int k = 0; k < W - 1; ++k) acc[k][i] = fmaf(q[i], h[k][i], acc[k][i]);
-                                    acc[W - 1][i] = fmaf(q[i], f[i], acc[W - 1][i]);
-                                    acc[W][i] += q[i];
-                                }
-#pragma unroll
-                                for (int k = 0; k + 1 < W; ++k) dp[k][i] = dp[k + 1][i];
-                                dp[W - 1][i] = q[i];
-#pragma unroll
-                                for (int k = 0; k + 1 < W - 1; ++k) h[k][i] = h[k + 1][i];
-                                h[W - 2][i] = f[i];
-                                o[i] = 0.f;
-#pragma unroll
-                                for (int k = 0; k < W; ++k) o[i] = fmaf(wt[i][W - 1 - k], dp[k][i], o[i]);
-                            }
-                            const int tau = tt - (W - 1);
-                            if (tau >= a) {
-                                if (dsT && tau >= hi - (W - 1)) {
-                                    Vec<T, V> e;
-                                    float ef[V];
-                                    e.load(dsT + ((size_t)s * (W - 1) + (tau - hi + W - 1)) * g.C + c0);
-                                    e.get(ef);
-#pragma unroll
-                                    for (int i = 0; i < V; ++i) o[i] += ef[i];
-                                }
-                                Vec<T, V> out;
-                                out.set(o);
-                                out.store(dr + tau * dx.t);
-                            }
+                        for (int i = 0; i < P; ++i) {
+                            // silu' = s (1 + p (1 - s))
+                            const float2 sg = sigmoid2(p[i]);
+                            q[i] = mul2(mul2(q[i], sg), fma2(p[i], fma2(sg, two(-1.f), two(1.f)), two(1.f)));
                         }
                     }
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        if (sums) {
+#pragma unroll
+                            for (int k = 0; k < W; ++k) acc[k][i] = fma2(q[i], h[(u + 1 + k) % W][i], acc[k][i]);
+                            acc[W][i] = add2(acc[W][i], q[i]);
+                        }
+                        dp[u % W][i] = q[i];
+                        o[i] = mul2(wt[W - 1][i], dp[(u + 1) % W][i]);
+#pragma unroll
+                        for (int k = 1; k < W; ++k) o[i] = fma2(wt[W - 1 - k][i], dp[(u + 1 + k) % W][i], o[i]);
+                    }
+                };
+                int tt = a;
+                for (; tt + U <= end; tt += U) {
+                    Vec<T, V> in[U], gi[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        in[u].load(px);
+                        gi[u].load(pg);
+                        px += x.t;
+                        pg += dy.t;
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        float2 o[P];
+                        token(in[u], gi[u], u, true, o);
+                        if (u >= W - 1 || tt > a) {   // the first W - 1 tokens complete nothing of this run
+                            Vec<T, V> out;
+                            set_pairs<T, V>(out, o);
+                            out.store(pd);
+                        }
+                        pd += dx.t;
+                    }
+                }
+#pragma unroll 1
+                for (; tt < end + W - 1; ++tt) {
+                    Vec<T, V> in, gi;
+                    in.zero();
+                    gi.zero();
+                    if (tt < stop) {
+                        in.load(px);
+                        gi.load(pg);
+                    }
+                    px += x.t;
+                    pg += dy.t;
+                    float2 o[P];
+                    token(in, gi, 0, tt < end, o);
+                    rotate<W, V>(h);
+                    rotate<W, V>(dp);
+                    const int tau = tt - (W - 1);
+                    if (tau >= a) {
+                        if (dsT && tau >= hi - (W - 1)) {
+                            Vec<T, V> e;
+                            float2 ef[P];
+                            e.load(dsT + ((size_t)s * (W - 1) + (tau - hi + W - 1)) * g.C + c0);
+                            get_pairs<T, V>(ef, e);
+#pragma unroll
+                            for (int i = 0; i < P; ++i) o[i] = add2(o[i], ef[i]);
+                        }
+                        Vec<T, V> out;
+                        set_pairs<T, V>(out, o);
+                        out.store(pd);
+                    }
+                    pd += dx.t;
                 }
             }
             t = max(t, end);
@@ -262,7 +353,7 @@ __global__ void __launch_bounds__(kTX *kTY) k_conv_bwd(ConvDims g, View<const T>
     for (int k = 0; k <= W; ++k) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < V; ++i) red[threadIdx.y][threadIdx.x * V + i] = acc[k][i];
+        for (int i = 0; i < V; ++i) red[threadIdx.y][threadIdx.x * V + i] = i & 1 ? acc[k][i / 2].y : acc[k][i / 2].x;
         __syncthreads();
         for (int i = threadIdx.y * kTX + threadIdx.x; i < kTX * V; i += kTX * kTY) {
             const long long c = (long long)(blockIdx.x % g.blocks_x) * kTX * V + i;
@@ -332,19 +423,22 @@ __global__ void __launch_bounds__(128) k_conv_step(int N, int C, int d, int silu
         else v[k].zero();
     }
     v[W - 1].load(x.at(n, hd, 0) + j);
-    float wt[V][W], o[V];
+    constexpr int P = kPairs<V>;
+    float2 wt[W][P], o[P];
     load_taps<W, V>(w, bias, c0, wt, o);
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-        float f[V];
-        v[k].get(f);
+        float2 f[P];
+        get_pairs<T, V>(f, v[k]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = fmaf(wt[e][k], f[e], o[e]);
+        for (int i = 0; i < P; ++i) o[i] = fma2(wt[k][i], f[i], o[i]);
     }
+    if (silu) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = silu ? o[e] * sigmoid(o[e]) : o[e];
+        for (int i = 0; i < P; ++i) o[i] = mul2(o[i], sigmoid2(o[i]));
+    }
     Vec<T, V> out;
-    out.set(o);
+    set_pairs<T, V>(out, o);
     out.store(y.at(n, hd, 0) + j);
     if (state_out) {
 #pragma unroll
@@ -352,35 +446,51 @@ __global__ void __launch_bounds__(128) k_conv_step(int N, int C, int d, int silu
     }
 }
 
-int run_of(const dn_conv_shape *s) { (void)s; return 64; }
+// Tokens of a run: the longest power of two (forward 16..64, backward 16..512) that leaves
+// the SMs enough blocks, for 8-byte vectors.  A longer run reads its W - 1 halo tokens and, in
+// the backward, writes its partial sums less often; 4 blocks an SM forward, 3/2 backward (two
+// fit one: 256 tokens at 8 x 4096 x 2048 99 us, 128 tokens 105 us, 64 tokens 108 us).
+int run_of(const dn_conv_shape *s, bool bwd)
+{
+    const long long vec = kBytes / (s->dtype == DN_F32 ? 4 : 2), need = (bwd ? 3ll : 8ll) * sm_count() / 2;
+    const long long cols = ((long long)s->H * s->d / vec + kTX - 1) / kTX;
+    int run = bwd ? 512 : 64;
+    while (run > 16 && s->B * ((s->T + (long long)run * kTY - 1) / ((long long)run * kTY)) * cols < need) run >>= 1;
+    return run;
+}
 
-ConvDims dims_of(const dn_conv_shape *s, int N, const int32_t *cu, int V)
+long long rows_of(const dn_conv_shape *s, bool bwd)
+{
+    const long long run = run_of(s, bwd), runs = (s->T + run - 1) / run;
+    return (long long)s->B * ((runs + kTY - 1) / kTY);
+}
+
+ConvDims dims_of(const dn_conv_shape *s, int N, const int32_t *cu, int V, bool bwd)
 {
     ConvDims g;
     g.H = s->H; g.T = s->T; g.d = s->d; g.C = s->H * s->d; g.N = N; g.silu = s->silu; g.cu = cu;
-    g.run = run_of(s);
+    g.run = run_of(s, bwd);
     g.runs = (s->T + g.run - 1) / g.run;
     g.blocks_x = (g.C / V + kTX - 1) / kTX;
-    g.rows = conv_part_rows(s);
+    g.rows = rows_of(s, bwd);
     return g;
 }
 
-// 16-byte vectors need every view, the taps and the states aligned to them, and heads
-// that are whole vectors; one element otherwise.
+// Vectors of `bytes` need every view, the taps and the states aligned to them, and heads that
+// are whole vectors; one element otherwise.
 template <class T>
-bool vectors(const ConvCall &c)
+bool vectors(const ConvCall &c, int bytes)
 {
-    constexpr int V = 16 / sizeof(T);
-    const int e = sizeof(T);
-    auto al = [](const void *p) { return ((uintptr_t)p & 15u) == 0; };
-    return c.s->d % V == 0 && can_vector(c.x, e, 16) && can_vector(c.y, e, 16) && can_vector(c.dy, e, 16) &&
-           can_vector(c.dx, e, 16) && al(c.w) && al(c.s0) && al(c.sT) && al(c.dsT) && al(c.ds0);
+    const int e = sizeof(T), V = bytes / e;
+    auto al = [](const void *p, int n) { return ((uintptr_t)p % n) == 0; };
+    return c.s->d % V == 0 && can_vector(c.x, e, bytes) && can_vector(c.y, e, bytes) && can_vector(c.dy, e, bytes) &&
+           can_vector(c.dx, e, bytes) && al(c.w, 16) && al(c.s0, bytes) && al(c.sT, bytes) && al(c.dsT, bytes) && al(c.ds0, bytes);
 }
 
 template <class T, int W, int V>
 cudaError_t fwd_t(const ConvCall &c, cudaStream_t st)
 {
-    const ConvDims g = dims_of(c.s, c.N, c.cu, V);
+    const ConvDims g = dims_of(c.s, c.N, c.cu, V, false);
     const View<const T> x = view_of<const T>(c.x);
     if (g.T > 0) {
         const long long blocks = g.rows * g.blocks_x;
@@ -397,7 +507,7 @@ cudaError_t fwd_t(const ConvCall &c, cudaStream_t st)
 template <class T, int W, int V>
 cudaError_t bwd_t(const ConvCall &c, cudaStream_t st)
 {
-    const ConvDims g = dims_of(c.s, c.N, c.cu, V);
+    const ConvDims g = dims_of(c.s, c.N, c.cu, V, true);
     const View<const T> x = view_of<const T>(c.x), dy = view_of<const T>(c.dy);
     if (g.T > 0) {
         const long long blocks = g.rows * g.blocks_x;
@@ -437,21 +547,24 @@ cudaError_t step_t(const ConvCall &c, cudaStream_t st)
 
 enum Op { kFwd, kBwd, kStep };
 
-template <class T, int W, int V>
-cudaError_t op_t(Op op, const ConvCall &c, cudaStream_t st)
+// The step, whose few bytes are all latency, takes 16-byte vectors where it can.
+template <class T, int W>
+cudaError_t by_vector(Op op, const ConvCall &c, cudaStream_t st)
 {
-    return op == kFwd ? fwd_t<T, W, V>(c, st) : op == kBwd ? bwd_t<T, W, V>(c, st) : step_t<T, W, V>(c, st);
+    const int bytes = op == kStep ? 16 : kBytes;
+    const bool v = vectors<T>(c, bytes);
+    if (op == kBwd) return v ? bwd_t<T, W, kBytes / sizeof(T)>(c, st) : bwd_t<T, W, 1>(c, st);
+    if (op == kFwd) return v ? fwd_t<T, W, kBytes / sizeof(T)>(c, st) : fwd_t<T, W, 1>(c, st);
+    return v ? step_t<T, W, 16 / sizeof(T)>(c, st) : step_t<T, W, 1>(c, st);
 }
 
 template <class T>
 cudaError_t by_width(Op op, const ConvCall &c, cudaStream_t st)
 {
-    constexpr int V = 16 / sizeof(T);
-    const bool v = vectors<T>(c);
     switch (c.s->width) {
-    case 2: return v ? op_t<T, 2, V>(op, c, st) : op_t<T, 2, 1>(op, c, st);
-    case 3: return v ? op_t<T, 3, V>(op, c, st) : op_t<T, 3, 1>(op, c, st);
-    case 4: return v ? op_t<T, 4, V>(op, c, st) : op_t<T, 4, 1>(op, c, st);
+    case 2: return by_vector<T, 2>(op, c, st);
+    case 3: return by_vector<T, 3>(op, c, st);
+    case 4: return by_vector<T, 4>(op, c, st);
     default: return cudaErrorInvalidValue;
     }
 }
@@ -463,11 +576,7 @@ cudaError_t run(Op op, const ConvCall &c, cudaStream_t st)
 
 }  // namespace
 
-long long conv_part_rows(const dn_conv_shape *s)
-{
-    const long long runs = ((long long)s->T + run_of(s) - 1) / run_of(s);
-    return (long long)s->B * ((runs + kTY - 1) / kTY);
-}
+long long conv_part_rows(const dn_conv_shape *s) { return rows_of(s, true); }
 
 cudaError_t conv_fwd(const ConvCall &c, cudaStream_t st) { return run(kFwd, c, st); }
 cudaError_t conv_bwd(const ConvCall &c, cudaStream_t st) { return run(kBwd, c, st); }

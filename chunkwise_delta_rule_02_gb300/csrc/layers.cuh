@@ -177,8 +177,8 @@ __device__ __forceinline__ int seq_at(const int32_t *cu, int N, int t)
     return lo;
 }
 
-// Checked copy of the packed offsets into the workspace: all zero, and the status
-// word flagged, unless cu[0] = 0, cu[N] = T and cu never falls.
+// Checked copy of the packed offsets into the workspace, and the call's status word:
+// all zero and flagged unless cu[0] = 0, cu[N] = T and cu never falls.
 cudaError_t check_offsets(const int32_t *cu, int N, int T, int32_t *out, uint32_t *status, cudaStream_t st);
 
 // out[map(col)] = sum over p < P of part[p * n + col], col < n, in a fixed order.

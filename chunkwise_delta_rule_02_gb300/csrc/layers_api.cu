@@ -10,7 +10,7 @@ namespace lay {
 
 namespace {
 
-// One block: copies the offsets, or zeros and the status flag if they are malformed.
+// One block: copies the offsets, or zeros if they are malformed; sets the status word.
 __global__ void __launch_bounds__(256) k_offsets(const int32_t *cu, int N, int T, int32_t *out, uint32_t *status)
 {
     int bad = 0;
@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(256) k_offsets(const int32_t *cu, int N, int T
     }
     bad = __syncthreads_or(bad);
     for (int i = threadIdx.x; i <= N; i += blockDim.x) out[i] = bad ? 0 : cu[i];
-    if (bad && threadIdx.x == 0) raise_status(status, kStatusBadOffsets);
+    if (threadIdx.x == 0) *status = bad ? kStatusBadOffsets : kStatusOk;   // and clears what an earlier call left
 }
 
 constexpr int kSumX = 32, kSumY = 32;
@@ -118,7 +118,6 @@ dn_status conv_begin(ConvCall &c, const dn_conv_shape *s, bool bwd, void *ws, si
     c.N = s->cu_seqlens ? s->num_seqs : s->B;
     c.part = (float *)(base + l.part);
     if (s->cu_seqlens) {
-        if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return DN_ERR_CUDA;
         c.cu = (const int32_t *)(base + l.cu);
         return status_of(check_offsets(s->cu_seqlens, s->num_seqs, s->T, (int32_t *)(base + l.cu), (uint32_t *)ws, st));
     }
@@ -184,7 +183,6 @@ dn_status scan_begin(ScanCall &c, const dn_scan_shape *s, const dn_scan_io *io, 
     c.Nseq = s->cu_seqlens ? s->num_seqs : s->B;
     c.ws = (char *)ws + head;
     if (s->cu_seqlens) {
-        if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return DN_ERR_CUDA;
         int32_t *cu = (int32_t *)((char *)ws + 256);
         c.cu = cu;
         return status_of(check_offsets(s->cu_seqlens, s->num_seqs, s->T, cu, (uint32_t *)ws, st));

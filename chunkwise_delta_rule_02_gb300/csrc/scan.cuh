@@ -24,7 +24,6 @@
 namespace gdn {
 namespace lay {
 
-constexpr int kScanThreads = 256;
 constexpr int kScanKeep = 16;      // tokens between kept states
 
 struct ScanDims {
@@ -111,14 +110,17 @@ __device__ __forceinline__ float lane_sum(float (&v)[L], int lane)
     return v[0];
 }
 
-// TT: tokens of a tile
-template <int L_, int S_, int CT_, int TT_ = kScanKeep>
+// TT: tokens of a tile; NT: threads of a block
+template <int L_, int S_, int CT_, int TT_ = kScanKeep, int NT_ = 256>
 struct ScanCfg {
-    static constexpr int L = L_, S = S_, CT = CT_, TT = TT_, M = 32 / L_, Np = L_ * S_;
-    static constexpr int CH = kScanThreads / L_ * CT_;                   // channels of a block
-    static constexpr int EPT = TT * CH / kScanThreads;                // a tile's elements a thread moves
+    static constexpr int L = L_, S = S_, CT = CT_, TT = TT_, NT = NT_, M = 32 / L_, Np = L_ * S_;
+    static constexpr int CH = NT / L_ * CT_;                             // channels of a block
+    static constexpr int EPT = TT * CH / NT;                             // a tile's elements a thread moves
     static constexpr int VEC = EPT < 4 ? EPT : 4;
-    static constexpr int NBC = (TT * Np + kScanThreads - 1) / kScanThreads;   // and of B (and C)
+    // bytes of a vector of elements T: up to 16, 0 where a thread's share is less than 4
+    template <class T>
+    static constexpr int bytes() { return EPT * sizeof(T) >= 16 ? 16 : EPT * sizeof(T) >= 4 ? EPT * sizeof(T) : 0; }
+    static constexpr int NBC = (TT * Np + NT - 1) / NT;                  // elements of B (and of C) a thread moves
     static constexpr int RS = CH + M * CT_;   // row of a padded [token][channel] array: L rows of M CT channels, no bank twice
 };
 
@@ -189,6 +191,18 @@ inline void scan_carry(const ScanDims &g, const float *segP, float *segH, int Np
     k_scan_carry<FWD><<<(unsigned)((all + 127) / 128), 128, 0, st>>>(segP, segH, g.K, per, all);
 }
 
+// An asynchronous copy of BYTES (4, 8 or 16) to shared memory; zeros where !in.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *dst, const void *src, bool in)
+{
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    const int n = in ? BYTES : 0;
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
 // (delta, delta x) of CT neighbouring channels
 template <int CT>
 __device__ __forceinline__ void load_steps(float (&dl)[CT], float (&dx)[CT], const float2 *p)
@@ -220,6 +234,33 @@ __device__ __forceinline__ void store_ct(float *p, const float (&v)[CT])
     Vec<float, CT> q;
     q.set(v);
     q.store(p);
+}
+
+// N neighbouring floats, 16 bytes at a time where N allows
+template <int N>
+__device__ __forceinline__ void load_wide(float (&v)[N], const float *p)
+{
+    constexpr int Q = N < 4 ? N : 4;
+#pragma unroll
+    for (int i = 0; i < N; i += Q) {
+        float q[Q];
+        load_ct<Q>(q, p + i);
+#pragma unroll
+        for (int u = 0; u < Q; ++u) v[i + u] = q[u];
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void store_wide(float *p, const float (&v)[N])
+{
+    constexpr int Q = N < 4 ? N : 4;
+#pragma unroll
+    for (int i = 0; i < N; i += Q) {
+        float q[Q];
+#pragma unroll
+        for (int u = 0; u < Q; ++u) q[u] = v[i + u];
+        store_ct<Q>(p + i, q);
+    }
 }
 
 struct ScanCall {
@@ -256,11 +297,11 @@ cudaError_t fwd_layout(int N, F f)
 template <class F>
 cudaError_t bwd_layout(int N, F f)
 {
-    if (N <= 8) return f(ScanCfg<4, 2, 2>{});
-    if (N <= 16) return f(ScanCfg<4, 4, 2>{});
-    if (N <= 32) return f(ScanCfg<8, 4, 2>{});
-    if (N <= 64) return f(ScanCfg<16, 4, 1>{});
-    return f(ScanCfg<16, 8, 1>{});
+    if (N <= 8) return f(ScanCfg<4, 2, 2, 16, 128>{});
+    if (N <= 16) return f(ScanCfg<4, 4, 2, 16, 128>{});
+    if (N <= 32) return f(ScanCfg<8, 4, 2, 16, 128>{});
+    if (N <= 64) return f(ScanCfg<16, 4, 1, 16, 128>{});
+    return f(ScanCfg<16, 8, 1, 16, 128>{});
 }
 
 }  // namespace lay

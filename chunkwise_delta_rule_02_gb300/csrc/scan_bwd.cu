@@ -29,7 +29,6 @@ namespace lay {
 namespace {
 
 constexpr int kTile = kScanKeep;
-constexpr int kWarps = kScanThreads / 32;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <class T>
@@ -44,26 +43,31 @@ struct BwdIo {
     float *part_bc;         // [B][channel tiles][T][2 Np]
 };
 
-template <class Cfg>
+template <class T, class Cfg, int VB>
 struct BwdShared {
+    static constexpr int VEC = VB ? VB / sizeof(T) : 1, NV = Cfg::EPT / VEC, WARPS = Cfg::NT / 32;
+    // the next tile's x, dt, dy, z as copied; a thread reads back only what it copied itself
+    __align__(16) char raw[4][NV][Cfg::NT][VB ? VB : 1];
     float2 dd[kTile][Cfg::CH];                        // delta, delta x
     float g[kTile][Cfg::RS];
     float x[kTile][Cfg::RS], s[kTile][Cfg::RS], gz[kTile][Cfg::RS];   // x, softplus', dy silu'(z); then dx, ddt, dz
     __align__(16) float b[kTile][Cfg::Np];
     __align__(16) float c[kTile][Cfg::Np];
-    __align__(16) float st[(kTile / Cfg::L) * Cfg::CT * kScanThreads * Cfg::S];   // states entering the groups
-    float bc[kTile][kWarps][2 * Cfg::Np];
+    __align__(16) float st[(kTile / Cfg::L) * Cfg::CT * Cfg::NT * Cfg::S];   // states entering the groups
+    float bc[kTile][WARPS][2 * Cfg::Np];
     int seq[32];
     uint32_t edge[2];
 };
 
-template <class T, class Cfg, int VEC, bool SUM>
-__global__ void __launch_bounds__(kScanThreads, 2) k_scan_bwd(ScanDims g, BwdIo<T> io)
+// VB: bytes of an asynchronous copy; 0: element loads where they are used.
+template <class T, class Cfg, int VB, bool SUM>
+__global__ void __launch_bounds__(Cfg::NT, 3) k_scan_bwd(ScanDims g, BwdIo<T> io)
 {
     constexpr int L = Cfg::L, S = Cfg::S, CT = Cfg::CT, M = Cfg::M, Np = Cfg::Np, CH = Cfg::CH, P = S / 2;
-    constexpr int NV = Cfg::EPT / VEC, NBC = Cfg::NBC;
+    using Shared = BwdShared<T, Cfg, VB>;
+    constexpr int VEC = Shared::VEC, NV = Shared::NV, NBC = Cfg::NBC;
     extern __shared__ __align__(16) char smem_raw[];
-    BwdShared<Cfg> &sm = *reinterpret_cast<BwdShared<Cfg> *>(smem_raw);
+    Shared &sm = *reinterpret_cast<Shared *>(smem_raw);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = lane / M, n0 = l * S;
     const int ch = (warp * M + lane % M) * CT;
@@ -99,33 +103,28 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_bwd(ScanDims g, BwdIo<
         }
     }
 
-    constexpr int RV = CH / VEC, ES = kScanThreads / RV;
+    constexpr int RV = CH / VEC, ES = Cfg::NT / RV;
     const int vt = tid / RV, vc = tid % RV * VEC;
     const bool col = cg0 + vc < g.Dg;
     const int cv = c0 + (col ? vc : 0);
-    Vec<T, VEC> xn[NV], dn[NV], zn[NV], gn[NV];
     T br[NBC], cr[NBC];
-    float bias[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) bias[i] = col && g.bias ? g.bias[cv + i] : 0.f;
     auto fetch = [&](int t0) {
+        if constexpr (VB > 0) {
 #pragma unroll
-        for (int e = 0; e < NV; ++e) {
-            const int t = t0 + vt + e * ES;
-            xn[e].zero();
-            dn[e].zero();
-            zn[e].zero();
-            gn[e].zero();
-            if (col && t >= ts && t < te) {
-                if (!SUM) xn[e].load(io.x.at(b, 0, t) + cv);
-                dn[e].load(io.dt.at(b, 0, t) + cv);
-                gn[e].load(io.dy.at(b, 0, t) + cv);
-                if (gated) zn[e].load(io.z.at(b, 0, t) + cv);
+            for (int e = 0; e < NV; ++e) {
+                const int t = t0 + vt + e * ES;
+                const bool in = col && t >= ts && t < te;
+                const int ta = in ? t : ts;   // an address inside, whether it is read or not
+                if (!SUM) copy_async<VB>(sm.raw[0][e][tid], io.x.at(b, 0, ta) + cv, in);
+                copy_async<VB>(sm.raw[1][e][tid], io.dt.at(b, 0, ta) + cv, in);
+                copy_async<VB>(sm.raw[2][e][tid], io.dy.at(b, 0, ta) + cv, in);
+                if (gated) copy_async<VB>(sm.raw[3][e][tid], io.z.at(b, 0, ta) + cv, in);
             }
+            copy_commit();
         }
 #pragma unroll
         for (int e = 0; e < NBC; ++e) {
-            const int i = tid + e * kScanThreads, t = t0 + i / Np, n = i % Np;
+            const int i = tid + e * Cfg::NT, t = t0 + i / Np, n = i % Np;
             st_out(&br[e], 0.f);
             st_out(&cr[e], 0.f);
             if (i < kTile * Np && t >= ts && t < te && n < g.N) {
@@ -134,47 +133,61 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_bwd(ScanDims g, BwdIo<
             }
         }
     };
+    // vector e of x (0), dt (1), dy (2) or z (3) of the tile at t0
+    auto element = [&](float (&f)[VEC], const View<const T> &v, int which, int e, int t0) {
+        Vec<T, VEC> q;
+        if constexpr (VB > 0) {
+            q.load(reinterpret_cast<const T *>(sm.raw[which][e][tid]));
+        } else {
+            q.zero();
+            const int t = t0 + vt + e * ES;
+            if (col && t < te) q.load(v.at(b, 0, t) + cv);
+        }
+        q.get(f);
+    };
     const int last = ts + (te - ts - 1) / kTile * kTile;
     fetch(last);
 
     for (int t0 = last; t0 >= ts; t0 -= kTile) {
         // 1. the tile into shared memory
+        if constexpr (VB > 0) copy_wait();
 #pragma unroll
         for (int e = 0; e < NV; ++e) {
             float x[VEC], d[VEC], z[VEC], gy[VEC], sp[VEC], gz[VEC];
-            xn[e].get(x);
-            dn[e].get(d);
-            zn[e].get(z);
-            gn[e].get(gy);
+            if constexpr (!SUM) element(x, io.x, 0, e, t0);
+            element(d, io.dt, 1, e, t0);
+            element(gy, io.dy, 2, e, t0);
+            if (gated) element(z, io.z, 3, e, t0);
             const int t = vt + e * ES;
             const bool in = col && t0 + t < te;
 #pragma unroll
             for (int i = 0; i < VEC; i += 2) {
-                float2 v = add2(pair_at(d, i), pair_at(bias, i)), der = two(1.f);
+                float2 v = pair_at(d, i), der = two(1.f), w = two(0.f);
+                if (g.bias) v = add2(v, make_float2(g.bias[cv + i], g.bias[cv + (VEC > 1 ? i + 1 : i)]));
                 if (g.softplus) softplus(v, v, der);
-                if (!in) v = two(0.f);
-                const float2 w = in ? mul2(v, pair_at(x, i)) : two(0.f);
+                if constexpr (!SUM) w = mul2(v, pair_at(x, i));
+                if (!in) v = w = two(0.f);
                 if constexpr (VEC > 1) *reinterpret_cast<float4 *>(&sm.dd[t][vc + i]) = make_float4(v.x, w.x, v.y, w.y);
                 else sm.dd[t][vc] = make_float2(v.x, w.x);
                 put_pair(sp, i, der);
                 float2 gg = pair_at(gy, i);
                 if (gated) {
                     const float2 zz = pair_at(z, i), sg = sigmoid2(zz);
-                    put_pair(gz, i, mul2(gg, make_float2(dsilu(zz.x, sg.x), dsilu(zz.y, sg.y))));
+                    if (!SUM) put_pair(gz, i, mul2(gg, make_float2(dsilu(zz.x, sg.x), dsilu(zz.y, sg.y))));
                     gg = mul2(gg, mul2(zz, sg));
                 }
                 put_pair(gy, i, gg);
             }
-            store_ct<VEC>(&sm.g[t][vc], gy);
+            store_wide<VEC>(&sm.g[t][vc], gy);
             if constexpr (!SUM) {
-                store_ct<VEC>(&sm.x[t][vc], x);
-                store_ct<VEC>(&sm.s[t][vc], sp);
-                if (gated) store_ct<VEC>(&sm.gz[t][vc], gz);
+                store_wide<VEC>(&sm.x[t][vc], x);
+                store_wide<VEC>(&sm.s[t][vc], sp);
+                if (gated) store_wide<VEC>(&sm.gz[t][vc], gz);
             }
         }
 #pragma unroll
         for (int e = 0; e < NBC; ++e) {
-            const int i = tid + e * kScanThreads;
+            const int i = tid + e * Cfg::NT;
             if (i < kTile * Np) {
                 if (!SUM) sm.b[i / Np][i % Np] = ld_in(&br[e]);
                 sm.c[i / Np][i % Np] = ld_in(&cr[e]);
@@ -253,7 +266,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_bwd(ScanDims g, BwdIo<
                     }
                 }
             };
-            auto group_state = [&](int gi, int e) { return &sm.st[((gi * CT + e) * kScanThreads + tid) * S]; };
+            auto group_state = [&](int gi, int e) { return &sm.st[((gi * CT + e) * Cfg::NT + tid) * S]; };
 #pragma unroll 1
             for (int gi = 0; gi < kTile / L - 1; ++gi) {
 #pragma unroll
@@ -381,14 +394,14 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_bwd(ScanDims g, BwdIo<
                 if (col && t0 + t < te) {
                     Vec<T, VEC> out;
                     float f[VEC];
-                    load_ct<VEC>(f, &sm.x[t][vc]);
+                    load_wide<VEC>(f, &sm.x[t][vc]);
                     out.set(f);
                     out.store(io.dx.at(b, 0, t0 + t) + cv);
-                    load_ct<VEC>(f, &sm.s[t][vc]);
+                    load_wide<VEC>(f, &sm.s[t][vc]);
                     out.set(f);
                     out.store(io.ddt.at(b, 0, t0 + t) + cv);
                     if (gated) {
-                        load_ct<VEC>(f, &sm.gz[t][vc]);
+                        load_wide<VEC>(f, &sm.gz[t][vc]);
                         out.set(f);
                         out.store(io.dz.at(b, 0, t0 + t) + cv);
                     }
@@ -396,10 +409,10 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_bwd(ScanDims g, BwdIo<
             }
             float *pb = io.part_bc + (((size_t)b * tiles + tile) * g.T + t0) * (2 * Np);
             const int n = min(kTile, te - t0) * 2 * Np;
-            for (int i = tid; i < n; i += kScanThreads) {
+            for (int i = tid; i < n; i += Cfg::NT) {
                 float s = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) s += sm.bc[i / (2 * Np)][w][i % (2 * Np)];
+                for (int w = 0; w < Shared::WARPS; ++w) s += sm.bc[i / (2 * Np)][w][i % (2 * Np)];
                 pb[i] = s;
             }
             __syncthreads();
@@ -494,7 +507,7 @@ Plan plan_of(const dn_scan_shape *s)
     return p;
 }
 
-template <class T, class Cfg, int VEC>
+template <class T, class Cfg, int VB>
 cudaError_t launch(const ScanCall &c, cudaStream_t st)
 {
     const Plan p = plan_of(c.s);
@@ -514,17 +527,17 @@ cudaError_t launch(const ScanCall &c, cudaStream_t st)
     io.part_a = F(p.part_a); io.part_d = F(p.part_d); io.part_bc = F(p.part_bc);
     const long long per = (long long)g.B * g.G * g.tiles;
     if (per * g.K > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const size_t smem = sizeof(BwdShared<Cfg>);
+    const size_t smem = sizeof(BwdShared<T, Cfg, VB>);
     cudaError_t e;
     if (g.K > 1) {
-        e = cudaFuncSetAttribute(k_scan_bwd<T, Cfg, VEC, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(k_scan_bwd<T, Cfg, VB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        k_scan_bwd<T, Cfg, VEC, true><<<(unsigned)(per * (g.K - 1)), kScanThreads, smem, st>>>(g, io);
+        k_scan_bwd<T, Cfg, VB, true><<<(unsigned)(per * (g.K - 1)), Cfg::NT, smem, st>>>(g, io);
         scan_carry<false>(g, io.segP, io.segH, Cfg::Np, st);
     }
-    e = cudaFuncSetAttribute(k_scan_bwd<T, Cfg, VEC, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(k_scan_bwd<T, Cfg, VB, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    k_scan_bwd<T, Cfg, VEC, false><<<(unsigned)(per * g.K), kScanThreads, smem, st>>>(g, io);
+    k_scan_bwd<T, Cfg, VB, false><<<(unsigned)(per * g.K), Cfg::NT, smem, st>>>(g, io);
     const long long n = (long long)g.B * g.G * g.T * 2 * Cfg::Np;
     if ((n + 255) / 256 > 0x7fffffffLL) return cudaErrorInvalidValue;
     k_scan_bc<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(io.part_bc, view_of<T>(&gr->db), view_of<T>(&gr->dc), g.B, g.T, g.N,
@@ -550,14 +563,14 @@ cudaError_t bwd_t(const ScanCall &c, cudaStream_t st)
     if (s->T > 0) {
         const cudaError_t e = bwd_layout(s->N, [&](auto cfg) {
             using Cfg = decltype(cfg);
-            constexpr int VEC = Cfg::VEC;
-            const dn_view *all[] = {&io->x, &io->dt, &io->z, &gr->dy, &gr->dx, &gr->ddt, &gr->dz};
-            bool v = (s->D / s->G) % VEC == 0;
-            for (const dn_view *q : all) v = v && can_vector(q, sizeof(T), VEC * sizeof(T));
-            if constexpr (VEC > 1) {
-                if (v) return launch<T, Cfg, VEC>(c, st);
+            constexpr int VB = Cfg::template bytes<T>();
+            if constexpr (VB > 0) {
+                const dn_view *all[] = {&io->x, &io->dt, &io->z, &gr->dy, &gr->dx, &gr->ddt, &gr->dz};
+                bool v = (s->D / s->G) % (VB / sizeof(T)) == 0;
+                for (const dn_view *q : all) v = v && can_vector(q, sizeof(T), VB);
+                if (v) return launch<T, Cfg, VB>(c, st);
             }
-            return launch<T, Cfg, 1>(c, st);
+            return launch<T, Cfg, 0>(c, st);
         });
         if (e != cudaSuccess) return e;
     }

@@ -23,7 +23,7 @@ namespace lay {
 namespace {
 
 template <class T, class Cfg, int VEC, bool SUM>
-__global__ void __launch_bounds__(kScanThreads) k_scan_fwd(ScanDims g, ScanIo<T> io)
+__global__ void __launch_bounds__(Cfg::NT) k_scan_fwd(ScanDims g, ScanIo<T> io)
 {
     constexpr int L = Cfg::L, S = Cfg::S, CT = Cfg::CT, M = Cfg::M, Np = Cfg::Np, CH = Cfg::CH, P = S / 2;
     constexpr int TT = Cfg::TT, NV = Cfg::EPT / VEC, NBC = Cfg::NBC;
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_fwd(ScanDims g, ScanIo<T>
 
     // This thread's vectors of a tile: tokens vt, vt + ES, ..., always channels vc .. vc + VEC - 1
     // (a token's vectors divide the threads).
-    constexpr int RV = CH / VEC, ES = kScanThreads / RV;
+    constexpr int RV = CH / VEC, ES = Cfg::NT / RV;
     const int vt = tid / RV, vc = tid % RV * VEC;
     const bool col = cg0 + vc < g.Dg, gated = !SUM && io.z.p != nullptr;
     const int cv = c0 + (col ? vc : 0);
@@ -83,9 +83,9 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_fwd(ScanDims g, ScanIo<T>
         skip[i] = !SUM && col && g.Dskip ? g.Dskip[cv + i] : 0.f;
     }
     // this thread's elements of B and C: state bn of tokens bt, bt + BS, ...
-    constexpr int BS = kScanThreads / Np;
+    constexpr int BS = Cfg::NT / Np;
     const int bt = tid / Np, bn = tid % Np;
-    const bool bc_in = bn < g.N && (NBC * kScanThreads == TT * Np || tid < TT * Np);
+    const bool bc_in = bn < g.N && (NBC * Cfg::NT == TT * Np || tid < TT * Np);
     const T *pb = io.b.at(b, grp, ts + bt) + bn, *pc = SUM ? nullptr : io.c.at(b, grp, ts + bt) + bn;
     const bool whole = cg0 + CH <= g.Dg;   // no channel of the block is behind its group's end
     // whole tiles (the same for every thread) take the loads without their checks
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_fwd(ScanDims g, ScanIo<T>
         }
 #pragma unroll
         for (int e = 0; e < NBC; ++e) {
-            if (NBC * kScanThreads == TT * Np || tid < TT * Np) {
+            if (NBC * Cfg::NT == TT * Np || tid < TT * Np) {
                 sb[bt + e * BS][bn] = ld_in(&br[e]);
                 if constexpr (!SUM) sc[bt + e * BS][bn] = ld_in(&cr[e]);
             }
@@ -388,10 +388,10 @@ cudaError_t launch(const ScanCall &c, cudaStream_t st)
     if (g.K > 1) {
         io.segP = (float *)c.ws;
         io.segH = io.segP + (size_t)g.B * g.K * g.D * Cfg::Np;
-        k_scan_fwd<T, Cfg, VEC, true><<<(unsigned)(per * (g.K - 1)), kScanThreads, 0, st>>>(g, io);
+        k_scan_fwd<T, Cfg, VEC, true><<<(unsigned)(per * (g.K - 1)), Cfg::NT, 0, st>>>(g, io);
         scan_carry<true>(g, io.segP, io.segH, Cfg::Np, st);
     }
-    k_scan_fwd<T, Cfg, VEC, false><<<(unsigned)(per * g.K), kScanThreads, 0, st>>>(g, io);
+    k_scan_fwd<T, Cfg, VEC, false><<<(unsigned)(per * g.K), Cfg::NT, 0, st>>>(g, io);
     return cudaPeekAtLastError();
 }
 

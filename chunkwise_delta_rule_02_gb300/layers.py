@@ -72,30 +72,28 @@ def _L():
 
 def _tokens(t: torch.Tensor, name: str, shape, dtype) -> torch.Tensor:
     """A token array: CUDA, the call's dtype and shape, contiguous features."""
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and (t.stride(-1) == 1 or shape[-1] <= 1):
+        return t
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s like the call's other token arrays, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError("%s: the feature axis must be contiguous (stride 1), got strides %s" % (name, t.stride()))
     if not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
-    return t
+    raise ValueError("%s: the feature axis must be contiguous (stride 1), got strides %s" % (name, t.stride()))
 
 
 def _dense(t: Optional[torch.Tensor], name: str, shape, dtype=torch.float32):
     """A dense array (parameter, state) or None."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+        return t
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
     if not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
-    return t
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _dtype_code(t: torch.Tensor, name: str) -> int:
@@ -110,7 +108,7 @@ def _result(t: Optional[torch.Tensor], name: str, like: torch.Tensor) -> torch.T
     if t is None:
         return torch.empty(like.shape, dtype=like.dtype, device=like.device)
     _tokens(t, name, like.shape, like.dtype)
-    if t.device != like.device:
+    if t.get_device() != like.get_device():
         raise ValueError("%s is on %s, the inputs are on %s" % (name, t.device, like.device))
     if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
         raise ValueError("%s must not repeat memory along an axis (stride 0)" % name)
@@ -119,12 +117,12 @@ def _result(t: Optional[torch.Tensor], name: str, like: torch.Tensor) -> torch.T
 
 def _same_device(first: torch.Tensor, *rest):
     """All arguments on one device, and that device current (its stream is the one used)."""
-    dev = first.device
+    dev = first.get_device()
     for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError("tensors on different devices: %s and %s" % (dev, t.device))
-    if torch.cuda.current_device() != dev.index:
-        raise ValueError("%s is not the current CUDA device: call under torch.cuda.device(%d)" % (dev, dev.index))
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors on different devices: %s and %s" % (first.device, t.device))
+    if torch.cuda.current_device() != dev:
+        raise ValueError("%s is not the current CUDA device: call under torch.cuda.device(%d)" % (first.device, dev))
 
 
 def _p(t):
@@ -133,21 +131,26 @@ def _p(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _view4(t: Optional[torch.Tensor]) -> Optional[bytes]:
-    """[B,H,T,d] as a dn_view record."""
+def _dims(t: torch.Tensor):
+    """B, H, T, d of a token array [B,H,T,d], [B,T,d] (one head) or [R,d] (rows)."""
+    s = t.shape
+    n = len(s)
+    return s if n == 4 else (s[0], 1, s[1], s[2]) if n == 3 else (1, 1, s[0], s[1])
+
+
+def _view(t: Optional[torch.Tensor]) -> Optional[bytes]:
+    """Its dn_view record (None: absent)."""
     if t is None:
         return None
-    b, h, tm, _ = t.stride()
-    return _VIEW.pack(t.data_ptr(), b, h, tm)
-
-
-def _four(t: Optional[torch.Tensor]):
-    """[B,T,C] as [B,1,T,C]; [B,H,T,d] as it is."""
-    return t if t is None or t.dim() == 4 else t.unsqueeze(1)
+    s = t.stride()
+    n = len(s)
+    if n == 4:
+        return _VIEW.pack(t.data_ptr(), s[0], s[1], s[2])
+    return _VIEW.pack(t.data_ptr(), s[0], 0, s[1]) if n == 3 else _VIEW.pack(t.data_ptr(), 0, 0, s[0])
 
 
 def _cu(cu_seqlens, B):
@@ -172,8 +175,8 @@ def _ws(nbytes: int, device, where: str) -> torch.Tensor:
 # ------------------------------------------------------------------ convolution
 
 def conv_shape(x: torch.Tensor, width: int, silu: bool = True, cu_seqlens=None) -> bytes:
-    """dn_conv_shape record of x [B,H,T,d]."""
-    B, H, T, d = x.shape
+    """dn_conv_shape record of x [B,H,T,d] or [B,T,C]."""
+    B, H, T, d = _dims(x)
     cu, n = _cu(cu_seqlens, B)
     return _CONV_SHAPE.pack(B, H, T, d, width, _dtype_code(x, "x"), 1 if silu else 0, n, cu)
 
@@ -183,27 +186,26 @@ def dn_conv_workspace_size(shape: bytes, for_backward: bool = False) -> int:
 
 
 def dn_conv_fwd(shape, x, w, bias, s0, y, sT, ws, stream=None):
-    _check(_L().dn_conv_fwd(shape, _view4(x), _p(w), _p(bias), _p(s0), _view4(y), _p(sT), _p(ws),
+    _check(_L().dn_conv_fwd(shape, _view(x), _p(w), _p(bias), _p(s0), _view(y), _p(sT), _p(ws),
                             ws.numel() * ws.element_size(), _stream(stream)), "dn_conv_fwd")
 
 
 def dn_conv_bwd(shape, x, w, bias, s0, dy, dsT, dx, dw, dbias, ds0, ws, stream=None):
-    _check(_L().dn_conv_bwd(shape, _view4(x), _p(w), _p(bias), _p(s0), _view4(dy), _p(dsT), _view4(dx),
+    _check(_L().dn_conv_bwd(shape, _view(x), _p(w), _p(bias), _p(s0), _view(dy), _p(dsT), _view(dx),
                             _p(dw), _p(dbias), _p(ds0), _p(ws), ws.numel() * ws.element_size(),
                             _stream(stream)), "dn_conv_bwd")
 
 
 def dn_conv_step(shape, x, w, bias, state_in, state_out, y, stream=None):
-    _check(_L().dn_conv_step(shape, _view4(x), _p(w), _p(bias), _p(state_in), _p(state_out), _view4(y),
+    _check(_L().dn_conv_step(shape, _view(x), _p(w), _p(bias), _p(state_in), _p(state_out), _view(y),
                              _stream(stream)), "dn_conv_step")
 
 
 def _conv_args(x, w, bias, state, cu_seqlens):
     if x.dim() not in (3, 4):
         raise ValueError("x must be [B,H,T,d] or [B,T,C], got %d axes" % x.dim())
-    x4 = _four(x)
-    B, H, T, d = x4.shape
-    _tokens(x4, "x", x4.shape, x.dtype)
+    B, H, T, d = _dims(x)
+    _tokens(x, "x", x.shape, x.dtype)
     if w.dim() != 2:
         raise ValueError("w must be [channels, width]")
     width = w.shape[1]
@@ -212,7 +214,7 @@ def _conv_args(x, w, bias, state, cu_seqlens):
     n = B if cu_seqlens is None else cu_seqlens.numel() - 1
     _dense(state, "state", (n, width - 1, H * d), x.dtype)
     _same_device(x, w, bias, state, cu_seqlens)
-    return x4, n, width
+    return n, width
 
 
 def conv_forward(x, w, bias=None, state=None, cu_seqlens=None, silu=True, out=None, want_state=True, ws=None,
@@ -221,13 +223,13 @@ def conv_forward(x, w, bias=None, state=None, cu_seqlens=None, silu=True, out=No
     w [C,width] and bias [C] float32 with C = H d, width 2..4; state [N,width-1,C] in x's dtype:
     the inputs before each sequence (None: zero).  Returns (y, final state or None); y is a new
     contiguous tensor of x's shape, or ``out``."""
-    x4, n, width = _conv_args(x, w, bias, state, cu_seqlens)
+    n, width = _conv_args(x, w, bias, state, cu_seqlens)
     y = _result(out, "out", x)
     sT = torch.empty((n, width - 1, w.shape[0]), dtype=x.dtype, device=x.device) if want_state else None
-    shape = conv_shape(x4, width, silu, cu_seqlens)
+    shape = conv_shape(x, width, silu, cu_seqlens)
     if ws is None:
         ws = _ws(dn_conv_workspace_size(shape, False), x.device, "dn_conv_fwd")
-    dn_conv_fwd(shape, x4, w, bias, state, _four(y), sT, ws)
+    dn_conv_fwd(shape, x, w, bias, state, y, sT, ws)
     if check_status and cu_seqlens is not None:
         _check(dn_device_status(ws), "dn_conv_fwd (device status)")
     return y, sT
@@ -236,17 +238,17 @@ def conv_forward(x, w, bias=None, state=None, cu_seqlens=None, silu=True, out=No
 def conv_backward(x, w, bias, state, dy, dstate=None, cu_seqlens=None, silu=True, out=None, ws=None, check_status=True):
     """Gradients of <y, dy> + <final state, dstate>: dict dx (x's shape; contiguous, or ``out``), dw, dbias
     (None without bias), dstate (of the initial state, None without one)."""
-    x4, n, width = _conv_args(x, w, bias, state, cu_seqlens)
+    n, width = _conv_args(x, w, bias, state, cu_seqlens)
     _tokens(dy, "dy", x.shape, x.dtype)
     _dense(dstate, "dstate", (n, width - 1, w.shape[0]), x.dtype)
     _same_device(x, dy, dstate)
     dx = _result(out, "out", x)
     g = dict(dx=dx, dw=torch.empty_like(w), dbias=None if bias is None else torch.empty_like(bias),
              dstate=None if state is None else torch.empty_like(state))
-    shape = conv_shape(x4, width, silu, cu_seqlens)
+    shape = conv_shape(x, width, silu, cu_seqlens)
     if ws is None:
         ws = _ws(dn_conv_workspace_size(shape, True), x.device, "dn_conv_bwd")
-    dn_conv_bwd(shape, x4, w, bias, state, _four(dy), dstate, _four(dx), g["dw"], g["dbias"], g["dstate"], ws)
+    dn_conv_bwd(shape, x, w, bias, state, dy, dstate, dx, g["dw"], g["dbias"], g["dstate"], ws)
     if check_status and cu_seqlens is not None:
         _check(dn_device_status(ws), "dn_conv_bwd (device status)")
     return g
@@ -279,17 +281,18 @@ def conv_step(x, w, bias=None, state=None, out_state=None, silu=True, out=None):
 # ------------------------------------------------------------------ selective scan
 
 def _flat(t: Optional[torch.Tensor]):
-    """[B,T,D] as the four numbers of a dn_view."""
+    """[B,T,D], or [n,D] (one token each), as the four numbers of a dn_view."""
     if t is None:
         return 0, 0, 0, 0
-    b, tm, _ = t.stride()
-    return t.data_ptr(), b, 0, tm
+    s = t.stride()
+    return t.data_ptr(), s[0], 0, s[1] if len(s) == 3 else 0
 
 
-def _grouped(t: torch.Tensor):
-    """[B,T,G,N] likewise (head = group)."""
-    b, tm, g, _ = t.stride()
-    return t.data_ptr(), b, g, tm
+def _grouped(t: torch.Tensor, tokens: bool = True):
+    """B or C likewise (head = group): [B,T,G,N] or [B,T,N], without the T axis for single tokens."""
+    s = t.stride()
+    tm, s = (s[1], (s[0],) + s[2:]) if tokens else (0, s)
+    return t.data_ptr(), s[0], s[1] if len(s) == 3 else 0, tm
 
 
 def _ptr(t) -> int:
@@ -297,16 +300,19 @@ def _ptr(t) -> int:
 
 
 def scan_shape(x: torch.Tensor, Bm: torch.Tensor, dt_softplus: bool = True, cu_seqlens=None) -> bytes:
-    """dn_scan_shape record of x [B,T,D] and Bm [B,T,G,N]."""
-    B, T, D = x.shape
-    cu, n = _cu(cu_seqlens, B)
-    return _SCAN_SHAPE.pack(B, T, D, Bm.shape[3], Bm.shape[2], _dtype_code(x, "x"), 1 if dt_softplus else 0, n, cu)
+    """dn_scan_shape record of x [B,T,D] and Bm [B,T,G,N] or [B,T,N] (x [n,D]: single tokens)."""
+    xs, bs = x.shape, Bm.shape
+    tokens = len(xs) == 3
+    cu, n = _cu(cu_seqlens, xs[0])
+    G = bs[-2] if len(bs) == (4 if tokens else 3) else 1
+    return _SCAN_SHAPE.pack(xs[0], xs[1] if tokens else 1, xs[-1], bs[-1], G, _dtype_code(x, "x"), 1 if dt_softplus else 0, n, cu)
 
 
 def scan_io(x, dt, A, B, C, D, z, dt_bias, h0, y, hT) -> bytes:
-    """dn_scan_io record; x, dt, z, y [B,T,D], B, C [B,T,G,N]."""
-    return _SCAN_IO.pack(*_flat(x), *_flat(dt), *_grouped(B), *_grouped(C), *_flat(z), *_flat(y), A.data_ptr(),
-                         _ptr(D), _ptr(dt_bias), _ptr(h0), _ptr(hT))
+    """dn_scan_io record; x, dt, z, y [B,T,D], B, C [B,T,G,N] or [B,T,N] (x [n,D]: single tokens)."""
+    tokens = x.dim() == 3
+    return _SCAN_IO.pack(*_flat(x), *_flat(dt), *_grouped(B, tokens), *_grouped(C, tokens), *_flat(z), *_flat(y),
+                         A.data_ptr(), _ptr(D), _ptr(dt_bias), _ptr(h0), _ptr(hT))
 
 
 def scan_grads(dy, dx, ddt, dB, dC, dz, dhT, dA, dD, ddt_bias, dh0) -> bytes:
@@ -337,33 +343,36 @@ def dn_scan_step(shape, io, stream=None):
     _check(_L().dn_scan_step(shape, io, _stream(stream)), "dn_scan_step")
 
 
-def _scan_args(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens):
-    if x.dim() != 3:
-        raise ValueError("x must be [B,T,D], got %d axes" % x.dim())
-    nb, T, Dc = x.shape
+def _scan_args(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, axes):
+    """Checks a scan's arguments (axes: of x, 3 or 2); the number of sequences."""
+    xs = x.shape
+    if len(xs) != axes:
+        raise ValueError("x must be %s, got %d axes" % ("[B,T,D]" if axes == 3 else "[n,D]", len(xs)))
     if A.dim() != 2:
         raise ValueError("A must be [D,N]")
-    N = A.shape[1]
-    # one group: B and C may come without the group axis
-    B4 = B.unsqueeze(2) if B.dim() == 3 else B
-    C4 = C.unsqueeze(2) if C.dim() == 3 else C
-    if B4.dim() != 4 or B4.shape[2] < 1 or Dc % B4.shape[2]:
-        raise ValueError("B must be [B,T,G,N] (or [B,T,N]) with G dividing the %d channels" % Dc)
-    dtype = x.dtype
+    Dc, N = xs[-1], A.shape[1]
+    dtype, lead = x.dtype, xs[:-1]
     _dtype_code(x, "x")
-    _tokens(x, "x", x.shape, dtype)
-    _tokens(dt, "dt", x.shape, dtype)
+    # one group: B and C may come without the group axis
+    bs = B.shape
+    G = bs[-2] if len(bs) == axes + 1 else 1
+    if len(bs) not in (axes, axes + 1) or G < 1 or Dc % G:
+        raise ValueError("B must be %s[G,N] (or %s[N]) with G dividing the %d channels" % (("[B,T]", "[B,T]", Dc) if axes == 3 else
+                                                                                   ("[n]", "[n]", Dc)))
+    _tokens(x, "x", xs, dtype)
+    _tokens(dt, "dt", xs, dtype)
     if z is not None:
-        _tokens(z, "z", x.shape, dtype)
-    _tokens(B4, "B", (nb, T, B4.shape[2], N), dtype)
-    _tokens(C4, "C", B4.shape, dtype)
+        _tokens(z, "z", xs, dtype)
+    want = lead + (N,) if len(bs) == axes else lead + (G, N)
+    _tokens(B, "B", want, dtype)
+    _tokens(C, "C", want, dtype)
     _dense(A, "A", (Dc, N))
     _dense(D, "D", (Dc,))
     _dense(dt_bias, "dt_bias", (Dc,))
-    n = nb if cu_seqlens is None else cu_seqlens.numel() - 1
+    n = xs[0] if cu_seqlens is None else cu_seqlens.numel() - 1
     _dense(h0, "h0", (n, Dc, N))
     _same_device(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens)
-    return B4, C4, n
+    return n
 
 
 def scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=None, dt_softplus=True, out=None,
@@ -373,14 +382,14 @@ def scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqle
     softplus(dt + dt_bias) (dt + dt_bias with dt_softplus=False); A <= 0 and steps >= 0 decay.
     Returns (y, hT), or (y, hT, saved) with save=True for scan_backward(saved=saved): the states
     entering every 16th token, N / 4 bytes a token and channel."""
-    B4, C4, n = _scan_args(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens)
+    n = _scan_args(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, 3)
     y = _result(out, "out", x)
     hT = torch.empty((n,) + tuple(A.shape), dtype=torch.float32, device=x.device) if want_state else None
-    shape = scan_shape(x, B4, dt_softplus, cu_seqlens)
+    shape = scan_shape(x, B, dt_softplus, cu_seqlens)
     if ws is None:
         ws = _ws(dn_scan_workspace_size(shape, False), x.device, "dn_scan_fwd")
     saved = _ws(dn_scan_saved_size(shape), x.device, "dn_scan_fwd") if save else None
-    dn_scan_fwd(shape, scan_io(x, dt, A, B4, C4, D, z, dt_bias, h0, y, hT), saved, ws)
+    dn_scan_fwd(shape, scan_io(x, dt, A, B, C, D, z, dt_bias, h0, y, hT), saved, ws)
     if check_status and cu_seqlens is not None:
         _check(dn_device_status(ws), "dn_scan_fwd (device status)")
     return (y, hT, saved) if save else (y, hT)
@@ -390,7 +399,7 @@ def scan_backward(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, dy=None
                   dt_softplus=True, ws=None, check_status=True):
     """Gradients of <y, dy> + <hT, dhT>, from scan_forward's arguments and ``saved`` buffer.  Returns dict
     dx, ddt, dA, dB, dC, and dD, dz, ddt_bias, dh0 (None for an argument that was not given)."""
-    B4, C4, n = _scan_args(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens)
+    n = _scan_args(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, 3)
     if dy is None or saved is None:
         raise ValueError("scan_backward needs dy and saved (scan_forward(save=True))")
     _tokens(dy, "dy", x.shape, x.dtype)
@@ -398,13 +407,11 @@ def scan_backward(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, dy=None
     _same_device(x, dy, dhT, saved)
     new = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
     g = dict(dx=new(x), ddt=new(x), dA=new(A), dB=new(B), dC=new(C), dD=new(D), dz=new(z), ddt_bias=new(dt_bias), dh0=new(h0))
-    shape = scan_shape(x, B4, dt_softplus, cu_seqlens)
+    shape = scan_shape(x, B, dt_softplus, cu_seqlens)
     if ws is None:
         ws = _ws(dn_scan_workspace_size(shape, True), x.device, "dn_scan_bwd")
-    dB4 = g["dB"].view(B4.shape)
-    dC4 = g["dC"].view(C4.shape)
-    dn_scan_bwd(shape, scan_io(x, dt, A, B4, C4, D, z, dt_bias, h0, None, None),
-                scan_grads(dy, g["dx"], g["ddt"], dB4, dC4, g["dz"], dhT, g["dA"], g["dD"], g["ddt_bias"], g["dh0"]), saved, ws)
+    dn_scan_bwd(shape, scan_io(x, dt, A, B, C, D, z, dt_bias, h0, None, None),
+                scan_grads(dy, g["dx"], g["ddt"], g["dB"], g["dC"], g["dz"], dhT, g["dA"], g["dD"], g["ddt_bias"], g["dh0"]), saved, ws)
     if check_status and cu_seqlens is not None:
         _check(dn_device_status(ws), "dn_scan_bwd (device status)")
     return g
@@ -413,28 +420,24 @@ def scan_backward(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, dy=None
 def scan_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, state=None, out_state=None, dt_softplus=True, out=None):
     """One token per sequence: x, dt, z [n,D], B, C [n,G,N] or [n,N], state [n,D,N] float32 (None: zero).
     Returns (y, new state); pass out_state=state to update the states in place."""
-    if x.dim() != 2:
-        raise ValueError("x must be [n,D], got %d axes" % x.dim())
-    one = lambda t: None if t is None else t.unsqueeze(1)  # noqa: E731
-    x3 = one(x)
-    B4, C4, n = _scan_args(x3, one(dt), A, one(B), one(C), D, one(z), dt_bias, state, None)
+    n = _scan_args(x, dt, A, B, C, D, z, dt_bias, state, None, 2)
     y = _result(out, "out", x)
-    sshape = (n,) + tuple(A.shape)
+    sshape = (n,) + A.shape
     if out_state is None:
         out_state = torch.empty(sshape, dtype=torch.float32, device=x.device)
     else:
         _dense(out_state, "out_state", sshape)
         _same_device(x, out_state)
-    dn_scan_step(scan_shape(x3, B4, dt_softplus), scan_io(x3, one(dt), A, B4, C4, D, one(z), dt_bias, state, one(y), out_state))
+    dn_scan_step(scan_shape(x, B, dt_softplus), scan_io(x, dt, A, B, C, D, z, dt_bias, state, y, out_state))
     return y, out_state
 
 
 # ------------------------------------------------------------------ norm
 
-def norm_shape(x4: torch.Tensor, w: torch.Tensor, eps: float) -> bytes:
-    """dn_norm_shape record of x [B,H,T,d] and w [d] or [H,d]."""
-    B, H, T, d = x4.shape
-    return _NORM_SHAPE.pack(B, H, T, d, _dtype_code(x4, "x"), 1 if w.dim() == 2 else 0, eps, 0)
+def norm_shape(x: torch.Tensor, w: torch.Tensor, eps: float) -> bytes:
+    """dn_norm_shape record of x [B,H,T,d], [B,T,d] or [R,d] and w [d] or [H,d]."""
+    B, H, T, d = _dims(x)
+    return _NORM_SHAPE.pack(B, H, T, d, _dtype_code(x, "x"), 1 if w.dim() == 2 else 0, eps, 0)
 
 
 def dn_norm_workspace_size(shape: bytes) -> int:
@@ -442,46 +445,39 @@ def dn_norm_workspace_size(shape: bytes) -> int:
 
 
 def dn_norm_fwd(shape, x, w, z, residual, res_scale, y, sum, stream=None):
-    _check(_L().dn_norm_fwd(shape, _view4(x), _p(w), _view4(z), _view4(residual), _p(res_scale), _view4(y),
-                            _view4(sum), _stream(stream)), "dn_norm_fwd")
+    _check(_L().dn_norm_fwd(shape, _view(x), _p(w), _view(z), _view(residual), _p(res_scale), _view(y),
+                            _view(sum), _stream(stream)), "dn_norm_fwd")
 
 
 def dn_norm_bwd(shape, x, w, z, res_scale, sum, dy, dsum, dx, dw, dz, dresidual, dres_scale, ws, stream=None):
-    _check(_L().dn_norm_bwd(shape, _view4(x), _p(w), _view4(z), _p(res_scale), _view4(sum), _view4(dy),
-                            _view4(dsum), _view4(dx), _p(dw), _view4(dz), _view4(dresidual), _p(dres_scale),
+    _check(_L().dn_norm_bwd(shape, _view(x), _p(w), _view(z), _p(res_scale), _view(sum), _view(dy),
+                            _view(dsum), _view(dx), _p(dw), _view(dz), _view(dresidual), _p(dres_scale),
                             _p(ws), ws.numel() * ws.element_size(), _stream(stream)), "dn_norm_bwd")
 
 
-def _rows(t, name, x):
-    """x [..., d] of 2, 3 or 4 axes as [B,H,T,d]: [R,d] -> [1,1,R,d], [B,T,d] -> [B,1,T,d]."""
-    if t is None:
-        return None
-    _tokens(t, name, x.shape, x.dtype)
-    return t[None, None] if t.dim() == 2 else _four(t)
-
-
-def _norm_args(x, w):
+def _norm_args(x, w, res_scale, **more):
     if x.dim() not in (2, 3, 4):
         raise ValueError("x must be [R,d], [B,T,d] or [B,H,T,d], got %d axes" % x.dim())
-    x4 = _rows(x, "x", x)
-    H, d = x4.shape[1], x4.shape[3]
+    _tokens(x, "x", x.shape, x.dtype)
+    _, H, _, d = _dims(x)
     _dense(w, "w", (H, d) if w.dim() == 2 else (d,))
-    return x4, d
+    _dense(res_scale, "res_scale", (d,))
+    for name, t in more.items():
+        if t is not None:
+            _tokens(t, name, x.shape, x.dtype)
+    _same_device(x, w, res_scale, *more.values())
 
 
 def norm_forward(x, w, z=None, residual=None, res_scale=None, eps=1e-6, out=None, out_sum=None):
     """RMS norm over the last axis.  x [R,d], [B,T,d] or [B,H,T,d]; w [d], or [H,d] for a weight per head.
     z: gate, y = rms(r) w silu(z).  residual: r = residual + res_scale x (res_scale [d] float32 or
     None: 1), otherwise r = x.  Returns y, or (y, r) with a residual."""
-    x4, d = _norm_args(x, w)
-    _dense(res_scale, "res_scale", (d,))
+    _norm_args(x, w, res_scale, z=z, residual=residual)
     if residual is None and (res_scale is not None or out_sum is not None):
         raise ValueError("res_scale and out_sum need a residual")
-    _same_device(x, w, z, residual, res_scale)
     y = _result(out, "out", x)
     r = None if residual is None else _result(out_sum, "out_sum", x)
-    dn_norm_fwd(norm_shape(x4, w, eps), x4, w, _rows(z, "z", x), _rows(residual, "residual", x), res_scale,
-                _rows(y, "out", x), _rows(r, "out_sum", x))
+    dn_norm_fwd(norm_shape(x, w, eps), x, w, z, residual, res_scale, y, r)
     return y if residual is None else (y, r)
 
 
@@ -489,21 +485,17 @@ def norm_backward(x, w, dy, z=None, sum=None, dsum=None, res_scale=None, eps=1e-
     """Gradients of <y, dy> + <r, dsum>.  Without a residual r = x; with one pass ``sum`` = r as norm_forward
     returned it, and x.  Returns dict dx, dw, dz (with z), dresidual (with sum), dres_scale (with
     res_scale); the others are None."""
-    x4, d = _norm_args(x, w)
-    _dense(res_scale, "res_scale", (d,))
+    _norm_args(x, w, res_scale, dy=dy, z=z, sum=sum, dsum=dsum)
     if sum is None and (res_scale is not None or dsum is not None):
         raise ValueError("res_scale and dsum need sum (the residual sum of the forward pass)")
-    _same_device(x, w, dy, z, sum, dsum, res_scale)
     new = lambda: torch.empty(x.shape, dtype=x.dtype, device=x.device)  # noqa: E731
     dres = None if sum is None else new()
     # without a scale dx and dresidual are the same gradient: one tensor
     dx = new() if sum is None or res_scale is not None else None
     g = dict(dx=dres if dx is None else dx, dw=torch.empty_like(w), dz=None if z is None else new(), dresidual=dres,
              dres_scale=None if res_scale is None else torch.empty_like(res_scale))
-    shape = norm_shape(x4, w, eps)
+    shape = norm_shape(x, w, eps)
     if ws is None:
         ws = _ws(dn_norm_workspace_size(shape), x.device, "dn_norm_bwd")
-    v = lambda t, name: _rows(t, name, x)  # noqa: E731
-    dn_norm_bwd(shape, x4, w, v(z, "z"), res_scale, v(sum, "sum"), v(dy, "dy"), v(dsum, "dsum"), v(dx, "dx"), g["dw"],
-                v(g["dz"], "dz"), v(dres, "dresidual"), g["dres_scale"], ws)
+    dn_norm_bwd(shape, x, w, z, res_scale, sum, dy, dsum, dx, g["dw"], g["dz"], dres, g["dres_scale"], ws)
     return g
