@@ -153,7 +153,7 @@ size_t scan_offsets(const dn_scan_shape *s)
 
 size_t scan_saved(const dn_scan_shape *s)
 {
-    const size_t n = (size_t)s->B * ((s->T + kScanKeep - 1) / kScanKeep) * s->D * scan_padded(s->N) * sizeof(float);
+    const size_t n = (size_t)s->B * ((s->T + keep_of(scan_padded(s->N)) - 1) / keep_of(scan_padded(s->N))) * s->D * scan_padded(s->N) * sizeof(float);
     return n ? n : 256;
 }
 

@@ -24,7 +24,9 @@
 namespace gdn {
 namespace lay {
 
-constexpr int kScanKeep = 16;      // tokens between kept states
+// Tokens between the states that the forward pass keeps for the backward, by the padded
+// number of states: what the backward's shared memory holds of one tile's states.
+__host__ __device__ constexpr int keep_of(int Np) { return Np <= 32 ? 8 : 16; }
 
 struct ScanDims {
     int B, T, D, N, G, Dg;         // Dg = D / G channels a group
@@ -40,7 +42,7 @@ template <class T>
 struct ScanIo {
     View<const T> x, dt, b, c, z;
     View<T> y;
-    float *hT, *keep;              // keep: state entering every 16th token, [B][ceil(T/16)][D][Np], or null
+    float *hT, *keep;              // keep: state entering every keep_of(Np)-th token, [B][ceil(T / that)][D][Np], or null
     float *segP, *segH;            // per segment: product of the decays, end state from zero [B][K][D][Np]
 };
 
@@ -111,7 +113,7 @@ __device__ __forceinline__ float lane_sum(float (&v)[L], int lane)
 }
 
 // TT: tokens of a tile; NT: threads of a block
-template <int L_, int S_, int CT_, int TT_ = kScanKeep, int NT_ = 256>
+template <int L_, int S_, int CT_, int TT_ = 16, int NT_ = 256>
 struct ScanCfg {
     static constexpr int L = L_, S = S_, CT = CT_, TT = TT_, NT = NT_, M = 32 / L_, Np = L_ * S_;
     static constexpr int CH = NT / L_ * CT_;                             // channels of a block
@@ -149,6 +151,32 @@ __device__ __forceinline__ void tile_edges(const ScanDims &g, int b, int t0, int
         masks[0] = ms;
         masks[1] = me;
     }
+}
+
+// Time segments of a pass whose blocks are `tiles` a segment: the K that leaves the busiest SM
+// the least to do.  An SM runs R blocks at once at full speed and n < R of them at
+// 0.6 + 0.4 n / R of it; the first pass (all but one segment, R1 at once) does w1 of the main
+// pass's work a token; a block's start costs as much as 8 tokens.  K = 1 has no first pass.
+// At 4 x 8192 tokens of 2048 channels (64 tiles) this says 6931, 5909, 6024, 5683, 5609, 5837 (in
+// tokens) for K = 4, 7, 9, 14, 19, 28, and the forward pass took 699, 598, 610, 579, 569, 583 us.
+inline int plan_segments(long long tiles, int T, int R, int R1, double w1)
+{
+    const int sms = sm_count();
+    auto busiest = [&](long long blocks, int r) {   // rounds of the SM with the most blocks, in blocks at full speed
+        const long long m = (blocks + sms - 1) / sms, full = m / r * r, n = m - full;
+        return (double)full + (n ? (double)n / (0.6 + 0.4 * (double)n / r) : 0.0);
+    };
+    int best = 1;
+    double least = 0.0;
+    for (int k = 1; k <= 64 && (k == 1 || T / k >= 64); ++k) {
+        const int len = ((T + k - 1) / k + 15) / 16 * 16, used = (T + len - 1) / len;
+        const double cost = (len + 8) * (busiest(tiles * used, R) + (used > 1 ? w1 * busiest(tiles * (used - 1), R1) : 0.0));
+        if (k == 1 || cost < 0.98 * least) {
+            best = k;
+            least = cost;
+        }
+    }
+    return best;
 }
 
 // Composes the K segments of every (row, channel, state) in place: segH[k] becomes what
@@ -297,9 +325,9 @@ cudaError_t fwd_layout(int N, F f)
 template <class F>
 cudaError_t bwd_layout(int N, F f)
 {
-    if (N <= 8) return f(ScanCfg<4, 2, 2, 16, 128>{});
-    if (N <= 16) return f(ScanCfg<4, 4, 2, 16, 128>{});
-    if (N <= 32) return f(ScanCfg<8, 4, 2, 16, 128>{});
+    if (N <= 8) return f(ScanCfg<4, 2, 2, 8, 128>{});
+    if (N <= 16) return f(ScanCfg<4, 4, 2, 8, 128>{});
+    if (N <= 32) return f(ScanCfg<8, 4, 2, 8, 128>{});
     if (N <= 64) return f(ScanCfg<16, 4, 1, 16, 128>{});
     return f(ScanCfg<16, 8, 1, 16, 128>{});
 }

@@ -7,11 +7,10 @@
 //     dx = delta p + D g,  ddt = (sum_n e A + x p) softplus'(dt),  dz = dy o silu'(z)
 //     dA += delta e,  dB_t = sum_c delta x dh_t,  dC_t = sum_c g h_t,  dh0 = a_0 dh_0
 //
-// A block walks its channels' tokens backwards in tiles of 16.  The forward pass kept the
-// state entering every tile; from it the tile is run forward once for the states that
-// enter its groups of L tokens (shared memory), then, from the last group back, each
-// group once more with its states and decays left in registers, and back.  That is two
-// exponentials a (token, channel, state) less those of the last group's first run.
+// A block walks its channels' tokens backwards in tiles of 8 (16 from 33 states on).  The
+// forward pass kept the state entering every tile; from it the tile is run forward once, the
+// state behind every token into shared memory, and then back.  a_t is an exponential in both:
+// registers for the tile's would cost the occupancy that hides the latencies here.
 //
 // Sums.  Over a channel's states (o, p, sum e A): the lanes' butterfly.  Over channels
 // (dB, dC): a butterfly over the warp's channels that leaves a share of the 2 S values in
@@ -21,6 +20,8 @@
 //
 // Few rows: segments of the time axis, the entering dh composed from a first pass (SUM)
 // over all but the first segment, as in the forward pass.
+#include <type_traits>
+
 #include "scan.cuh"
 
 namespace gdn {
@@ -28,7 +29,6 @@ namespace lay {
 
 namespace {
 
-constexpr int kTile = kScanKeep;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <class T>
@@ -43,29 +43,26 @@ struct BwdIo {
     float *part_bc;         // [B][channel tiles][T][2 Np]
 };
 
-template <class T, class Cfg, int VB>
+template <class Cfg>
 struct BwdShared {
-    static constexpr int VEC = VB ? VB / sizeof(T) : 1, NV = Cfg::EPT / VEC, WARPS = Cfg::NT / 32;
-    // the next tile's x, dt, dy, z as copied; a thread reads back only what it copied itself
-    __align__(16) char raw[4][NV][Cfg::NT][VB ? VB : 1];
-    float2 dd[kTile][Cfg::CH];                        // delta, delta x
-    float g[kTile][Cfg::RS];
-    float x[kTile][Cfg::RS], s[kTile][Cfg::RS], gz[kTile][Cfg::RS];   // x, softplus', dy silu'(z); then dx, ddt, dz
-    __align__(16) float b[kTile][Cfg::Np];
-    __align__(16) float c[kTile][Cfg::Np];
-    __align__(16) float st[(kTile / Cfg::L) * Cfg::CT * Cfg::NT * Cfg::S];   // states entering the groups
-    float bc[kTile][WARPS][2 * Cfg::Np];
+    static constexpr int WARPS = Cfg::NT / 32;
+    float2 dd[Cfg::TT][Cfg::CH];                       // delta, delta x
+    float g[Cfg::TT][Cfg::RS];
+    float x[Cfg::TT][Cfg::RS], s[Cfg::TT][Cfg::RS], gz[Cfg::TT][Cfg::RS];   // x, softplus', dy silu'(z); then dx, ddt, dz
+    __align__(16) float b[Cfg::TT][Cfg::Np];
+    __align__(16) float c[Cfg::TT][Cfg::Np];
+    __align__(16) float st[Cfg::TT][Cfg::CT][Cfg::NT][Cfg::S];              // the state before every token
+    float bc[Cfg::TT][WARPS][2 * Cfg::Np];
     int seq[32];
     uint32_t edge[2];
 };
 
-// VB: bytes of an asynchronous copy; 0: element loads where they are used.
-template <class T, class Cfg, int VB, bool SUM>
-__global__ void __launch_bounds__(Cfg::NT, 3) k_scan_bwd(ScanDims g, BwdIo<T> io)
+template <class T, class Cfg, int VEC, bool SUM>
+__global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, BwdIo<T> io)
 {
-    constexpr int L = Cfg::L, S = Cfg::S, CT = Cfg::CT, M = Cfg::M, Np = Cfg::Np, CH = Cfg::CH, P = S / 2;
-    using Shared = BwdShared<T, Cfg, VB>;
-    constexpr int VEC = Shared::VEC, NV = Shared::NV, NBC = Cfg::NBC;
+    constexpr int L = Cfg::L, S = Cfg::S, CT = Cfg::CT, M = Cfg::M, Np = Cfg::Np, CH = Cfg::CH, P = S / 2, TT = Cfg::TT;
+    constexpr int NV = Cfg::EPT / VEC, NBC = Cfg::NBC, KEEP = keep_of(Np);
+    using Shared = BwdShared<Cfg>;
     extern __shared__ __align__(16) char smem_raw[];
     Shared &sm = *reinterpret_cast<Shared *>(smem_raw);
 
@@ -103,67 +100,69 @@ __global__ void __launch_bounds__(Cfg::NT, 3) k_scan_bwd(ScanDims g, BwdIo<T> io
         }
     }
 
+    // this thread's vectors of a tile: tokens vt, vt + ES, ..., channels vc .. vc + VEC - 1
     constexpr int RV = CH / VEC, ES = Cfg::NT / RV;
     const int vt = tid / RV, vc = tid % RV * VEC;
     const bool col = cg0 + vc < g.Dg;
     const int cv = c0 + (col ? vc : 0);
+    Vec<T, VEC> xn[NV], dn[NV], zn[NV], gn[NV];
     T br[NBC], cr[NBC];
-    auto fetch = [&](int t0) {
-        if constexpr (VB > 0) {
+    float2 kn[CT][P];   // the state that enters the tile
+    float bias[VEC];
 #pragma unroll
-            for (int e = 0; e < NV; ++e) {
-                const int t = t0 + vt + e * ES;
-                const bool in = col && t >= ts && t < te;
-                const int ta = in ? t : ts;   // an address inside, whether it is read or not
-                if (!SUM) copy_async<VB>(sm.raw[0][e][tid], io.x.at(b, 0, ta) + cv, in);
-                copy_async<VB>(sm.raw[1][e][tid], io.dt.at(b, 0, ta) + cv, in);
-                copy_async<VB>(sm.raw[2][e][tid], io.dy.at(b, 0, ta) + cv, in);
-                if (gated) copy_async<VB>(sm.raw[3][e][tid], io.z.at(b, 0, ta) + cv, in);
+    for (int i = 0; i < VEC; ++i) bias[i] = col && g.bias ? g.bias[cv + i] : 0.f;
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int e = 0; e < NV; ++e) {
+            const int t = t0 + vt + e * ES;
+            xn[e].zero();
+            dn[e].zero();
+            zn[e].zero();
+            gn[e].zero();
+            if (col && t >= ts && t < te) {
+                if (!SUM) xn[e].load(io.x.at(b, 0, t) + cv);
+                dn[e].load(io.dt.at(b, 0, t) + cv);
+                gn[e].load(io.dy.at(b, 0, t) + cv);
+                if (gated) zn[e].load(io.z.at(b, 0, t) + cv);
             }
-            copy_commit();
         }
 #pragma unroll
         for (int e = 0; e < NBC; ++e) {
             const int i = tid + e * Cfg::NT, t = t0 + i / Np, n = i % Np;
             st_out(&br[e], 0.f);
             st_out(&cr[e], 0.f);
-            if (i < kTile * Np && t >= ts && t < te && n < g.N) {
+            if (i < TT * Np && t >= ts && t < te && n < g.N) {
                 if (!SUM) br[e] = io.b.at(b, grp, t)[n];
                 cr[e] = io.c.at(b, grp, t)[n];
             }
         }
-    };
-    // vector e of x (0), dt (1), dy (2) or z (3) of the tile at t0
-    auto element = [&](float (&f)[VEC], const View<const T> &v, int which, int e, int t0) {
-        Vec<T, VEC> q;
-        if constexpr (VB > 0) {
-            q.load(reinterpret_cast<const T *>(sm.raw[which][e][tid]));
-        } else {
-            q.zero();
-            const int t = t0 + vt + e * ES;
-            if (col && t < te) q.load(v.at(b, 0, t) + cv);
+        if constexpr (!SUM) {
+#pragma unroll
+            for (int e = 0; e < CT; ++e) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) kn[e][i] = two(0.f);
+                if (live[e] && t0 >= ts)
+                    load_pairs<S>(kn[e], io.keep + (((size_t)b * ((g.T + KEEP - 1) / KEEP) + t0 / KEEP) * g.D + c + e) * Np + n0);
+            }
         }
-        q.get(f);
     };
-    const int last = ts + (te - ts - 1) / kTile * kTile;
+    const int last = ts + (te - ts - 1) / TT * TT;
     fetch(last);
 
-    for (int t0 = last; t0 >= ts; t0 -= kTile) {
+    for (int t0 = last; t0 >= ts; t0 -= TT) {
         // 1. the tile into shared memory
-        if constexpr (VB > 0) copy_wait();
 #pragma unroll
         for (int e = 0; e < NV; ++e) {
             float x[VEC], d[VEC], z[VEC], gy[VEC], sp[VEC], gz[VEC];
-            if constexpr (!SUM) element(x, io.x, 0, e, t0);
-            element(d, io.dt, 1, e, t0);
-            element(gy, io.dy, 2, e, t0);
-            if (gated) element(z, io.z, 3, e, t0);
+            xn[e].get(x);
+            dn[e].get(d);
+            zn[e].get(z);
+            gn[e].get(gy);
             const int t = vt + e * ES;
             const bool in = col && t0 + t < te;
 #pragma unroll
             for (int i = 0; i < VEC; i += 2) {
-                float2 v = pair_at(d, i), der = two(1.f), w = two(0.f);
-                if (g.bias) v = add2(v, make_float2(g.bias[cv + i], g.bias[cv + (VEC > 1 ? i + 1 : i)]));
+                float2 v = add2(pair_at(d, i), pair_at(bias, i)), der = two(1.f), w = two(0.f);
                 if (g.softplus) softplus(v, v, der);
                 if constexpr (!SUM) w = mul2(v, pair_at(x, i));
                 if (!in) v = w = two(0.f);
@@ -188,17 +187,24 @@ __global__ void __launch_bounds__(Cfg::NT, 3) k_scan_bwd(ScanDims g, BwdIo<T> io
 #pragma unroll
         for (int e = 0; e < NBC; ++e) {
             const int i = tid + e * Cfg::NT;
-            if (i < kTile * Np) {
+            if (i < TT * Np) {
                 if (!SUM) sm.b[i / Np][i % Np] = ld_in(&br[e]);
                 sm.c[i / Np][i % Np] = ld_in(&cr[e]);
             }
         }
-        if (tid < 32) tile_edges(g, b, t0, min(kTile, te - t0), sm.seq, sm.edge);
+        if (tid < 32) tile_edges(g, b, t0, min(TT, te - t0), sm.seq, sm.edge);
         __syncthreads();
-        fetch(t0 - kTile);
+        float2 h[CT][P];   // forward: the state before the token at hand; back: the one behind it
+        if constexpr (!SUM) {
+#pragma unroll
+            for (int e = 0; e < CT; ++e)
+#pragma unroll
+                for (int i = 0; i < P; ++i) h[e][i] = kn[e][i];
+        }
+        fetch(t0 - TT);
         const uint32_t starts = sm.edge[0], ends = sm.edge[1];
-        auto steps = [&](int t, float (&dl)[CT], float (&dx)[CT]) { load_steps<CT>(dl, dx, &sm.dd[t][ch]); };
-        // gradients that arrive at a sequence's final state
+        // Sequence starts and ends: the states and gradients that come and go there.  Tiles without one,
+        // nearly all, run a copy of the loops without this.
         auto end_of = [&](int t) {
             if ((ends >> t & 1) && io.dhT) {
 #pragma unroll
@@ -210,16 +216,18 @@ __global__ void __launch_bounds__(Cfg::NT, 3) k_scan_bwd(ScanDims g, BwdIo<T> io
                 }
             }
         };
+        auto initial = [&](float2 (&v)[P], int t, int e) {
+            load_states<S>(v, g.h0 + ((size_t)sm.seq[t] * g.D + c + e) * g.N, n0, g.N, live[e] && g.h0);
+        };
 
         if constexpr (SUM) {
-#pragma unroll 4
-            for (int t = kTile - 1; t >= 0; --t) {
+            auto back = [&](int t, auto edges) {
                 float dl[CT], dx[CT], gg[CT];
-                steps(t, dl, dx);
+                load_steps<CT>(dl, dx, &sm.dd[t][ch]);
                 load_ct<CT>(gg, &sm.g[t][ch]);
                 float2 cc[P];
                 load_pairs<S>(cc, &sm.c[t][n0]);
-                end_of(t);
+                if constexpr (decltype(edges)::value) end_of(t);
 #pragma unroll
                 for (int e = 0; e < CT; ++e) {
                     total[e] += dl[e];
@@ -227,159 +235,164 @@ __global__ void __launch_bounds__(Cfg::NT, 3) k_scan_bwd(ScanDims g, BwdIo<T> io
                     for (int i = 0; i < P; ++i)
                         dh[e][i] = mul2(ex2_2(mul2(two(dl[e]), a2[e][i])), fma2(two(gg[e]), cc[i], dh[e][i]));
                 }
-                if (starts >> t & 1) {
-#pragma unroll
-                    for (int e = 0; e < CT; ++e) {
-                        prod[e] = two(0.f);
-                        total[e] = 0.f;
-#pragma unroll
-                        for (int i = 0; i < P; ++i) dh[e][i] = two(0.f);
-                    }
-                }
-            }
-            __syncthreads();
-        } else {
-            // 2. forward from the kept state: what enters each group of L tokens
-            float2 h[CT][P], tA[CT][P];
-#pragma unroll
-            for (int e = 0; e < CT; ++e) {
-#pragma unroll
-                for (int i = 0; i < P; ++i) h[e][i] = tA[e][i] = two(0.f);
-                if (live[e])
-                    load_pairs<S>(h[e], io.keep + (((size_t)b * ((g.T + kScanKeep - 1) / kScanKeep) + t0 / kScanKeep) * g.D + c + e) * Np + n0);
-            }
-            // one token on: from h to the state behind it; `a`, and `before` the state that entered
-            auto forward = [&](int t, float2 (&a)[CT][P], float2 (&before)[CT][P]) {
-                float dl[CT], dx[CT];
-                steps(t, dl, dx);
-                float2 bb[P];
-                load_pairs<S>(bb, &sm.b[t][n0]);
-#pragma unroll
-                for (int e = 0; e < CT; ++e) {
-                    if (starts >> t & 1)
-                        load_states<S>(h[e], g.h0 + ((size_t)sm.seq[t] * g.D + c + e) * g.N, n0, g.N, live[e] && g.h0);
-#pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        before[e][i] = h[e][i];
-                        a[e][i] = ex2_2(mul2(two(dl[e]), a2[e][i]));
-                        h[e][i] = fma2(a[e][i], h[e][i], mul2(two(dx[e]), bb[i]));
-                    }
-                }
-            };
-            auto group_state = [&](int gi, int e) { return &sm.st[((gi * CT + e) * Cfg::NT + tid) * S]; };
-#pragma unroll 1
-            for (int gi = 0; gi < kTile / L - 1; ++gi) {
-#pragma unroll
-                for (int e = 0; e < CT; ++e) store_pairs<S>(group_state(gi, e), h[e]);
-#pragma unroll
-                for (int j = 0; j < L; ++j) {
-                    float2 a[CT][P], before[CT][P];
-                    forward(gi * L + j, a, before);
-                }
-            }
-            // 3. back through the tile, a group at a time: its states again, now kept with the decays
-#pragma unroll 1
-            for (int gi = kTile / L - 1; gi >= 0; --gi) {
-                const int g0 = gi * L;
-                float2 a[L][CT][P], hist[L][CT][P];
-                if (gi < kTile / L - 1) {
-#pragma unroll
-                    for (int e = 0; e < CT; ++e) load_pairs<S>(h[e], group_state(gi, e));
-                }
-#pragma unroll
-                for (int j = 0; j < L; ++j) forward(g0 + j, a[j], hist[j]);
-                float po[CT][L], pp[CT][L], pe[CT][L];
-#pragma unroll
-                for (int j = L - 1; j >= 0; --j) {
-                    const int t = g0 + j;
-                    float dl[CT], dx[CT], gg[CT];
-                    steps(t, dl, dx);
-                    load_ct<CT>(gg, &sm.g[t][ch]);
-                    float2 bb[P], cc[P], vb[P], vc2[P];
-                    load_pairs<S>(bb, &sm.b[t][n0]);
-                    load_pairs<S>(cc, &sm.c[t][n0]);
-                    end_of(t);
-#pragma unroll
-                    for (int e = 0; e < CT; ++e) {
-                        float2 o, p, e2;
-#pragma unroll
-                        for (int i = 0; i < P; ++i) {
-                            const float2 ah = mul2(a[j][e][i], hist[j][e][i]), hn = fma2(two(dx[e]), bb[i], ah);
-                            dh[e][i] = fma2(two(gg[e]), cc[i], dh[e][i]);
-                            const float2 q = mul2(dh[e][i], ah);
-                            o = i == 0 ? mul2(cc[i], hn) : fma2(cc[i], hn, o);
-                            p = i == 0 ? mul2(dh[e][i], bb[i]) : fma2(dh[e][i], bb[i], p);
-                            e2 = i == 0 ? mul2(q, a2[e][i]) : fma2(q, a2[e][i], e2);
-                            tA[e][i] = fma2(two(dl[e]), q, tA[e][i]);
-                            vb[i] = e == 0 ? mul2(two(dx[e]), dh[e][i]) : fma2(two(dx[e]), dh[e][i], vb[i]);
-                            vc2[i] = e == 0 ? mul2(two(gg[e]), hn) : fma2(two(gg[e]), hn, vc2[i]);
-                            dh[e][i] = mul2(a[j][e][i], dh[e][i]);
-                        }
-                        po[e][j] = o.x + o.y;
-                        pp[e][j] = p.x + p.y;
-                        pe[e][j] = e2.x + e2.y;
-                    }
+                if constexpr (decltype(edges)::value) {
                     if (starts >> t & 1) {
 #pragma unroll
                         for (int e = 0; e < CT; ++e) {
-                            if (io.dh0) store_states<S>(io.dh0 + ((size_t)sm.seq[t] * g.D + c + e) * g.N, dh[e], n0, g.N, live[e]);
+                            prod[e] = two(0.f);
+                            total[e] = 0.f;
 #pragma unroll
                             for (int i = 0; i < P; ++i) dh[e][i] = two(0.f);
                         }
                     }
-                    // dB, dC over the warp's channels
-                    float v[2 * S];
+                }
+            };
+            if ((starts | ends) == 0) {
+#pragma unroll 4
+                for (int t = TT - 1; t >= 0; --t) back(t, std::false_type());
+            } else {
+#pragma unroll 1
+                for (int t = TT - 1; t >= 0; --t) back(t, std::true_type());
+            }
+            __syncthreads();
+        } else {
+            float2 tA[CT][P];
 #pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        v[2 * i] = vb[i].x;
-                        v[2 * i + 1] = vb[i].y;
-                        v[S + 2 * i] = vc2[i].x;
-                        v[S + 2 * i + 1] = vc2[i].y;
+            for (int e = 0; e < CT; ++e)
+#pragma unroll
+                for (int i = 0; i < P; ++i) tA[e][i] = two(0.f);
+            auto tile_back = [&](auto edges) {
+                // 2. the tile's states, forward from the kept one
+                auto forward = [&](int t) {
+                    float dl[CT], dx[CT];
+                    load_steps<CT>(dl, dx, &sm.dd[t][ch]);
+                    float2 bb[P];
+                    load_pairs<S>(bb, &sm.b[t][n0]);
+#pragma unroll
+                    for (int e = 0; e < CT; ++e) {
+                        store_pairs<S>(sm.st[t][e][tid], h[e]);
+                        if constexpr (decltype(edges)::value) {
+                            if (starts >> t & 1) initial(h[e], t, e);
+                        }
+#pragma unroll
+                        for (int i = 0; i < P; ++i) h[e][i] = fma2(ex2_2(mul2(two(dl[e]), a2[e][i])), h[e][i], mul2(two(dx[e]), bb[i]));
                     }
-                    constexpr int left = 2 * S > M ? 2 * S / M : 1;   // values a lane ends with
-                    int off = 0, cur = 2 * S;
+                };
+                if constexpr (decltype(edges)::value) {
+#pragma unroll 1
+                    for (int t = 0; t < TT; ++t) forward(t);
+                } else {
+#pragma unroll 4
+                    for (int t = 0; t < TT; ++t) forward(t);
+                }
+                // 3. back through the tile
+#pragma unroll 1
+                for (int g0 = TT - L; g0 >= 0; g0 -= L) {
+                    float po[CT][L], pp[CT][L], pe[CT][L];
 #pragma unroll
-                    for (int bit = M / 2; bit > 0; bit >>= 1) {
-                        const bool up = lane & bit;
-                        if (cur > 1) {
-                            cur >>= 1;
+                    for (int j = L - 1; j >= 0; --j) {
+                        const int t = g0 + j;
+                        float dl[CT], dx[CT], gg[CT];
+                        load_steps<CT>(dl, dx, &sm.dd[t][ch]);
+                        load_ct<CT>(gg, &sm.g[t][ch]);
+                        float2 bb[P], cc[P], vb[P], vc2[P], before[CT][P];
+                        load_pairs<S>(bb, &sm.b[t][n0]);
+                        load_pairs<S>(cc, &sm.c[t][n0]);
 #pragma unroll
-                            for (int i = 0; i < cur; ++i) {
-                                const float send = up ? v[i] : v[i + cur], mine = up ? v[i + cur] : v[i];
-                                v[i] = mine + __shfl_xor_sync(0xffffffffu, send, bit);
+                        for (int e = 0; e < CT; ++e) load_pairs<S>(before[e], sm.st[t][e][tid]);
+                        if constexpr (decltype(edges)::value) end_of(t);
+#pragma unroll
+                        for (int e = 0; e < CT; ++e) {
+                            float2 o, p, e2, hp[P];
+#pragma unroll
+                            for (int i = 0; i < P; ++i) hp[i] = before[e][i];
+                            if constexpr (decltype(edges)::value) {
+                                if (starts >> t & 1) initial(hp, t, e);
                             }
-                            off += up ? cur : 0;
-                        } else {
-                            v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+#pragma unroll
+                            for (int i = 0; i < P; ++i) {
+                                dh[e][i] = fma2(two(gg[e]), cc[i], dh[e][i]);
+                                const float2 da = mul2(ex2_2(mul2(two(dl[e]), a2[e][i])), dh[e][i]);   // what goes on to t - 1
+                                const float2 q = mul2(da, hp[i]);
+                                o = i == 0 ? mul2(cc[i], h[e][i]) : fma2(cc[i], h[e][i], o);
+                                p = i == 0 ? mul2(dh[e][i], bb[i]) : fma2(dh[e][i], bb[i], p);
+                                e2 = i == 0 ? mul2(q, a2[e][i]) : fma2(q, a2[e][i], e2);
+                                tA[e][i] = fma2(two(dl[e]), q, tA[e][i]);
+                                vb[i] = e == 0 ? mul2(two(dx[e]), dh[e][i]) : fma2(two(dx[e]), dh[e][i], vb[i]);
+                                vc2[i] = e == 0 ? mul2(two(gg[e]), h[e][i]) : fma2(two(gg[e]), h[e][i], vc2[i]);
+                                dh[e][i] = da;
+                                h[e][i] = before[e][i];
+                            }
+                            po[e][j] = o.x + o.y;
+                            pp[e][j] = p.x + p.y;
+                            pe[e][j] = e2.x + e2.y;
+                        }
+                        if constexpr (decltype(edges)::value) {
+                            if (starts >> t & 1) {
+#pragma unroll
+                                for (int e = 0; e < CT; ++e) {
+                                    if (io.dh0) store_states<S>(io.dh0 + ((size_t)sm.seq[t] * g.D + c + e) * g.N, dh[e], n0, g.N, live[e]);
+#pragma unroll
+                                    for (int i = 0; i < P; ++i) dh[e][i] = two(0.f);
+                                }
+                            }
+                        }
+                        // dB, dC over the warp's channels
+                        float v[2 * S];
+#pragma unroll
+                        for (int i = 0; i < P; ++i) {
+                            v[2 * i] = vb[i].x;
+                            v[2 * i + 1] = vb[i].y;
+                            v[S + 2 * i] = vc2[i].x;
+                            v[S + 2 * i + 1] = vc2[i].y;
+                        }
+                        constexpr int left = 2 * S > M ? 2 * S / M : 1;   // values a lane ends with
+                        int off = 0, cur = 2 * S;
+#pragma unroll
+                        for (int bit = M / 2; bit > 0; bit >>= 1) {
+                            const bool up = lane & bit;
+                            if (cur > 1) {
+                                cur >>= 1;
+#pragma unroll
+                                for (int i = 0; i < cur; ++i) {
+                                    const float send = up ? v[i] : v[i + cur], mine = up ? v[i + cur] : v[i];
+                                    v[i] = mine + __shfl_xor_sync(0xffffffffu, send, bit);
+                                }
+                                off += up ? cur : 0;
+                            } else {
+                                v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < left; ++i) {
+                            const int w = off + i;
+                            sm.bc[t][warp][(w >= S ? Np : 0) + n0 + (w & (S - 1))] = v[i];
                         }
                     }
+                    const int t = g0 + l;
+                    float dl[CT], dx[CT], x[CT], gg[CT], sp[CT], gz[CT];
+                    load_steps<CT>(dl, dx, &sm.dd[t][ch]);
+                    load_ct<CT>(x, &sm.x[t][ch]);
+                    load_ct<CT>(gg, &sm.g[t][ch]);
+                    load_ct<CT>(sp, &sm.s[t][ch]);
+                    if (gated) load_ct<CT>(gz, &sm.gz[t][ch]);
 #pragma unroll
-                    for (int i = 0; i < left; ++i) {
-                        const int w = off + i;
-                        sm.bc[t][warp][(w >= S ? Np : 0) + n0 + (w & (S - 1))] = v[i];
+                    for (int e = 0; e < CT; ++e) {
+                        const float o = lane_sum<L>(po[e], lane), p = lane_sum<L>(pp[e], lane), q = lane_sum<L>(pe[e], lane) * kLn2;
+                        const float ddt = fmaf(p, x[e], q) * sp[e];
+                        aD[e] = fmaf(gg[e], x[e], aD[e]);
+                        aBias[e] += ddt;
+                        if (gated) gz[e] *= fmaf(Dc[e], x[e], o);
+                        x[e] = fmaf(dl[e], p, Dc[e] * gg[e]);
+                        sp[e] = ddt;
                     }
+                    store_ct<CT>(&sm.x[t][ch], x);
+                    store_ct<CT>(&sm.s[t][ch], sp);
+                    if (gated) store_ct<CT>(&sm.gz[t][ch], gz);
                 }
-                const int t = g0 + l;
-                float dl[CT], dx[CT], x[CT], gg[CT], sp[CT], gz[CT];
-                steps(t, dl, dx);
-                load_ct<CT>(x, &sm.x[t][ch]);
-                load_ct<CT>(gg, &sm.g[t][ch]);
-                load_ct<CT>(sp, &sm.s[t][ch]);
-                if (gated) load_ct<CT>(gz, &sm.gz[t][ch]);
-#pragma unroll
-                for (int e = 0; e < CT; ++e) {
-                    const float o = lane_sum<L>(po[e], lane), p = lane_sum<L>(pp[e], lane), q = lane_sum<L>(pe[e], lane) * kLn2;
-                    const float ddt = fmaf(p, x[e], q) * sp[e];
-                    aD[e] = fmaf(gg[e], x[e], aD[e]);
-                    aBias[e] += ddt;
-                    if (gated) gz[e] *= fmaf(Dc[e], x[e], o);
-                    x[e] = fmaf(dl[e], p, Dc[e] * gg[e]);
-                    sp[e] = ddt;
-                }
-                store_ct<CT>(&sm.x[t][ch], x);
-                store_ct<CT>(&sm.s[t][ch], sp);
-                if (gated) store_ct<CT>(&sm.gz[t][ch], gz);
-            }
+            };
+            if ((starts | ends) == 0) tile_back(std::false_type());
+            else tile_back(std::true_type());
             // a tile's sum first, then the total: fewer roundings on the long axis
 #pragma unroll
             for (int e = 0; e < CT; ++e)
@@ -408,7 +421,7 @@ __global__ void __launch_bounds__(Cfg::NT, 3) k_scan_bwd(ScanDims g, BwdIo<T> io
                 }
             }
             float *pb = io.part_bc + (((size_t)b * tiles + tile) * g.T + t0) * (2 * Np);
-            const int n = min(kTile, te - t0) * 2 * Np;
+            const int n = min(TT, te - t0) * 2 * Np;
             for (int i = tid; i < n; i += Cfg::NT) {
                 float s = 0.f;
 #pragma unroll
@@ -487,13 +500,9 @@ Plan plan_of(const dn_scan_shape *s)
     bwd_layout(s->N, [&](auto cfg) { CH = decltype(cfg)::CH; return cudaSuccess; });
     const int Dg = s->D / s->G, Np = scan_padded(s->N);
     p.tiles = (Dg + CH - 1) / CH;
-    const long long blocks = (long long)s->B * s->G * p.tiles, want = 2 * sm_count();
-    long long k = blocks >= want / 2 ? 1 : want / blocks;
-    const long long most = (s->T + 127) / 128;
-    if (k > most) k = most;
-    if (k > 64) k = 64;
-    if (k < 1) k = 1;
-    p.seg = (int)((((long long)s->T + k - 1) / k + kTile - 1) / kTile * kTile);
+    // two blocks of the main pass fit an SM, four of the first, which does a fifth of the work
+    const int k = plan_segments((long long)s->B * s->G * p.tiles, s->T, 2, 4, 0.2);
+    p.seg = (int)((((long long)s->T + k - 1) / k + 15) / 16 * 16);   // whole tiles, whole spans between kept states
     p.K = p.seg > 0 ? (s->T + p.seg - 1) / p.seg : 1;
     size_t off = 0;
     auto take = [&](size_t floats) { const size_t o = off; off += align256(floats * sizeof(float)); return o; };
@@ -507,7 +516,7 @@ Plan plan_of(const dn_scan_shape *s)
     return p;
 }
 
-template <class T, class Cfg, int VB>
+template <class T, class Cfg, int VEC>
 cudaError_t launch(const ScanCall &c, cudaStream_t st)
 {
     const Plan p = plan_of(c.s);
@@ -527,17 +536,17 @@ cudaError_t launch(const ScanCall &c, cudaStream_t st)
     io.part_a = F(p.part_a); io.part_d = F(p.part_d); io.part_bc = F(p.part_bc);
     const long long per = (long long)g.B * g.G * g.tiles;
     if (per * g.K > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const size_t smem = sizeof(BwdShared<T, Cfg, VB>);
+    const size_t smem = sizeof(BwdShared<Cfg>);
     cudaError_t e;
     if (g.K > 1) {
-        e = cudaFuncSetAttribute(k_scan_bwd<T, Cfg, VB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(k_scan_bwd<T, Cfg, VEC, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        k_scan_bwd<T, Cfg, VB, true><<<(unsigned)(per * (g.K - 1)), Cfg::NT, smem, st>>>(g, io);
+        k_scan_bwd<T, Cfg, VEC, true><<<(unsigned)(per * (g.K - 1)), Cfg::NT, smem, st>>>(g, io);
         scan_carry<false>(g, io.segP, io.segH, Cfg::Np, st);
     }
-    e = cudaFuncSetAttribute(k_scan_bwd<T, Cfg, VB, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(k_scan_bwd<T, Cfg, VEC, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    k_scan_bwd<T, Cfg, VB, false><<<(unsigned)(per * g.K), Cfg::NT, smem, st>>>(g, io);
+    k_scan_bwd<T, Cfg, VEC, false><<<(unsigned)(per * g.K), Cfg::NT, smem, st>>>(g, io);
     const long long n = (long long)g.B * g.G * g.T * 2 * Cfg::Np;
     if ((n + 255) / 256 > 0x7fffffffLL) return cudaErrorInvalidValue;
     k_scan_bc<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(io.part_bc, view_of<T>(&gr->db), view_of<T>(&gr->dc), g.B, g.T, g.N,
@@ -563,14 +572,14 @@ cudaError_t bwd_t(const ScanCall &c, cudaStream_t st)
     if (s->T > 0) {
         const cudaError_t e = bwd_layout(s->N, [&](auto cfg) {
             using Cfg = decltype(cfg);
-            constexpr int VB = Cfg::template bytes<T>();
-            if constexpr (VB > 0) {
+            constexpr int VEC = Cfg::VEC;
+            if constexpr (VEC > 1) {
                 const dn_view *all[] = {&io->x, &io->dt, &io->z, &gr->dy, &gr->dx, &gr->ddt, &gr->dz};
-                bool v = (s->D / s->G) % (VB / sizeof(T)) == 0;
-                for (const dn_view *q : all) v = v && can_vector(q, sizeof(T), VB);
-                if (v) return launch<T, Cfg, VB>(c, st);
+                bool v = (s->D / s->G) % VEC == 0;
+                for (const dn_view *q : all) v = v && can_vector(q, sizeof(T), VEC * sizeof(T));
+                if (v) return launch<T, Cfg, VEC>(c, st);
             }
-            return launch<T, Cfg, 0>(c, st);
+            return launch<T, Cfg, 1>(c, st);
         });
         if (e != cudaSuccess) return e;
     }

@@ -15,6 +15,8 @@
 // but the last segment from a zero state and keeps its end state and its decay product;
 // the second pass composes what lies before its segment and runs it.  That costs the
 // recurrence twice, so it is done only while the blocks do not fill the SMs.
+#include <type_traits>
+
 #include "scan.cuh"
 
 namespace gdn {
@@ -174,61 +176,64 @@ __global__ void __launch_bounds__(Cfg::NT) k_scan_fwd(ScanDims g, ScanIo<T> io)
 
         // 2. the recurrence
         const uint32_t starts = edge[0], ends = edge[1];
-        if constexpr (!SUM) {
-            if (io.keep && t0 % kScanKeep == 0) {
-#pragma unroll
-                for (int e = 0; e < CT; ++e)
-                    if (live[e])
-                        store_pairs<S>(io.keep + (((size_t)b * ((g.T + kScanKeep - 1) / kScanKeep) + t0 / kScanKeep) * g.D + c + e) * Np + n0, h[e]);
-            }
-        }
+        // Tiles without a sequence start or end, nearly all, run a copy of the loop without what happens there.
+        auto run = [&](auto edges) {
+            constexpr bool EDGES = decltype(edges)::value;
 #pragma unroll 1
-        for (int g0 = 0; g0 < TT; g0 += L) {
-            const uint32_t in_group = ((starts | ends) >> g0) & (uint32_t)((1ull << L) - 1);
-            float yp[CT][L];
-            auto token = [&](int j, bool edges) {
-                const int t = g0 + j;
-                float dl[CT], dx[CT];
-                load_steps<CT>(dl, dx, &dd[t][ch]);
-                float2 bb[P], cc[P];
-                load_pairs<S>(bb, &sb[t][n0]);
-                if constexpr (!SUM) load_pairs<S>(cc, &sc[t][n0]);
+            for (int g0 = 0; g0 < TT; g0 += L) {
+                if constexpr (!SUM) {
+                    constexpr int KEEP = keep_of(Cfg::Np);
+                    if (io.keep && g0 % KEEP == 0 && t0 + g0 < te) {
 #pragma unroll
-                for (int e = 0; e < CT; ++e) {
-                    if (edges && (starts >> t & 1)) {
-                        load_states<S>(h[e], g.h0 + ((size_t)seq[t] * g.D + c + e) * g.N, n0, g.N, live[e] && g.h0);
-                        prod[e] = two(0.f);
-                        total[e] = 0.f;
-                    }
-                    if constexpr (SUM) total[e] += dl[e];
-                    float2 yy = two(0.f);
-#pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        const float2 a = ex2_2(mul2(two(dl[e]), a2[e][i]));
-                        h[e][i] = fma2(a, h[e][i], mul2(two(dx[e]), bb[i]));
-                        if constexpr (!SUM) yy = i == 0 ? mul2(cc[i], h[e][i]) : fma2(cc[i], h[e][i], yy);
-                    }
-                    yp[e][j] = yy.x + yy.y;
-                    if constexpr (!SUM) {
-                        if (edges && (ends >> t & 1) && io.hT)
-                            store_states<S>(io.hT + ((size_t)seq[t] * g.D + c + e) * g.N, h[e], n0, g.N, live[e]);
+                        for (int e = 0; e < CT; ++e)
+                            if (live[e])
+                                store_pairs<S>(io.keep + (((size_t)b * ((g.T + KEEP - 1) / KEEP) + (t0 + g0) / KEEP) * g.D + c + e) * Np + n0, h[e]);
                     }
                 }
-            };
-            if (in_group == 0) {
+                float yp[CT][L];
 #pragma unroll
-                for (int j = 0; j < L; ++j) token(j, false);
-            } else {
+                for (int j = 0; j < L; ++j) {
+                    const int t = g0 + j;
+                    float dl[CT], dx[CT];
+                    load_steps<CT>(dl, dx, &dd[t][ch]);
+                    float2 bb[P];
+                    [[maybe_unused]] float2 cc[P];
+                    load_pairs<S>(bb, &sb[t][n0]);
+                    if constexpr (!SUM) load_pairs<S>(cc, &sc[t][n0]);
 #pragma unroll
-                for (int j = 0; j < L; ++j) token(j, true);
+                    for (int e = 0; e < CT; ++e) {
+                        if constexpr (EDGES) {
+                            if (starts >> t & 1) {
+                                load_states<S>(h[e], g.h0 + ((size_t)seq[t] * g.D + c + e) * g.N, n0, g.N, live[e] && g.h0);
+                                prod[e] = two(0.f);
+                                total[e] = 0.f;
+                            }
+                        }
+                        if constexpr (SUM) total[e] += dl[e];
+                        float2 yy = two(0.f);
+#pragma unroll
+                        for (int i = 0; i < P; ++i) {
+                            const float2 a = ex2_2(mul2(two(dl[e]), a2[e][i]));
+                            h[e][i] = fma2(a, h[e][i], mul2(two(dx[e]), bb[i]));
+                            if constexpr (!SUM) yy = i == 0 ? mul2(cc[i], h[e][i]) : fma2(cc[i], h[e][i], yy);
+                        }
+                        yp[e][j] = yy.x + yy.y;
+                        if constexpr (!SUM && EDGES) {
+                            if ((ends >> t & 1) && io.hT)
+                                store_states<S>(io.hT + ((size_t)seq[t] * g.D + c + e) * g.N, h[e], n0, g.N, live[e]);
+                        }
+                    }
+                }
+                if constexpr (!SUM) {
+                    float y[CT];
+#pragma unroll
+                    for (int e = 0; e < CT; ++e) y[e] = lane_sum<L>(yp[e], lane);
+                    store_ct<CT>(&sy[g0 + l][ch], y);
+                }
             }
-            if constexpr (!SUM) {
-                float y[CT];
-#pragma unroll
-                for (int e = 0; e < CT; ++e) y[e] = lane_sum<L>(yp[e], lane);
-                store_ct<CT>(&sy[g0 + l][ch], y);
-            }
-        }
+        };
+        if ((starts | ends) == 0) run(std::false_type());
+        else run(std::true_type());
         __syncthreads();
 
         // 3. the results
@@ -283,77 +288,117 @@ __global__ void k_scan_empty(const float *h0, float *hT, const int32_t *cu, int 
     if (i < per) hT[s * per + i] = h0 ? h0[s * per + i] : 0.f;
 }
 
-// One token a sequence: lanes of a channel take V states at a time (16 bytes where N and
-// the states' alignment allow), so that a warp moves whole rows of the states, which are
-// what this is bound by (HBM: states read and written once).
-template <class T, int V>
-__global__ void __launch_bounds__(256) k_scan_step(ScanDims g, ScanIo<T> io, int L)
+// One token a sequence.  Lanes of a channel take V states at a time (16 bytes where N and the
+// states' alignment allow), so that a warp moves whole rows of the states, which are what this is
+// bound by (HBM: states read and written once), and U sequences each, whose states are in flight
+// together and share A.
+template <class T, int V, int U>
+__global__ void __launch_bounds__(256) k_scan_step(ScanDims g, ScanIo<T> io, int L, bool wide)
 {
     const long long i = (blockIdx.x * 256ll + threadIdx.x) / L;
     const int l = threadIdx.x & (L - 1);
-    const bool live = i < (long long)g.B * g.D;   // the whole warp takes part in the sum
-    const long long j = live ? i : 0;
-    const int b = (int)(j / g.D), c = (int)(j - (long long)b * g.D), grp = c / g.Dg;
-    const float x = ld_in(io.x.at(b, 0, 0) + c);
-    float d = ld_in(io.dt.at(b, 0, 0) + c) + (g.bias ? g.bias[c] : 0.f);
-    if (g.softplus) {
-        float2 v, der;
-        softplus(two(d), v, der);
-        d = v.x;
+    const long long all = (long long)((g.B + U - 1) / U) * g.D;
+    const bool any = i < all;   // the whole warp takes part in the sums
+    const long long j = any ? i : 0;
+    const int b0 = (int)(j / g.D) * U, c = (int)(j % g.D), grp = c / g.Dg;
+    bool live[U];
+    int b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        live[u] = any && b0 + u < g.B;
+        b[u] = live[u] ? b0 + u : 0;
     }
-    const float dx = d * x;
-    const T *bp = io.b.at(b, grp, 0), *cp = io.c.at(b, grp, 0);
-    const float *hi = g.h0 ? g.h0 + j * g.N : nullptr;
-    float *ho = io.hT ? io.hT + j * g.N : nullptr;
-    float y = 0.f;
-    if (live) {
-        for (int n = l * V; n < g.N; n += L * V) {
-            Vec<float, V> hv, av;
-            float h[V], a[V];
-            hv.zero();
-            if (hi) hv.load(hi + n);
-            av.load(g.A + (size_t)c * g.N + n);
-            hv.get(h);
-            av.get(a);
+    // the states' loads go out first: the step's arithmetic then runs under their latency
+    Vec<float, V> hv[U], av;
+    Vec<T, V> bv[U], cv[U];
+    auto load = [&](int n) {
+        av.load(g.A + (size_t)c * g.N + n);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            hv[u].zero();
+            if (g.h0 && live[u]) hv[u].load(g.h0 + ((size_t)b[u] * g.D + c) * g.N + n);
+            const T *pb = io.b.at(b[u], grp, 0) + n, *pc = io.c.at(b[u], grp, 0) + n;
+            if (wide) {
+                bv[u].load(pb);
+                cv[u].load(pc);
+            } else {
+                T eb[V], ec[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    eb[e] = pb[e];
+                    ec[e] = pc[e];
+                }
+                memcpy(&bv[u].raw, eb, sizeof(eb));
+                memcpy(&cv[u].raw, ec, sizeof(ec));
+            }
+        }
+    };
+    int n = l * V;
+    if (n < g.N) load(n);
+    const float skip = g.Dskip ? g.Dskip[c] : 0.f, bias = g.bias ? g.bias[c] : 0.f;
+    float x[U], d[U], z[U], y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        x[u] = ld_in(io.x.at(b[u], 0, 0) + c);
+        d[u] = ld_in(io.dt.at(b[u], 0, 0) + c) + bias;
+        z[u] = io.z.p ? ld_in(io.z.at(b[u], 0, 0) + c) : 0.f;
+        y[u] = 0.f;
+    }
+    if (g.softplus) {
+#pragma unroll
+        for (int u = 0; u < U; u += 2) {
+            float2 v, der;
+            softplus(make_float2(d[u], d[U > 1 ? u + 1 : u]), v, der);
+            d[u] = v.x;
+            if (U > 1) d[U > 1 ? u + 1 : u] = v.y;
+        }
+    }
+    while (n < g.N) {
+        float a[V];
+        av.get(a);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float h[V], bf[V], cf[V];
+            hv[u].get(h);
+            bv[u].get(bf);
+            cv[u].get(cf);
+            const float dx = d[u] * x[u];
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                h[e] = fmaf(ex2(d * (a[e] * kLog2e)), h[e], dx * ld_in(bp + n + e));
-                y = fmaf(ld_in(cp + n + e), h[e], y);
+                h[e] = fmaf(ex2(d[u] * (a[e] * kLog2e)), h[e], dx * bf[e]);
+                y[u] = fmaf(cf[e], h[e], y[u]);
             }
-            if (ho) {
-                hv.set(h);
-                hv.store(ho + n);
+            if (io.hT && live[u]) {
+                hv[u].set(h);
+                hv[u].store(io.hT + ((size_t)b[u] * g.D + c) * g.N + n);
             }
         }
+        n += L * V;
+        if (n < g.N) load(n);
     }
-    for (int o = L >> 1; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (live && l == 0) {
-        y = fmaf(g.Dskip ? g.Dskip[c] : 0.f, x, y);
-        if (io.z.p) {
-            const float z = ld_in(io.z.at(b, 0, 0) + c);
-            y *= z * sigmoid(z);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        for (int o = L >> 1; o > 0; o >>= 1) y[u] += __shfl_xor_sync(0xffffffffu, y[u], o);
+    // the results, a sequence a lane
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (live[u] && l == u % L) {
+            float o = fmaf(skip, x[u], y[u]);
+            if (io.z.p) o *= z[u] * sigmoid(z[u]);
+            st_out(io.y.at(b0 + u, 0, 0) + c, o);
         }
-        st_out(io.y.at(b, 0, 0) + c, y);
     }
 }
 
-// Time segments: while a row of blocks leaves SMs without work, at most one per 128 tokens.
-int segments(const dn_scan_shape *s, int blocks)
-{
-    const int want = 4 * sm_count();
-    int k = blocks >= want / 2 ? 1 : want / (blocks > 0 ? blocks : 1);
-    const int most = (s->T + 127) / 128;
-    if (k > most) k = most;
-    if (k > 64) k = 64;
-    return k < 1 ? 1 : k;
-}
-
-int scan_blocks(const dn_scan_shape *s, int CH)
+// Blocks of a segment.
+long long tiles_of(const dn_scan_shape *s, int CH)
 {
     const int Dg = s->D / s->G;
-    const long long n = (long long)s->B * s->G * ((Dg + CH - 1) / CH);
-    return n > 0x3fffffff ? 0x3fffffff : (int)n;
+    return (long long)s->B * s->G * ((Dg + CH - 1) / CH);
 }
+
+// two blocks of the main pass fit an SM, three of the first, which does 0.6 of the work
+int segments(const dn_scan_shape *s, int CH) { return plan_segments(tiles_of(s, CH), s->T, 2, 3, 0.6); }
 
 int channels_of(int N)
 {
@@ -379,8 +424,8 @@ cudaError_t launch(const ScanCall &c, cudaStream_t st)
 {
     ScanDims g = scan_dims(c);
     g.tiles = (g.Dg + Cfg::CH - 1) / Cfg::CH;
-    g.K = segments(c.s, scan_blocks(c.s, Cfg::CH));
-    g.seg = ((g.T + g.K - 1) / g.K + kScanKeep - 1) / kScanKeep * kScanKeep;
+    g.K = segments(c.s, Cfg::CH);
+    g.seg = ((g.T + g.K - 1) / g.K + 15) / 16 * 16;   // whole tiles, whole spans between kept states
     g.K = (g.T + g.seg - 1) / g.seg;
     ScanIo<T> io = io_of<T>(c);
     const long long per = (long long)g.B * g.G * g.tiles;
@@ -432,10 +477,18 @@ cudaError_t step_t(const ScanCall &c, cudaStream_t st)
     const int V = ok(4) ? 4 : 1;
     int L = 1;
     while (L < 32 && L * V < g.N) L <<= 1;
-    const long long blocks = ((long long)g.B * g.D * L + 255) / 256;
+    // two sequences a lane once that leaves the SMs four blocks each (256 sequences, 2048 channels, 16
+    // states: 33 us with one, 23 us with two and with four)
+    const int U = (long long)g.B * g.D * L / 2 / 256 >= 4ll * sm_count() ? 2 : 1;
+    const long long blocks = ((long long)((g.B + U - 1) / U) * g.D * L + 255) / 256;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    if (V == 4) k_scan_step<T, 4><<<(unsigned)blocks, 256, 0, st>>>(g, io, L);
-    else k_scan_step<T, 1><<<(unsigned)blocks, 256, 0, st>>>(g, io, L);
+    const bool wide = can_vector(&c.io->b, sizeof(T), V * sizeof(T)) && can_vector(&c.io->c, sizeof(T), V * sizeof(T));
+    auto go = [&](auto v, auto u) { k_scan_step<T, decltype(v)::value, decltype(u)::value><<<(unsigned)blocks, 256, 0, st>>>(g, io, L, wide); };
+    using one = std::integral_constant<int, 1>;
+    using two_ = std::integral_constant<int, 2>;
+    using four = std::integral_constant<int, 4>;
+    if (V == 4) U == 2 ? go(four(), two_()) : go(four(), one());
+    else U == 2 ? go(one(), two_()) : go(one(), one());
     return cudaPeekAtLastError();
 }
 
@@ -460,7 +513,7 @@ ScanDims scan_dims(const ScanCall &c)
 
 size_t scan_fwd_bytes(const dn_scan_shape *s)
 {
-    const int K = segments(s, scan_blocks(s, channels_of(s->N)));
+    const int K = segments(s, channels_of(s->N));
     return K > 1 ? align256(2 * sizeof(float) * (size_t)s->B * K * s->D * scan_padded(s->N)) : 0;
 }
 

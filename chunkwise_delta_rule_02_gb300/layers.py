@@ -381,7 +381,7 @@ def scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqle
     A [D,N], D, dt_bias [D] and the initial states h0 [N_seq,D,N] float32; 1 <= N <= 128.  The step is
     softplus(dt + dt_bias) (dt + dt_bias with dt_softplus=False); A <= 0 and steps >= 0 decay.
     Returns (y, hT), or (y, hT, saved) with save=True for scan_backward(saved=saved): the states
-    entering every 16th token, N / 4 bytes a token and channel."""
+    entering every 8th token (16th for N > 32), N / 2 (N / 4) bytes a token and channel."""
     n = _scan_args(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, 3)
     y = _result(out, "out", x)
     hT = torch.empty((n,) + tuple(A.shape), dtype=torch.float32, device=x.device) if want_state else None

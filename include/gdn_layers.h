@@ -114,8 +114,8 @@ typedef struct {
 
 size_t dn_scan_workspace_size(const dn_scan_shape *shape, int for_backward);
 
-/* Bytes of the buffer that dn_scan_fwd fills for dn_scan_bwd: the state entering every 16th
- * token, float32 (4 N bytes per 16 tokens and channel). */
+/* Bytes of the buffer that dn_scan_fwd fills for dn_scan_bwd: the state entering every 8th token
+ * (every 16th for N > 32), float32: N / 2 (N / 4) bytes a token and channel. */
 size_t dn_scan_saved_size(const dn_scan_shape *shape);
 
 /* saved may be NULL (nothing kept). */
