@@ -5,8 +5,9 @@
 //     h_t[n] = exp(delta A[n]) h_{t-1}[n] + delta x B_t[n],  o_t = sum_n C_t[n] h_t[n] + D x
 //
 // Lane layout.  L lanes share a channel, S states each (L S = Np >= N, padded states
-// have A = B = C = 0 and stay 0), and a lane holds CT neighbouring channels; 256 threads
-// hold CH = 256 CT / L channels.  Splitting a channel's states over lanes gives the
+// have A = B = C = 0 and stay 0), and a lane holds CT neighbouring channels; a block of NT
+// threads holds CH = NT CT / L channels (NT 128: 554 us at 4 x 8192 tokens of 2048 channels, 256
+// 582 us, 64 561 us, 32 629 us).  Splitting a channel's states over lanes gives the
 // threads that a few thousand channels need to fill the SMs; the price, sums over the L
 // lanes, is paid once for L tokens: the L partial sums of a lane are exchanged in a
 // halving butterfly (L - 1 shuffles) that leaves token l's sum in lane l, instead of
@@ -315,11 +316,11 @@ ScanDims scan_dims(const ScanCall &c);
 template <class F>
 cudaError_t fwd_layout(int N, F f)
 {
-    if (N <= 8) return f(ScanCfg<4, 2, 2>{});
-    if (N <= 16) return f(ScanCfg<4, 4, 2>{});
-    if (N <= 32) return f(ScanCfg<8, 4, 2>{});
-    if (N <= 64) return f(ScanCfg<16, 4, 1>{});
-    return f(ScanCfg<16, 8, 1>{});
+    if (N <= 8) return f(ScanCfg<4, 2, 2, 16, 128>{});
+    if (N <= 16) return f(ScanCfg<4, 4, 2, 16, 128>{});
+    if (N <= 32) return f(ScanCfg<8, 4, 2, 16, 128>{});
+    if (N <= 64) return f(ScanCfg<16, 4, 1, 16, 128>{});
+    return f(ScanCfg<16, 8, 1, 16, 128>{});
 }
 
 template <class F>

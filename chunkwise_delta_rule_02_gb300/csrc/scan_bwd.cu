@@ -57,6 +57,15 @@ struct BwdShared {
     uint32_t edge[2];
 };
 
+// sum += v with the rounding error kept in rest and put into the next term (Kahan): the sums over
+// a whole row of tokens whose terms largely cancel
+__device__ __forceinline__ void add_kept(float &sum, float &rest, float v)
+{
+    const float y = v - rest, t = sum + y;
+    rest = (t - sum) - y;
+    sum = t;
+}
+
 template <class T, class Cfg, int VEC, bool SUM>
 __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, BwdIo<T> io)
 {
@@ -82,7 +91,7 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
     const bool gated = io.z.p != nullptr;
 
     float2 a2[CT][P], dh[CT][P], dA[CT][P], prod[CT];
-    float Dc[CT], aD[CT], aBias[CT], total[CT];
+    float Dc[CT], aD[CT], aBias[CT], rD[CT], rBias[CT], total[CT];
 #pragma unroll
     for (int e = 0; e < CT; ++e) {
         load_states<S>(a2[e], g.A + (c + e) * g.N, n0, g.N, live[e]);
@@ -93,7 +102,7 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
         }
         prod[e] = two(1.f);
         Dc[e] = !SUM && g.Dskip && live[e] ? g.Dskip[c + e] : 0.f;
-        aD[e] = aBias[e] = total[e] = 0.f;
+        aD[e] = aBias[e] = rD[e] = rBias[e] = total[e] = 0.f;
         // what the segments behind this one send back
         if constexpr (!SUM) {
             if (k < g.K - 1 && live[e]) load_pairs<S>(dh[e], io.segH + (((size_t)b * g.K + k) * g.D + c + e) * Np + n0);
@@ -380,8 +389,8 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
                     for (int e = 0; e < CT; ++e) {
                         const float o = lane_sum<L>(po[e], lane), p = lane_sum<L>(pp[e], lane), q = lane_sum<L>(pe[e], lane) * kLn2;
                         const float ddt = fmaf(p, x[e], q) * sp[e];
-                        aD[e] = fmaf(gg[e], x[e], aD[e]);
-                        aBias[e] += ddt;
+                        add_kept(aD[e], rD[e], gg[e] * x[e]);
+                        add_kept(aBias[e], rBias[e], ddt);
                         if (gated) gz[e] *= fmaf(Dc[e], x[e], o);
                         x[e] = fmaf(dl[e], p, Dc[e] * gg[e]);
                         sp[e] = ddt;
