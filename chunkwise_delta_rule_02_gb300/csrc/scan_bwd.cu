@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
                     total[e] += dl[e];
 #pragma unroll
                     for (int i = 0; i < P; ++i)
-                        dh[e][i] = mul2(ex2_2(mul2(two(dl[e]), a2[e][i])), fma2(two(gg[e]), cc[i], dh[e][i]));
+                        dh[e][i] = mul2(decay2(dl[e], a2[e][i]), fma2(two(gg[e]), cc[i], dh[e][i]));
                 }
                 if constexpr (decltype(edges)::value) {
                     if (starts >> t & 1) {
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
                             if (starts >> t & 1) initial(h[e], t, e);
                         }
 #pragma unroll
-                        for (int i = 0; i < P; ++i) h[e][i] = fma2(ex2_2(mul2(two(dl[e]), a2[e][i])), h[e][i], mul2(two(dx[e]), bb[i]));
+                        for (int i = 0; i < P; ++i) h[e][i] = fma2(decay2(dl[e], a2[e][i]), h[e][i], mul2(two(dx[e]), bb[i]));
                     }
                 };
                 if constexpr (decltype(edges)::value) {
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
 #pragma unroll
                             for (int i = 0; i < P; ++i) {
                                 dh[e][i] = fma2(two(gg[e]), cc[i], dh[e][i]);
-                                const float2 da = mul2(ex2_2(mul2(two(dl[e]), a2[e][i])), dh[e][i]);   // what goes on to t - 1
+                                const float2 da = mul2(decay2(dl[e], a2[e][i]), dh[e][i]);   // what goes on to t - 1
                                 const float2 q = mul2(da, hp[i]);
                                 o = i == 0 ? mul2(cc[i], h[e][i]) : fma2(cc[i], h[e][i], o);
                                 p = i == 0 ? mul2(dh[e][i], bb[i]) : fma2(dh[e][i], bb[i], p);

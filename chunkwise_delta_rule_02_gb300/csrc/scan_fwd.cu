@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(Cfg::NT) k_scan_fwd(ScanDims g, ScanIo<T> io)
                         float2 yy = two(0.f);
 #pragma unroll
                         for (int i = 0; i < P; ++i) {
-                            const float2 a = ex2_2(mul2(two(dl[e]), a2[e][i]));
+                            const float2 a = decay2(dl[e], a2[e][i]);
                             h[e][i] = fma2(a, h[e][i], mul2(two(dx[e]), bb[i]));
                             if constexpr (!SUM) yy = i == 0 ? mul2(cc[i], h[e][i]) : fma2(cc[i], h[e][i], yy);
                         }
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(256) k_scan_step(ScanDims g, ScanIo<T> io, int
             const float dx = d[u] * x[u];
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                h[e] = fmaf(ex2(d[u] * (a[e] * kLog2e)), h[e], dx * bf[e]);
+                h[e] = fmaf(ex2(fmaf(d[u], a[e] * kLog2e, kDecayUp)), h[e], dx * bf[e]);
                 y[u] = fmaf(cf[e], h[e], y[u]);
             }
             if (io.hT && live[u]) {
@@ -423,12 +423,35 @@ ScanIo<T> io_of(const ScanCall &c)
     return io;
 }
 
+// One channel a lane, no segments.
+template <class T, class Cfg, int VEC>
+cudaError_t launch_narrow(const ScanCall &c, cudaStream_t st)
+{
+    ScanDims g = scan_dims(c);
+    g.tiles = (g.Dg + Cfg::CH - 1) / Cfg::CH;
+    g.K = 1;
+    g.seg = (g.T + 15) / 16 * 16;
+    const long long per = (long long)g.B * g.G * g.tiles;
+    if (per > 0x7fffffffLL) return cudaErrorInvalidValue;
+    k_scan_fwd<T, Cfg, VEC, false><<<(unsigned)per, Cfg::NT, 0, st>>>(g, io_of<T>(c));
+    return cudaPeekAtLastError();
+}
+
 template <class T, class Cfg, int VEC>
 cudaError_t launch(const ScanCall &c, cudaStream_t st)
 {
     ScanDims g = scan_dims(c);
     g.tiles = (g.Dg + Cfg::CH - 1) / Cfg::CH;
     g.K = segments(c.s, Cfg::CH);
+    // One segment, and at most two blocks an SM of the four that fit: one channel a lane, in twice
+    // the blocks, hides more latency than two channels' shared reads of B and C save (8 x 4096
+    // tokens of 2048 channels, 1.7 blocks an SM: 520 us against 598 us).
+    if constexpr (Cfg::CT == 2) {
+        if (g.K == 1 && tiles_of(c.s, Cfg::CH) <= 2ll * sm_count()) {
+            using Narrow = ScanCfg<Cfg::L, Cfg::S, 1, Cfg::TT, Cfg::NT>;
+            return launch_narrow<T, Narrow, (VEC < Narrow::VEC ? VEC : Narrow::VEC)>(c, st);
+        }
+    }
     g.seg = ((g.T + g.K - 1) / g.K + 15) / 16 * 16;   // whole tiles, whole spans between kept states
     g.K = (g.T + g.seg - 1) / g.seg;
     ScanIo<T> io = io_of<T>(c);
