@@ -316,6 +316,10 @@ def whole_job_value(tokens_per_rank: int, world: int, ms: float) -> float:
 # the translation unit and headers each profiled kernel is built from
 KERNEL_SOURCES = {
     "k_coop_fwd": ["coop.cu", "fast.h", "prep_math.cuh", "sm100.cuh", "common.cuh"],
+    # the whole training step: every source of the delta rule (the layer operators are others)
+    "step": ["affine.cu", "affine.h", "api.cu", "bscan_tc.cu", "bscan_tc.h", "bwd_tc.cu", "bwd_tc.h", "common.cuh",
+             "coop.cu", "decode.cu", "decode.h", "fast.cu", "fast.h", "general.cu", "general.h", "prep_math.cuh",
+             "sm100.cuh"],
 }
 
 
@@ -395,7 +399,7 @@ def record_step_traffic(csv_path: str, workload: str, capture: str, out: str = N
     d = json.load(open(p)) if os.path.exists(p) else {}
     d["step@" + workload] = {
         "dram_bytes_per_launch": rd + wr, "dram_read": rd, "dram_write": wr,
-        "source_sha": kernel_source_sha("step"), "sources": "csrc/*, include/gdn.h",
+        "source_sha": kernel_source_sha("step"), "sources": "csrc/* of the delta rule, include/gdn.h",
         "kernels": ", ".join(STEP_KERNELS), "capture": capture}
     with open(p, "w") as f:
         json.dump(d, f, indent=1, sort_keys=True)
