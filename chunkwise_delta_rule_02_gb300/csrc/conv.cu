@@ -144,7 +144,7 @@ constexpr int kUnroll = (kInFlight + W - 1) / W * W;
 
 template <class T, int W, int V>
 __global__ void __launch_bounds__(kTX *kTY, 2) k_conv_fwd(ConvDims g, View<const T> x, View<T> y, const float *__restrict__ w,
-                                                       const float *__restrict__ bias, const T *__restrict__ s0)
+                                                       const float *__restrict__ bias, const T *s0, T *sT)
 {
     constexpr int U = kUnroll<W>, P = kPairs<V>;
     int cv, b, t0;
@@ -196,29 +196,31 @@ __global__ void __launch_bounds__(kTX *kTY, 2) k_conv_fwd(ConvDims g, View<const
             token(in, 0);
             rotate<W, V>(h);
         }
+        if (sT && t == hi && hi > lo) {   // the ring holds the sequence's last inputs, initial taps included
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) {
+                Vec<T, V> out;
+                set_pairs<T, V>(out, h[k + 1]);
+                out.store(sT + ((size_t)s * (W - 1) + k) * g.C + c0);
+            }
+        }
         ++s;
     }
 }
 
-// Final taps: the last W - 1 inputs of every sequence, its initial taps in front.
-template <class T, int W>
-__global__ void k_conv_state(ConvDims g, View<const T> x, const T *s0, T *sT)
+// Final taps of empty sequences: their initial ones.
+template <class T>
+__global__ void k_conv_empty(ConvDims g, int taps, const T *s0, T *sT)
 {
     const long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x;
     if (i >= (long long)g.N * g.C) return;
-    const int s = (int)(i / g.C), c = (int)(i - (long long)s * g.C), hd = c / g.d;
-    const int lo = g.cu ? g.cu[s] : 0, len = g.cu ? g.cu[s + 1] - lo : g.T;
-    const T *xr = x.at(g.cu ? 0 : s, hd, 0) + (c - hd * g.d);
-    T v[W - 1];
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) {
-        const int q = len + k - (W - 1);   // token of the sequence, negative: an initial tap
-        if (q >= 0) v[k] = xr[(long long)(lo + q) * x.t];
-        else if (s0) v[k] = s0[((size_t)s * (W - 1) + len + k) * g.C + c];
-        else st_out(&v[k], 0.f);
+    const int s = (int)(i / g.C), c = (int)(i - (long long)s * g.C);
+    if (g.cu ? g.cu[s + 1] > g.cu[s] : g.T > 0) return;
+    for (int k = 0; k < taps; ++k) {
+        const size_t at = ((size_t)s * taps + k) * g.C + c;
+        if (s0) sT[at] = s0[at];
+        else st_out(sT + at, 0.f);
     }
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) sT[((size_t)s * (W - 1) + k) * g.C + c] = v[k];
 }
 
 // Backward.  For the run's tokens t0 .. t1-1 and the W - 1 behind them (of the same
@@ -495,11 +497,11 @@ cudaError_t fwd_t(const ConvCall &c, cudaStream_t st)
     if (g.T > 0) {
         const long long blocks = g.rows * g.blocks_x;
         if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-        k_conv_fwd<T, W, V><<<(unsigned)blocks, dim3(kTX, kTY), 0, st>>>(g, x, view_of<T>(c.y), c.w, c.bias, (const T *)c.s0);
+        k_conv_fwd<T, W, V><<<(unsigned)blocks, dim3(kTX, kTY), 0, st>>>(g, x, view_of<T>(c.y), c.w, c.bias, (const T *)c.s0, (T *)c.sT);
     }
-    if (c.sT && c.N > 0) {
+    if (c.sT && c.N > 0 && (g.cu || g.T == 0)) {
         const long long n = (long long)c.N * g.C;
-        k_conv_state<T, W><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g, x, (const T *)c.s0, (T *)c.sT);
+        k_conv_empty<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g, W - 1, (const T *)c.s0, (T *)c.sT);
     }
     return cudaPeekAtLastError();
 }
@@ -516,6 +518,8 @@ cudaError_t bwd_t(const ConvCall &c, cudaStream_t st)
                                                                         (const T *)c.s0, (const T *)c.dsT, c.part);
     }
     ColSum r;
+    r.part = c.part;
+    r.P = g.T > 0 ? g.rows : 0;
     r.kinds = W + 1;
     r.C = g.C;
     for (int k = 0; k < W; ++k) {
@@ -524,7 +528,7 @@ cudaError_t bwd_t(const ConvCall &c, cudaStream_t st)
     }
     r.dst[W] = c.dbias;
     r.step[W] = 1;
-    cudaError_t e = col_sum(c.part, g.T > 0 ? g.rows : 0, r, st);
+    cudaError_t e = col_sum(r, nullptr, st);
     if (e != cudaSuccess) return e;
     if (c.ds0 && c.N > 0) {
         const long long n = (long long)c.N * g.C;

@@ -181,16 +181,17 @@ __device__ __forceinline__ int seq_at(const int32_t *cu, int N, int t)
 // all zero and flagged unless cu[0] = 0, cu[N] = T and cu never falls.
 cudaError_t check_offsets(const int32_t *cu, int N, int T, int32_t *out, uint32_t *status, cudaStream_t st);
 
-// out[map(col)] = sum over p < P of part[p * n + col], col < n, in a fixed order.
-// Columns are split into `kinds` runs of n / kinds: run k of width C goes to
-// dst[k] with element stride step[k].
+// Sums of partial results in a fixed order: out[map(col)] = sum over p < P of part[p * n + col],
+// col < n.  Columns are split into `kinds` runs of n / kinds: run k of width C goes to dst[k]
+// (null: nowhere) with element stride step[k].  Two such sums go in one launch.
 struct ColSum {
+    const float *part;
+    long long P, C;
     int kinds;
-    long long C;
-    float *dst[6];
-    int step[6];
+    float *dst[5];
+    int step[5];
 };
-cudaError_t col_sum(const float *part, long long P, const ColSum &c, cudaStream_t st);
+cudaError_t col_sum(const ColSum &a, const ColSum *b, cudaStream_t st);
 
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 int sm_count();

@@ -2,6 +2,8 @@
 // the two kernels they share (packed offsets, sums of partial results).
 #include <string.h>
 
+#include <atomic>
+
 #include "layers.h"
 #include "scan.cuh"
 
@@ -26,16 +28,18 @@ __global__ void __launch_bounds__(256) k_offsets(const int32_t *cu, int N, int T
 
 constexpr int kSumX = 32, kSumY = 32;
 
-__global__ void __launch_bounds__(kSumX *kSumY) k_col_sum(const float *__restrict__ part, long long P, ColSum c)
+__global__ void __launch_bounds__(kSumX *kSumY) k_col_sum(ColSum a, ColSum b, unsigned blocks_a)
 {
     __shared__ float sm[kSumY][kSumX + 1];
-    const long long n = c.C * c.kinds, col = blockIdx.x * (long long)kSumX + threadIdx.x;
-    float a = 0.f;
+    const bool second = blockIdx.x >= blocks_a;
+    const ColSum &c = second ? b : a;
+    const long long n = c.C * c.kinds, col = (blockIdx.x - (second ? blocks_a : 0)) * (long long)kSumX + threadIdx.x;
+    float v = 0.f;
     if (col < n) {
 #pragma unroll 4
-        for (long long p = threadIdx.y; p < P; p += kSumY) a += part[p * n + col];
+        for (long long p = threadIdx.y; p < c.P; p += kSumY) v += c.part[p * n + col];
     }
-    sm[threadIdx.y][threadIdx.x] = a;
+    sm[threadIdx.y][threadIdx.x] = v;
     __syncthreads();
     if (threadIdx.y == 0 && col < n) {
         float s = 0.f;
@@ -54,19 +58,25 @@ cudaError_t check_offsets(const int32_t *cu, int N, int T, int32_t *out, uint32_
     return cudaPeekAtLastError();
 }
 
-cudaError_t col_sum(const float *part, long long P, const ColSum &c, cudaStream_t st)
+cudaError_t col_sum(const ColSum &a, const ColSum *b, cudaStream_t st)
 {
-    const long long n = c.C * c.kinds;
-    if (n == 0) return cudaSuccess;
-    k_col_sum<<<(unsigned)((n + kSumX - 1) / kSumX), dim3(kSumX, kSumY), 0, st>>>(part, P, c);
+    auto blocks = [](const ColSum &c) { return (unsigned)((c.C * c.kinds + kSumX - 1) / kSumX); };
+    const unsigned na = blocks(a), nb = b ? blocks(*b) : 0;
+    if (na + nb == 0) return cudaSuccess;
+    k_col_sum<<<na + nb, dim3(kSumX, kSumY), 0, st>>>(a, b ? *b : a, na);
     return cudaPeekAtLastError();
 }
 
 int sm_count()
 {
+    // asked once a device: the answer does not change, and calls of a few microseconds ask several times
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 152;
+    if (dev < kDevices && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+    if (dev < kDevices) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 

@@ -457,18 +457,19 @@ cudaError_t launch(const NormCall &c, const Shape &sh, bool bwd, cudaStream_t st
     k_norm_bwd<T, V, NV, WIDE, GATE, RES><<<grid, sh.threads, smem, st>>>(
         g, x, z, view_of<const T>(c.sum), view_of<const T>(c.dy), view_of<const T>(c.dsum), view_of<T>(c.dx), view_of<T>(c.dz),
         view_of<T>(c.dresidual), c.w, c.res_scale, pg);
-    ColSum r;
-    r.kinds = 1;
-    r.C = (long long)grid.y * g.d;
-    r.dst[0] = c.dw;
-    r.step[0] = 1;
-    cudaError_t e = col_sum(pg.part_w, grid.x, r, st);
-    if (e == cudaSuccess && c.dres_scale) {
-        r.C = g.d;
-        r.dst[0] = c.dres_scale;
-        e = col_sum(pg.part_s, (long long)grid.x * grid.y, r, st);
-    }
-    return e;
+    ColSum rw, rs;
+    rw.part = pg.part_w;
+    rw.P = grid.x;
+    rw.C = (long long)grid.y * g.d;
+    rw.kinds = 1;
+    rw.dst[0] = c.dw;
+    rw.step[0] = 1;
+    rs = rw;
+    rs.part = pg.part_s;
+    rs.P = (long long)grid.x * grid.y;
+    rs.C = g.d;
+    rs.dst[0] = c.dres_scale;
+    return col_sum(rw, c.dres_scale ? &rs : nullptr, st);
 }
 
 template <class T, int V, int NV, bool WIDE>

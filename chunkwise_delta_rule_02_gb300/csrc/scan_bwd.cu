@@ -593,19 +593,21 @@ cudaError_t bwd_t(const ScanCall &c, cudaStream_t st)
         if (e != cudaSuccess) return e;
     }
     const long long rows = s->T > 0 ? (long long)s->B * p.K : 0;
-    ColSum r;
-    r.kinds = 1;
-    r.C = (long long)s->D * s->N;
-    r.dst[0] = gr->dA;
-    r.step[0] = 1;
-    cudaError_t e = col_sum((float *)(c.ws + p.part_a), rows, r, st);
-    if (e != cudaSuccess || (!gr->dD && !gr->ddt_bias)) return e;
-    r.kinds = 2;
-    r.C = s->D;
-    r.dst[0] = gr->dD;
-    r.dst[1] = gr->ddt_bias;
-    r.step[1] = 1;
-    return col_sum((float *)(c.ws + p.part_d), rows, r, st);
+    ColSum ra, rd;
+    ra.part = (float *)(c.ws + p.part_a);
+    ra.P = rows;
+    ra.C = (long long)s->D * s->N;
+    ra.kinds = 1;
+    ra.dst[0] = gr->dA;
+    ra.step[0] = 1;
+    rd.part = (float *)(c.ws + p.part_d);
+    rd.P = rows;
+    rd.C = s->D;
+    rd.kinds = 2;
+    rd.dst[0] = gr->dD;
+    rd.dst[1] = gr->ddt_bias;
+    rd.step[0] = rd.step[1] = 1;
+    return col_sum(ra, gr->dD || gr->ddt_bias ? &rd : nullptr, st);
 }
 
 }  // namespace

@@ -20,6 +20,7 @@ stream, and raises if they were malformed.  Other calls never wait.
 """
 from __future__ import annotations
 
+import functools
 import struct
 from typing import Optional
 
@@ -166,10 +167,34 @@ def _cu(cu_seqlens, B):
     return cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
 
 
-def _ws(nbytes: int, device, where: str) -> torch.Tensor:
-    if nbytes == 0:
+_STATUS_ONLY = 256       # a workspace of this size holds the status word and nothing else
+_status_only = {}
+
+
+@functools.lru_cache(maxsize=4096)
+def _size(what: str, shape: bytes, for_backward: int, device: int) -> int:
+    """Bytes of a call's buffer, by its sizes (the library plans anew for each new shape)."""
+    f = getattr(_L(), what)
+    return int(f(shape, for_backward)) if for_backward >= 0 else int(f(shape))
+
+
+def _ws(what: str, shape: bytes, for_backward: int, like: torch.Tensor, packed: bool, where: str) -> torch.Tensor:
+    """Workspace, or (for_backward -1) saved buffer.  Calls that are not packed leave the status word alone:
+    where they need nothing else, all of a device share one buffer that nothing is written to."""
+    dev = like.get_device()
+    if packed:          # the record holds an address: nothing to remember
+        f = getattr(_L(), what)
+        n = int(f(shape, for_backward)) if for_backward >= 0 else int(f(shape))
+    else:
+        n = _size(what, shape, for_backward, dev)
+    if n == 0:
         raise GdnError(DN_ERR_INVALID_ARG, where)
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if n == _STATUS_ONLY and not packed and for_backward >= 0:
+        ws = _status_only.get(dev)
+        if ws is None:
+            ws = _status_only[dev] = torch.zeros(_STATUS_ONLY, dtype=torch.uint8, device=like.device)
+        return ws
+    return torch.empty(n, dtype=torch.uint8, device=like.device)
 
 
 # ------------------------------------------------------------------ convolution
@@ -228,7 +253,7 @@ def conv_forward(x, w, bias=None, state=None, cu_seqlens=None, silu=True, out=No
     sT = torch.empty((n, width - 1, w.shape[0]), dtype=x.dtype, device=x.device) if want_state else None
     shape = conv_shape(x, width, silu, cu_seqlens)
     if ws is None:
-        ws = _ws(dn_conv_workspace_size(shape, False), x.device, "dn_conv_fwd")
+        ws = _ws("dn_conv_workspace_size", shape, 0, x, cu_seqlens is not None, "dn_conv_fwd")
     dn_conv_fwd(shape, x, w, bias, state, y, sT, ws)
     if check_status and cu_seqlens is not None:
         _check(dn_device_status(ws), "dn_conv_fwd (device status)")
@@ -247,7 +272,7 @@ def conv_backward(x, w, bias, state, dy, dstate=None, cu_seqlens=None, silu=True
              dstate=None if state is None else torch.empty_like(state))
     shape = conv_shape(x, width, silu, cu_seqlens)
     if ws is None:
-        ws = _ws(dn_conv_workspace_size(shape, True), x.device, "dn_conv_bwd")
+        ws = _ws("dn_conv_workspace_size", shape, 1, x, cu_seqlens is not None, "dn_conv_bwd")
     dn_conv_bwd(shape, x, w, bias, state, dy, dstate, dx, g["dw"], g["dbias"], g["dstate"], ws)
     if check_status and cu_seqlens is not None:
         _check(dn_device_status(ws), "dn_conv_bwd (device status)")
@@ -387,8 +412,8 @@ def scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqle
     hT = torch.empty((n,) + tuple(A.shape), dtype=torch.float32, device=x.device) if want_state else None
     shape = scan_shape(x, B, dt_softplus, cu_seqlens)
     if ws is None:
-        ws = _ws(dn_scan_workspace_size(shape, False), x.device, "dn_scan_fwd")
-    saved = _ws(dn_scan_saved_size(shape), x.device, "dn_scan_fwd") if save else None
+        ws = _ws("dn_scan_workspace_size", shape, 0, x, cu_seqlens is not None, "dn_scan_fwd")
+    saved = _ws("dn_scan_saved_size", shape, -1, x, cu_seqlens is not None, "dn_scan_fwd") if save else None
     dn_scan_fwd(shape, scan_io(x, dt, A, B, C, D, z, dt_bias, h0, y, hT), saved, ws)
     if check_status and cu_seqlens is not None:
         _check(dn_device_status(ws), "dn_scan_fwd (device status)")
@@ -409,7 +434,7 @@ def scan_backward(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, dy=None
     g = dict(dx=new(x), ddt=new(x), dA=new(A), dB=new(B), dC=new(C), dD=new(D), dz=new(z), ddt_bias=new(dt_bias), dh0=new(h0))
     shape = scan_shape(x, B, dt_softplus, cu_seqlens)
     if ws is None:
-        ws = _ws(dn_scan_workspace_size(shape, True), x.device, "dn_scan_bwd")
+        ws = _ws("dn_scan_workspace_size", shape, 1, x, cu_seqlens is not None, "dn_scan_bwd")
     dn_scan_bwd(shape, scan_io(x, dt, A, B, C, D, z, dt_bias, h0, None, None),
                 scan_grads(dy, g["dx"], g["ddt"], g["dB"], g["dC"], g["dz"], dhT, g["dA"], g["dD"], g["ddt_bias"], g["dh0"]), saved, ws)
     if check_status and cu_seqlens is not None:
@@ -496,6 +521,6 @@ def norm_backward(x, w, dy, z=None, sum=None, dsum=None, res_scale=None, eps=1e-
              dres_scale=None if res_scale is None else torch.empty_like(res_scale))
     shape = norm_shape(x, w, eps)
     if ws is None:
-        ws = _ws(dn_norm_workspace_size(shape), x.device, "dn_norm_bwd")
+        ws = _ws("dn_norm_workspace_size", shape, -1, x, False, "dn_norm_bwd")
     dn_norm_bwd(shape, x, w, z, res_scale, sum, dy, dsum, dx, g["dw"], g["dz"], dres, g["dres_scale"], ws)
     return g
