@@ -26,27 +26,34 @@ __global__ void __launch_bounds__(256) k_offsets(const int32_t *cu, int N, int T
     if (threadIdx.x == 0) *status = bad ? kStatusBadOffsets : kStatusOk;   // and clears what an earlier call left
 }
 
-constexpr int kSumX = 32, kSumY = 32;
+// Columns of a block (one 32-byte sector of each row) and threads a column: each sums every
+// kSumY-th row, then pairs of threads in a fixed tree.  8 x 16 threads for the convolution's
+// 10240 columns of 16 rows: 7 us (8 x 64: 18 us; 32 x 32: 12 us); for the norm's 128 columns of
+// 456 rows 8 x 64 is 0.7 us faster, the scan's training step 36 us slower.
+constexpr int kSumX = 8, kSumY = 16;
 
 __global__ void __launch_bounds__(kSumX *kSumY) k_col_sum(ColSum a, ColSum b, unsigned blocks_a)
 {
-    __shared__ float sm[kSumY][kSumX + 1];
+    __shared__ float sm[kSumY][kSumX];
     const bool second = blockIdx.x >= blocks_a;
-    const ColSum &c = second ? b : a;
-    const long long n = c.C * c.kinds, col = (blockIdx.x - (second ? blocks_a : 0)) * (long long)kSumX + threadIdx.x;
+    // field by field: a reference to either would put the arguments into local memory
+    const float *part = second ? b.part : a.part;
+    const long long P = second ? b.P : a.P, C = second ? b.C : a.C, n = C * (second ? b.kinds : a.kinds);
+    const long long col = (blockIdx.x - (second ? blocks_a : 0)) * (long long)kSumX + threadIdx.x;
     float v = 0.f;
     if (col < n) {
-#pragma unroll 4
-        for (long long p = threadIdx.y; p < c.P; p += kSumY) v += c.part[p * n + col];
+#pragma unroll 8
+        for (long long p = threadIdx.y; p < P; p += kSumY) v += part[p * n + col];
     }
     sm[threadIdx.y][threadIdx.x] = v;
-    __syncthreads();
+    for (int h = kSumY / 2; h > 0; h >>= 1) {
+        __syncthreads();
+        if (threadIdx.y < h) sm[threadIdx.y][threadIdx.x] += sm[threadIdx.y + h][threadIdx.x];
+    }
     if (threadIdx.y == 0 && col < n) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < kSumY; ++i) s += sm[i][threadIdx.x];
-        const int k = (int)(col / c.C);
-        if (c.dst[k]) c.dst[k][(col - k * c.C) * c.step[k]] = s;
+        const int k = (int)(col / C);
+        float *dst = second ? b.dst[k] : a.dst[k];
+        if (dst) dst[(col - k * C) * (second ? b.step[k] : a.step[k])] = sm[0][threadIdx.x];
     }
 }
 

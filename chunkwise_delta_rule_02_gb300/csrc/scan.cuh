@@ -129,9 +129,6 @@ struct ScanCfg {
     static constexpr int CH = NT / L_ * CT_;                             // channels of a block
     static constexpr int EPT = TT * CH / NT;                             // a tile's elements a thread moves
     static constexpr int VEC = EPT < 4 ? EPT : 4;
-    // bytes of a vector of elements T: up to 16, 0 where a thread's share is less than 4
-    template <class T>
-    static constexpr int bytes() { return EPT * sizeof(T) >= 16 ? 16 : EPT * sizeof(T) >= 4 ? EPT * sizeof(T) : 0; }
     static constexpr int NBC = (TT * Np + NT - 1) / NT;                  // elements of B (and of C) a thread moves
     static constexpr int RS = CH + M * CT_;   // row of a padded [token][channel] array: L rows of M CT channels, no bank twice
 };
@@ -228,18 +225,6 @@ inline void scan_carry(const ScanDims &g, const float *segP, float *segH, int Np
     const long long per = (long long)g.D * Np, all = g.B * per;
     k_scan_carry<FWD><<<(unsigned)((all + 127) / 128), 128, 0, st>>>(segP, segH, g.K, per, all);
 }
-
-// An asynchronous copy of BYTES (4, 8 or 16) to shared memory; zeros where !in.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void *dst, const void *src, bool in)
-{
-    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-    const int n = in ? BYTES : 0;
-    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 // (delta, delta x) of CT neighbouring channels
 template <int CT>
