@@ -43,7 +43,7 @@ template <class T>
 struct ScanIo {
     View<const T> x, dt, b, c, z;
     View<T> y;
-    float *hT, *keep;              // keep: state entering every keep_of(Np)-th token, [B][ceil(T / that)][D][Np], or null
+    float *hT, *keep;              // keep: state entering every keep_of(Np)-th token, [B][ceil(T / that)][D][Np] with keep_place's order in [D][Np], or null
     float *segP, *segH;            // per segment: product of the decays, end state from zero [B][K][D][Np]
 };
 
@@ -132,6 +132,19 @@ struct ScanCfg {
     static constexpr int NBC = (TT * Np + NT - 1) / NT;                  // elements of B (and of C) a thread moves
     static constexpr int RS = CH + M * CT_;   // row of a padded [token][channel] array: L rows of M CT channels, no bank twice
 };
+
+// Where a lane's S states of channel cg of a group lie among a token's kept states: the channels that
+// one warp holds two a lane in the order of its lanes, so that a warp's access is one run of memory
+// (in [channel][state] order 8 neighbouring lanes' 16 bytes touch 8 lines; KEPT_FIGURES).
+// Channels behind the last such set keep the plain order.
+template <class Cfg>
+__device__ __forceinline__ unsigned keep_place(const ScanDims &g, int grp, int cg, int l)
+{
+    constexpr int L = Cfg::L, S = Cfg::S, M = Cfg::M, Np = Cfg::Np;
+    const int first = cg & ~(2 * M - 1), e = cg & 1, m = (cg - first) >> 1;
+    const int in = first + 2 * M <= g.Dg ? first * Np + ((e * L + l) * M + m) * S : cg * Np + l * S;
+    return (unsigned)grp * g.Dg * Np + in;
+}
 
 // Sequence starts and ends among the tile's tokens t0 .. t0+n-1 (n <= 32): bit masks,
 // and for each such token its sequence.  Called by one whole warp.

@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
 {
     constexpr int L = Cfg::L, S = Cfg::S, CT = Cfg::CT, M = Cfg::M, Np = Cfg::Np, CH = Cfg::CH, P = S / 2, TT = Cfg::TT;
     constexpr int NV = Cfg::EPT / VEC, NBC = Cfg::NBC, KEEP = keep_of(Np);
+    static_assert(TT == KEEP, "a tile starts from the state kept for it");
     using Shared = BwdShared<Cfg>;
     extern __shared__ __align__(16) char smem_raw[];
     Shared &sm = *reinterpret_cast<Shared *>(smem_raw);
@@ -125,6 +126,10 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
     Vec<T, VEC> xn[NV], dn[NV], zn[NV], gn[NV];
     T br[NBC], cr[NBC];
     float2 kn[CT][P];   // the state that enters the tile
+    const float *kp = SUM ? nullptr : io.keep + ((size_t)b * ((g.T + KEEP - 1) / KEEP) + (te - 1) / KEEP) * g.D * Np;
+    unsigned place[CT];
+#pragma unroll
+    for (int e = 0; e < CT; ++e) place[e] = keep_place<Cfg>(g, grp, cg0 + ch + e, l);
     float bias[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) bias[i] = col && g.bias ? g.bias[cv + i] : 0.f;
@@ -158,9 +163,9 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
             for (int e = 0; e < CT; ++e) {
 #pragma unroll
                 for (int i = 0; i < P; ++i) kn[e][i] = two(0.f);
-                if (live[e] && t0 >= ts)
-                    load_pairs<S>(kn[e], io.keep + (((size_t)b * ((g.T + KEEP - 1) / KEEP) + t0 / KEEP) * g.D + c + e) * Np + n0);
+                if (live[e] && t0 >= ts) load_pairs<S>(kn[e], kp + place[e]);
             }
+            kp -= (size_t)g.D * Np;   // read no further than the segment's first tile
         }
     };
     const int last = ts + (te - ts - 1) / TT * TT;

@@ -71,6 +71,16 @@ __global__ void __launch_bounds__(Cfg::NT) k_scan_fwd(ScanDims g, ScanIo<T> io)
         }
     }
 
+    // where this lane's kept states go
+    [[maybe_unused]] constexpr int KEEP = keep_of(Np);
+    float *kp = nullptr;
+    unsigned place[CT];
+    if constexpr (!SUM) {
+        if (io.keep) kp = io.keep + ((size_t)b * ((g.T + KEEP - 1) / KEEP) + ts / KEEP) * g.D * Np;
+#pragma unroll
+        for (int e = 0; e < CT; ++e) place[e] = keep_place<Cfg>(g, grp, cg0 + ch + e, l);
+    }
+
     // This thread's vectors of a tile: tokens vt, vt + ES, ..., always channels vc .. vc + VEC - 1
     // (a token's vectors divide the threads).
     constexpr int RV = CH / VEC, ES = Cfg::NT / RV;
@@ -186,12 +196,11 @@ __global__ void __launch_bounds__(Cfg::NT) k_scan_fwd(ScanDims g, ScanIo<T> io)
 #pragma unroll 1
             for (int g0 = 0; g0 < TT; g0 += L) {
                 if constexpr (!SUM) {
-                    constexpr int KEEP = keep_of(Cfg::Np);
-                    if (io.keep && g0 % KEEP == 0 && t0 + g0 < te) {
+                    if (kp && g0 % KEEP == 0 && t0 + g0 < te) {
 #pragma unroll
                         for (int e = 0; e < CT; ++e)
-                            if (live[e])
-                                store_pairs<S>(io.keep + (((size_t)b * ((g.T + KEEP - 1) / KEEP) + (t0 + g0) / KEEP) * g.D + c + e) * Np + n0, h[e]);
+                            if (live[e]) store_pairs<S>(kp + place[e], h[e]);
+                        kp += (size_t)g.D * Np;
                     }
                 }
                 float yp[CT][L];
