@@ -135,7 +135,8 @@ struct ScanCfg {
 
 // Where a lane's S states of channel cg of a group lie among a token's kept states: the channels that
 // one warp holds two a lane in the order of its lanes, so that a warp's access is one run of memory
-// (in [channel][state] order 8 neighbouring lanes' 16 bytes touch 8 lines; KEPT_FIGURES).
+// (in [channel][state] order 8 neighbouring lanes' 16 bytes touch 8 lines: the forward pass of 4 x 4096
+// tokens of 2048 channels took 219 us instead of 187, the backward of 8 x 4096 1632 us instead of 1553).
 // Channels behind the last such set keep the plain order.
 template <class Cfg>
 __device__ __forceinline__ unsigned keep_place(const ScanDims &g, int grp, int cg, int l)

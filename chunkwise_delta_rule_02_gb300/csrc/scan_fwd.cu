@@ -452,10 +452,11 @@ cudaError_t launch(const ScanCall &c, cudaStream_t st)
     ScanDims g = scan_dims(c);
     g.tiles = (g.Dg + Cfg::CH - 1) / Cfg::CH;
     g.K = segments(c.s, Cfg::CH);
-    // One segment, and at most two blocks an SM of the four that fit: one channel a lane, in twice
-    // the blocks, hides more latency than two channels' shared reads of B and C save (8 x 4096
-    // tokens of 2048 channels, 1.7 blocks an SM: 520 us against 598 us).
-    if constexpr (Cfg::CT == 2) {
+    // Up to 8 states, one segment, and at most two blocks an SM of the four that fit: one channel a
+    // lane, in twice the blocks, hides more latency than two channels' shared reads of B and C save
+    // (2048 channels of 8 states, 8 x 4096 tokens 460 us against 612 us, 8 x 2048 244 us against 324;
+    // of 16 states 545 us against 537, of 32 states and 4 x 2048 tokens 267 us against 243).
+    if constexpr (Cfg::CT == 2 && Cfg::Np <= 8) {
         if (g.K == 1 && tiles_of(c.s, Cfg::CH) <= 2ll * sm_count()) {
             using Narrow = ScanCfg<Cfg::L, Cfg::S, 1, Cfg::TT, Cfg::NT>;
             return launch_narrow<T, Narrow, (VEC < Narrow::VEC ? VEC : Narrow::VEC)>(c, st);
