@@ -334,9 +334,9 @@ cudaError_t fwd_layout(int N, F f)
 template <class F>
 cudaError_t bwd_layout(int N, F f)
 {
-    if (N <= 8) return f(ScanCfg<4, 2, 2, 8, 128>{});
-    if (N <= 16) return f(ScanCfg<4, 4, 2, 8, 128>{});
-    if (N <= 32) return f(ScanCfg<8, 4, 2, 8, 128>{});
+    if (N <= 8) return f(ScanCfg<4, 2, 2, 16, 128>{});
+    if (N <= 16) return f(ScanCfg<4, 4, 2, 16, 128>{});
+    if (N <= 32) return f(ScanCfg<8, 4, 2, 16, 128>{});
     if (N <= 64) return f(ScanCfg<16, 4, 1, 16, 128>{});
     return f(ScanCfg<16, 8, 1, 16, 128>{});
 }

@@ -7,9 +7,12 @@
 //     dx = delta p + D g,  ddt = (sum_n e A + x p) softplus'(dt),  dz = dy o silu'(z)
 //     dA += delta e,  dB_t = sum_c delta x dh_t,  dC_t = sum_c g h_t,  dh0 = a_0 dh_0
 //
-// A block walks its channels' tokens backwards in tiles of 8 (16 from 33 states on).  The
-// forward pass kept the state entering every tile; from it the tile is run forward once, the
-// state before every token into shared memory, and then back.  a_t is an exponential in both.
+// A block walks its channels' tokens backwards in tiles of 16.  From the kept state that enters
+// it the tile is run forward once, the state before every token into shared memory, and then back.
+// a_t is an exponential in both.  Tiles of 8 were 1553 us for the training step below instead of
+// 1450: barriers, and the elementwise steps' latency, twice as often.  Both of a tile's kept
+// states, as two recurrences at once, with asynchronous copies: no faster (2067 us the whole step
+// against 2070).
 // Tried instead: the tile's states in registers (16 tokens of them spill: 4.0 ms for the training
 // step below), groups of 4 tokens with states and decays in registers, run forward twice (2.7 ms),
 // one channel a lane (2.8 ms: shared-memory reads double), dB and dC summed over channels on the
@@ -79,7 +82,7 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
 {
     constexpr int L = Cfg::L, S = Cfg::S, CT = Cfg::CT, M = Cfg::M, Np = Cfg::Np, CH = Cfg::CH, P = S / 2, TT = Cfg::TT;
     constexpr int NV = Cfg::EPT / VEC, NBC = Cfg::NBC, KEEP = keep_of(Np);
-    static_assert(TT == KEEP, "a tile starts from the state kept for it");
+    static_assert(TT % KEEP == 0, "a tile starts from a kept state");
     using Shared = BwdShared<Cfg>;
     extern __shared__ __align__(16) char smem_raw[];
     Shared &sm = *reinterpret_cast<Shared *>(smem_raw);
@@ -126,7 +129,7 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
     Vec<T, VEC> xn[NV], dn[NV], zn[NV], gn[NV];
     T br[NBC], cr[NBC];
     float2 kn[CT][P];   // the state that enters the tile
-    const float *kp = SUM ? nullptr : io.keep + ((size_t)b * ((g.T + KEEP - 1) / KEEP) + (te - 1) / KEEP) * g.D * Np;
+    const float *kp = SUM ? nullptr : io.keep + ((size_t)b * ((g.T + KEEP - 1) / KEEP) + (te - 1) / TT * (TT / KEEP)) * g.D * Np;
     unsigned place[CT];
 #pragma unroll
     for (int e = 0; e < CT; ++e) place[e] = keep_place<Cfg>(g, grp, cg0 + ch + e, l);
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
                 for (int i = 0; i < P; ++i) kn[e][i] = two(0.f);
                 if (live[e] && t0 >= ts) load_pairs<S>(kn[e], kp + place[e]);
             }
-            kp -= (size_t)g.D * Np;   // read no further than the segment's first tile
+            kp -= (size_t)g.D * Np * (TT / KEEP);   // read no further than the segment's first tile
         }
     };
     const int last = ts + (te - ts - 1) / TT * TT;
