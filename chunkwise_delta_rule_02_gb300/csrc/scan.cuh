@@ -26,7 +26,7 @@ namespace gdn {
 namespace lay {
 
 // Tokens between the states that the forward pass keeps for the backward, by the padded
-// number of states: what the backward's shared memory holds of one tile's states.
+// number of states (the backward's tiles are whole spans of it).
 __host__ __device__ constexpr int keep_of(int Np) { return Np <= 32 ? 8 : 16; }
 
 struct ScanDims {

@@ -13,15 +13,15 @@
 // 1450: barriers, and the elementwise steps' latency, twice as often.  Both of a tile's kept
 // states, as two recurrences at once, with asynchronous copies: no faster (2067 us the whole step
 // against 2070).
-// Tried instead: the tile's states in registers (16 tokens of them spill: 4.0 ms for the training
-// step below), groups of 4 tokens with states and decays in registers, run forward twice (2.7 ms),
+// Tried with tiles of 8, the training step then at 2.3 ms: the tile's states in registers (16 tokens
+// of them spill: 4.0 ms), groups of 4 tokens with states and decays in registers, run forward twice (2.7 ms),
 // one channel a lane (2.8 ms: shared-memory reads double), dB and dC summed over channels on the
 // tensor cores in tf32 (2.3 ms, no gain: the butterfly is not what it waits for).
 //
-// Bound by latency and issue: 210 instructions a token and 16 channels (a warp), 52 of them
+// Bound by latency and issue: 203 instructions a token and 16 channels (a warp), 52 of them
 // packed multiply-adds, 16 exponentials, 46 for the sums over lanes; two blocks of 4 warps fit an
-// SM (registers), and 8 x 4096 tokens of 2048 channels are 1.7 a SM: issue slots 47 % used, the
-// shared-memory port 54 %, 1.6 ms.  The whole training step: 2.2 ms.
+// SM (registers, shared memory), and 8 x 4096 tokens of 2048 channels are 1.7 a SM: issue slots 51 %
+// used, the shared-memory port 55 %, 1.45 ms.  The whole training step: 1.98 ms.
 //
 // Sums.  Over a channel's states (o, p, sum e A): the lanes' butterfly.  Over channels
 // (dB, dC): a butterfly over the warp's channels that leaves a share of the 2 S values in

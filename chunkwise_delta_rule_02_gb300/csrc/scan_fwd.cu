@@ -432,9 +432,9 @@ ScanIo<T> io_of(const ScanCall &c)
     return io;
 }
 
-// One channel a lane, no segments.
+// One segment, in a layout for few blocks.
 template <class T, class Cfg, int VEC>
-cudaError_t launch_narrow(const ScanCall &c, cudaStream_t st)
+cudaError_t launch_few(const ScanCall &c, cudaStream_t st)
 {
     ScanDims g = scan_dims(c);
     g.tiles = (g.Dg + Cfg::CH - 1) / Cfg::CH;
@@ -452,14 +452,16 @@ cudaError_t launch(const ScanCall &c, cudaStream_t st)
     ScanDims g = scan_dims(c);
     g.tiles = (g.Dg + Cfg::CH - 1) / Cfg::CH;
     g.K = segments(c.s, Cfg::CH);
-    // Up to 8 states, one segment, and at most two blocks an SM of the four that fit: one channel a
-    // lane, in twice the blocks, hides more latency than two channels' shared reads of B and C save
-    // (2048 channels of 8 states, 8 x 4096 tokens 460 us against 612 us, 8 x 2048 244 us against 324;
-    // of 16 states 545 us against 537, of 32 states and 4 x 2048 tokens 267 us against 243).
-    if constexpr (Cfg::CT == 2 && Cfg::Np <= 8) {
+    // One segment, at most two blocks an SM of the four that fit, up to 16 states: what counts is
+    // latency.  Up to 8 states, one channel a lane in twice the blocks hides more of it than two channels'
+    // shared reads of B and C save (2048 channels of 8 states, 8 x 4096 tokens: 460 us against 612;
+    // of 16 states 545 against 537).  With 9 to 16 states, tiles of 32 tokens halve the barriers and the
+    // elementwise steps' waits (8 x 4096: 499 us against 536; where four blocks run on an SM, 4 x 8192, 563
+    // against 554; 32 states, 4 x 4096, 455 against 450).
+    if constexpr (Cfg::CT == 2 && Cfg::Np <= 16) {
         if (g.K == 1 && tiles_of(c.s, Cfg::CH) <= 2ll * sm_count()) {
-            using Narrow = ScanCfg<Cfg::L, Cfg::S, 1, Cfg::TT, Cfg::NT>;
-            return launch_narrow<T, Narrow, (VEC < Narrow::VEC ? VEC : Narrow::VEC)>(c, st);
+            using Few = ScanCfg<Cfg::L, Cfg::S, Cfg::Np <= 8 ? 1 : 2, Cfg::Np <= 8 ? Cfg::TT : 32, Cfg::NT>;
+            return launch_few<T, Few, (VEC < Few::VEC ? VEC : Few::VEC)>(c, st);
         }
     }
     g.seg = ((g.T + g.K - 1) / g.K + 15) / 16 * 16;   // whole tiles, whole spans between kept states
