@@ -19,6 +19,7 @@
 // what enters it.  That costs the recurrence 1.6 times, so plan_segments weighs it against the
 // SMs left idle.  4 x 8192 tokens of 2048 channels, 16 states, bf16 with gate: 553 us
 // (197 us the first pass, 347 us the second); one row of 16384 tokens, 1024 channels: 160 us.
+#include <algorithm>
 #include <type_traits>
 
 #include "scan.cuh"
@@ -306,14 +307,13 @@ __global__ void k_scan_empty(const float *h0, float *hT, const int32_t *cu, int 
 // bound by (HBM: states read and written once), and U sequences each, whose states are in flight
 // together and share A.
 template <class T, int V, int U>
-__global__ void __launch_bounds__(256) k_scan_step(ScanDims g, ScanIo<T> io, int L, bool wide)
+__global__ void __launch_bounds__(256, 4) k_scan_step(ScanDims g, ScanIo<T> io, int shift, bool wide, int first)
 {
-    const long long i = (blockIdx.x * 256ll + threadIdx.x) / L;
-    const int l = threadIdx.x & (L - 1);
-    const long long all = (long long)((g.B + U - 1) / U) * g.D;
-    const bool any = i < all;   // the whole warp takes part in the sums
-    const long long j = any ? i : 0;
-    const int b0 = (int)(j / g.D) * U, c = (int)(j % g.D), grp = c / g.Dg;
+    // L = 2^shift lanes a channel; sequences from `first` on, so few that 32 bits count their channels
+    const int L = 1 << shift, l = threadIdx.x & (L - 1);
+    const unsigned i = blockIdx.x * (256u >> shift) + (threadIdx.x >> shift), q = i / (unsigned)g.D;
+    const bool any = q * U + first < (unsigned)g.B;   // the whole warp takes part in the sums
+    const int b0 = any ? (int)q * U + first : 0, c = any ? (int)(i - q * g.D) : 0, grp = g.G == 1 ? 0 : c / g.Dg;
     bool live[U];
     int b[U];
 #pragma unroll
@@ -514,15 +514,23 @@ cudaError_t step_t(const ScanCall &c, cudaStream_t st)
     auto al = [](const void *p, int n) { return ((uintptr_t)p % n) == 0; };
     auto ok = [&](int V) { return g.N % V == 0 && al(g.A, 4 * V) && al(g.h0, 4 * V) && al(io.hT, 4 * V); };
     const int V = ok(4) ? 4 : 1;
-    int L = 1;
-    while (L < 32 && L * V < g.N) L <<= 1;
+    int shift = 0;
+    while (shift < 5 && (V << shift) < g.N) ++shift;
     // two sequences a lane once that leaves the SMs four blocks each (256 sequences, 2048 channels, 16
-    // states: 33 us with one, 23 us with two and with four)
-    const int U = (long long)g.B * g.D * L / 2 / 256 >= 4ll * sm_count() ? 2 : 1;
-    const long long blocks = ((long long)((g.B + U - 1) / U) * g.D * L + 255) / 256;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    // states: 33 us with one, 23 us with two and with four).  The kernel's 64 registers let four blocks run on an
+    // SM: 21.5 us, at 70 registers 24 us
+    const int U = ((long long)g.B * g.D << shift) / 2 / 256 >= 4ll * sm_count() ? 2 : 1;
     const bool wide = can_vector(&c.io->b, sizeof(T), V * sizeof(T)) && can_vector(&c.io->c, sizeof(T), V * sizeof(T));
-    auto go = [&](auto v, auto u) { k_scan_step<T, decltype(v)::value, decltype(u)::value><<<(unsigned)blocks, 256, 0, st>>>(g, io, L, wide); };
+    const int most = (int)std::max(1ll, std::min<long long>(g.B, (1ll << 29) / g.D)) * U;   // sequences of a launch
+    auto go = [&](auto v, auto u) {
+        for (long long first = 0; first < g.B; first += most) {
+            const int n = (int)std::min<long long>(g.B - first, most);
+            const unsigned blocks = (unsigned)(((((long long)(n + U - 1) / U) * g.D << shift) + 255) / 256);
+            ScanDims part = g;
+            part.B = (int)first + n;
+            k_scan_step<T, decltype(v)::value, decltype(u)::value><<<blocks, 256, 0, st>>>(part, io, shift, wide, (int)first);
+        }
+    };
     using one = std::integral_constant<int, 1>;
     using two_ = std::integral_constant<int, 2>;
     using four = std::integral_constant<int, 4>;
