@@ -182,6 +182,7 @@ __device__ __forceinline__ void tile_edges(const ScanDims &g, int b, int t0, int
 // tokens) for K = 4, 7, 9, 14, 19, 28, and the forward pass took 699, 598, 610, 579, 569, 583 us.
 inline int plan_segments(long long tiles, int T, int R, int R1, double w1)
 {
+    if (T <= 0) return 1;   // no tokens: nothing to cut (and no length to divide by)
     const int sms = sm_count();
     auto busiest = [&](long long blocks, int r) {   // rounds of the SM with the most blocks, in blocks at full speed
         const long long m = (blocks + sms - 1) / sms, full = m / r * r, n = m - full;
