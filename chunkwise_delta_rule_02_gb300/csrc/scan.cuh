@@ -44,7 +44,7 @@ struct ScanIo {
     View<const T> x, dt, b, c, z;
     View<T> y;
     float *hT, *keep;              // keep: state entering every keep_of(Np)-th token, [B][ceil(T / that)][D][Np] with keep_place's order in [D][Np], or null
-    float *segP, *segH;            // per segment: product of the decays, end state from zero [B][K][D][Np]
+    float *segP, *segH;            // per segment: product of the decays (kCut: a sequence starts in it), end state from zero [B][K][D][Np]
 };
 
 // exp(delta A) of two states, a2 = A log2 e.  ex2.approx rounds towards zero rather than to the
@@ -201,9 +201,14 @@ inline int plan_segments(long long tiles, int T, int R, int R1, double w1)
     return best;
 }
 
+// In the place of a segment's decay product: a sequence starts in the segment.  A product is never
+// negative, and is 0 wherever it underflows, which a few tokens of a fast decay are enough for.
+constexpr float kCut = -1.f;
+
 // Composes the K segments of every (row, channel, state) in place: segH[k] becomes what
-// enters segment k, from the segments before it (FWD) or behind it.  A product of 0 is a
-// sequence start inside a segment: nothing from before it, not even an infinity, goes on.
+// enters segment k, from the segments before it (FWD) or behind it.  Nothing from before a
+// sequence start, not even an infinity or NaN, goes on; through any other segment these
+// do, as they do in the recurrence, whose decays of single tokens are not 0 where their product is.
 // Segment k of the last one in that order is never read.
 template <bool FWD>
 __global__ void __launch_bounds__(128) k_scan_carry(const float *__restrict__ segP, float *segH, int K, long long per, long long all)
@@ -228,7 +233,7 @@ __global__ void __launch_bounds__(128) k_scan_carry(const float *__restrict__ se
             const int k = FWD ? k0 + u : K - 1 - k0 - u;
             if (k0 + u < K) {
                 segH[at + k * per] = h;
-                if (k0 + u < K - 1) h = p[u] == 0.f ? e[u] : fmaf(p[u], h, e[u]);
+                if (k0 + u < K - 1) h = p[u] == kCut ? e[u] : p[u] == 0.f ? (isfinite(h) ? 0.f : h) + e[u] : fmaf(p[u], h, e[u]);
             }
         }
     }
