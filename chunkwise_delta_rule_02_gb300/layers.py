@@ -221,8 +221,13 @@ def dn_conv_bwd(shape, x, w, bias, s0, dy, dsT, dx, dw, dbias, ds0, ws, stream=N
                             _stream(stream)), "dn_conv_bwd")
 
 
+def _step_view(t: torch.Tensor) -> bytes:
+    """dn_view record of one token a sequence, [n,C] (or a token array [n,H,1,d], [n,1,C])."""
+    return _VIEW.pack(t.data_ptr(), t.stride(0), 0, 0) if t.dim() == 2 else _view(t)
+
+
 def dn_conv_step(shape, x, w, bias, state_in, state_out, y, stream=None):
-    _check(_L().dn_conv_step(shape, _view(x), _p(w), _p(bias), _p(state_in), _p(state_out), _view(y),
+    _check(_L().dn_conv_step(shape, _step_view(x), _p(w), _p(bias), _p(state_in), _p(state_out), _step_view(y),
                              _stream(stream)), "dn_conv_step")
 
 
@@ -298,8 +303,7 @@ def conv_step(x, w, bias=None, state=None, out_state=None, silu=True, out=None):
     else:
         _dense(out_state, "out_state", sshape, x.dtype)
     shape = _CONV_SHAPE.pack(N, 1, 1, C, width, _dtype_code(x, "x"), 1 if silu else 0, 0, 0)
-    _check(_L().dn_conv_step(shape, _VIEW.pack(x.data_ptr(), x.stride(0), 0, 0), _p(w), _p(bias), _p(state),
-                             _p(out_state), _VIEW.pack(y.data_ptr(), y.stride(0), 0, 0), _stream(None)), "dn_conv_step")
+    dn_conv_step(shape, x, w, bias, state, out_state, y)
     return y, out_state
 
 
