@@ -167,6 +167,17 @@ def _cu(cu_seqlens, B):
     return cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
 
 
+def _buffer(t: torch.Tensor, name: str, like: torch.Tensor) -> torch.Tensor:
+    """A caller's workspace or saved buffer: the library writes (reads) its bytes from the first one on."""
+    if not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.get_device() != like.get_device():
+        raise ValueError("%s is on %s, the inputs are on %s" % (name, t.device, like.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t
+
+
 _STATUS_ONLY = 256       # a workspace of this size holds the status word and nothing else
 _status_only = {}
 
@@ -257,8 +268,7 @@ def conv_forward(x, w, bias=None, state=None, cu_seqlens=None, silu=True, out=No
     y = _result(out, "out", x)
     sT = torch.empty((n, width - 1, w.shape[0]), dtype=x.dtype, device=x.device) if want_state else None
     shape = conv_shape(x, width, silu, cu_seqlens)
-    if ws is None:
-        ws = _ws("dn_conv_workspace_size", shape, 0, x, cu_seqlens is not None, "dn_conv_fwd")
+    ws = _ws("dn_conv_workspace_size", shape, 0, x, cu_seqlens is not None, "dn_conv_fwd") if ws is None else _buffer(ws, "ws", x)
     dn_conv_fwd(shape, x, w, bias, state, y, sT, ws)
     if check_status and cu_seqlens is not None:
         _check(dn_device_status(ws), "dn_conv_fwd (device status)")
@@ -276,8 +286,7 @@ def conv_backward(x, w, bias, state, dy, dstate=None, cu_seqlens=None, silu=True
     g = dict(dx=dx, dw=torch.empty_like(w), dbias=None if bias is None else torch.empty_like(bias),
              dstate=None if state is None else torch.empty_like(state))
     shape = conv_shape(x, width, silu, cu_seqlens)
-    if ws is None:
-        ws = _ws("dn_conv_workspace_size", shape, 1, x, cu_seqlens is not None, "dn_conv_bwd")
+    ws = _ws("dn_conv_workspace_size", shape, 1, x, cu_seqlens is not None, "dn_conv_bwd") if ws is None else _buffer(ws, "ws", x)
     dn_conv_bwd(shape, x, w, bias, state, dy, dstate, dx, g["dw"], g["dbias"], g["dstate"], ws)
     if check_status and cu_seqlens is not None:
         _check(dn_device_status(ws), "dn_conv_bwd (device status)")
@@ -415,8 +424,7 @@ def scan_forward(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqle
     y = _result(out, "out", x)
     hT = torch.empty((n,) + tuple(A.shape), dtype=torch.float32, device=x.device) if want_state else None
     shape = scan_shape(x, B, dt_softplus, cu_seqlens)
-    if ws is None:
-        ws = _ws("dn_scan_workspace_size", shape, 0, x, cu_seqlens is not None, "dn_scan_fwd")
+    ws = _ws("dn_scan_workspace_size", shape, 0, x, cu_seqlens is not None, "dn_scan_fwd") if ws is None else _buffer(ws, "ws", x)
     saved = _ws("dn_scan_saved_size", shape, -1, x, cu_seqlens is not None, "dn_scan_fwd") if save else None
     dn_scan_fwd(shape, scan_io(x, dt, A, B, C, D, z, dt_bias, h0, y, hT), saved, ws)
     if check_status and cu_seqlens is not None:
@@ -433,12 +441,12 @@ def scan_backward(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, dy=None
         raise ValueError("scan_backward needs dy and saved (scan_forward(save=True))")
     _tokens(dy, "dy", x.shape, x.dtype)
     _dense(dhT, "dhT", (n,) + tuple(A.shape))
-    _same_device(x, dy, dhT, saved)
+    _same_device(x, dy, dhT)
+    _buffer(saved, "saved", x)
     new = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
     g = dict(dx=new(x), ddt=new(x), dA=new(A), dB=new(B), dC=new(C), dD=new(D), dz=new(z), ddt_bias=new(dt_bias), dh0=new(h0))
     shape = scan_shape(x, B, dt_softplus, cu_seqlens)
-    if ws is None:
-        ws = _ws("dn_scan_workspace_size", shape, 1, x, cu_seqlens is not None, "dn_scan_bwd")
+    ws = _ws("dn_scan_workspace_size", shape, 1, x, cu_seqlens is not None, "dn_scan_bwd") if ws is None else _buffer(ws, "ws", x)
     dn_scan_bwd(shape, scan_io(x, dt, A, B, C, D, z, dt_bias, h0, None, None),
                 scan_grads(dy, g["dx"], g["ddt"], g["dB"], g["dC"], g["dz"], dhT, g["dA"], g["dD"], g["ddt_bias"], g["dh0"]), saved, ws)
     if check_status and cu_seqlens is not None:
@@ -524,7 +532,6 @@ def norm_backward(x, w, dy, z=None, sum=None, dsum=None, res_scale=None, eps=1e-
     g = dict(dx=dres if dx is None else dx, dw=torch.empty_like(w), dz=None if z is None else new(), dresidual=dres,
              dres_scale=None if res_scale is None else torch.empty_like(res_scale))
     shape = norm_shape(x, w, eps)
-    if ws is None:
-        ws = _ws("dn_norm_workspace_size", shape, -1, x, False, "dn_norm_bwd")
+    ws = _ws("dn_norm_workspace_size", shape, -1, x, False, "dn_norm_bwd") if ws is None else _buffer(ws, "ws", x)
     dn_norm_bwd(shape, x, w, z, res_scale, sum, dy, dsum, dx, g["dw"], g["dz"], dres, g["dres_scale"], ws)
     return g

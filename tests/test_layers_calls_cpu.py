@@ -31,3 +31,9 @@ def test_conv_step_records_step_from_sequence_to_sequence(lay, n, C, wide):
         (px, bx, _, _), (py, by, _, _) = layers._VIEW.unpack(got[1]), layers._VIEW.unpack(got[6])
         assert (px, bx) == (x.data_ptr(), wide) and (py, by) == (y.data_ptr(), C)
         assert got[0] == shape and got[2:6] == (w.data_ptr(), bias.data_ptr(), state.data_ptr(), state.data_ptr())
+
+
+def test_buffers_are_cuda_tensors():
+    from chunkwise_delta_rule_02_gb300 import layers
+    with pytest.raises(TypeError):
+        layers._buffer(torch.zeros(256, dtype=torch.uint8), "ws", torch.zeros(1))
