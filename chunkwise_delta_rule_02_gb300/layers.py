@@ -13,6 +13,10 @@ slices and transposed views of a projection go in, and come out (``out=``), with
 a copy.  They are float32 or bfloat16, all of one type in a call; parameters (weights,
 A, D, biases), scan states and their gradients are float32.
 
+A result must not overlap an input or another result (a single token's new state may be the
+old one).  ``conv_forward`` and ``conv_backward``, whose neighbouring tokens would read what
+was written over them, refuse an ``out`` that does; the other calls do not look.
+
 Packed sequences: B = 1 and ``cu_seqlens``, int32 offsets on the device, as in
 ``binding.forward``.  The kernels check the offsets; with ``check_status`` (the
 default) a packed call reads the status word afterwards, which waits for the
@@ -114,6 +118,45 @@ def _result(t: Optional[torch.Tensor], name: str, like: torch.Tensor) -> torch.T
     if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
         raise ValueError("%s must not repeat memory along an axis (stride 0)" % name)
     return t
+
+
+def _meet(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two tensors of one type share an element: whether some offset into a minus some offset into b is the
+    distance of their first elements.  Axes are tried from the longest stride on, each only over the steps that the
+    shorter ones can still make up for; False where that is not decided within 1000 steps (layouts that interleave oddly)."""
+    if not a.numel() or not b.numel():
+        return False
+    span = {}                                # stride -> fewest and most steps of it
+    for t, sign in ((a, 1), (b, -1)):
+        for n, st in zip(t.shape, t.stride()):
+            if n > 1 and st:
+                lo, hi = span.get(st, (0, 0))
+                span[st] = (lo, hi + n - 1) if sign > 0 else (lo - n + 1, hi)
+    axes = sorted(span.items(), reverse=True)
+    left = [(0, 0)]                          # least and greatest sum of the axes behind each one
+    for st, (lo, hi) in reversed(axes):
+        left.append((left[-1][0] + lo * st, left[-1][1] + hi * st))
+    left.reverse()
+    todo, tries = [(0, (b.data_ptr() - a.data_ptr()) // a.element_size())], 0
+    while todo and tries < 1000:
+        i, d = todo.pop()
+        tries += 1
+        if not left[i][0] <= d <= left[i][1]:
+            continue
+        if i == len(axes):
+            return True
+        st, (lo, hi) = axes[i]
+        lo, hi = max(lo, -((left[i + 1][1] - d) // st)), min(hi, (d - left[i + 1][0]) // st)
+        todo.extend((i + 1, d - k * st) for k in range(lo, min(hi, lo + 1000) + 1))
+    return False
+
+
+def _apart(t: Optional[torch.Tensor], name: str, **inputs):
+    """Refuses a caller's result (None: none given) that shares memory with an input."""
+    if t is not None:
+        for n, other in inputs.items():
+            if other is not None and _meet(t, other):
+                raise ValueError("%s must not overlap %s" % (name, n))
 
 
 def _same_device(first: torch.Tensor, *rest):
@@ -263,9 +306,10 @@ def conv_forward(x, w, bias=None, state=None, cu_seqlens=None, silu=True, out=No
     """Short causal convolution.  x [B,H,T,d] or [B,T,C] (any strides, contiguous features),
     w [C,width] and bias [C] float32 with C = H d, width 2..4; state [N,width-1,C] in x's dtype:
     the inputs before each sequence (None: zero).  Returns (y, final state or None); y is a new
-    contiguous tensor of x's shape, or ``out``."""
+    contiguous tensor of x's shape, or ``out``, which must not overlap x or state."""
     n, width = _conv_args(x, w, bias, state, cu_seqlens)
     y = _result(out, "out", x)
+    _apart(out, "out", x=x, state=state)
     sT = torch.empty((n, width - 1, w.shape[0]), dtype=x.dtype, device=x.device) if want_state else None
     shape = conv_shape(x, width, silu, cu_seqlens)
     ws = _ws("dn_conv_workspace_size", shape, 0, x, cu_seqlens is not None, "dn_conv_fwd") if ws is None else _buffer(ws, "ws", x)
@@ -276,13 +320,14 @@ def conv_forward(x, w, bias=None, state=None, cu_seqlens=None, silu=True, out=No
 
 
 def conv_backward(x, w, bias, state, dy, dstate=None, cu_seqlens=None, silu=True, out=None, ws=None, check_status=True):
-    """Gradients of <y, dy> + <final state, dstate>: dict dx (x's shape; contiguous, or ``out``), dw, dbias
-    (None without bias), dstate (of the initial state, None without one)."""
+    """Gradients of <y, dy> + <final state, dstate>: dict dx (x's shape; contiguous, or ``out``, which must
+    not overlap x, dy or a state), dw, dbias (None without bias), dstate (of the initial state, None without one)."""
     n, width = _conv_args(x, w, bias, state, cu_seqlens)
     _tokens(dy, "dy", x.shape, x.dtype)
     _dense(dstate, "dstate", (n, width - 1, w.shape[0]), x.dtype)
     _same_device(x, dy, dstate)
     dx = _result(out, "out", x)
+    _apart(out, "out", x=x, dy=dy, state=state, dstate=dstate)
     g = dict(dx=dx, dw=torch.empty_like(w), dbias=None if bias is None else torch.empty_like(bias),
              dstate=None if state is None else torch.empty_like(state))
     shape = conv_shape(x, width, silu, cu_seqlens)

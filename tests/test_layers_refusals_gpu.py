@@ -45,3 +45,34 @@ def test_buffers_of_the_caller(gdn, i):
         call(room[:64])
     with pytest.raises(gdn.GdnError):
         call(room[4:])                       # not 16-byte aligned
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_convolution_results_over_its_inputs(gdn, dtype):
+    """Tokens would be read after they were written over: refused.  Another slice of the same projection is not."""
+    B, H, T, d = 2, 3, 50, 16
+    C = H * d
+    wide = torch.randn(B, T, 3 * C, device=DEV).to(dtype)
+    x, z, rest = wide.split(C, -1)
+    w, state = torch.randn(C, 4, device=DEV), torch.zeros(B, 3, C, dtype=dtype, device=DEV)
+    dy = torch.randn(B, T, C, device=DEV).to(dtype)
+    by_head = lambda t: t.unflatten(-1, (H, d)).transpose(1, 2)  # noqa: E731
+    for out in (x, wide[..., 8:8 + C], wide[:, :, C - 1:2 * C - 1]):
+        with pytest.raises(ValueError):
+            gdn.conv_forward(x, w, out=out)
+        with pytest.raises(ValueError):
+            gdn.conv_forward(by_head(x), w, out=by_head(out))
+        with pytest.raises(ValueError):
+            gdn.conv_backward(dy, w, None, None, x, out=out)
+        with pytest.raises(ValueError):
+            gdn.conv_backward(x, w, None, None, dy, out=out)
+    with pytest.raises(ValueError):
+        gdn.conv_forward(x[:, :3], w, state=state, out=state)
+    with pytest.raises(ValueError):
+        gdn.conv_backward(x[:, :3], w, None, state, dy[:, :3], state, out=state)
+    with pytest.raises(ValueError):
+        gdn.conv_backward(x[:, :3], w, None, None, dy[:, :3], state, out=state)
+    want, _ = gdn.conv_forward(x, w)
+    grad = gdn.conv_backward(x, w, None, None, dy)["dx"]
+    assert torch.equal(gdn.conv_forward(x, w, out=z)[0], want) and torch.equal(z, want)
+    assert torch.equal(gdn.conv_backward(x, w, None, None, dy, out=rest)["dx"], grad) and torch.equal(rest, grad)
