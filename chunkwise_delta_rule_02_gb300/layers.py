@@ -201,7 +201,7 @@ def _cu(cu_seqlens, B):
     """(pointer, num_seqs) of packed offsets."""
     if cu_seqlens is None:
         return 0, 0
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise TypeError("cu_seqlens must be a one-dimensional int32 tensor of at least one offset")
     if not cu_seqlens.is_cuda or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be a contiguous CUDA tensor")
@@ -285,17 +285,21 @@ def dn_conv_step(shape, x, w, bias, state_in, state_out, y, stream=None):
                              _stream(stream)), "dn_conv_step")
 
 
+def _width(w) -> int:
+    if w.dim() != 2 or w.shape[1] < 1:
+        raise ValueError("w must be [channels, width]")
+    return w.shape[1]
+
+
 def _conv_args(x, w, bias, state, cu_seqlens):
     if x.dim() not in (3, 4):
         raise ValueError("x must be [B,H,T,d] or [B,T,C], got %d axes" % x.dim())
     B, H, T, d = _dims(x)
     _tokens(x, "x", x.shape, x.dtype)
-    if w.dim() != 2:
-        raise ValueError("w must be [channels, width]")
-    width = w.shape[1]
+    width = _width(w)
     _dense(w, "w", (H * d, width))
     _dense(bias, "bias", (H * d,))
-    n = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    n = B if cu_seqlens is None else _cu(cu_seqlens, B)[1]
     _dense(state, "state", (n, width - 1, H * d), x.dtype)
     _same_device(x, w, bias, state, cu_seqlens)
     return n, width
@@ -345,7 +349,7 @@ def conv_step(x, w, bias=None, state=None, out_state=None, silu=True, out=None):
         raise ValueError("x must be [N,C], got %d axes" % x.dim())
     N, C = x.shape
     _tokens(x, "x", x.shape, x.dtype)
-    width = w.shape[1]
+    width = _width(w)
     _dense(w, "w", (C, width))
     _dense(bias, "bias", (C,))
     sshape = (N, width - 1, C)
@@ -452,7 +456,7 @@ def _scan_args(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, axes):
     _dense(A, "A", (Dc, N))
     _dense(D, "D", (Dc,))
     _dense(dt_bias, "dt_bias", (Dc,))
-    n = xs[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+    n = xs[0] if cu_seqlens is None else _cu(cu_seqlens, xs[0])[1]
     _dense(h0, "h0", (n, Dc, N))
     _same_device(x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens)
     return n

@@ -76,3 +76,18 @@ def test_convolution_results_over_its_inputs(gdn, dtype):
     grad = gdn.conv_backward(x, w, None, None, dy)["dx"]
     assert torch.equal(gdn.conv_forward(x, w, out=z)[0], want) and torch.equal(z, want)
     assert torch.equal(gdn.conv_backward(x, w, None, None, dy, out=rest)["dx"], grad) and torch.equal(rest, grad)
+
+
+def test_malformed_arguments_raise_the_documented_errors(gdn):
+    x, w = torch.ones(1, 20, 16, device=DEV), torch.ones(16, 4, device=DEV)
+    A, B = -torch.ones(16, 4, device=DEV), torch.ones(1, 20, 4, device=DEV)
+    empty = torch.zeros(0, dtype=torch.int32, device=DEV)
+    for f, e in ((lambda: gdn.conv_step(x[0], w[:, 0]), ValueError), (lambda: gdn.conv_step(x[0], w[:, :0]), ValueError),
+                 (lambda: gdn.conv_forward(x, w[:, :0]), ValueError), (lambda: gdn.conv_forward(x, w[:, 0]), ValueError),
+                 (lambda: gdn.conv_forward(x, w, cu_seqlens=empty), TypeError),
+                 (lambda: gdn.conv_forward(x, w, cu_seqlens=[0, 20]), TypeError),
+                 (lambda: gdn.conv_backward(x, w, None, None, x, cu_seqlens=empty), TypeError),
+                 (lambda: gdn.scan_forward(x, x, A, B, B, cu_seqlens=empty), TypeError),
+                 (lambda: gdn.scan_forward(x, x, A, B, B, cu_seqlens=(0, 20)), TypeError)):
+        with pytest.raises(e):
+            f()
