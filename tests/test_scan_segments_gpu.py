@@ -1,13 +1,14 @@
 """GPU tests of the selective state space scan over several time segments: what is not finite stays in its
-sequence and goes through the segments as through one recurrence."""
+sequence and goes through the segments as through one recurrence; every layout of states over lanes, dense and
+packed.  Bounds as in test_scan_gpu: the inputs are made alike, with memories of the same length."""
 import pytest
 import torch
 
 import layers_ref as ref
+from test_scan_gpu import BF, F32, TOL, close, make
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
-F32 = torch.float32
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -27,8 +28,11 @@ def segmented(x, Bm):
     segments' states (the backward's beside dB's and dC's partial results and one row of sums over tokens)."""
     from chunkwise_delta_rule_02_gb300 import layers
     shape = layers.scan_shape(x, Bm)
-    T, D, Np = x.shape[1], x.shape[2], max(8, 1 << (Bm.shape[-1] - 1).bit_length())
-    uncut = 4 * (2 * T * Np + D * Np + 2 * D) + 4 * 256
+    T, D, G, N = x.shape[1], x.shape[2], Bm.shape[2], Bm.shape[3]
+    Np = max(8, 1 << (N - 1).bit_length())
+    CH = 64 if N <= 16 else 32 if N <= 32 else 8            # channels of a block
+    tiles = G * -(-(D // G) // CH)
+    uncut = 4 * (tiles * T * 2 * Np + D * Np + 2 * D) + 4 * 256
     return layers.dn_scan_workspace_size(shape) > 256 and layers.dn_scan_workspace_size(shape, True) > uncut
 
 
@@ -97,3 +101,38 @@ def test_a_gradient_that_is_not_finite_reaches_the_start_of_its_sequence(gdn, pa
     assert torch.equal(got["dh0"][others], clean["dh0"][others])
     assert not torch.isfinite(got["dB"][0, first:1401]).any()
     assert torch.equal(got["dB"][0, :first], clean["dB"][0, :first]) and torch.equal(got["dB"][0, 1401:], clean["dB"][0, 1401:])
+
+
+LAYOUTS = [  # D, N, G, dtype, T, lengths
+    (100, 8, 1, F32, 400, None),
+    (100, 8, 1, F32, 400, [150, 0, 1, 249]),
+    (140, 16, 2, BF, 400, [63, 1, 0, 336]),
+    (16, 32, 2, F32, 400, None),
+    (80, 32, 2, F32, 400, [150, 0, 1, 249]),
+    (70, 30, 1, BF, 400, [17, 383]),
+    (20, 64, 1, F32, 300, None),
+    (20, 64, 1, F32, 300, [150, 0, 1, 149]),
+    (18, 33, 2, BF, 300, [0, 128, 172]),
+    (12, 100, 1, F32, 300, None),
+    (12, 100, 1, F32, 300, [150, 0, 1, 149]),
+    (24, 128, 3, BF, 300, [1, 1, 298, 0]),
+]
+
+
+@pytest.mark.parametrize("c", LAYOUTS)
+def test_every_layout_over_segments(gdn, c):
+    """Forward and backward with initial states and gradients of the final ones."""
+    D, N, G, dtype, T, lens = c
+    k, cu, _, dy, dhT = make((1, T, D, N, G, dtype, True, True, True, True, True, lens), 5)
+    assert segmented(k["x"], k["B"])
+    y, hT, saved = gdn.scan_forward(**k, cu_seqlens=cu, save=True)
+    g = gdn.scan_backward(**k, dy=dy, dhT=dhT, saved=saved, cu_seqlens=cu)
+    v = {n: ref.leaf(t) for n, t in k.items()}
+    outs = ref.scan(v["x"], v["dt"], v["A"], v["B"], v["C"], v["D"], v["z"], v["dt_bias"], v["h0"], cu=cu)
+    close(y, outs[0])
+    close(hT, outs[1])
+    want = dict(zip(k, ref.grads(outs, (ref.d64(dy), ref.d64(dhT)), list(v.values()))))
+    for n in k:
+        got = g["d" + n]
+        # sums over tokens and channels of terms of both signs: what they cancel stays as error
+        assert ref.err(got, want[n]) <= (4 if n in ("A", "dt_bias", "dt", "h0") and got.dtype == F32 else 1) * TOL[got.dtype], n
