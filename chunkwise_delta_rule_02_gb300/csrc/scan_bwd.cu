@@ -103,7 +103,6 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
     const bool gated = io.z.p != nullptr;
 
     float2 a2[CT][P], dh[CT][P], dA[CT][P];
-    bool cut = false;   // SUM: a sequence starts in the segment
     float Dc[CT], aD[CT], aBias[CT], rD[CT], rBias[CT], total[CT];
 #pragma unroll
     for (int e = 0; e < CT; ++e) {
@@ -262,7 +261,6 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
                 }
                 if constexpr (decltype(edges)::value) {
                     if (starts >> t & 1) {
-                        cut = true;
 #pragma unroll
                         for (int e = 0; e < CT; ++e) {
                             total[e] = 0.f;
@@ -457,6 +455,7 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
         }
     }
     if constexpr (SUM) {
+        const bool cut = starts_in(g, ts, te);
 #pragma unroll
         for (int e = 0; e < CT; ++e) {
             if (!live[e]) continue;

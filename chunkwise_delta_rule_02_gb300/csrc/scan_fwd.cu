@@ -57,7 +57,6 @@ __global__ void __launch_bounds__(Cfg::NT) k_scan_fwd(ScanDims g, ScanIo<T> io)
     float total[CT];   // SUM: of delta since the last sequence start
 
     float2 a2[CT][P], h[CT][P];
-    bool cut = false;  // SUM: a sequence starts in the segment
 #pragma unroll
     for (int e = 0; e < CT; ++e) {
         load_states<S>(a2[e], g.A + (c + e) * g.N, n0, g.N, live[e]);
@@ -219,7 +218,6 @@ __global__ void __launch_bounds__(Cfg::NT) k_scan_fwd(ScanDims g, ScanIo<T> io)
                         if constexpr (EDGES) {
                             if (starts >> t & 1) {
                                 load_states<S>(h[e], g.h0 + ((size_t)seq[t] * g.D + c + e) * g.N, n0, g.N, live[e] && g.h0);
-                                cut = true;
                                 total[e] = 0.f;
                             }
                         }
@@ -279,6 +277,7 @@ __global__ void __launch_bounds__(Cfg::NT) k_scan_fwd(ScanDims g, ScanIo<T> io)
         }
     }
     if constexpr (SUM) {
+        const bool cut = starts_in(g, ts, te);
 #pragma unroll
         for (int e = 0; e < CT; ++e) {
             if (!live[e]) continue;
