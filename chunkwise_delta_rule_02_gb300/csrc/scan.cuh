@@ -174,14 +174,6 @@ __device__ __forceinline__ void tile_edges(const ScanDims &g, int b, int t0, int
     }
 }
 
-// Whether a sequence starts among a segment's tokens ts .. te-1: the one that holds the last of them, then.
-__device__ __forceinline__ bool starts_in(const ScanDims &g, int ts, int te)
-{
-    if (!g.cu) return ts == 0;
-    const int s = seq_at(g.cu, g.Nseq, te - 1);
-    return s < g.Nseq && g.cu[s] >= ts;
-}
-
 // Time segments of a pass whose blocks are `tiles` a segment: the K that leaves the busiest SM
 // the least to do.  An SM runs R blocks at once at full speed and n < R of them at
 // 0.6 + 0.4 n / R of it; the first pass (all but one segment, R1 at once) does w1 of the main

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
     const int ts = k * g.seg, te = min(ts + g.seg, g.T);
     const bool gated = io.z.p != nullptr;
 
-    float2 a2[CT][P], dh[CT][P], dA[CT][P];
+    float2 a2[CT][P], dh[CT][P], dA[CT][P], open[CT];   // open: 1, 0 before a sequence start
     float Dc[CT], aD[CT], aBias[CT], rD[CT], rBias[CT], total[CT];
 #pragma unroll
     for (int e = 0; e < CT; ++e) {
@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
             a2[e][i] = mul2(a2[e][i], two(kLog2e));
             dh[e][i] = dA[e][i] = two(0.f);
         }
+        open[e] = two(1.f);
         Dc[e] = !SUM && g.Dskip && live[e] ? g.Dskip[c + e] : 0.f;
         aD[e] = aBias[e] = rD[e] = rBias[e] = total[e] = 0.f;
         // what the segments behind this one send back
@@ -263,6 +264,7 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
                     if (starts >> t & 1) {
 #pragma unroll
                         for (int e = 0; e < CT; ++e) {
+                            open[e] = two(0.f);
                             total[e] = 0.f;
 #pragma unroll
                             for (int i = 0; i < P; ++i) dh[e][i] = two(0.f);
@@ -455,14 +457,13 @@ __global__ void __launch_bounds__(Cfg::NT, SUM ? 4 : 2) k_scan_bwd(ScanDims g, B
         }
     }
     if constexpr (SUM) {
-        const bool cut = starts_in(g, ts, te);
 #pragma unroll
         for (int e = 0; e < CT; ++e) {
             if (!live[e]) continue;
             const size_t at = (((size_t)b * g.K + k) * g.D + c + e) * Np + n0;
             float2 p[P];
 #pragma unroll
-            for (int i = 0; i < P; ++i) p[i] = cut ? two(kCut) : ex2_2(mul2(two(total[e]), a2[e][i]));
+            for (int i = 0; i < P; ++i) p[i] = open[e].x == 0.f ? two(kCut) : ex2_2(mul2(two(total[e]), a2[e][i]));
             store_pairs<S>(io.segP + at, p);
             store_pairs<S>(io.segH + at, dh[e]);
         }

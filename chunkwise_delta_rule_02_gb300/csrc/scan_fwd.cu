@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(Cfg::NT) k_scan_fwd(ScanDims g, ScanIo<T> io)
     const int ts = k * g.seg, te = min(ts + g.seg, g.T);
     float total[CT];   // SUM: of delta since the last sequence start
 
-    float2 a2[CT][P], h[CT][P];
+    float2 a2[CT][P], h[CT][P], open[CT];   // open: 1, 0 after a sequence start
 #pragma unroll
     for (int e = 0; e < CT; ++e) {
         load_states<S>(a2[e], g.A + (c + e) * g.N, n0, g.N, live[e]);
@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(Cfg::NT) k_scan_fwd(ScanDims g, ScanIo<T> io)
             a2[e][i] = mul2(a2[e][i], two(kLog2e));
             h[e][i] = two(0.f);
         }
+        open[e] = two(1.f);
         total[e] = 0.f;
         if constexpr (!SUM) {
             if (k > 0 && live[e]) load_pairs<S>(h[e], io.segH + (((size_t)b * g.K + k) * g.D + c + e) * Np + n0);
@@ -218,6 +219,7 @@ __global__ void __launch_bounds__(Cfg::NT) k_scan_fwd(ScanDims g, ScanIo<T> io)
                         if constexpr (EDGES) {
                             if (starts >> t & 1) {
                                 load_states<S>(h[e], g.h0 + ((size_t)seq[t] * g.D + c + e) * g.N, n0, g.N, live[e] && g.h0);
+                                open[e] = two(0.f);
                                 total[e] = 0.f;
                             }
                         }
@@ -277,7 +279,6 @@ __global__ void __launch_bounds__(Cfg::NT) k_scan_fwd(ScanDims g, ScanIo<T> io)
         }
     }
     if constexpr (SUM) {
-        const bool cut = starts_in(g, ts, te);
 #pragma unroll
         for (int e = 0; e < CT; ++e) {
             if (!live[e]) continue;
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(Cfg::NT) k_scan_fwd(ScanDims g, ScanIo<T> io)
             // the product of the decays is one exponential of the steps' sum
             float2 p[P];
 #pragma unroll
-            for (int i = 0; i < P; ++i) p[i] = cut ? two(kCut) : ex2_2(mul2(two(total[e]), a2[e][i]));
+            for (int i = 0; i < P; ++i) p[i] = open[e].x == 0.f ? two(kCut) : ex2_2(mul2(two(total[e]), a2[e][i]));
             store_pairs<S>(io.segP + at, p);
             store_pairs<S>(io.segH + at, h[e]);
         }
