@@ -570,7 +570,8 @@ def norm_forward(x, w, z=None, residual=None, res_scale=None, eps=1e-6, out=None
 def norm_backward(x, w, dy, z=None, sum=None, dsum=None, res_scale=None, eps=1e-6, ws=None):
     """Gradients of <y, dy> + <r, dsum>.  Without a residual r = x; with one pass ``sum`` = r as norm_forward
     returned it, and x.  Returns dict dx, dw, dz (with z), dresidual (with sum), dres_scale (with
-    res_scale); the others are None."""
+    res_scale); the others are None.  Without res_scale the gradients of x and of the residual are equal, and
+    dx and dresidual are one tensor: clone one before changing either in place."""
     _norm_args(x, w, res_scale, dy=dy, z=z, sum=sum, dsum=dsum)
     if sum is None and (res_scale is not None or dsum is not None):
         raise ValueError("res_scale and dsum need sum (the residual sum of the forward pass)")

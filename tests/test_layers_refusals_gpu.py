@@ -91,3 +91,12 @@ def test_malformed_arguments_raise_the_documented_errors(gdn):
                  (lambda: gdn.scan_forward(x, x, A, B, B, cu_seqlens=(0, 20)), TypeError)):
         with pytest.raises(e):
             f()
+
+
+def test_residual_gradients_without_a_scale_are_one_tensor(gdn):
+    """As documented: equal gradients under two names; with a scale, two tensors."""
+    x, w, dy = (torch.randn(3, 5, 32, device=DEV) for _ in range(3))
+    g = gdn.norm_backward(x, w[0, 0], dy, sum=x)
+    assert g["dx"] is g["dresidual"]
+    g = gdn.norm_backward(x, w[0, 0], dy, sum=x, res_scale=torch.full((32,), 2.0, device=DEV))
+    assert g["dx"].data_ptr() != g["dresidual"].data_ptr() and torch.equal(g["dx"], 2 * g["dresidual"])
