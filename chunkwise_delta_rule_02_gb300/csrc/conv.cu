@@ -9,7 +9,10 @@
 // one element) and walks a run of tokens with the last W inputs in registers, so
 // that an input is read once plus W - 1 halo tokens a run; a warp covers 32
 // neighbouring vectors of one token.  Measured: forward 4.9 TB/s (72 % of a copy),
-// backward 4.05 TB/s (60 %): 25 instructions an element stand against it there.
+// backward 4.05 TB/s (60 %).  What stands against more is latency: a thread loads 8 tokens,
+// then computes them with nothing in flight, and registers allow three blocks (backward
+// two) an SM.  Issue slots are 43 % (42 %) used, by 11 (20) instructions an element, the
+// DRAM 57 % (54 %), and a warp waits for its loads most of the time.
 #include "layers.h"
 
 namespace gdn {
@@ -20,7 +23,7 @@ namespace {
 constexpr int kTX = 32, kTY = 8;     // threads: channel vectors x runs
 
 // Vectors of 8 bytes, and 8 tokens' loads in flight, measured at 4 x 8192 (forward) and
-// 8 x 4096 tokens (backward) of 2048 bf16 channels: forward 59 us (16-byte vectors: 63 us with
+// 8 x 4096 tokens (backward) of 2048 bf16 channels: forward 59 us then, 55 now (16-byte vectors: 63 us with
 // twice the registers, 4 tokens in flight 69 us), backward 99 us (16 bytes: 190 us; 4 tokens 119 us).
 constexpr int kBytes = 8, kInFlight = 8;
 
@@ -450,8 +453,8 @@ __global__ void __launch_bounds__(128) k_conv_step(int N, int C, int d, int silu
 
 // Tokens of a run: the longest power of two (forward 16..64, backward 16..512) that leaves
 // the SMs enough blocks, for 8-byte vectors.  A longer run reads its W - 1 halo tokens and, in
-// the backward, writes its partial sums less often; 4 blocks an SM forward, 3/2 backward (two
-// fit one: 256 tokens at 8 x 4096 x 2048 99 us, 128 tokens 105 us, 64 tokens 108 us).
+// the backward, writes its partial sums less often; 4 blocks an SM forward (three run at once),
+// 3/2 backward (two run at once: 256 tokens at 8 x 4096 x 2048 99 us, 128 tokens 105 us, 64 tokens 108 us).
 int run_of(const dn_conv_shape *s, bool bwd)
 {
     const long long vec = kBytes / (s->dtype == DN_F32 ? 4 : 2), need = (bwd ? 3ll : 8ll) * sm_count() / 2;

@@ -8,10 +8,11 @@
 // Bound by HBM: every operand is read once and every result written once, in one
 // pass; a row stays in registers between its loads and its results.  R threads
 // share a row: part of a warp (sums by shuffles, several rows a warp) while a
-// thread then holds at most kSmall vectors, else one block.  mean r^2 and
+// thread then holds at most 4 vectors, else one block.  mean r^2 and
 // mean(g r) come out of one reduction.  Both sums, and the row, are float32.
 // Measured, gate and rows of 128 bf16: forward 5.6 TB/s (83 % of a copy), backward
-// 4.9 TB/s (72 %).
+// 4.8 TB/s (71 %).  Residual, rows of 2048 bf16: forward 107 us for 8 x 4096 rows (74 %),
+// backward 402 us (30 %), which spills: see k_norm_bwd.
 #include "layers.h"
 
 namespace gdn {
@@ -21,7 +22,8 @@ namespace {
 
 constexpr int kThreads = 256;
 // Most blocks an SM of a pass: the backward's write partial sums, so that they are as many as
-// run together (3; 4 were 162 us, 6 141 us, 3 138 us at 8 x 16 x 4096 x 128); the forward's are
+// run together (3; 4 were 162 us, 6 141 us, 3 138 us at 8 x 16 x 4096 x 128 with the gate, the only
+// instance that the number and the register bound were measured on); the forward's are
 // four rounds of six (24: 72 us; 12: 76 us; 48: 74 us at 4 x 16 x 8192 x 128).
 constexpr long long kFwdBlocks = 24, kBwdBlocks = 3;
 
@@ -215,6 +217,11 @@ struct NormGrad {
 };
 
 // RES: r is read from `sum`, x only for ds; else r = x.
+// The bounds leave 80 registers (64 for a block a row).  Instances without a residual and with one vector a
+// thread fit them or nearly; those with a residual, whose sums of dw and ds and five operands are all in
+// registers, spill: 120 to 1400 bytes of stack with 8 bf16 an access, up to 600 with 4 float32.  Residual backward
+// of 8 x 4096 rows: 477, 402, 948 us for 1024, 2048, 4096 bf16 features (bytes: 59, 119, 237 us), 161, 342, 659 us
+// for float32 (119, 237, 475 us).
 template <class T, int V, int NV, bool WIDE, bool GATE, bool RES>
 __global__ void __launch_bounds__(WIDE ? 1024 : kThreads, WIDE ? 1 : 3)
     k_norm_bwd(NormDims g, View<const T> x, View<const T> z, View<const T> sum, View<const T> dy, View<const T> dsum,

@@ -178,8 +178,9 @@ __device__ __forceinline__ void tile_edges(const ScanDims &g, int b, int t0, int
 // the least to do.  An SM runs R blocks at once at full speed and n < R of them at
 // 0.6 + 0.4 n / R of it; the first pass (all but one segment, R1 at once) does w1 of the main
 // pass's work a token; a block's start costs as much as 8 tokens.  K = 1 has no first pass.
-// At 4 x 8192 tokens of 2048 channels (64 tiles) this says 6931, 5909, 6024, 5683, 5609, 5837 (in
-// tokens) for K = 4, 7, 9, 14, 19, 28, and the forward pass took 699, 598, 610, 579, 569, 583 us.
+// At 4 x 8192 tokens of 2048 channels (128 tiles) this says 11714, 12850, 12039, 11283, 11500, 11289,
+// 11426, 11514 (in tokens) for K = 1, 4, 7, 8, 9, 14, 19, 28, and the forward pass took 681, 644, 595, 560, 564,
+// 553, 553, 552 us: ratios within 8 % from 3 segments on (12, 16 and 24 are the worst), the uncut pass 15 % too cheap.
 inline int plan_segments(long long tiles, int T, int R, int R1, double w1)
 {
     if (T <= 0) return 1;   // no tokens: nothing to cut (and no length to divide by)

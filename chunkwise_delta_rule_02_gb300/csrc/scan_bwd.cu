@@ -525,7 +525,10 @@ Plan plan_of(const dn_scan_shape *s)
     bwd_layout(s->N, [&](auto cfg) { CH = decltype(cfg)::CH; return cudaSuccess; });
     const int Dg = s->D / s->G, Np = scan_padded(s->N);
     p.tiles = (Dg + CH - 1) / CH;
-    // two blocks of the main pass fit an SM, four of the first, which does a fifth of the work
+    // Counted as two blocks of the main pass an SM and four of the first, which does a fifth of the work.
+    // That is what their registers allow; shared memory, of which the first pass is given as much as the
+    // main one, allows three of either up to 8 states, two up to 64 and one above.  With these counts the same
+    // model would take 19 segments instead of 38 for one row of 16384 tokens and 1024 channels of 16 states
     const int k = plan_segments((long long)s->B * s->G * p.tiles, s->T, 2, 4, 0.2);
     p.seg = (int)((((long long)s->T + k - 1) / k + 15) / 16 * 16);   // whole tiles, whole spans between kept states
     p.K = p.seg > 0 ? (s->T + p.seg - 1) / p.seg : 1;

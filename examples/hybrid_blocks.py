@@ -4,8 +4,8 @@ space blocks, trained on a synthetic copy task and then decoded token by token.
 Each block is a residual norm (the sum of the stream and the block before it, its scale and the norm in one
 pass), projections, short causal convolutions, the delta rule or the scan, a gated norm (delta rule) or the
 scan's own gate, and an output projection.  The convolutions read the token-major projections and write what
-the delta rule reads; the gated norm reads that layout and writes the projection's: no transposition or copy
-in between.  Decoding keeps, per block, the last taps of the convolutions and the recurrent states.
+the delta rule reads; the gated norm reads that layout and writes the projection's: the forward pass has no
+transposition or copy in between (gradients come back in the axes' order, contiguous).  Decoding keeps, per block, the last taps of the convolutions and the recurrent states.
 
     python examples/hybrid_blocks.py
 """

@@ -9,8 +9,11 @@
  * token-major [B][T][H*d], the delta rule's head-major [B][H][T][d] and a slice of
  * a wider projection are all read and written in place.  A view may have any
  * strides (0 in an input repeats it along that axis); outputs must not overlap
- * each other or the inputs.  Where a view is 16-byte aligned (pointer and
- * strides) the kernels move 16 bytes an access, else one element.
+ * each other or the inputs.  Vector accesses need every view of the call aligned to
+ * them (pointer and strides), else the kernels move one element at a time; 16-byte
+ * alignment is always enough.  The norm and the single-token convolution move 16
+ * bytes an access, the convolution over tokens 8, the scan 4 elements (one above
+ * 32 states, and of x, dt, z and y for single tokens).
  *
  * Dtypes: shape->dtype (DN_F32 or DN_BF16) is that of every token array and of the
  * convolution's taps; parameters (weights, A, D, biases), scan states and their
