@@ -13,6 +13,6 @@ from .binding import (  # noqa: F401
     make_shape, saved_supported,
 )
 from .layers import (  # noqa: F401
-    conv_backward, conv_forward, conv_step, norm_backward, norm_forward, scan_backward, scan_forward,
-    scan_step,
+    conv_backward, conv_forward, conv_step, dropout_backward, dropout_forward, norm_backward, norm_forward,
+    recur_backward, recur_forward, recur_step, scan_backward, scan_forward, scan_step,
 )

@@ -34,5 +34,12 @@ long long norm_part_rows(const dn_norm_shape *s);
 cudaError_t norm_fwd(const NormCall &c, cudaStream_t st);
 cudaError_t norm_bwd(const NormCall &c, cudaStream_t st);
 
+struct DropCall {
+    const dn_dropout_shape *s;
+    const dn_view *x, *residual, *y;
+    const int64_t *rng;
+};
+cudaError_t dropout(const DropCall &c, cudaStream_t st);
+
 }  // namespace lay
 }  // namespace gdn

@@ -5,6 +5,7 @@
 #include <atomic>
 
 #include "layers.h"
+#include "recur.cuh"
 #include "scan.cuh"
 
 namespace gdn {
@@ -207,6 +208,67 @@ dn_status scan_begin(ScanCall &c, const dn_scan_shape *s, const dn_scan_io *io, 
     return DN_OK;
 }
 
+// ------------------------------------------------------------------ gated linear recurrence
+dn_status recur_shape_ok(const dn_recur_shape *s)
+{
+    if (!s || s->B < 1 || s->T < 0 || s->D < 1) return DN_ERR_INVALID_ARG;
+    if (s->dtype != DN_F32 && s->dtype != DN_BF16) return DN_ERR_INVALID_ARG;
+    if (!(s->c >= 0.f && s->c <= 1e30f)) return DN_ERR_INVALID_ARG;
+    if (s->D > (1 << 24) || s->T > kMaxT || (double)s->B * ((s->D + kChans - 1) / kChans) > (1 << 27)) return DN_ERR_UNSUPPORTED;
+    return check_packed(s->cu_seqlens, s->B, s->num_seqs);
+}
+
+struct RecurWs {
+    size_t cu, part, total;
+};
+
+RecurWs recur_ws(const dn_recur_shape *s, bool bwd)
+{
+    RecurWs w;
+    w.cu = 256;
+    w.part = w.cu + (s->cu_seqlens ? align256(sizeof(int32_t) * ((size_t)s->num_seqs + 1)) : 0);
+    w.total = w.part + (bwd ? align256(sizeof(float) * 3 * (size_t)s->B * recur_cluster(s, true) * s->D) : 0);
+    return w;
+}
+
+size_t recur_saved(const dn_recur_shape *s)
+{
+    const size_t n = (size_t)s->B * ((s->T + kRun - 1) / kRun) * s->D * sizeof(float);
+    return n ? n : 256;
+}
+
+dn_status recur_io_ok(const dn_recur_shape *s, const dn_recur_io *io, bool need_y)
+{
+    if (!io || !io->lam) return DN_ERR_INVALID_ARG;
+    const size_t e = s->dtype == DN_F32 ? 4 : 2;
+    const float *params[] = {io->lam, io->rg_bias, io->ig_bias, io->h0, io->hT};
+    for (const float *p : params)
+        if (!aligned(p, 4)) return DN_ERR_INVALID_ARG;
+    if (s->T > 0 && (!io->x.data || !io->rg.data || !io->ig.data || (need_y && !io->y.data))) return DN_ERR_INVALID_ARG;
+    const dn_view *views[] = {&io->x, &io->rg, &io->ig, &io->z, &io->y};
+    for (const dn_view *v : views)
+        if (v->data && !aligned(v->data, e)) return DN_ERR_INVALID_ARG;
+    return DN_OK;
+}
+
+dn_status recur_begin(RecurCall &c, const dn_recur_shape *s, const dn_recur_io *io, bool bwd, void *ws, size_t ws_bytes,
+                      cudaStream_t st)
+{
+    const RecurWs l = recur_ws(s, bwd);
+    if (!ws || !aligned(ws, 16) || ws_bytes < l.total) return DN_ERR_WORKSPACE;
+    memset(&c, 0, sizeof(c));
+    c.s = s;
+    c.io = io;
+    c.Nseq = s->cu_seqlens ? s->num_seqs : s->B;
+    c.part = (float *)((char *)ws + l.part);
+    if (s->cu_seqlens) {
+        int32_t *cu = (int32_t *)((char *)ws + l.cu);
+        c.cu = cu;
+        return status_of(check_offsets(s->cu_seqlens, s->num_seqs, s->T, cu, (uint32_t *)ws, st));
+    }
+    return DN_OK;
+}
+
 }  // namespace
 }  // namespace lay
 }  // namespace gdn
@@ -333,6 +395,81 @@ dn_status dn_scan_step(const dn_scan_shape *shape, const dn_scan_io *io, void *s
     c.io = io;
     c.Nseq = shape->B;
     return status_of(scan_step(c, (cudaStream_t)stream));
+}
+
+size_t dn_recur_workspace_size(const dn_recur_shape *shape, int for_backward)
+{
+    return recur_shape_ok(shape) == DN_OK ? recur_ws(shape, for_backward != 0).total : 0;
+}
+
+size_t dn_recur_saved_size(const dn_recur_shape *shape) { return recur_shape_ok(shape) == DN_OK ? recur_saved(shape) : 0; }
+
+dn_status dn_recur_fwd(const dn_recur_shape *shape, const dn_recur_io *io, void *saved, size_t saved_bytes, void *ws,
+                       size_t ws_bytes, void *stream)
+{
+    dn_status rc = recur_shape_ok(shape);
+    if (rc != DN_OK) return rc;
+    if ((rc = recur_io_ok(shape, io, true)) != DN_OK) return rc;
+    if (saved && (!aligned(saved, 16) || saved_bytes < recur_saved(shape))) return DN_ERR_WORKSPACE;
+    RecurCall c;
+    if ((rc = recur_begin(c, shape, io, false, ws, ws_bytes, (cudaStream_t)stream)) != DN_OK) return rc;
+    c.keep = (float *)saved;
+    return status_of(recur_fwd(c, (cudaStream_t)stream));
+}
+
+dn_status dn_recur_bwd(const dn_recur_shape *shape, const dn_recur_io *io, const dn_recur_grads *grads, const void *saved,
+                       size_t saved_bytes, void *ws, size_t ws_bytes, void *stream)
+{
+    dn_status rc = recur_shape_ok(shape);
+    if (rc != DN_OK) return rc;
+    if ((rc = recur_io_ok(shape, io, false)) != DN_OK) return rc;
+    const size_t e = shape->dtype == DN_F32 ? 4 : 2;
+    if (!grads || !grads->dlam) return DN_ERR_INVALID_ARG;
+    const float *params[] = {grads->dhT, grads->dlam, grads->drg_bias, grads->dig_bias, grads->dh0};
+    for (const float *p : params)
+        if (!aligned(p, 4)) return DN_ERR_INVALID_ARG;
+    if (shape->T > 0 && (!grads->dy.data || !grads->dx.data || !grads->drg.data || !grads->dig.data || (io->z.data && !grads->dz.data)))
+        return DN_ERR_INVALID_ARG;
+    const dn_view *views[] = {&grads->dy, &grads->dx, &grads->drg, &grads->dig, &grads->dz};
+    for (const dn_view *v : views)
+        if (v->data && !aligned(v->data, e)) return DN_ERR_INVALID_ARG;
+    if (!saved || !aligned(saved, 16) || saved_bytes < recur_saved(shape)) return DN_ERR_WORKSPACE;
+    RecurCall c;
+    if ((rc = recur_begin(c, shape, io, true, ws, ws_bytes, (cudaStream_t)stream)) != DN_OK) return rc;
+    c.gr = grads;
+    c.keep = (float *)saved;
+    return status_of(recur_bwd(c, (cudaStream_t)stream));
+}
+
+dn_status dn_recur_step(const dn_recur_shape *shape, const dn_recur_io *io, void *stream)
+{
+    dn_status rc = recur_shape_ok(shape);
+    if (rc != DN_OK) return rc;
+    if (shape->T != 1 || shape->cu_seqlens) return DN_ERR_INVALID_ARG;
+    if ((rc = recur_io_ok(shape, io, true)) != DN_OK) return rc;
+    RecurCall c;
+    memset(&c, 0, sizeof(c));
+    c.s = shape;
+    c.io = io;
+    c.Nseq = shape->B;
+    return status_of(recur_step(c, (cudaStream_t)stream));
+}
+
+dn_status dn_dropout(const dn_dropout_shape *shape, const dn_view *x, const dn_view *residual, const int64_t *rng, const dn_view *y,
+                     void *stream)
+{
+    if (!shape || shape->B < 0 || shape->H < 1 || shape->T < 0 || shape->d < 1) return DN_ERR_INVALID_ARG;
+    if (shape->dtype != DN_F32 && shape->dtype != DN_BF16) return DN_ERR_INVALID_ARG;
+    if (!(shape->p >= 0.0 && shape->p < 1.0) || !rng || !aligned(rng, 8)) return DN_ERR_INVALID_ARG;
+    if ((double)shape->B * shape->H * shape->T * shape->d > 9e18) return DN_ERR_UNSUPPORTED;
+    if (shape->B == 0 || shape->T == 0) return DN_OK;
+    if (!has(x) || !has(y)) return DN_ERR_INVALID_ARG;
+    const size_t e = shape->dtype == DN_F32 ? 4 : 2;
+    const dn_view *views[] = {x, residual, y};
+    for (const dn_view *v : views)
+        if (has(v) && !aligned(v->data, e)) return DN_ERR_INVALID_ARG;
+    DropCall c = {shape, x, residual, y, rng};
+    return status_of(dropout(c, (cudaStream_t)stream));
 }
 
 dn_status dn_norm_fwd(const dn_norm_shape *shape, const dn_view *x, const float *w, const dn_view *z,

@@ -1,11 +1,12 @@
 """The layer operators around the delta rule (include/gdn_layers.h): short causal
-convolution, selective state space scan, RMS norm with gate or residual sum.
+convolution, selective state space scan, gated linear recurrence, dropout, RMS norm with
+gate or residual sum.
 
 As in ``binding``: argument checks and marshalling only, every step of the
 computation runs in the library's CUDA kernels on the current torch stream, and a
 call that cannot run raises (TypeError, ValueError, or GdnError with the library's
 status).  The ``dn_*`` functions take caller-owned buffers and carry the C names;
-``conv_*``, ``scan_*`` and ``norm_*`` allocate the results (and workspaces) with
+``conv_*``, ``scan_*``, ``recur_*``, ``dropout_*`` and ``norm_*`` allocate the results (and workspaces) with
 torch and call them.
 
 Token arrays may have any strides as long as the feature axis is contiguous, so
@@ -35,13 +36,17 @@ from .binding import DN_BF16, DN_ERR_INVALID_ARG, DN_F32, GdnError, _check, dn_d
 
 EXPORTS = ["dn_conv_workspace_size", "dn_conv_fwd", "dn_conv_bwd", "dn_conv_step", "dn_norm_fwd",
            "dn_norm_workspace_size", "dn_norm_bwd", "dn_scan_workspace_size", "dn_scan_saved_size",
-           "dn_scan_fwd", "dn_scan_bwd", "dn_scan_step"]
+           "dn_scan_fwd", "dn_scan_bwd", "dn_scan_step", "dn_recur_workspace_size", "dn_recur_saved_size",
+           "dn_recur_fwd", "dn_recur_bwd", "dn_recur_step", "dn_dropout"]
 
 _DTYPES = {torch.float32: DN_F32, torch.bfloat16: DN_BF16}
 _CONV_SHAPE = struct.Struct("8iq")        # dn_conv_shape
 _NORM_SHAPE = struct.Struct("6ifi")       # dn_norm_shape
 _SCAN_SHAPE = struct.Struct("8iq")        # dn_scan_shape
 _SCAN_IO = struct.Struct("29q")           # dn_scan_io, dn_scan_grads: six views, five pointers
+_RECUR_SHAPE = struct.Struct("4ifiq")     # dn_recur_shape
+_RECUR_IO = struct.Struct("25q")          # dn_recur_io, dn_recur_grads: five views, five pointers
+_DROPOUT_SHAPE = struct.Struct("6id")     # dn_dropout_shape
 _VIEW = struct.Struct("4q")               # dn_view
 
 _lib = None
@@ -66,6 +71,12 @@ def _L():
                 ("dn_scan_fwd", [R, R, P, S, P, S, P], I),
                 ("dn_scan_bwd", [R, R, R, P, S, P, S, P], I),
                 ("dn_scan_step", [R, R, P], I),
+                ("dn_recur_workspace_size", [R, I], S),
+                ("dn_recur_saved_size", [R], S),
+                ("dn_recur_fwd", [R, R, P, S, P, S, P], I),
+                ("dn_recur_bwd", [R, R, R, P, S, P, S, P], I),
+                ("dn_recur_step", [R, R, P], I),
+                ("dn_dropout", [R, R, R, P, R, P], I),
                 ("dn_norm_bwd", [R, R, P, R, P, R, R, R, R, P, R, R, P, P, S, P], I)):
             f = getattr(L, name)
             f.argtypes, f.restype = args, res
@@ -516,6 +527,164 @@ def scan_step(x, dt, A, B, C, D=None, z=None, dt_bias=None, state=None, out_stat
         _same_device(x, out_state)
     dn_scan_step(scan_shape(x, B, dt_softplus), scan_io(x, dt, A, B, C, D, z, dt_bias, state, y, out_state))
     return y, out_state
+
+
+# ------------------------------------------------------------------ gated linear recurrence
+
+def recur_shape(x: torch.Tensor, c: float = 8.0, cu_seqlens=None) -> bytes:
+    """dn_recur_shape record of x [B,T,D] (x [n,D]: single tokens)."""
+    xs = x.shape
+    cu, n = _cu(cu_seqlens, xs[0])
+    return _RECUR_SHAPE.pack(xs[0], xs[1] if len(xs) == 3 else 1, xs[-1], _dtype_code(x, "x"), c, n, cu)
+
+
+def recur_io(x, rg, ig, lam, rg_bias, ig_bias, z, h0, y, hT) -> bytes:
+    """dn_recur_io record."""
+    return _RECUR_IO.pack(*_flat(x), *_flat(rg), *_flat(ig), *_flat(z), *_flat(y), lam.data_ptr(), _ptr(rg_bias), _ptr(ig_bias),
+                          _ptr(h0), _ptr(hT))
+
+
+def recur_grads(dy, dx, drg, dig, dz, dhT, dlam, drg_bias, dig_bias, dh0) -> bytes:
+    """dn_recur_grads record."""
+    return _RECUR_IO.pack(*_flat(dy), *_flat(dx), *_flat(drg), *_flat(dig), *_flat(dz), _ptr(dhT), dlam.data_ptr(), _ptr(drg_bias),
+                          _ptr(dig_bias), _ptr(dh0))
+
+
+def dn_recur_workspace_size(shape: bytes, for_backward: bool = False) -> int:
+    return int(_L().dn_recur_workspace_size(shape, int(for_backward)))
+
+
+def dn_recur_saved_size(shape: bytes) -> int:
+    return int(_L().dn_recur_saved_size(shape))
+
+
+def dn_recur_fwd(shape, io, saved, ws, stream=None):
+    _check(_L().dn_recur_fwd(shape, io, _p(saved), 0 if saved is None else saved.numel() * saved.element_size(), _p(ws),
+                             ws.numel() * ws.element_size(), _stream(stream)), "dn_recur_fwd")
+
+
+def dn_recur_bwd(shape, io, grads, saved, ws, stream=None):
+    _check(_L().dn_recur_bwd(shape, io, grads, _p(saved), saved.numel() * saved.element_size(), _p(ws),
+                             ws.numel() * ws.element_size(), _stream(stream)), "dn_recur_bwd")
+
+
+def dn_recur_step(shape, io, stream=None):
+    _check(_L().dn_recur_step(shape, io, _stream(stream)), "dn_recur_step")
+
+
+def _recur_args(x, rg, ig, lam, rg_bias, ig_bias, z, h0, cu_seqlens, axes):
+    """Checks a recurrence's arguments (axes: of x, 3 or 2); the number of sequences."""
+    xs = x.shape
+    if len(xs) != axes:
+        raise ValueError("x must be %s, got %d axes" % ("[B,T,D]" if axes == 3 else "[n,D]", len(xs)))
+    _dtype_code(x, "x")
+    _tokens(x, "x", xs, x.dtype)
+    _tokens(rg, "rg", xs, x.dtype)
+    _tokens(ig, "ig", xs, x.dtype)
+    if z is not None:
+        _tokens(z, "z", xs, x.dtype)
+    width = (xs[-1],)
+    _dense(lam, "lam", width)
+    _dense(rg_bias, "rg_bias", width)
+    _dense(ig_bias, "ig_bias", width)
+    n = xs[0] if cu_seqlens is None else _cu(cu_seqlens, xs[0])[1]
+    _dense(h0, "h0", (n,) + width)
+    _same_device(x, rg, ig, lam, rg_bias, ig_bias, z, h0, cu_seqlens)
+    return n
+
+
+def recur_forward(x, rg, ig, lam, rg_bias=None, ig_bias=None, z=None, h0=None, c=8.0, cu_seqlens=None, out=None, want_state=True,
+                  save=False, ws=None, check_status=True):
+    """Gated linear recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(ig + ig_bias) x, a = exp(-c softplus(lam)
+    sigmoid(rg + rg_bias)), y = h or h silu(z).  x, rg, ig (the gates before their sigmoid) and z [B,T,D]; lam, rg_bias,
+    ig_bias [D] and the initial states h0 [N_seq,D] float32.  Returns (y, hT), or (y, hT, saved) with save=True for
+    recur_backward(saved=saved): the state entering every 8th token, half a byte a token and channel."""
+    n = _recur_args(x, rg, ig, lam, rg_bias, ig_bias, z, h0, cu_seqlens, 3)
+    y = _result(out, "out", x)
+    hT = torch.empty((n, x.shape[2]), dtype=torch.float32, device=x.device) if want_state else None
+    shape = recur_shape(x, c, cu_seqlens)
+    packed = cu_seqlens is not None
+    ws = _ws("dn_recur_workspace_size", shape, 0, x, packed, "dn_recur_fwd") if ws is None else _buffer(ws, "ws", x)
+    saved = _ws("dn_recur_saved_size", shape, -1, x, packed, "dn_recur_fwd") if save else None
+    dn_recur_fwd(shape, recur_io(x, rg, ig, lam, rg_bias, ig_bias, z, h0, y, hT), saved, ws)
+    if check_status and packed:
+        _check(dn_device_status(ws), "dn_recur_fwd (device status)")
+    return (y, hT, saved) if save else (y, hT)
+
+
+def recur_backward(x, rg, ig, lam, rg_bias=None, ig_bias=None, z=None, h0=None, dy=None, dhT=None, saved=None, c=8.0, cu_seqlens=None,
+                   ws=None, check_status=True):
+    """Gradients of <y, dy> + <hT, dhT>, from recur_forward's arguments and ``saved`` buffer.  Returns dict
+    dx, drg, dig, dlam, and drg_bias, dig_bias, dz, dh0 (None for an argument that was not given)."""
+    n = _recur_args(x, rg, ig, lam, rg_bias, ig_bias, z, h0, cu_seqlens, 3)
+    if dy is None or saved is None:
+        raise ValueError("recur_backward needs dy and saved (recur_forward(save=True))")
+    _tokens(dy, "dy", x.shape, x.dtype)
+    _dense(dhT, "dhT", (n, x.shape[2]))
+    _same_device(x, dy, dhT)
+    _buffer(saved, "saved", x)
+    new = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
+    g = dict(dx=new(x), drg=new(rg), dig=new(ig), dz=new(z), dlam=new(lam), drg_bias=new(rg_bias), dig_bias=new(ig_bias), dh0=new(h0))
+    shape = recur_shape(x, c, cu_seqlens)
+    packed = cu_seqlens is not None
+    ws = _ws("dn_recur_workspace_size", shape, 1, x, packed, "dn_recur_bwd") if ws is None else _buffer(ws, "ws", x)
+    dn_recur_bwd(shape, recur_io(x, rg, ig, lam, rg_bias, ig_bias, z, h0, None, None),
+                 recur_grads(dy, g["dx"], g["drg"], g["dig"], g["dz"], dhT, g["dlam"], g["drg_bias"], g["dig_bias"], g["dh0"]), saved, ws)
+    if check_status and packed:
+        _check(dn_device_status(ws), "dn_recur_bwd (device status)")
+    return g
+
+
+def recur_step(x, rg, ig, lam, rg_bias=None, ig_bias=None, z=None, state=None, out_state=None, c=8.0, out=None):
+    """One token per sequence: x, rg, ig, z [n,D], state [n,D] float32 (None: zero).  Returns (y, new state);
+    pass out_state=state to update the states in place."""
+    _recur_args(x, rg, ig, lam, rg_bias, ig_bias, z, state, None, 2)
+    y = _result(out, "out", x)
+    if out_state is None:
+        out_state = torch.empty(x.shape, dtype=torch.float32, device=x.device)
+    else:
+        _dense(out_state, "out_state", x.shape)
+        _same_device(x, out_state)
+    dn_recur_step(recur_shape(x, c), recur_io(x, rg, ig, lam, rg_bias, ig_bias, z, state, y, out_state))
+    return y, out_state
+
+
+# ------------------------------------------------------------------ dropout
+
+def dn_dropout(x, p, rng, residual, y, stream=None):
+    B, H, T, d = _dims(x)
+    _check(_L().dn_dropout(_DROPOUT_SHAPE.pack(B, H, T, d, _dtype_code(x, "x"), 0, p), _view(x), _view(residual), _p(rng), _view(y),
+                           _stream(stream)), "dn_dropout")
+
+
+def _dropout(x, p, rng, residual, out, name):
+    if x.dim() not in (2, 3, 4):
+        raise ValueError("%s must be [R,d], [B,T,d] or [B,H,T,d], got %d axes" % (name, x.dim()))
+    _dtype_code(x, name)
+    _tokens(x, name, x.shape, x.dtype)
+    if residual is not None:
+        _tokens(residual, "residual", x.shape, x.dtype)
+    if not 0.0 <= p < 1.0:
+        raise ValueError("p must be at least 0 and below 1, got %r" % (p,))
+    _dense(rng, "rng", (2,), torch.int64)
+    _same_device(x, rng, residual)
+    y = _result(out, "out", x)
+    if x.numel():
+        dn_dropout(x, p, rng, residual, y)
+    return y
+
+
+def dropout_forward(x, p, rng, residual=None, out=None):
+    """Dropout: y = residual + keep x / (1 - p), keep with probability 1 - p.  x [R,d], [B,T,d] or [B,H,T,d]; rng int64 [2] on the
+    device: seed and number of the call (one for each call and step), read by the kernel, so that a captured call draws a new
+    mask when they change.  The mask goes by the element's index in x's shape, not by strides, and is not stored.  ``out`` may be x or
+    residual itself."""
+    return _dropout(x, p, rng, residual, out, "x")
+
+
+def dropout_backward(dy, p, rng, out=None):
+    """Gradient of x: keep dy / (1 - p), with the mask of the forward call's rng.  That of the residual is dy."""
+    return _dropout(dy, p, rng, None, out, "dy")
 
 
 # ------------------------------------------------------------------ norm

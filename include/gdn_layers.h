@@ -135,6 +135,74 @@ dn_status dn_scan_bwd(const dn_scan_shape *shape, const dn_scan_io *io, const dn
  * may be the same buffer.  No workspace. */
 dn_status dn_scan_step(const dn_scan_shape *shape, const dn_scan_io *io, void *stream);
 
+/* ------------------------------------------------------- gated linear recurrence
+ * D channels with one state each, decay and input gated by projections of the tokens:
+ *     m = c softplus(lam) sigmoid(rg + rg_bias),  a = exp(-m),  s = sqrt(1 - a^2)
+ *     h_t = a_t h_{t-1} + s_t sigmoid(ig + ig_bias) x_t,   y_t = z ? h_t silu(z_t) : h_t
+ * c >= 0.  Gradients are finite where a is 1 (their limits there).                 */
+typedef struct {
+    int32_t B, T, D;
+    int32_t dtype;
+    float c;
+    int32_t num_seqs;
+    const int32_t *cu_seqlens;
+} dn_recur_shape;
+
+typedef struct {
+    dn_view x, rg, ig;            /* [B][T][D] (no head axis): input, gates before their sigmoid */
+    dn_view z, y;                 /* [B][T][D]; z.data == NULL: no output gate      */
+    const float *lam;             /* [D]                                           */
+    const float *rg_bias, *ig_bias; /* [D] or NULL (zero)                          */
+    const float *h0;              /* [N_seq][D] initial states or NULL (zero)       */
+    float *hT;                    /* final states or NULL                          */
+} dn_recur_io;
+
+typedef struct {
+    dn_view dy;                   /* gradient of y                                 */
+    dn_view dx, drg, dig;         /* all written                                   */
+    dn_view dz;                   /* written when io.z is given                     */
+    const float *dhT;             /* gradient of hT or NULL (zero)                 */
+    float *dlam;                  /* [D]                                           */
+    float *drg_bias, *dig_bias;   /* [D] or NULL (not written)                     */
+    float *dh0;                   /* [N_seq][D] or NULL (not written)              */
+} dn_recur_grads;
+
+size_t dn_recur_workspace_size(const dn_recur_shape *shape, int for_backward);
+
+/* Bytes of the buffer that dn_recur_fwd fills for dn_recur_bwd: the state entering every 8th token,
+ * float32: 1/2 byte a token and channel. */
+size_t dn_recur_saved_size(const dn_recur_shape *shape);
+
+/* saved may be NULL (nothing kept). */
+dn_status dn_recur_fwd(const dn_recur_shape *shape, const dn_recur_io *io, void *saved,
+                       size_t saved_bytes, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradients of <y, dy> + <hT, dhT>, from the buffer that dn_recur_fwd filled for the same
+ * arguments (the library does not check that they are the same). */
+dn_status dn_recur_bwd(const dn_recur_shape *shape, const dn_recur_io *io,
+                       const dn_recur_grads *grads, const void *saved, size_t saved_bytes, void *ws,
+                       size_t ws_bytes, void *stream);
+
+/* One token for each of B sequences (T must be 1, no packing), states io->h0 -> io->hT, which
+ * may be the same buffer.  No workspace. */
+dn_status dn_recur_step(const dn_recur_shape *shape, const dn_recur_io *io, void *stream);
+
+/* ------------------------------------------------------------------------ dropout
+ *     y = residual + (word(i) >= round(p 2^32) ? x / (1 - p) : 0)
+ * i is the element's index in [B][H][T][d] order, whatever the strides; word(i) is word i mod 4 of
+ * Philox 4x32 of 10 rounds (Salmon et al. 2011) of the counter (i / 4, rng[1]) under the key rng[0].
+ * rng: device int64 [2], seed and number of the call, read when the kernel runs: a replayed graph
+ * draws what they are then.  The gradient is the same call on dy without a residual.  An x that is
+ * dropped is not used, whatever its value.  y may be the view x or residual itself. */
+typedef struct {
+    int32_t B, H, T, d;
+    int32_t dtype, reserved;
+    double p;                     /* 0 <= p < 1 */
+} dn_dropout_shape;
+
+dn_status dn_dropout(const dn_dropout_shape *shape, const dn_view *x, const dn_view *residual,
+                     const int64_t *rng, const dn_view *y, void *stream);
+
 /* --------------------------------------------------------------------------- norm
  * Per row of d features:
  *     r = residual ? residual + res_scale * x : x     (res_scale [d] or NULL: 1)
