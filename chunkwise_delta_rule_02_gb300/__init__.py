@@ -14,5 +14,6 @@ from .binding import (  # noqa: F401
 )
 from .layers import (  # noqa: F401
     conv_backward, conv_forward, conv_step, dropout_backward, dropout_forward, norm_backward, norm_forward,
-    recur_backward, recur_forward, recur_step, scan_backward, scan_forward, scan_step,
+    recur_backward, recur_forward, recur_step, scan_backward, scan_forward, scan_step, xent_backward,
+    xent_forward,
 )

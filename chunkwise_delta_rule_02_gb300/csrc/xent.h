@@ -1,0 +1,40 @@
+// Launchers of the linear softmax cross entropy, called by xent_api.cu with checked arguments.
+#pragma once
+
+#include "layers.h"
+
+namespace gdn {
+namespace xent {
+
+// An operand matrix as the tensor maps take it: bf16 [planes][rows][pitch]
+struct Operand {
+    const void *p;
+    long long pitch, plane;         // elements
+};
+
+// A launch's sizes.  M tokens, K features, V vocabulary entries; float32 inputs are held as
+// three bf16 planes (x = x0 + x1 + x2), bf16 ones as one.
+struct Call {
+    const dn_xent_shape *s;
+    const dn_view *x, *w, *targets, *dloss, *dx;
+    int M, K, V, planes;
+    int piece;                      // vocabulary entries of a piece (backward)
+    Operand xo, wo;
+    bool pack_x, pack_w;
+    uint32_t *status;
+    int32_t *tgt;                   // [M] targets, -1: none
+    float *row;                     // [M] forward: the target's logit; backward: dloss, 0 without a target
+    float2 *part;                   // forward: [2 tiles][M] maximum and sum
+    char *d;                        // backward: [planes][M][piece] bf16 gradients of the logits of a piece
+    float *acc;                     // backward: [M][K] sums of dx over pieces (more than one)
+    float *loss, *lse;
+    void *dw;
+};
+
+bool usable();                      // the tensor maps' encoder is there
+int tiles_of(int n);                // of 256
+cudaError_t forward(const Call &c, cudaStream_t st);
+cudaError_t backward(const Call &c, cudaStream_t st);
+
+}  // namespace xent
+}  // namespace gdn

@@ -1,12 +1,12 @@
 """The layer operators around the delta rule (include/gdn_layers.h): short causal
 convolution, selective state space scan, gated linear recurrence, dropout, RMS norm with
-gate or residual sum.
+gate or residual sum, and the loss of the model that they make (linear softmax cross entropy).
 
 As in ``binding``: argument checks and marshalling only, every step of the
 computation runs in the library's CUDA kernels on the current torch stream, and a
 call that cannot run raises (TypeError, ValueError, or GdnError with the library's
 status).  The ``dn_*`` functions take caller-owned buffers and carry the C names;
-``conv_*``, ``scan_*``, ``recur_*``, ``dropout_*`` and ``norm_*`` allocate the results (and workspaces) with
+``conv_*``, ``scan_*``, ``recur_*``, ``dropout_*``, ``norm_*`` and ``xent_*`` allocate the results (and workspaces) with
 torch and call them.
 
 Token arrays may have any strides as long as the feature axis is contiguous, so
@@ -37,7 +37,8 @@ from .binding import DN_BF16, DN_ERR_INVALID_ARG, DN_F32, GdnError, _check, dn_d
 EXPORTS = ["dn_conv_workspace_size", "dn_conv_fwd", "dn_conv_bwd", "dn_conv_step", "dn_norm_fwd",
            "dn_norm_workspace_size", "dn_norm_bwd", "dn_scan_workspace_size", "dn_scan_saved_size",
            "dn_scan_fwd", "dn_scan_bwd", "dn_scan_step", "dn_recur_workspace_size", "dn_recur_saved_size",
-           "dn_recur_fwd", "dn_recur_bwd", "dn_recur_step", "dn_dropout"]
+           "dn_recur_fwd", "dn_recur_bwd", "dn_recur_step", "dn_dropout", "dn_xent_workspace_size", "dn_xent_fwd",
+           "dn_xent_bwd"]
 
 _DTYPES = {torch.float32: DN_F32, torch.bfloat16: DN_BF16}
 _CONV_SHAPE = struct.Struct("8iq")        # dn_conv_shape
@@ -47,6 +48,7 @@ _SCAN_IO = struct.Struct("29q")           # dn_scan_io, dn_scan_grads: six views
 _RECUR_SHAPE = struct.Struct("4ifiq")     # dn_recur_shape
 _RECUR_IO = struct.Struct("25q")          # dn_recur_io, dn_recur_grads: five views, five pointers
 _DROPOUT_SHAPE = struct.Struct("6id")     # dn_dropout_shape
+_XENT_SHAPE = struct.Struct("6iq")        # dn_xent_shape
 _VIEW = struct.Struct("4q")               # dn_view
 
 _lib = None
@@ -77,6 +79,9 @@ def _L():
                 ("dn_recur_bwd", [R, R, R, P, S, P, S, P], I),
                 ("dn_recur_step", [R, R, P], I),
                 ("dn_dropout", [R, R, R, P, R, P], I),
+                ("dn_xent_workspace_size", [R, R, R, I], S),
+                ("dn_xent_fwd", [R, R, R, R, P, P, P, S, P], I),
+                ("dn_xent_bwd", [R, R, R, R, P, R, R, P, P, S, P], I),
                 ("dn_norm_bwd", [R, R, P, R, P, R, R, R, R, P, R, R, P, P, S, P], I)):
             f = getattr(L, name)
             f.argtypes, f.restype = args, res
@@ -753,4 +758,98 @@ def norm_backward(x, w, dy, z=None, sum=None, dsum=None, res_scale=None, eps=1e-
     shape = norm_shape(x, w, eps)
     ws = _ws("dn_norm_workspace_size", shape, -1, x, False, "dn_norm_bwd") if ws is None else _buffer(ws, "ws", x)
     dn_norm_bwd(shape, x, w, z, res_scale, sum, dy, dsum, dx, g["dw"], g["dz"], dres, g["dres_scale"], ws)
+    return g
+
+
+# ------------------------------------------------------------------ linear softmax cross entropy
+
+def xent_shape(x: torch.Tensor, w: torch.Tensor, ignore_index: int = -100) -> bytes:
+    """dn_xent_shape record of x [R,K] or [B,T,K] and w [V,K]."""
+    B, _, T, K = _dims(x)
+    return _XENT_SHAPE.pack(B, T, K, w.shape[0], _dtype_code(x, "x"), 0, ignore_index)
+
+
+def _weight_view(w: torch.Tensor) -> bytes:
+    return _VIEW.pack(w.data_ptr(), 0, 0, w.stride(0))
+
+
+def _token_view(t: torch.Tensor) -> bytes:
+    """dn_view record of one value a token, [R] or [B,T]."""
+    s = t.stride()
+    return _VIEW.pack(t.data_ptr(), s[0] if len(s) == 2 else 0, 0, s[-1])
+
+
+def dn_xent_workspace_size(shape: bytes, x, w, for_backward: bool = False) -> int:
+    return int(_L().dn_xent_workspace_size(shape, _view(x), _weight_view(w), int(for_backward)))
+
+
+def dn_xent_fwd(shape, x, w, targets, loss, lse, ws, stream=None):
+    _check(_L().dn_xent_fwd(shape, _view(x), _weight_view(w), _token_view(targets), _p(loss), _p(lse), _p(ws),
+                            ws.numel() * ws.element_size(), _stream(stream)), "dn_xent_fwd")
+
+
+def dn_xent_bwd(shape, x, w, targets, lse, dloss, dx, dw, ws, stream=None):
+    _check(_L().dn_xent_bwd(shape, _view(x), _weight_view(w), _token_view(targets), _p(lse), _token_view(dloss), _view(dx), _p(dw), _p(ws),
+                            ws.numel() * ws.element_size(), _stream(stream)), "dn_xent_bwd")
+
+
+def _per_token(t: torch.Tensor, name: str, shape, dtype) -> torch.Tensor:
+    """One value a token, any strides."""
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    return t
+
+
+def _xent_args(x, w, targets):
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [R,K] or [B,T,K], got %d axes" % x.dim())
+    if w.dim() != 2 or w.shape[0] < 1 or w.shape[1] < 1:
+        raise ValueError("w must be [vocabulary, K]")
+    _dtype_code(x, "x")
+    _tokens(x, "x", x.shape, x.dtype)
+    _tokens(w, "w", (w.shape[0], x.shape[-1]), x.dtype)
+    _per_token(targets, "targets", x.shape[:-1], torch.int64)
+    _same_device(x, w, targets)
+
+
+def _xent_ws(shape, x, w, backward, where):
+    n = dn_xent_workspace_size(shape, x, w, backward)
+    if n == 0:
+        raise GdnError(DN_ERR_INVALID_ARG, where)
+    return torch.empty(n, dtype=torch.uint8, device=x.device)
+
+
+def xent_forward(x, w, targets, ignore_index=-100, ws=None, check_status=True):
+    """Softmax cross entropy of the logits x w^T, which are not kept.  x [R,K] or [B,T,K] and w [V,K] of one type, targets int64 of
+    x's leading shape.  Returns (loss, lse) of that shape, float32: the loss of each token (0 where its target is ignore_index) and the
+    log of the sum of its exponentials, for xent_backward.  A target outside the vocabulary counts as none; with check_status (which
+    waits for the stream) it raises."""
+    _xent_args(x, w, targets)
+    loss = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    lse = torch.empty_like(loss)
+    shape = xent_shape(x, w, ignore_index)
+    ws = _xent_ws(shape, x, w, False, "dn_xent_fwd") if ws is None else _buffer(ws, "ws", x)
+    dn_xent_fwd(shape, x, w, targets, loss, lse, ws)
+    if check_status:
+        _check(dn_device_status(ws), "dn_xent_fwd (device status)")
+    return loss, lse
+
+
+def xent_backward(x, w, targets, lse, dloss, ignore_index=-100, ws=None, check_status=True):
+    """Gradients of <loss, dloss>: dict dx, dw, in x's type.  lse as xent_forward returned it, dloss float32 of its shape (any
+    strides: one value expanded to all tokens will do).  The logits are made again by pieces of the vocabulary."""
+    _xent_args(x, w, targets)
+    _dense(lse, "lse", x.shape[:-1])
+    _per_token(dloss, "dloss", x.shape[:-1], torch.float32)
+    _same_device(x, lse, dloss)
+    g = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=x.device), dw=torch.empty(w.shape, dtype=w.dtype, device=w.device))
+    shape = xent_shape(x, w, ignore_index)
+    ws = _xent_ws(shape, x, w, True, "dn_xent_bwd") if ws is None else _buffer(ws, "ws", x)
+    dn_xent_bwd(shape, x, w, targets, lse, dloss, g["dx"], g["dw"], ws)
+    if check_status:
+        _check(dn_device_status(ws), "dn_xent_bwd (device status)")
     return g

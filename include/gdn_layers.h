@@ -203,6 +203,37 @@ typedef struct {
 dn_status dn_dropout(const dn_dropout_shape *shape, const dn_view *x, const dn_view *residual,
                      const int64_t *rng, const dn_view *y, void *stream);
 
+/* ------------------------------------------------------ linear softmax cross entropy
+ * The loss of M = B T tokens from their last hidden states and an output weight, without the logits:
+ *     l_v = x . w_v,   lse = log sum_v exp l_v,   loss = lse - l[target]
+ *     D_v = (exp(l_v - lse) - [v == target]) dloss,   dx = sum_v D_v w_v,   dw_v = sum over tokens of D_v x
+ * x, dx [B][T][K] and w, dw [V][K] in the shape's dtype (the views without a head axis; of w `time` is the
+ * distance of its rows, dw is dense); targets int64 and dloss float32, views [B][T] whose elements lie at
+ * b batch + t time (their feature axis is one element); loss, lse float32 [M].
+ * A token whose target is ignore_index has no loss (0) and no gradient; one whose target is outside
+ * 0 .. V - 1 likewise, and the workspace's status word says so (dn_device_status: DN_ERR_INVALID_ARG).
+ * Such tokens still take part in dw with weight 0: their x has to be finite.
+ * Products are sums in float32 of bf16 operands, float32 ones as three bf16 planes; D is rounded to the dtype.
+ * Memory: the backward pass holds D for a piece of the vocabulary at a time. */
+typedef struct {
+    int32_t B, T, K, V;
+    int32_t dtype, reserved;
+    int64_t ignore_index;
+} dn_xent_shape;
+
+/* Goes by the views' alignment too: rows that start at 16 bytes are read in place, others from a copy. */
+size_t dn_xent_workspace_size(const dn_xent_shape *shape, const dn_view *x, const dn_view *w,
+                              int for_backward);
+
+dn_status dn_xent_fwd(const dn_xent_shape *shape, const dn_view *x, const dn_view *w,
+                      const dn_view *targets, float *loss, float *lse, void *ws, size_t ws_bytes,
+                      void *stream);
+
+/* Gradients of <loss, dloss>; lse as dn_xent_fwd wrote it. */
+dn_status dn_xent_bwd(const dn_xent_shape *shape, const dn_view *x, const dn_view *w,
+                      const dn_view *targets, const float *lse, const dn_view *dloss,
+                      const dn_view *dx, void *dw, void *ws, size_t ws_bytes, void *stream);
+
 /* --------------------------------------------------------------------------- norm
  * Per row of d features:
  *     r = residual ? residual + res_scale * x : x     (res_scale [d] or NULL: 1)
