@@ -1,5 +1,6 @@
 // C ABI of the layer operators: argument checks, workspace layout, dispatch; and
 // the two kernels they share (packed offsets, sums of partial results).
+#include <cudaTypedefs.h>
 #include <string.h>
 
 #include <atomic>
@@ -86,6 +87,35 @@ int sm_count()
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
     if (dev < kDevices) known[dev].store(n, std::memory_order_relaxed);
     return n;
+}
+
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return (PFN_cuTensorMapEncodeTiled_v12000)ptr;
+    }();
+    return fn;
+}
+
+bool has_tensor_maps() { return encode_fn() != nullptr; }
+
+bool tensor_map(CUtensorMap *m, bool f32, const void *p, long long cols, long long rows, long long planes, long long row_pitch,
+                long long plane_pitch, int wide, int high, bool swizzle)
+{
+    const long long e = f32 ? 4 : 2, row = row_pitch * e, plane = (planes > 1 ? plane_pitch : row_pitch) * e, most = 1ll << 40;
+    if (!encode_fn() || (uintptr_t)p % 16 || row % 16 || plane % 16 || row < cols * e || plane <= 0 || row >= most || plane >= most ||
+        rows > 0x7fffffff || cols > 0x7fffffff || planes > 0x7fffffff)
+        return false;
+    const cuuint64_t dim[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes}, stride[2] = {(cuuint64_t)row, (cuuint64_t)plane};
+    const cuuint32_t box[3] = {(cuuint32_t)wide, (cuuint32_t)high, 1}, es[3] = {1, 1, 1};
+    return encode_fn()(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dim, stride, box, es,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 namespace {
@@ -214,7 +244,7 @@ dn_status recur_shape_ok(const dn_recur_shape *s)
     if (!s || s->B < 1 || s->T < 0 || s->D < 1) return DN_ERR_INVALID_ARG;
     if (s->dtype != DN_F32 && s->dtype != DN_BF16) return DN_ERR_INVALID_ARG;
     if (!(s->c >= 0.f && s->c <= 1e30f)) return DN_ERR_INVALID_ARG;
-    if (s->D > (1 << 24) || s->T > kMaxT || (double)s->B * ((s->D + kChans - 1) / kChans) > (1 << 27)) return DN_ERR_UNSUPPORTED;
+    if (s->D > (1 << 24) || s->T > kMaxT || (double)s->B * ((s->D + 15) / 16) > (1 << 27)) return DN_ERR_UNSUPPORTED;
     return check_packed(s->cu_seqlens, s->B, s->num_seqs);
 }
 
@@ -227,7 +257,7 @@ RecurWs recur_ws(const dn_recur_shape *s, bool bwd)
     RecurWs w;
     w.cu = 256;
     w.part = w.cu + (s->cu_seqlens ? align256(sizeof(int32_t) * ((size_t)s->num_seqs + 1)) : 0);
-    w.total = w.part + (bwd ? align256(sizeof(float) * 3 * (size_t)s->B * recur_cluster(s, true) * s->D) : 0);
+    w.total = w.part + (bwd ? align256(sizeof(float) * 3 * (size_t)s->B * recur_plan(s, true).CL * s->D) : 0);
     return w;
 }
 
@@ -259,6 +289,7 @@ dn_status recur_begin(RecurCall &c, const dn_recur_shape *s, const dn_recur_io *
     memset(&c, 0, sizeof(c));
     c.s = s;
     c.io = io;
+    c.status = (uint32_t *)ws;
     c.Nseq = s->cu_seqlens ? s->num_seqs : s->B;
     c.part = (float *)((char *)ws + l.part);
     if (s->cu_seqlens) {

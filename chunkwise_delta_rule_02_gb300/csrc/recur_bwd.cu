@@ -16,115 +16,141 @@ namespace lay {
 
 namespace {
 
-template <class T, bool WIDE, bool PACKED>
-__global__ void __launch_bounds__(kRecurThreads) k_recur_bwd(RecurDims g, RecurIo<T> io)
+template <class T, int Q, int MODE, bool PACKED>
+__global__ void __launch_bounds__(32 * bwd_warps(sizeof(T))) k_recur_bwd(const __grid_constant__ RecurMaps maps, RecurDims g, RecurIo<T> io)
 {
-    __shared__ RecurShared sm;
-    __shared__ float2 red[3][kWarps][32];
+    constexpr int W = bwd_warps(sizeof(T)), S = bwd_stages(sizeof(T)), L = 32 / Q, R = kRun * Q;
+    extern __shared__ __align__(128) char raw[];
+    __shared__ RecurShared<W, Q> sm;
+    __shared__ float2 red[3][W][L];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = g.CL > 1 ? cluster_rank() : 0;
-    const int id = blockIdx.x / g.CL, b = id / g.tiles, c = (id - b * g.tiles) * kChans + 2 * lane;
+    const int id = blockIdx.x / g.CL, b = id / g.tiles, c0 = (id - b * g.tiles) * (64 / Q), c = c0 + 2 * (lane % L), q = lane / L * kRun;
     const bool in0 = c < g.D, in1 = c + 1 < g.D;
-    const int cc = in0 ? c : 0;
-    const bool gated = io.z.p != nullptr;
+    const bool gated = io.in[kZ].p != nullptr;
+    Ring<T, W, Q, S, MODE> ring;
+    ring.init(raw, sm.bar[warp], &io, &maps, gated ? 31 : 23, b, c0, g.D);
+    const int te = PACKED ? g.cu[g.Nseq] : g.T;
+    const int span = W * R * g.CL, steps = (te + span - 1) / span;
+    const int first = (rank * W + warp) * R;
+    auto token = [&](int st) { return (steps - 1 - st) * span + first; };   // step st handles the st-th span from the end
+    for (int st = 0; st < S - 1; ++st) {
+        if (st < steps) ring.ask(st, token(st), te - token(st));
+        ring.asked();
+    }
     RecurParams par;
     float2 dk;
     par.load(g, c, in0, in1, &dk);
-    const int te = PACKED ? g.cu[g.Nseq] : g.T;
+    const bool far = par.far();
     float2 carry = two(0.f);   // the gradient that reaches a token's state from behind it
     if (!PACKED && io.dhT) carry = load2(io.dhT + (size_t)b * g.D + c, in0, in1);
-    const int span = kSpan * g.CL, steps = (te + span - 1) / span;
     const size_t kept = (g.T + kRun - 1) / kRun;
+    auto kept_at = [&](int st) {   // the state that enters this lane's run
+        const int t = token(st) + q;
+        return st < steps && t < te ? load2(io.keep + ((size_t)b * kept + t / kRun) * g.D + c, in0, in1) : two(0.f);
+    };
+    float2 next = kept_at(0);
     float2 sq = two(0.f), sr = two(0.f), si = two(0.f);
+    Edges edges = {0, 0};
     if (g.CL > 1) cluster_barrier();   // all of the cluster's blocks run before one writes to another
 
-    for (int st = steps - 1; st >= 0; --st) {
-        const int t = st * span + rank * kSpan + warp * kRun, n = max(0, min(kRun, te - t));
-        Two<T, WIDE> x[kRun], r[kRun], i[kRun], z[kRun], dy[kRun];
-#pragma unroll
-        for (int k = 0; k < kRun; ++k) {
-            const bool in = k < n;
-            x[k].load(io.x.at(b, 0, in ? t + k : 0) + cc, in && in0, in && in1);
-            r[k].load(io.rg.at(b, 0, in ? t + k : 0) + cc, in && in0, in && in1);
-            i[k].load(io.ig.at(b, 0, in ? t + k : 0) + cc, in && in0, in && in1);
-            dy[k].load(io.dy.at(b, 0, in ? t + k : 0) + cc, in && in0, in && in1);
-            if (gated) z[k].load(io.z.at(b, 0, in ? t + k : 0) + cc, in && in0, in && in1);
-        }
+    for (int st = 0; st < steps; ++st) {
+        const int tw = token(st), nw = min(R, te - tw), t = tw + q, n = max(0, min(kRun, te - t));
         uint32_t starts = 0, ends = 0;
-        int seq = 0;
-        if (PACKED) run_edges(g, t, n, starts, ends, seq);
-        float2 h = n > 0 ? load2(io.keep + ((size_t)b * kept + t / kRun) * g.D + c, in0, in1) : two(0.f);
+        if (PACKED) edges.find(g, tw, nw, t, n, starts, ends);
+        float2 h = next;
+        next = kept_at(st + 1);
+        ring.get(st, tw, nw, g.status);
 
         // the run's states, and of each token what dh is multiplied with
         float2 a[kRun], gy[kRun], fq[kRun], f1[kRun], fx[kRun], fi[kRun];
+        auto states = [&](auto wide) {
 #pragma unroll
-        for (int k = 0; k < kRun; ++k) {
-            const float2 rr = sigmoid2(add2(r[k].get(), par.rb)), m = mul2(par.km, rr);
-            const float2 ii = sigmoid2(add2(i[k].get(), par.ib)), u = mul2(ii, x[k].get());
-            float2 y, rs;
-            decay_of(m, a[k], y, rs);
-            const float2 s = mul2(y, rs);
-            if (PACKED && (starts >> k & 1)) {
-                const int q = __shfl_sync(0xffffffffu, seq, k);
-                h = g.h0 ? load2(g.h0 + (size_t)q * g.D + c, in0, in1) : two(0.f);
+            for (int k = 0; k < kRun; ++k) {
+                const float2 r = gate(ring.at(st, kRg, k), par.rb), m = mul2(par.km, r);
+                const float2 i = gate(ring.at(st, kIg, k), par.ib), u = mul2(i, ring.at(st, kX, k));
+                float2 y, rs;
+                decay_of<decltype(wide)::value>(m, a[k], y, rs);
+                const float2 s = mul2(y, rs), su = mul2(s, u);
+                if (PACKED && (starts >> k & 1))
+                    h = g.h0 ? load2(g.h0 + (size_t)seq_at(g.cu, g.Nseq, t + k) * g.D + c, in0, in1) : two(0.f);
+                // u a / s comes with m / s: m rs u a, which is 0 where m is
+                fq[k] = mul2(mul2(m, a[k]), sub2(mul2(mul2(rs, u), a[k]), h));
+                f1[k] = sub2(two(1.f), r);
+                fx[k] = mul2(s, i);
+                fi[k] = mul2(su, sub2(two(1.f), i));
+                h = fma2(a[k], h, su);
+                gy[k] = ring.at(st, kDy, k);
+                if (gated) {
+                    const float2 z = ring.at(st, kZ, k), p = sigmoid2(z);
+                    // silu'(z) = p (1 + z (1 - p))
+                    const float2 ds = mul2(p, fma2(z, sub2(two(1.f), p), two(1.f)));
+                    ring.put(st, kZ, k, mul2(mul2(gy[k], h), ds));
+                    gy[k] = mul2(gy[k], mul2(z, p));
+                }
             }
-            // u a / s comes with m / s: m rs u a, which is 0 where m is
-            const float2 ma = mul2(m, a[k]);
-            fq[k] = mul2(ma, fma2(mul2(rs, u), a[k], mul2(two(-1.f), h)));
-            f1[k] = fma2(two(-1.f), rr, two(1.f));
-            fx[k] = mul2(s, ii);
-            fi[k] = mul2(mul2(s, u), fma2(two(-1.f), ii, two(1.f)));
-            h = fma2(a[k], h, mul2(s, u));
-            gy[k] = dy[k].get();
-            if (gated) {
-                const float2 zz = z[k].get(), p = sigmoid2(zz);
-                const float2 dz = mul2(mul2(gy[k], h), make_float2(dsilu(zz.x, p.x), dsilu(zz.y, p.y)));
-                if (k < n) put_two<T, WIDE>(io.dz.at(b, 0, t + k) + cc, dz, in0, in1);
-                gy[k] = mul2(gy[k], mul2(zz, p));
-            }
-            if (k >= n) {   // behind the end: nothing changes
-                a[k] = two(1.f);
-                gy[k] = two(0.f);
+        };
+        if (far) states(std::true_type{});
+        else states(std::false_type{});
+        if (n < kRun) {   // behind the end: nothing changes
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) {
+                if (k >= n) {
+                    a[k] = two(1.f);
+                    gy[k] = fq[k] = fi[k] = two(0.f);
+                }
             }
         }
         float2 A = two(1.f), H = two(0.f);
 #pragma unroll
         for (int k = kRun - 1; k >= 0; --k) {
-            if (PACKED && (ends >> k & 1)) {
-                A = two(-1.f);
-                H = io.dhT ? load2(io.dhT + (size_t)__shfl_sync(0xffffffffu, seq, k) * g.D + c, in0, in1) : two(0.f);
-            }
+            if (PACKED && (ends >> k & 1))
+                H = io.dhT ? load2(io.dhT + (size_t)seq_at(g.cu, g.Nseq, t + k) * g.D + c, in0, in1) : two(0.f);
             A = mul2(A, a[k]);
             H = mul2(a[k], add2(gy[k], H));
         }
-        float2 back = exchange(sm, st & 1, g.CL, g.CL - 1 - rank, kWarps - 1 - warp, A, H, carry);
+        A = make_float2(fmaxf(A.x, kLeast), fmaxf(A.y, kLeast));
+        if (PACKED && ends) A = two(-1.f);
+        float2 back = exchange<W, Q, PACKED, true>(sm, st & 1, g.CL, rank, A, H, carry);
+        if (st + S - 1 < steps) ring.ask(st + S - 1, token(st + S - 1), te - token(st + S - 1));
+        ring.asked();
 #pragma unroll
         for (int k = kRun - 1; k >= 0; --k) {
             if (PACKED && (ends >> k & 1))
-                back = io.dhT ? load2(io.dhT + (size_t)__shfl_sync(0xffffffffu, seq, k) * g.D + c, in0, in1) : two(0.f);
+                back = io.dhT ? load2(io.dhT + (size_t)seq_at(g.cu, g.Nseq, t + k) * g.D + c, in0, in1) : two(0.f);
             const float2 dh = add2(gy[k], back), q = mul2(dh, fq[k]), drg = mul2(q, f1[k]), dig = mul2(dh, fi[k]);
             back = mul2(a[k], dh);
             if (PACKED && (starts >> k & 1) && io.dh0)
-                store2(io.dh0 + (size_t)__shfl_sync(0xffffffffu, seq, k) * g.D + c, back, in0, in1);
+                store2(io.dh0 + (size_t)seq_at(g.cu, g.Nseq, t + k) * g.D + c, back, in0, in1);
+            ring.put(st, kX, k, mul2(dh, fx[k]));
+            ring.put(st, kRg, k, drg);
+            ring.put(st, kIg, k, dig);
             if (k < n) {
-                put_two<T, WIDE>(io.dx.at(b, 0, t + k) + cc, mul2(dh, fx[k]), in0, in1);
-                put_two<T, WIDE>(io.drg.at(b, 0, t + k) + cc, drg, in0, in1);
-                put_two<T, WIDE>(io.dig.at(b, 0, t + k) + cc, dig, in0, in1);
                 sq = add2(sq, q);
                 sr = add2(sr, drg);
                 si = add2(si, dig);
             }
         }
+        ring.flush(st, gated ? 15 : 7, tw, nw);
     }
-    if (!PACKED && io.dh0 && rank == 0 && warp == 0) store2(io.dh0 + (size_t)b * g.D + c, carry, in0, in1);
+    ring.end();
+    if (!PACKED && io.dh0 && rank == 0 && warp == 0 && lane < L) store2(io.dh0 + (size_t)b * g.D + c, carry, in0, in1);
 
-    red[0][warp][lane] = mul2(sq, dk);
-    red[1][warp][lane] = sr;
-    red[2][warp][lane] = si;
+    auto put = [&](int i, float2 v) {   // the sum over a warp's runs, in a fixed order
+#pragma unroll
+        for (int d = L; d < 32; d *= 2) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, d);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
+        }
+        if (lane < L) red[i][warp][lane] = v;
+    };
+    put(0, mul2(sq, dk));
+    put(1, sr);
+    put(2, si);
     __syncthreads();
-    if (warp < 3) {
+    if (warp < 3 && lane < L) {
         float2 v = red[warp][0][lane];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) v = add2(v, red[warp][w][lane]);
+        for (int w = 1; w < W; ++w) v = add2(v, red[warp][w][lane]);
         store2(io.part + (((size_t)b * g.CL + rank) * 3 + warp) * g.D + c, v, in0, in1);
     }
 }
@@ -144,18 +170,19 @@ cudaError_t bwd(const RecurCall &c, cudaStream_t st)
     RecurIo<T> io = {};
     const dn_recur_io *f = c.io;
     const dn_recur_grads *r = c.gr;
-    io.x = view_of<const T>(&f->x); io.rg = view_of<const T>(&f->rg); io.ig = view_of<const T>(&f->ig); io.z = view_of<const T>(&f->z);
-    io.dy = view_of<const T>(&r->dy); io.dx = view_of<T>(&r->dx); io.drg = view_of<T>(&r->drg); io.dig = view_of<T>(&r->dig);
-    io.dz = view_of<T>(&r->dz);
+    io.in[kX] = view_of<const T>(&f->x); io.in[kRg] = view_of<const T>(&f->rg); io.in[kIg] = view_of<const T>(&f->ig);
+    io.in[kZ] = view_of<const T>(&f->z); io.in[kDy] = view_of<const T>(&r->dy);
+    io.out[kX] = view_of<T>(&r->dx); io.out[kRg] = view_of<T>(&r->drg); io.out[kIg] = view_of<T>(&r->dig); io.out[kZ] = view_of<T>(&r->dz);
     io.keep = c.keep; io.dhT = r->dhT; io.dh0 = r->dh0; io.part = c.part;
-    const int e = sizeof(T);
-    bool wide = g.D % 2 == 0;
-    const dn_view *views[] = {&f->x, &f->rg, &f->ig, &f->z, &r->dy, &r->dx, &r->drg, &r->dig, &r->dz};
-    for (const dn_view *v : views) wide = wide && can_vector(v, e, 2 * e);
     if (g.cu && io.dh0 && g.Nseq > 0) k_recur_empty_grad<<<g.Nseq, 256, 0, st>>>(g.cu, g.D, io.dhT, io.dh0);
-    cudaError_t rc;
-    if (g.cu) rc = wide ? recur_launch(k_recur_bwd<T, true, true>, g, st, io) : recur_launch(k_recur_bwd<T, false, true>, g, st, io);
-    else rc = wide ? recur_launch(k_recur_bwd<T, true, false>, g, st, io) : recur_launch(k_recur_bwd<T, false, false>, g, st, io);
+    constexpr int W = bwd_warps(sizeof(T)), S = bwd_stages(sizeof(T));
+    const bool gated = io.in[kZ].p != nullptr;
+    const int smem = S * (gated ? 5 : 4) * W * kRun * 64 * (int)sizeof(T);
+    RecurMaps m = {};
+    const int mode = recur_mode(m, io, gated ? 31 : 23, gated ? 15 : 7, g);
+    const cudaError_t rc = recur_variant<T>(g, mode, [&](auto q, auto how, auto packed) {
+        return recur_launch(k_recur_bwd<T, decltype(q)::value, decltype(how)::value, decltype(packed)::value>, g, 32 * W, smem, st, m, g, io);
+    });
     if (rc != cudaSuccess) return rc;
     const ColSum s = {c.part, (long long)g.B * g.CL, g.D, 3, {r->dlam, r->drg_bias, r->dig_bias}, {1, 1, 1}};
     return col_sum(s, nullptr, st);

@@ -12,9 +12,6 @@
 // D in bf16 (2^-9 of each value) is what a bf16 input's gradient is computed from: the sums over the vocabulary and over the tokens
 // are float32.  float32 inputs are split into three bf16 planes, 8 bits each, and six of their nine products kept: what is
 // left out is 2^-24 of the whole.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "pair.cuh"
 #include "xent.h"
 
@@ -390,27 +387,10 @@ __global__ void __launch_bounds__(256) k_pack(lay::View<const T> v, int R, int T
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            ptr = nullptr;
-        return (PFN_cuTensorMapEncodeTiled_v12000)ptr;
-    }();
-    return fn;
-}
-
-// bf16 [planes][rows][cols], boxes of 64 columns x `high` rows, 128-byte swizzle; zero outside
+// bf16 [planes][rows][cols], boxes of 64 columns x `high` rows
 bool make_map(CUtensorMap *m, const Operand &o, long long cols, long long rows, int planes, int high)
 {
-    cuuint64_t dim[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
-    cuuint64_t stride[2] = {(cuuint64_t)o.pitch * 2, (cuuint64_t)(planes > 1 ? o.plane : o.pitch) * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)high, 1}, es[3] = {1, 1, 1};
-    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(o.p), dim, stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return lay::tensor_map(m, false, o.p, cols, rows, planes, o.pitch, o.plane, 64, high, true);
 }
 
 template <bool A_MN, bool B_MN, int EPI, bool SEG>
@@ -472,7 +452,6 @@ cudaError_t begin(const Call &c, bool bwd, cudaStream_t st)
 
 }  // namespace
 
-bool usable() { return encode_fn() != nullptr; }
 int tiles_of(int n) { return (int)(((long long)n + TILE - 1) / TILE); }
 
 cudaError_t forward(const Call &c, cudaStream_t st)

@@ -31,7 +31,6 @@ struct Call {
     void *dw;
 };
 
-bool usable();                      // the tensor maps' encoder is there
 int tiles_of(int n);                // of 256
 cudaError_t forward(const Call &c, cudaStream_t st);
 cudaError_t backward(const Call &c, cudaStream_t st);

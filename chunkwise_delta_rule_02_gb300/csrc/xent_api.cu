@@ -121,7 +121,7 @@ dn_status dn_xent_fwd(const dn_xent_shape *shape, const dn_view *x, const dn_vie
     Call c;
     const size_t need = layout(c, shape, x, w, false, (char *)ws);
     if (!ws || !aligned(ws, 16) || ws_bytes < need) return DN_ERR_WORKSPACE;
-    if (!usable()) return DN_ERR_CUDA;
+    if (!lay::has_tensor_maps()) return DN_ERR_CUDA;
     c.targets = targets; c.loss = loss; c.lse = lse;
     return status_of(forward(c, (cudaStream_t)stream));
 }
@@ -141,7 +141,7 @@ dn_status dn_xent_bwd(const dn_xent_shape *shape, const dn_view *x, const dn_vie
     Call c;
     const size_t need = layout(c, shape, x, w, true, (char *)ws);
     if (!ws || !aligned(ws, 16) || ws_bytes < need) return DN_ERR_WORKSPACE;
-    if (!usable()) return DN_ERR_CUDA;
+    if (!lay::has_tensor_maps()) return DN_ERR_CUDA;
     c.targets = targets; c.lse = const_cast<float *>(lse); c.dloss = dloss; c.dx = dx; c.dw = dw;
     return status_of(backward(c, (cudaStream_t)stream));
 }

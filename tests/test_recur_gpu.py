@@ -52,6 +52,16 @@ CASES = [  # B, T, D, dtype, bias, gate, state, lengths
     (1, 700, 128, F32, False, True, True, [1, 511, 1, 187]),
     (1, 24, 8, BF, True, False, True, [1] * 24),
     (1, 0, 8, BF, True, False, True, [0, 0]),
+    # channels enough for tiles of 64, in clusters and alone, by boxes, words and elements
+    (5, 300, 640, BF, True, True, True, None),
+    (3, 200, 1000, F32, True, True, True, None),
+    (2, 330, 1302, BF, True, True, True, None),
+    (2, 330, 1301, BF, True, False, True, None),
+    (2, 130, 1301, F32, True, True, False, None),
+    (1, 700, 1304, BF, True, True, True, [0, 100, 1, 300, 299, 0]),
+    (1, 600, 1301, BF, True, True, True, [599, 1]),
+    (1, 300, 1301, F32, False, True, True, [1, 2, 3, 294]),
+    (1, 2100, 24, BF, True, True, True, [700, 1400]),
 ]
 
 
