@@ -5,17 +5,17 @@
 //     h_t = a_t h_{t-1} + s_t u_t,  u = sigmoid(ig + ig_bias) x,  y = z ? h silu(z) : h
 //
 // Layout.  A lane holds two neighbouring channels of a run of kRun tokens; a warp holds Q runs one after
-// another of 64 / Q channels (Q = 4 where 64-channel tiles would leave most SMs idle), a block W warps, a
+// another of 64 / Q channels (Q = 2 or 4 where wider tiles would leave SMs idle), a block W warps, a
 // cluster up to 8 blocks.  A run is a linear map h -> A h + H of what enters it; the runs of a warp exchange
 // their maps by shuffles, a block's warps through shared memory, the cluster's blocks through each
 // other's shared memory, and every thread then steps through its run.  So each input is read once whatever
 // the number of rows: splitting the time axis over blocks costs a barrier a step, and no second pass
 // over the inputs.
 //
-// Every warp has a ring of stages of its inputs in shared memory, filled by TMA ahead of their use (a box of
-// 64 / Q channels x kRun Q tokens an array) and emptied the same way: a result takes the place of the input it
-// belongs to.  Arrays that a tensor map cannot describe (rows that do not start at 16 bytes) go through the same
-// ring in words of 4 bytes, or, bf16 that do not start at those, element by element in the step that needs them.
+// The inputs of two steps lie in shared memory, filled by TMA (a box of 64 / Q channels and the block's tokens an
+// array): a step's are in registers when its maps are exchanged, and the barrier there frees their place for the
+// step after the next.  Arrays that a tensor map cannot describe (rows that do not start at 16 bytes) get there in
+// words of 4 bytes, or, bf16 that do not start at those, element by element in the step that needs them.
 #pragma once
 
 #include <type_traits>
@@ -30,14 +30,15 @@ constexpr int kRun = 8;                       // tokens of a lane and step (and 
 constexpr int kMaxCluster = 8;
 constexpr long long kRecurBudget = 4000000000LL;   // clock cycles (about 2 s) for any one wait
 
-// Warps of a block, stages of the ring, blocks an SM holds, by the type's bytes
-__host__ __device__ constexpr int fwd_warps(int bytes) { return bytes == 2 ? 8 : 4; }
-__host__ __device__ constexpr int bwd_warps(int bytes) { return bytes == 2 ? 6 : 4; }
-__host__ __device__ constexpr int fwd_stages(int) { return 3; }
-__host__ __device__ constexpr int bwd_stages(int bytes) { return bytes == 2 ? 3 : 2; }
-constexpr int kResident = 2;
+// Warps of a block by the type's bytes, blocks that an SM holds.  bf16 forward: 12 warps twice, what 80 registers allow (4 x 8192
+// tokens of 2048 channels with the output gate: 148 us; 8 warps three times 157, 16 warps 186).  Backward: 6 warps
+// twice at 164 registers (training step of 8 x 4096 tokens: 437 us; 4 warps three times 459; runs of 4 tokens, 8
+// warps twice: 436, with twice the kept states).
+__host__ __device__ constexpr int fwd_warps(int bytes) { return bytes == 2 ? 12 : 6; }
+__host__ __device__ constexpr int bwd_warps(int bytes) { return bytes == 2 ? 6 : 5; }
+constexpr int kFwdResident = 2, kBwdResident = 2;
 
-enum { kElements, kWords, kTma };             // how a ring is filled
+enum { kElements, kWords, kTma };             // how inputs get to shared memory
 
 struct RecurDims {
     int B, T, D, Nseq, tiles, CL, Q;   // tiles: channel tiles of a row; CL: blocks that share a row's tokens
@@ -47,20 +48,19 @@ struct RecurDims {
     uint32_t *status;
 };
 
-// Arrays: inputs first; a result lies in its input's place
 enum { kX, kRg, kIg, kZ, kDy, kArrays };
 
 template <class T>
 struct RecurIo {
     View<const T> in[kArrays];     // x, rg, ig, z or null, dy
-    View<T> out[kArrays];          // forward: y at kX; backward: dx, drg, dig, dz
+    View<T> out[4];                // forward: y at kX; backward: dx, drg, dig, dz
     float *hT, *keep;              // keep: state entering every kRun-th token, [B][ceil(T / kRun)][D], or null
     const float *dhT;
     float *dh0, *part;             // part: [B][CL][3][D] sums of dlam, drg_bias, dig_bias
 };
 
 struct RecurMaps {
-    CUtensorMap in[kArrays], out[kArrays];
+    CUtensorMap in[kArrays];
 };
 
 struct RecurCall {
@@ -228,30 +228,28 @@ __device__ __forceinline__ void box_load(void *dst, const CUtensorMap *map, uint
         : "memory");
 }
 
-__device__ __forceinline__ void box_store(const CUtensorMap *map, const void *src, int c, int t, int b)
-{
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"((uint64_t)map),
-                 "r"(sm100::smem_u32(src)), "r"(c), "r"(t), "r"(b)
-                 : "memory");
-}
+__host__ __device__ constexpr int recur_block_bytes(int CL, int Q) { return CL > 1 ? 2 * CL * (32 / Q) * 16 : 0; }
 
 template <int W, int Q>
 struct RecurShared {
     float4 warp[2][W][32 / Q];
-    float4 block[2][kMaxCluster][32 / Q];
-    uint64_t bar[W][3];
+    float2 carry[2][32 / Q];
+    uint64_t bar[2];
 };
 
 // The maps of a step's runs, exchanged: (A, H) of this thread's run in, what enters it out (the state before it in the order
-// of the pass, BACK: from the last run to the first); `carry`, what entered the step, becomes what leaves it.  `rank` is the block's
-// place in the cluster.  Maps of a step lie in buffer `par`, so that one barrier a level suffices.
-template <int W, int Q, bool CUT, bool BACK>
-__device__ __forceinline__ float2 exchange(RecurShared<W, Q> &sm, int par, int CL, int rank, float2 A, float2 H, float2 &carry)
+// of the pass, BACK: from the last run to the first).  What entered the step is `carry` in a cluster, and becomes what leaves it;
+// a block alone has it in shared memory, where the step's last run leaves it (leave()).  `rank` is the block's place in the
+// cluster.  Maps of a step lie in buffer `par`, so that one barrier a level suffices; `block`: [2][CL][32 / Q] of the cluster's blocks.
+// `freed` is called behind the first barrier.
+template <int W, int Q, bool CUT, bool BACK, class F>
+__device__ __forceinline__ float2 exchange(RecurShared<W, Q> &sm, float4 *block, int par, int CL, int rank, float2 A, float2 H, float2 &carry,
+                                           F freed)
 {
     constexpr int L = 32 / Q;
     const int lane = threadIdx.x & 31, l = lane % L, warp = threadIdx.x >> 5;
     const int mine = BACK ? W - 1 - warp : warp, at = BACK ? CL - 1 - rank : rank, q = BACK ? Q - 1 - lane / L : lane / L;
-    float2 pA = two(1.f), pH = two(0.f);   // of what lies before this run: in the warp, then in the block
+    float2 pA = two(1.f), pH = two(0.f);   // of what lies before this run in its warp
     if constexpr (Q > 1) {
         auto before = [&](float2 v, int d) {
             return BACK ? make_float2(__shfl_down_sync(0xffffffffu, v.x, d * L), __shfl_down_sync(0xffffffffu, v.y, d * L))
@@ -274,13 +272,14 @@ __device__ __forceinline__ float2 exchange(RecurShared<W, Q> &sm, int par, int C
     }
     if (q == Q - 1) sm.warp[par][mine][l] = make_float4(A.x, A.y, H.x, H.y);
     __syncthreads();
-    float2 h = carry;
+    freed();
+    float2 h;
     if (CL == 1) {
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            if (w == mine) h = carry;
+        h = sm.carry[par][l];
+#pragma unroll 4
+        for (int w = 0; w < mine; ++w) {
             const float4 m = sm.warp[par][w][l];
-            carry = pass<CUT>(make_float2(m.x, m.y), make_float2(m.z, m.w), carry);
+            h = pass<CUT>(make_float2(m.x, m.y), make_float2(m.z, m.w), h);
         }
     } else {
         float2 wA = two(1.f), wH = two(0.f), oA = wA, oH = wH;   // of the warps before this one; of all
@@ -295,12 +294,13 @@ __device__ __forceinline__ float2 exchange(RecurShared<W, Q> &sm, int par, int C
         }
         // each warp tells some blocks
         if (lane < L)
-            for (int k = warp; k < CL; k += W) remote_store(&sm.block[par][at][l], k, make_float4(oA.x, oA.y, oH.x, oH.y));
+            for (int k = warp; k < CL; k += W) remote_store(block + (par * CL + at) * L + l, k, make_float4(oA.x, oA.y, oH.x, oH.y));
         __syncwarp();
         cluster_barrier();
+        h = carry;
         for (int k = 0; k < CL; ++k) {
             if (k == at) h = carry;
-            const float4 m = sm.block[par][k][l];
+            const float4 m = block[(par * CL + k) * L + l];
             carry = pass<CUT>(make_float2(m.x, m.y), make_float2(m.z, m.w), carry);
         }
         h = pass<CUT>(wA, wH, h);
@@ -308,10 +308,20 @@ __device__ __forceinline__ float2 exchange(RecurShared<W, Q> &sm, int par, int C
     return Q > 1 ? pass<CUT>(pA, pH, h) : h;
 }
 
-// Which of this lane's run's tokens t .. t+n-1 (n <= kRun) start and which end a sequence, as bit masks, and the sequence of the
-// first of them; the warp's tokens are w .. w+nw-1.  Tokens inside the sequence that the warp looked up last have neither.
+// What leaves the step's last run, for the next step
+template <int W, int Q, bool BACK>
+__device__ __forceinline__ void leave(RecurShared<W, Q> &sm, int par, float2 h)
+{
+    constexpr int L = 32 / Q;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x >> 5 == (BACK ? 0 : W - 1) && lane / L == (BACK ? 0 : Q - 1)) sm.carry[par ^ 1][lane % L] = h;
+}
+
+// Which of this lane's run's tokens t .. t+n-1 (n <= kRun) start and which end a sequence, as bit masks; the warp's tokens are
+// w .. w+nw-1.  Tokens inside the sequence that the warp looked up last have neither.
 struct Edges {
     int lo, hi;                    // that sequence
+    int first, last;               // the run's first and last token's, where there are edges
     __device__ __forceinline__ void find(const RecurDims &g, int w, int nw, int t, int n, uint32_t &starts, uint32_t &ends)
     {
         starts = ends = 0;
@@ -319,20 +329,42 @@ struct Edges {
         const int s = seq_at(g.cu, g.Nseq, w);
         lo = g.cu[s];
         hi = g.cu[s + 1];
-        if (lo < w && w + nw < hi) return;
+        if (n <= 0 || (lo < w && w + nw < hi)) return;
+        first = last = up(g.cu, s, t);
+#pragma unroll 1
         for (int k = 0; k < n; ++k) {
-            const int q = seq_at(g.cu, g.Nseq, t + k);
-            starts |= (g.cu[q] == t + k ? 1u : 0u) << k;
-            ends |= (g.cu[q + 1] == t + k + 1 ? 1u : 0u) << k;
+            last = up(g.cu, last, t + k);
+            starts |= (g.cu[last] == t + k ? 1u : 0u) << k;
+            ends |= (g.cu[last + 1] == t + k + 1 ? 1u : 0u) << k;
         }
+    }
+    // The sequence of a token from that of an earlier (later) one
+    __device__ __forceinline__ static int up(const int32_t *cu, int s, int t)
+    {
+        while (cu[s + 1] <= t) ++s;
+        return s;
+    }
+    __device__ __forceinline__ static int down(const int32_t *cu, int s, int t)
+    {
+        while (cu[s] > t) --s;
+        return s;
     }
 };
 
-// A warp's ring.  `sets`: bit mask of the input arrays that a call has; their places follow each other.
-template <class T, int W, int Q, int S, int MODE>
-struct Ring {
-    static constexpr int kSlot = kRun * 64 * (int)sizeof(T), C = 64 / Q, R = kRun * Q;   // bytes, channels, tokens of an array's place
-    char *base;                    // of this warp's first place
+// Tokens of a box: 256 at most
+template <int W>
+__host__ __device__ constexpr int box_rows(int Q)
+{
+    return W * kRun * Q / ((W * kRun * Q + 255) / 256);
+}
+
+// The inputs of a block's two steps.  `sets`: bit mask of the arrays that a call has; their places follow each other.
+template <class T, int W, int Q, int MODE>
+struct Inputs {
+    static constexpr int C = 64 / Q, R = kRun * Q, kPlace = W * kRun * 64 * (int)sizeof(T);   // channels, tokens of a warp, bytes of an array's place
+    static constexpr int kRows = box_rows<W>(Q), kBoxes = W * R / kRows;                         // of an array
+    static_assert(kRows * kBoxes == W * R, "boxes share the rows evenly");
+    char *base;
     uint64_t *bar;
     const RecurIo<T> *io;
     const RecurMaps *maps;
@@ -340,17 +372,26 @@ struct Ring {
     bool failed;
 
     __device__ __forceinline__ int place(int array) const { return __popc(sets & ((1 << array) - 1)); }
-    __device__ __forceinline__ char *slot(int st, int array) const { return base + ((size_t)(st % S) * count + place(array)) * W * kSlot; }
-    // of a lane's two channels of its run's token k
-    __device__ __forceinline__ T *cell(int st, int array, int k) const
+    __device__ __forceinline__ char *slot(int st, int array) const { return base + ((st & 1) * count + place(array)) * kPlace; }
+    // of a lane's two channels of its run's first token
+    __device__ __forceinline__ const T *cells(int st, int array) const
     {
         const int lane = threadIdx.x & 31, l = lane % (32 / Q), q = lane / (32 / Q);
-        return (T *)slot(st, array) + (q * kRun + k) * C + 2 * l;
+        return (const T *)slot(st, array) + (((threadIdx.x >> 5) * Q + q) * kRun) * C + 2 * l;
+    }
+    __device__ __forceinline__ static float2 at(const T *cells, int k)
+    {
+        Vec<T, 2> v;
+        float f[2];
+        v.load(cells + k * C);
+        v.get(f);
+        return make_float2(f[0], f[1]);
     }
 
+    // Before a block's first barrier
     __device__ __forceinline__ void init(char *sm, uint64_t *bars, const RecurIo<T> *io_, const RecurMaps *maps_, int sets_, int b_, int c0_, int D_)
     {
-        base = sm + (threadIdx.x >> 5) * kSlot;
+        base = sm;
         bar = bars;
         io = io_;
         maps = maps_;
@@ -358,39 +399,62 @@ struct Ring {
         count = __popc(sets);
         b = b_; c0 = c0_; D = D_;
         failed = false;
-        if (MODE == kTma) {
-            if ((threadIdx.x & 31) == 0) {
-                for (int i = 0; i < S; ++i) sm100::mbar_init(&bar[i], 1);
-                sm100::fence_barrier_init();
-            }
-            __syncwarp();
+        if (MODE == kTma && threadIdx.x == 0) {
+            sm100::mbar_init(&bar[0], 1);
+            sm100::mbar_init(&bar[1], 1);
+            sm100::fence_barrier_init();
         }
     }
-    // Asks for step `st`, the warp's tokens t .. t + n - 1; what it overwrites has been stored.
-    __device__ __forceinline__ void ask(int st, int t, int n) const
+    // Asks for step `st`, the block's tokens t0 .. te - 1 at most; nobody reads what it overwrites any more.
+    __device__ __forceinline__ void ask(int st, int t0, int te) const
     {
         if (MODE == kTma) {
-            if ((threadIdx.x & 31) == 0) {
-                uint64_t *full = &bar[st % S];
-                sm100::bulk_wait_read();
-                sm100::mbar_expect_tx(full, count * kSlot);
+            if (threadIdx.x == 0) {
+                uint64_t *full = &bar[st & 1];
+                sm100::mbar_expect_tx(full, count * kPlace);
 #pragma unroll
                 for (int a = 0; a < kArrays; ++a)
-                    if (sets >> a & 1) box_load(slot(st, a), &maps->in[a], full, c0, t, b);
+                    if (sets >> a & 1)
+#pragma unroll
+                        for (int i = 0; i < kBoxes; ++i) box_load(slot(st, a) + i * (kPlace / kBoxes), &maps->in[a], full, c0, t0 + i * kRows, b);
             }
         } else if (MODE == kWords) {
-            constexpr int P = 4 / sizeof(T), N = R * C / P / 32;   // elements of a word; words of a lane
+            constexpr int P = 4 / sizeof(T), RW = C / P;           // elements of a word, words of a row
+            constexpr int H = RW > 32 ? RW / 32 : 1, V = RW > 32 ? 1 : 32 / RW;   // words of a row a lane, rows at a time
+            const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k0 = lane / RW, c = c0 + lane % RW * P;
+            const int t = t0 + warp * R + k0, n = te - t;
+            int bytes[H];
+            bool whole = n > R - V;
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                bytes[h] = max(0, min(4, (D - c - h * 32 * P) * (int)sizeof(T)));
+                whole = whole && bytes[h] == 4;
+            }
+#pragma unroll
             for (int a = 0; a < kArrays; ++a) {
                 if (!(sets >> a & 1)) continue;
                 const View<const T> v = io->in[a];
-                const uint32_t to = sm100::smem_u32(slot(st, a));
+                const uint32_t to = sm100::smem_u32(slot(st, a)) + warp * (kPlace / W) + 4 * lane;
+                const T *from = v.at(b, 0, t) + c;
+                auto copy = [&](auto all) {
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const int w = j * 32 + (threadIdx.x & 31), k = w / (C / P), c = w % (C / P) * P;
-                    const int bytes = k < n ? max(0, min(4, (D - c0 - c) * (int)sizeof(T))) : 0;
-                    const T *from = v.at(b, 0, bytes ? t + k : 0) + (bytes ? c0 + c : 0);
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + 4 * w), "l"(from), "r"(bytes) : "memory");
-                }
+                    for (int k = 0; k < R; k += V) {
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+                            const uint32_t dst = to + 4 * (k * RW + 32 * h);
+                            if constexpr (decltype(all)::value) {
+                                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(from + 32 * P * h) : "memory");
+                            } else {
+                                const int m = k < n ? bytes[h] : 0;
+                                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(m ? from + 32 * P * h : io->in[a].p), "r"(m)
+                                             : "memory");
+                            }
+                        }
+                        from += V * v.t;
+                    }
+                };
+                if (whole) copy(std::true_type{});
+                else copy(std::false_type{});
             }
         }
     }
@@ -399,19 +463,19 @@ struct Ring {
     {
         if (MODE == kWords) asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    // Waits for step st (or, elements, loads it)
-    __device__ __forceinline__ void get(int st, int t, int n, uint32_t *status)
+    // Waits for step st (or, elements, loads it): the block's tokens from t0
+    __device__ __forceinline__ void get(int st, int t0, int te, uint32_t *status)
     {
         if (MODE == kTma) {
-            if (!sm100::mbar_wait(&bar[st % S], (uint32_t)(st / S) & 1u, failed ? 1000 : kRecurBudget, nullptr)) {
+            if (!sm100::mbar_wait(&bar[st & 1], (uint32_t)(st >> 1) & 1u, failed ? 1000 : kRecurBudget, nullptr)) {
                 failed = true;
                 raise_status(status, kStatusTimeout);
             }
         } else if (MODE == kWords) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncwarp();
         } else {
-            const int lane = threadIdx.x & 31;
+            const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = t0 + warp * R, n = te - t;
             T v[kArrays][2 * kRun];
 #pragma unroll
             for (int a = 0; a < kArrays; ++a) {
@@ -428,72 +492,43 @@ struct Ring {
             for (int a = 0; a < kArrays; ++a) {
                 if (!(sets >> a & 1)) continue;
 #pragma unroll
-                for (int j = 0; j < 2 * kRun; ++j) ((T *)slot(st, a))[j * 32 + lane] = v[a][j];
+                for (int j = 0; j < 2 * kRun; ++j) ((T *)(slot(st, a) + warp * (kPlace / W)))[j * 32 + lane] = v[a][j];
             }
             __syncwarp();
         }
-    }
-    __device__ __forceinline__ float2 at(int st, int array, int k) const
-    {
-        Vec<T, 2> v;
-        float f[2];
-        v.load(cell(st, array, k));
-        v.get(f);
-        return make_float2(f[0], f[1]);
-    }
-    __device__ __forceinline__ void put(int st, int array, int k, float2 x) const
-    {
-        Vec<T, 2> v;
-        const float f[2] = {x.x, x.y};
-        v.set(f);
-        v.store(cell(st, array, k));
-    }
-    // Stores the results that were put in the places of `arrays`
-    __device__ __forceinline__ void flush(int st, int arrays, int t, int n) const
-    {
-        const int lane = threadIdx.x & 31;
-        if (MODE == kTma) {
-            sm100::fence_async_smem();
-            __syncwarp();
-            if (lane == 0 && n > 0) {
-#pragma unroll
-                for (int a = 0; a < kArrays; ++a)
-                    if (arrays >> a & 1) box_store(&maps->out[a], slot(st, a), c0, t, b);
-                sm100::bulk_commit();
-            }
-        } else {
-            __syncwarp();
-            for (int a = 0; a < kArrays; ++a) {
-                if (!(arrays >> a & 1)) continue;
-                const T *from = (const T *)slot(st, a);
-#pragma unroll
-                for (int j = 0; j < 2 * kRun; ++j) {
-                    const int i = j * 32 + lane, k = i / C, c = i % C;
-                    if (k < n && c0 + c < D) io->out[a].at(b, 0, t + k)[c0 + c] = from[i];
-                }
-            }
-        }
-    }
-    __device__ __forceinline__ void end() const
-    {
-        if (MODE == kTma && (threadIdx.x & 31) == 0) sm100::bulk_wait_all();
     }
 };
 
-// How a call's arrays are moved; TMA: their maps.  `in`, `out`: bit masks of the arrays there.
-template <class T>
-int recur_mode(RecurMaps &m, const RecurIo<T> &io, int in, int out, const RecurDims &g)
+// Two channels of a token of a result.  Where the inputs come by TMA both exist (D is even) and lie in one word (of two).
+template <int MODE, class T>
+__device__ __forceinline__ void put_two(T *p, float2 f, bool in0, bool in1)
 {
-    bool tma = g.T > 0, words = true;
+    if constexpr (MODE == kTma) {
+        Vec<T, 2> v;
+        const float e[2] = {f.x, f.y};
+        v.set(e);
+        if (in0) v.store(p);
+    } else {
+        if (in0) st_out(p, f.x);
+        if (in1) st_out(p + 1, f.y);
+    }
+}
+
+// How a call's inputs get to shared memory; TMA: their maps, in boxes of `rows` tokens.  `in`: bit mask of the arrays there.
+template <class T>
+int recur_mode(RecurMaps &m, const RecurIo<T> &io, int in, int rows, const RecurDims &g)
+{
+    bool tma = g.T > 0 && g.D % 2 == 0, words = true;
     for (int a = 0; a < kArrays; ++a) {
         const View<const T> &i = io.in[a];
-        const View<T> &o = io.out[a];
-        const int c = 64 / g.Q, r = kRun * g.Q;
         if (in >> a & 1) {
-            tma = tma && tensor_map(&m.in[a], sizeof(T) == 4, i.p, g.D, g.T, g.B, i.t, i.b, c, r, false);
+            tma = tma && tensor_map(&m.in[a], sizeof(T) == 4, i.p, g.D, g.T, g.B, i.t, i.b, 64 / g.Q, rows, false);
             words = words && (uintptr_t)i.p % 4 == 0 && (sizeof(T) == 4 || (i.t % 2 == 0 && i.b % 2 == 0));
         }
-        if (out >> a & 1) tma = tma && tensor_map(&m.out[a], sizeof(T) == 4, o.p, g.D, g.T, g.B, o.t, o.b, c, r, false);
+        if (a < 4 && io.out[a].p) {
+            const View<T> &o = io.out[a];
+            tma = tma && (uintptr_t)o.p % (2 * sizeof(T)) == 0 && o.t % 2 == 0 && o.b % 2 == 0;
+        }
     }
     return tma ? kTma : words ? kWords : kElements;
 }
@@ -508,7 +543,7 @@ cudaError_t recur_variant(const RecurDims &g, int mode, F f)
         if (mode == kWords || sizeof(T) == 4) return how(std::integral_constant<int, kWords>{});
         return how(std::integral_constant<int, sizeof(T) == 4 ? kWords : kElements>{});
     };
-    return g.Q == 4 ? with(std::integral_constant<int, 4>{}) : with(std::integral_constant<int, 1>{});
+    return g.Q == 4 ? with(std::integral_constant<int, 4>{}) : g.Q == 2 ? with(std::integral_constant<int, 2>{}) : with(std::integral_constant<int, 1>{});
 }
 
 // One launch over channel tiles x rows, CL blocks of a cluster each.

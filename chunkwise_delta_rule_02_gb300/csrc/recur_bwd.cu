@@ -17,25 +17,27 @@ namespace lay {
 namespace {
 
 template <class T, int Q, int MODE, bool PACKED>
-__global__ void __launch_bounds__(32 * bwd_warps(sizeof(T))) k_recur_bwd(const __grid_constant__ RecurMaps maps, RecurDims g, RecurIo<T> io)
+__global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_recur_bwd(const __grid_constant__ RecurMaps maps, RecurDims g, RecurIo<T> io)
 {
-    constexpr int W = bwd_warps(sizeof(T)), S = bwd_stages(sizeof(T)), L = 32 / Q, R = kRun * Q;
+    constexpr int W = bwd_warps(sizeof(T)), L = 32 / Q, R = kRun * Q;
+    constexpr bool kShort = MODE != kTma || PACKED;   // one copy of each loop: these run fewer steps, and wait for instructions
     extern __shared__ __align__(128) char raw[];
+    float4 *block = reinterpret_cast<float4 *>(raw);   // maps of the cluster's blocks, then the inputs
     __shared__ RecurShared<W, Q> sm;
     __shared__ float2 red[3][W][L];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = g.CL > 1 ? cluster_rank() : 0;
-    const int id = blockIdx.x / g.CL, b = id / g.tiles, c0 = (id - b * g.tiles) * (64 / Q), c = c0 + 2 * (lane % L), q = lane / L * kRun;
+    const int id = blockIdx.x / g.CL, b = id / g.tiles, c0 = (id - b * g.tiles) * (64 / Q), c = c0 + 2 * (lane % L);
+    const int q = warp * R + lane / L * kRun;     // of this lane's run, in a block's tokens
     const bool in0 = c < g.D, in1 = c + 1 < g.D;
     const bool gated = io.in[kZ].p != nullptr;
-    Ring<T, W, Q, S, MODE> ring;
-    ring.init(raw, sm.bar[warp], &io, &maps, gated ? 31 : 23, b, c0, g.D);
+    Inputs<T, W, Q, MODE> inputs;
+    inputs.init(raw + recur_block_bytes(g.CL, Q), sm.bar, &io, &maps, gated ? 31 : 23, b, c0, g.D);
     const int te = PACKED ? g.cu[g.Nseq] : g.T;
     const int span = W * R * g.CL, steps = (te + span - 1) / span;
-    const int first = (rank * W + warp) * R;
-    auto token = [&](int st) { return (steps - 1 - st) * span + first; };   // step st handles the st-th span from the end
-    for (int st = 0; st < S - 1; ++st) {
-        if (st < steps) ring.ask(st, token(st), te - token(st));
-        ring.asked();
+    int t0 = (steps - 1) * span + rank * W * R;   // the block's first token of a step; step st handles the st-th span from the end
+    for (int st = 0; st < 2; ++st) {
+        if (st < steps) inputs.ask(st, t0 - st * span, te);
+        inputs.asked();
     }
     RecurParams par;
     float2 dk;
@@ -43,53 +45,62 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T))) k_recur_bwd(const _
     const bool far = par.far();
     float2 carry = two(0.f);   // the gradient that reaches a token's state from behind it
     if (!PACKED && io.dhT) carry = load2(io.dhT + (size_t)b * g.D + c, in0, in1);
-    const size_t kept = (g.T + kRun - 1) / kRun;
-    auto kept_at = [&](int st) {   // the state that enters this lane's run
-        const int t = token(st) + q;
-        return st < steps && t < te ? load2(io.keep + ((size_t)b * kept + t / kRun) * g.D + c, in0, in1) : two(0.f);
-    };
-    float2 next = kept_at(0);
+    if (warp == 0 && lane < L) sm.carry[0][lane] = carry;
+    const float *keep = io.keep + (size_t)b * ((g.T + kRun - 1) / kRun) * g.D + c;
+    auto kept_at = [&](int t) { return t >= 0 && t < te ? load2(keep + (size_t)(t / kRun) * g.D, in0, in1) : two(0.f); };
+    float2 next = kept_at(t0 + q);   // the state that enters this lane's run
     float2 sq = two(0.f), sr = two(0.f), si = two(0.f);
-    Edges edges = {0, 0};
-    if (g.CL > 1) cluster_barrier();   // all of the cluster's blocks run before one writes to another
+    Edges edges = {};
+    int seq = 0;
+    if (MODE == kTma) __syncthreads();   // the barriers exist
+    if (g.CL > 1) cluster_barrier();     // all of the cluster's blocks run before one writes to another
 
-    for (int st = 0; st < steps; ++st) {
-        const int tw = token(st), nw = min(R, te - tw), t = tw + q, n = max(0, min(kRun, te - t));
+    float2 back = carry;
+    for (int st = 0; st < steps; ++st, t0 -= span) {
+        const int t = t0 + q, n = te - t;   // tokens of the run that exist: 0 or less to kRun or more
         uint32_t starts = 0, ends = 0;
-        if (PACKED) edges.find(g, tw, nw, t, n, starts, ends);
+        if (PACKED) edges.find(g, t0 + warp * R, min(R, te - t0 - warp * R), t, min(kRun, n), starts, ends);
         float2 h = next;
-        next = kept_at(st + 1);
-        ring.get(st, tw, nw, g.status);
+        next = kept_at(t - span);
+        inputs.get(st, t0, te, g.status);
 
         // the run's states, and of each token what dh is multiplied with
         float2 a[kRun], gy[kRun], fq[kRun], f1[kRun], fx[kRun], fi[kRun];
+        const T *px = inputs.cells(st, kX), *pr = inputs.cells(st, kRg), *pi = inputs.cells(st, kIg), *pz = inputs.cells(st, kZ);
+        const T *pd = inputs.cells(st, kDy);
+        const bool whole = n >= kRun;
+        seq = edges.first;
         auto states = [&](auto wide) {
+            T *p = gated ? io.out[kZ].at(b, 0, t) + c : nullptr;
 #pragma unroll
             for (int k = 0; k < kRun; ++k) {
-                const float2 r = gate(ring.at(st, kRg, k), par.rb), m = mul2(par.km, r);
-                const float2 i = gate(ring.at(st, kIg, k), par.ib), u = mul2(i, ring.at(st, kX, k));
+                const float2 r = gate(inputs.at(pr, k), par.rb), m = mul2(par.km, r);
+                const float2 i = gate(inputs.at(pi, k), par.ib), u = mul2(i, inputs.at(px, k));
                 float2 y, rs;
                 decay_of<decltype(wide)::value>(m, a[k], y, rs);
                 const float2 s = mul2(y, rs), su = mul2(s, u);
-                if (PACKED && (starts >> k & 1))
-                    h = g.h0 ? load2(g.h0 + (size_t)seq_at(g.cu, g.Nseq, t + k) * g.D + c, in0, in1) : two(0.f);
+                if (PACKED && (starts >> k & 1)) {
+                    seq = edges.up(g.cu, seq, t + k);
+                    h = g.h0 ? load2(g.h0 + (size_t)seq * g.D + c, in0, in1) : two(0.f);
+                }
                 // u a / s comes with m / s: m rs u a, which is 0 where m is
                 fq[k] = mul2(mul2(m, a[k]), sub2(mul2(mul2(rs, u), a[k]), h));
                 f1[k] = sub2(two(1.f), r);
                 fx[k] = mul2(s, i);
                 fi[k] = mul2(su, sub2(two(1.f), i));
                 h = fma2(a[k], h, su);
-                gy[k] = ring.at(st, kDy, k);
+                gy[k] = inputs.at(pd, k);
                 if (gated) {
-                    const float2 z = ring.at(st, kZ, k), p = sigmoid2(z);
+                    const float2 z = inputs.at(pz, k), pp = sigmoid2(z);
                     // silu'(z) = p (1 + z (1 - p))
-                    const float2 ds = mul2(p, fma2(z, sub2(two(1.f), p), two(1.f)));
-                    ring.put(st, kZ, k, mul2(mul2(gy[k], h), ds));
-                    gy[k] = mul2(gy[k], mul2(z, p));
+                    const float2 ds = mul2(pp, fma2(z, sub2(two(1.f), pp), two(1.f)));
+                    if (whole || k < n) put_two<MODE>(p, mul2(mul2(gy[k], h), ds), in0, in1);
+                    p += io.out[kZ].t;
+                    gy[k] = mul2(gy[k], mul2(z, pp));
                 }
             }
         };
-        if (far) states(std::true_type{});
+        if (kShort || far) states(std::true_type{});
         else states(std::false_type{});
         if (n < kRun) {   // behind the end: nothing changes
 #pragma unroll
@@ -101,39 +112,61 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T))) k_recur_bwd(const _
             }
         }
         float2 A = two(1.f), H = two(0.f);
+        seq = edges.last;
 #pragma unroll
         for (int k = kRun - 1; k >= 0; --k) {
-            if (PACKED && (ends >> k & 1))
-                H = io.dhT ? load2(io.dhT + (size_t)seq_at(g.cu, g.Nseq, t + k) * g.D + c, in0, in1) : two(0.f);
+            if (PACKED && (ends >> k & 1)) {
+                seq = edges.down(g.cu, seq, t + k);
+                H = io.dhT ? load2(io.dhT + (size_t)seq * g.D + c, in0, in1) : two(0.f);
+            }
             A = mul2(A, a[k]);
             H = mul2(a[k], add2(gy[k], H));
         }
         A = make_float2(fmaxf(A.x, kLeast), fmaxf(A.y, kLeast));
         if (PACKED && ends) A = two(-1.f);
-        float2 back = exchange<W, Q, PACKED, true>(sm, st & 1, g.CL, rank, A, H, carry);
-        if (st + S - 1 < steps) ring.ask(st + S - 1, token(st + S - 1), te - token(st + S - 1));
-        ring.asked();
+        back = exchange<W, Q, PACKED, true>(sm, block, st & 1, g.CL, rank, A, H, carry, [&] {
+            if (st + 2 < steps) inputs.ask(st + 2, t0 - 2 * span, te);
+            inputs.asked();
+        });
+        T *pdx = io.out[kX].at(b, 0, t + kRun - 1) + c, *pdr = io.out[kRg].at(b, 0, t + kRun - 1) + c, *pdi = io.out[kIg].at(b, 0, t + kRun - 1) + c;
+        seq = edges.last;
+        auto outputs = [&](auto all) {
 #pragma unroll
-        for (int k = kRun - 1; k >= 0; --k) {
-            if (PACKED && (ends >> k & 1))
-                back = io.dhT ? load2(io.dhT + (size_t)seq_at(g.cu, g.Nseq, t + k) * g.D + c, in0, in1) : two(0.f);
-            const float2 dh = add2(gy[k], back), q = mul2(dh, fq[k]), drg = mul2(q, f1[k]), dig = mul2(dh, fi[k]);
-            back = mul2(a[k], dh);
-            if (PACKED && (starts >> k & 1) && io.dh0)
-                store2(io.dh0 + (size_t)seq_at(g.cu, g.Nseq, t + k) * g.D + c, back, in0, in1);
-            ring.put(st, kX, k, mul2(dh, fx[k]));
-            ring.put(st, kRg, k, drg);
-            ring.put(st, kIg, k, dig);
-            if (k < n) {
-                sq = add2(sq, q);
-                sr = add2(sr, drg);
-                si = add2(si, dig);
+            for (int k = kRun - 1; k >= 0; --k) {
+                if (PACKED && (ends >> k & 1)) {
+                    seq = edges.down(g.cu, seq, t + k);
+                    back = io.dhT ? load2(io.dhT + (size_t)seq * g.D + c, in0, in1) : two(0.f);
+                }
+                const float2 dh = add2(gy[k], back), q = mul2(dh, fq[k]), drg = mul2(q, f1[k]), dig = mul2(dh, fi[k]);
+                back = mul2(a[k], dh);
+                if (PACKED && (starts >> k & 1) && io.dh0) {
+                    seq = edges.down(g.cu, seq, t + k);
+                    store2(io.dh0 + (size_t)seq * g.D + c, back, in0, in1);
+                }
+                if (decltype(all)::value || k < n) {
+                    put_two<MODE>(pdx, mul2(dh, fx[k]), in0, in1);
+                    put_two<MODE>(pdr, drg, in0, in1);
+                    put_two<MODE>(pdi, dig, in0, in1);
+                    sq = add2(sq, q);
+                    sr = add2(sr, drg);
+                    si = add2(si, dig);
+                }
+                pdx -= io.out[kX].t;
+                pdr -= io.out[kRg].t;
+                pdi -= io.out[kIg].t;
             }
-        }
-        ring.flush(st, gated ? 15 : 7, tw, nw);
+        };
+        if (!kShort && whole) outputs(std::true_type{});
+        else outputs(std::false_type{});
+        if (g.CL == 1) leave<W, Q, true>(sm, st & 1, back);
     }
-    ring.end();
-    if (!PACKED && io.dh0 && rank == 0 && warp == 0 && lane < L) store2(io.dh0 + (size_t)b * g.D + c, carry, in0, in1);
+    if (!PACKED && io.dh0) {
+        if (g.CL > 1 || steps == 0) {
+            if (rank == 0 && warp == 0 && lane < L) store2(io.dh0 + (size_t)b * g.D + c, carry, in0, in1);
+        } else if (warp == 0 && lane < L) {
+            store2(io.dh0 + (size_t)b * g.D + c, back, in0, in1);
+        }
+    }
 
     auto put = [&](int i, float2 v) {   // the sum over a warp's runs, in a fixed order
 #pragma unroll
@@ -175,11 +208,11 @@ cudaError_t bwd(const RecurCall &c, cudaStream_t st)
     io.out[kX] = view_of<T>(&r->dx); io.out[kRg] = view_of<T>(&r->drg); io.out[kIg] = view_of<T>(&r->dig); io.out[kZ] = view_of<T>(&r->dz);
     io.keep = c.keep; io.dhT = r->dhT; io.dh0 = r->dh0; io.part = c.part;
     if (g.cu && io.dh0 && g.Nseq > 0) k_recur_empty_grad<<<g.Nseq, 256, 0, st>>>(g.cu, g.D, io.dhT, io.dh0);
-    constexpr int W = bwd_warps(sizeof(T)), S = bwd_stages(sizeof(T));
+    constexpr int W = bwd_warps(sizeof(T));
     const bool gated = io.in[kZ].p != nullptr;
-    const int smem = S * (gated ? 5 : 4) * W * kRun * 64 * (int)sizeof(T);
+    const int smem = 2 * (gated ? 5 : 4) * W * kRun * 64 * (int)sizeof(T) + recur_block_bytes(g.CL, g.Q);
     RecurMaps m = {};
-    const int mode = recur_mode(m, io, gated ? 31 : 23, gated ? 15 : 7, g);
+    const int mode = recur_mode(m, io, gated ? 31 : 23, box_rows<W>(g.Q), g);
     const cudaError_t rc = recur_variant<T>(g, mode, [&](auto q, auto how, auto packed) {
         return recur_launch(k_recur_bwd<T, decltype(q)::value, decltype(how)::value, decltype(packed)::value>, g, 32 * W, smem, st, m, g, io);
     });

@@ -11,51 +11,65 @@ namespace lay {
 namespace {
 
 template <class T, int Q, int MODE, bool PACKED>
-__global__ void __launch_bounds__(32 * fwd_warps(sizeof(T))) k_recur_fwd(const __grid_constant__ RecurMaps maps, RecurDims g, RecurIo<T> io)
+__global__ void __launch_bounds__(32 * fwd_warps(sizeof(T)), kFwdResident) k_recur_fwd(const __grid_constant__ RecurMaps maps, RecurDims g, RecurIo<T> io)
 {
-    constexpr int W = fwd_warps(sizeof(T)), S = fwd_stages(sizeof(T)), L = 32 / Q, R = kRun * Q;
+    constexpr int W = fwd_warps(sizeof(T)), L = 32 / Q, R = kRun * Q;
+    constexpr bool kShort = MODE != kTma || PACKED;   // one copy of each loop: these run fewer steps, and wait for instructions
     extern __shared__ __align__(128) char raw[];
+    float4 *block = reinterpret_cast<float4 *>(raw);   // maps of the cluster's blocks, then the inputs
     __shared__ RecurShared<W, Q> sm;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = g.CL > 1 ? cluster_rank() : 0;
-    const int id = blockIdx.x / g.CL, b = id / g.tiles, c0 = (id - b * g.tiles) * (64 / Q), c = c0 + 2 * (lane % L), q = lane / L * kRun;
+    const int id = blockIdx.x / g.CL, b = id / g.tiles, c0 = (id - b * g.tiles) * (64 / Q), c = c0 + 2 * (lane % L);
+    const int q = warp * R + lane / L * kRun;     // of this lane's run, in a block's tokens
     const bool in0 = c < g.D, in1 = c + 1 < g.D;
     const bool gated = io.in[kZ].p != nullptr;
-    Ring<T, W, Q, S, MODE> ring;
-    ring.init(raw, sm.bar[warp], &io, &maps, gated ? 15 : 7, b, c0, g.D);
+    Inputs<T, W, Q, MODE> inputs;
+    inputs.init(raw + recur_block_bytes(g.CL, Q), sm.bar, &io, &maps, gated ? 15 : 7, b, c0, g.D);
     const int te = PACKED ? g.cu[g.Nseq] : g.T;   // malformed offsets: every sequence is empty
     const int span = W * R * g.CL, steps = (te + span - 1) / span;
-    const int first = (rank * W + warp) * R;      // of the warp's tokens, in a step's span
-    for (int st = 0; st < S - 1; ++st) {
-        if (st < steps) ring.ask(st, st * span + first, te - st * span - first);
-        ring.asked();
+    int t0 = rank * W * R;                        // the block's first token of a step
+    for (int st = 0; st < 2; ++st) {
+        if (st < steps) inputs.ask(st, t0 + st * span, te);
+        inputs.asked();
     }
     RecurParams par;
     par.load(g, c, in0, in1);
     const bool far = par.far();
     float2 carry = two(0.f);
     if (!PACKED && g.h0) carry = load2(g.h0 + (size_t)b * g.D + c, in0, in1);
-    const size_t kept = (g.T + kRun - 1) / kRun;
-    Edges edges = {0, 0};
-    if (g.CL > 1) cluster_barrier();   // all of the cluster's blocks run before one writes to another
+    if (warp == 0 && lane < L) sm.carry[0][lane] = carry;
+    float *keep = io.keep ? io.keep + ((size_t)b * ((g.T + kRun - 1) / kRun) + (t0 + q) / kRun) * g.D + c : nullptr;
+    T *py = io.out[kX].at(b, 0, t0 + q) + c;
+    Edges edges = {};
+    int seq = 0;
+    if (MODE == kTma) __syncthreads();   // the barriers exist
+    if (g.CL > 1) cluster_barrier();     // all of the cluster's blocks run before one writes to another
 
-    for (int st = 0; st < steps; ++st) {
-        const int tw = st * span + first, nw = min(R, te - tw), t = tw + q, n = max(0, min(kRun, te - t));
+    float2 h = carry;
+    for (int st = 0; st < steps; ++st, t0 += span) {
+        const int t = t0 + q, n = te - t;   // tokens of the run that exist: 0 or less to kRun or more
         uint32_t starts = 0, ends = 0;
-        if (PACKED) edges.find(g, tw, nw, t, n, starts, ends);
-        ring.get(st, tw, nw, g.status);
+        if (PACKED) edges.find(g, t0 + warp * R, min(R, te - t0 - warp * R), t, min(kRun, n), starts, ends);
+        inputs.get(st, t0, te, g.status);
         float2 a[kRun], in[kRun], A = two(1.f), H = two(0.f);
+        Vec<T, 2> z[kRun];
+        const T *px = inputs.cells(st, kX), *pr = inputs.cells(st, kRg), *pi = inputs.cells(st, kIg), *pz = inputs.cells(st, kZ);
         auto decays = [&](auto wide) {
 #pragma unroll
             for (int k = 0; k < kRun; ++k) {
-                const float2 m = mul2(par.km, gate(ring.at(st, kRg, k), par.rb));
-                const float2 u = mul2(gate(ring.at(st, kIg, k), par.ib), ring.at(st, kX, k));
+                const float2 m = mul2(par.km, gate(inputs.at(pr, k), par.rb));
+                const float2 u = mul2(gate(inputs.at(pi, k), par.ib), inputs.at(px, k));
                 float2 y, rs;
                 decay_of<decltype(wide)::value>(m, a[k], y, rs);
                 in[k] = mul2(mul2(y, rs), u);
             }
         };
-        if (far) decays(std::true_type{});
+        if (kShort || far) decays(std::true_type{});
         else decays(std::false_type{});
+        if (gated) {
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) z[k].load(pz + k * inputs.C);
+        }
         if (n < kRun) {   // behind the end: nothing changes
 #pragma unroll
             for (int k = 0; k < kRun; ++k) {
@@ -65,10 +79,12 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T))) k_recur_fwd(const _
                 }
             }
         }
+        seq = edges.first;
 #pragma unroll
         for (int k = 0; k < kRun; ++k) {
             if (PACKED && (starts >> k & 1)) {
-                if (g.h0) in[k] = fma2(a[k], load2(g.h0 + (size_t)seq_at(g.cu, g.Nseq, t + k) * g.D + c, in0, in1), in[k]);
+                seq = edges.up(g.cu, seq, t + k);
+                if (g.h0) in[k] = fma2(a[k], load2(g.h0 + (size_t)seq * g.D + c, in0, in1), in[k]);
                 H = in[k];
             } else {
                 A = mul2(A, a[k]);
@@ -77,25 +93,48 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T))) k_recur_fwd(const _
         }
         A = make_float2(fmaxf(A.x, kLeast), fmaxf(A.y, kLeast));
         if (PACKED && starts) A = two(-1.f);
-        float2 h = exchange<W, Q, PACKED, false>(sm, st & 1, g.CL, rank, A, H, carry);
-        if (st + S - 1 < steps) ring.ask(st + S - 1, tw + (S - 1) * span, te - tw - (S - 1) * span);
-        ring.asked();
-        if (io.keep && n > 0) store2(io.keep + ((size_t)b * kept + t / kRun) * g.D + c, h, in0, in1);
-#pragma unroll
-        for (int k = 0; k < kRun; ++k) {
-            h = PACKED && (starts >> k & 1) ? in[k] : fma2(a[k], h, in[k]);
-            if (PACKED && (ends >> k & 1) && io.hT) store2(io.hT + (size_t)seq_at(g.cu, g.Nseq, t + k) * g.D + c, h, in0, in1);
-            float2 y = h;
-            if (gated) {
-                const float2 z = ring.at(st, kZ, k);
-                y = mul2(h, mul2(z, sigmoid2(z)));
-            }
-            ring.put(st, kX, k, y);
+        h = exchange<W, Q, PACKED, false>(sm, block, st & 1, g.CL, rank, A, H, carry, [&] {
+            if (st + 2 < steps) inputs.ask(st + 2, t0 + 2 * span, te);
+            inputs.asked();
+        });
+        if (keep) {
+            if (n > 0) store2(keep, h, in0, in1);
+            keep += (size_t)(span / kRun) * g.D;
         }
-        ring.flush(st, 1 << kX, tw, nw);
+        T *p = py;
+        seq = edges.first;
+        auto outputs = [&](auto whole) {
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) {
+                h = PACKED && (starts >> k & 1) ? in[k] : fma2(a[k], h, in[k]);
+                if (PACKED && (ends >> k & 1) && io.hT) {
+                    seq = edges.up(g.cu, seq, t + k);
+                    store2(io.hT + (size_t)seq * g.D + c, h, in0, in1);
+                }
+                float2 y = h;
+                if (gated) {
+                    float f[2];
+                    z[k].get(f);
+                    const float2 zz = make_float2(f[0], f[1]);
+                    y = mul2(h, mul2(zz, sigmoid2(zz)));
+                }
+                if (decltype(whole)::value || k < n) put_two<MODE>(p, y, in0, in1);
+                p += io.out[kX].t;
+            }
+        };
+        if (!kShort && n >= kRun) outputs(std::true_type{});
+        else outputs(std::false_type{});
+        py += span * io.out[kX].t;
+        if (g.CL == 1) leave<W, Q, false>(sm, st & 1, h);
     }
-    if (!PACKED && io.hT && rank == 0 && warp == 0 && lane < L) store2(io.hT + (size_t)b * g.D + c, carry, in0, in1);
-    ring.end();
+    // what leaves the last run: a cluster's blocks all have it, a block alone its last warp
+    if (!PACKED && io.hT) {
+        if (g.CL > 1 || steps == 0) {
+            if (rank == 0 && warp == 0 && lane < L) store2(io.hT + (size_t)b * g.D + c, carry, in0, in1);
+        } else if (warp == W - 1 && lane >= 32 - L) {
+            store2(io.hT + (size_t)b * g.D + c, h, in0, in1);
+        }
+    }
 }
 
 // Final states of empty sequences: the initial ones.
@@ -167,13 +206,13 @@ RecurIo<T> fwd_io(const RecurCall &c)
 template <class T>
 cudaError_t fwd(const RecurCall &c, cudaStream_t st)
 {
-    constexpr int W = fwd_warps(sizeof(T)), S = fwd_stages(sizeof(T));
+    constexpr int W = fwd_warps(sizeof(T));
     const RecurDims g = recur_dims(c, false);
     const RecurIo<T> io = fwd_io<T>(c);
     if (g.cu && io.hT && g.Nseq > 0) k_recur_empty<<<g.Nseq, 256, 0, st>>>(g.cu, g.D, g.h0, io.hT);
-    const int sets = io.in[kZ].p ? 15 : 7, smem = S * (io.in[kZ].p ? 4 : 3) * W * kRun * 64 * (int)sizeof(T);
+    const int arrays = io.in[kZ].p ? 4 : 3, smem = 2 * arrays * W * kRun * 64 * (int)sizeof(T) + recur_block_bytes(g.CL, g.Q);
     RecurMaps m = {};
-    const int mode = recur_mode(m, io, sets, 1 << kX, g);
+    const int mode = recur_mode(m, io, (1 << arrays) - 1, box_rows<W>(g.Q), g);
     return recur_variant<T>(g, mode, [&](auto q, auto how, auto packed) {
         return recur_launch(k_recur_fwd<T, decltype(q)::value, decltype(how)::value, decltype(packed)::value>, g, 32 * W, smem, st, m, g, io);
     });
@@ -197,18 +236,18 @@ cudaError_t step(const RecurCall &c, cudaStream_t st)
 
 }  // namespace
 
-// Blocks that share a row's tokens: as many as run at once, and no more than there are spans.  Where 64-channel tiles leave
-// three quarters of the places free all the same, tiles of 16.
+// Narrower tiles as long as all blocks run at once, then blocks of a cluster that share a row's tokens, no more than there
+// are spans: runs that share a warp exchange their maps more cheaply than blocks do.
 RecurPlan recur_plan(const dn_recur_shape *s, bool bwd)
 {
     const int e = s->dtype == DN_F32 ? 4 : 2, run = kRun * (bwd ? bwd_warps(e) : fwd_warps(e));
-    const long long most = (long long)kResident * sm_count();
+    const long long most = (long long)(bwd ? kBwdResident : kFwdResident) * sm_count();
+    auto tiles = [&](int Q) { return (long long)s->B * ((s->D + 64 / Q - 1) / (64 / Q)); };
     RecurPlan p = {1, 1};
-    for (p.Q = 1;; p.Q = 4) {
-        const long long tiles = (long long)s->B * ((s->D + 64 / p.Q - 1) / (64 / p.Q));
-        for (p.CL = 1; p.CL < kMaxCluster && tiles * p.CL * 2 <= most && (long long)p.CL * run * p.Q < s->T;) p.CL *= 2;
-        if (p.Q > 1 || tiles * p.CL * 4 > most || s->D <= 16) return p;
-    }
+    while (p.Q < 4 && tiles(2 * p.Q) <= most && (long long)run * p.Q < s->T) p.Q *= 2;
+    if (p.Q == 4)
+        while (p.CL < kMaxCluster && tiles(4) * p.CL * 2 <= most && (long long)p.CL * run * 4 < s->T) p.CL *= 2;
+    return p;
 }
 
 cudaError_t recur_fwd(const RecurCall &c, cudaStream_t st) { return c.s->dtype == DN_F32 ? fwd<float>(c, st) : fwd<__nv_bfloat16>(c, st); }
