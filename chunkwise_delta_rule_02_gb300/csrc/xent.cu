@@ -32,16 +32,29 @@ constexpr int GROUP = 16;                                            // row tile
 constexpr float kNone = -1e30f;                                      // maximum of no logits
 
 // Steps after which float32 inputs' sums leave TMEM: the tensor core cuts what it adds off rather than rounding it, the same way each
-// time, which a contraction of 70001 tokens added up to 8e-5 of dw; segments of 1024 are summed in registers, rounded.
-constexpr int kSegment = 16;
+// time, which a contraction of 70001 tokens added up to 8e-5 of dw; segments of 256 are summed in registers, rounded.
+constexpr int kSegment = 4;
 
 enum { STATS, GRAD, OUT };
 
-struct Gemm {
+// One product C = A B^T and how its tiles are cut: units of a tile and a part of the contraction.
+struct Product {
     int M, N;                       // rows and columns of C that exist
     int mt, nt, kb;                 // tiles; 64-wide steps of the contraction
+    int cuts, len;                  // parts of the contraction and their steps
     int b_row, b_k;                 // where B's rows and its contraction begin
-    int seg;                        // steps of a segment: kb, or kSegment (SEG)
+    // OUT: the sum, where cuts > 1 of one part, [cuts][M][N] in `part`
+    const float *add;               // [M][N] or null
+    float *sum;                     // [M][N], or null: out
+    float *part;
+    void *out;
+    long long out_b, out_t;         // row (b, t) of out at b out_b + t out_t
+    int T, f32, wide;               // wide: out's rows start at 16 bytes, and N is a multiple of 8
+};
+
+struct Gemm {
+    Product of[2];                  // the second of OUT only
+    int seg;                        // steps of a segment: all, or kSegment (SEG)
     int np;                         // plane products: nibbles of pa, pb
     uint32_t pa, pb;
     uint32_t *status;
@@ -53,19 +66,49 @@ struct Gemm {
     __nv_bfloat16 *d;
     long long d_pitch, d_plane;
     int v0, planes;
-    // OUT
-    const float *add;               // [M][N] or null
-    float *sum;                     // [M][N], or null: out
-    void *out;
-    long long out_b, out_t;         // row (b, t) of out at b out_b + t out_t
-    int T, f32;
+};
+
+// Units of the two products for pair `p` of `n`: the first product's dealt in turn, the second's so that pairs with fewer of the
+// first have the more of the second that its length makes up for.
+struct Deal {
+    int count[2], first[2], step[2];
+    __host__ __device__ Deal(const Gemm &g, int p, int n)
+    {
+        const int n0 = g.of[0].mt * g.of[0].nt * g.of[0].cuts, n1 = g.of[1].mt * g.of[1].nt * g.of[1].cuts;
+        const int r = n0 % n;   // pairs with one more of the first
+        count[0] = n0 / n + (p < r ? 1 : 0);
+        first[0] = p;
+        step[0] = n;
+        const int more = n1 > 0 ? (g.of[0].len + g.of[1].len / 2) / g.of[1].len : 0;
+        int base = n1 - (n - r) * more, low = 0, high;   // units a pair with more, with fewer of the first
+        if (r == 0) {
+            low = high = n1 / n;
+            base = n1 - n * low;
+        } else if (base >= 0) {
+            low = base / n;
+            high = low + more;
+            base -= n * low;
+        } else {
+            high = n1 / (n - r);
+            base = n1 - (n - r) * high;   // over the pairs with fewer
+        }
+        // the rest, one each: from the last pair on
+        const int rest = p >= n - base ? 1 : 0;
+        count[1] = (p < r ? low : high) + rest;
+        first[1] = (p < r ? p * low : r * low + (p - r) * high) + (rest ? p - (n - base) : 0);
+        step[1] = 1;
+    }
 };
 
 enum { FULL = 0, EMPTY = STAGES, TFULL = 2 * STAGES, TEMPTY = TFULL + 2, DONE = TEMPTY + 2, NBAR = DONE + 1 };
 
-template <bool A_MN, bool B_MN, int EPI, bool SEG>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    k_gemm(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const Gemm p)
+struct Maps {
+    CUtensorMap a[2], b[2];
+};
+
+// OUT: two products, D w and D^T x: B is MN-major in both, A in the second.  Otherwise one, both operands K-major.
+template <int EPI, bool SEG>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(const __grid_constant__ Maps maps, const __grid_constant__ Gemm p)
 {
     extern __shared__ char raw[];
     char *sm = (char *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
@@ -74,7 +117,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     volatile int *s_abort = (volatile int *)(s_tmem + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = pair_rank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = p.mt * p.nt;
+    const Deal deal(p, blockIdx.x >> 1, gridDim.x >> 1);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
@@ -88,8 +131,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         mbar_init(&bar[DONE], 1);
         *s_abort = 0;
         fence_barrier_init();
-        prefetch_tmap(&ta);
-        prefetch_tmap(&tb);
+        prefetch_tmap(&maps.a[0]);
+        prefetch_tmap(&maps.b[0]);
     }
     if (warp == 1) {
         pair_tmem_alloc(s_tmem, 512);
@@ -106,42 +149,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         raise_status(p.status, kStatusTimeout);
         return false;
     };
-    auto place = [&](int tile, int &m, int &n) {
-        const int per = GROUP * p.nt, grp = tile / per, r = tile - grp * per, gm = min(GROUP, p.mt - grp * GROUP);
-        m = (grp * GROUP + r % gm) * TILE;
-        n = r / gm * TILE;
+    // Unit u of product q: its tile and its steps of the contraction
+    struct Unit {
+        int m, n, k0, k1, cut;
     };
-    const int segs = SEG ? (p.kb + p.seg - 1) / p.seg : 1;
+    auto unit = [&](const Product &o, int u) {
+        Unit r;
+        const int tiles = o.mt * o.nt;
+        r.cut = u / tiles;
+        const int tile = u - r.cut * tiles, per = GROUP * o.nt, grp = tile / per, in = tile - grp * per, gm = min(GROUP, o.mt - grp * GROUP);
+        r.m = (grp * GROUP + in % gm) * TILE;
+        r.n = in / gm * TILE;
+        r.k0 = r.cut * o.len;
+        r.k1 = min(o.kb, r.k0 + o.len);
+        return r;
+    };
+    auto segments = [&](const Unit &u) { return SEG ? (u.k1 - u.k0 + p.seg - 1) / p.seg : 1; };
+    constexpr int PRODUCTS = EPI == OUT ? 2 : 1;
 
     if (warp == 0) {
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int tile = pair; ok && tile < tiles; tile += pairs) {
-                int m, n;
-                place(tile, m, n);
-                m += rank * HALF;
-                n += rank * HALF;
-                for (int sq = 0; ok && sq < segs * p.np; ++sq) {
-                    const int seg = sq / p.np, q = sq - seg * p.np;
-                    const int a = p.pa >> 4 * q & 15, b = p.pb >> 4 * q & 15, end = min(p.kb, (seg + 1) * p.seg);
-                    for (int k = seg * p.seg; k < end; ++k, ++it) {
-                        const int s = it % STAGES;
-                        if (!(ok = wait(EMPTY + s, it / STAGES + 1))) break;
-                        const uint32_t full = peer_addr(&bar[FULL + s], 0);
-                        char *sa = sm + s * STAGE, *sb = sa + OPERAND;
-                        if (rank == 0) mbar_expect_tx(&bar[FULL + s], 2 * STAGE);
-                        if (A_MN) {
-                            pair_load_3d(sa, &ta, full, m, k * BK, a);
-                            pair_load_3d(sa + OPERAND / 2, &ta, full, m + 64, k * BK, a);
-                        } else {
-                            pair_load_3d(sa, &ta, full, k * BK, m, a);
-                        }
-                        if (B_MN) {
-                            pair_load_3d(sb, &tb, full, n, p.b_k + k * BK, b);
-                            pair_load_3d(sb + OPERAND / 2, &tb, full, n + 64, p.b_k + k * BK, b);
-                        } else {
-                            pair_load_3d(sb, &tb, full, k * BK, p.b_row + n, b);
+            for (int o = 0; o < PRODUCTS; ++o) {
+                const Product &pr = p.of[o];
+                const CUtensorMap *ta = &maps.a[o], *tb = &maps.b[o];
+                const bool a_mn = EPI == OUT && o == 1;
+                constexpr bool B_MN = EPI == OUT;
+                for (int i = 0; ok && i < deal.count[o]; ++i) {
+                    const Unit u = unit(pr, deal.first[o] + i * deal.step[o]);
+                    const int m = u.m + rank * HALF, n = u.n + rank * HALF, segs = segments(u);
+                    for (int sq = 0; ok && sq < segs * p.np; ++sq) {
+                        const int seg = sq / p.np, q = sq - seg * p.np;
+                        const int a = p.pa >> 4 * q & 15, b = p.pb >> 4 * q & 15;
+                        const int begin = SEG ? u.k0 + seg * p.seg : u.k0, end = SEG ? min(u.k1, begin + p.seg) : u.k1;
+                        for (int k = begin; k < end; ++k, ++it) {
+                            const int s = it % STAGES;
+                            if (!(ok = wait(EMPTY + s, it / STAGES + 1))) break;
+                            const uint32_t full = peer_addr(&bar[FULL + s], 0);
+                            char *sa = sm + s * STAGE, *sb = sa + OPERAND;
+                            if (rank == 0) mbar_expect_tx(&bar[FULL + s], 2 * STAGE);
+                            if (a_mn) {
+                                pair_load_3d(sa, ta, full, m, k * BK, a);
+                                pair_load_3d(sa + OPERAND / 2, ta, full, m + 64, k * BK, a);
+                            } else {
+                                pair_load_3d(sa, ta, full, k * BK, m, a);
+                            }
+                            if (B_MN) {
+                                pair_load_3d(sb, tb, full, n, pr.b_k + k * BK, b);
+                                pair_load_3d(sb + OPERAND / 2, tb, full, n + 64, pr.b_k + k * BK, b);
+                            } else {
+                                pair_load_3d(sb, tb, full, k * BK, pr.b_row + n, b);
+                            }
                         }
                     }
                 }
@@ -154,28 +213,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            constexpr uint32_t id = idesc(1, TILE, TILE, A_MN, B_MN);
-            constexpr uint32_t astep = A_MN ? 2048 : 32, bstep = B_MN ? 2048 : 32;
+            constexpr bool B_MN = EPI == OUT;
+            constexpr uint32_t bstep = B_MN ? 2048 : 32;
             uint32_t it = 0, n = 0;
             bool ok = true;
-            for (int tile = pair; ok && tile < tiles; tile += pairs) {
-                for (int seg = 0; ok && seg < segs; ++seg, ++n) {
-                    const uint32_t acc = tmem + (n & 1) * TILE;
-                    if (!(ok = wait(TEMPTY + (n & 1), (n >> 1) + 1))) break;
-                    tc_fence_after();
-                    const int steps = p.np * (min(p.kb, (seg + 1) * p.seg) - seg * p.seg);
-                    for (int k = 0; k < steps; ++k, ++it) {
-                        const int s = it % STAGES;
-                        if (!(ok = wait(FULL + s, it / STAGES))) break;
+            for (int o = 0; o < PRODUCTS; ++o) {
+                const bool a_mn = EPI == OUT && o == 1;
+                const uint32_t id = a_mn ? idesc(1, TILE, TILE, true, B_MN) : idesc(1, TILE, TILE, false, B_MN);
+                const uint32_t astep = a_mn ? 2048 : 32, alead = a_mn ? OPERAND / 2 : 16;
+                for (int i = 0; ok && i < deal.count[o]; ++i) {
+                    const Unit u = unit(p.of[o], deal.first[o] + i * deal.step[o]);
+                    const int segs = segments(u);
+                    for (int seg = 0; ok && seg < segs; ++seg, ++n) {
+                        const uint32_t acc = tmem + (n & 1) * TILE;
+                        if (!(ok = wait(TEMPTY + (n & 1), (n >> 1) + 1))) break;
                         tc_fence_after();
-                        const uint32_t sa = smem_u32(sm + s * STAGE), sb = sa + OPERAND;
+                        const int steps = p.np * (SEG ? min(p.seg, u.k1 - u.k0 - seg * p.seg) : u.k1 - u.k0);
+                        for (int k = 0; k < steps; ++k, ++it) {
+                            const int s = it % STAGES;
+                            if (!(ok = wait(FULL + s, it / STAGES))) break;
+                            tc_fence_after();
+                            const uint32_t sa = smem_u32(sm + s * STAGE), sb = sa + OPERAND;
 #pragma unroll
-                        for (int j = 0; j < BK / 16; ++j)
-                            pair_mma_bf16(acc, sdesc(sa + j * astep, A_MN ? OPERAND / 2 : 16, 1024),
-                                          sdesc(sb + j * bstep, B_MN ? OPERAND / 2 : 16, 1024), id, k > 0 || j > 0);
-                        pair_commit(&bar[EMPTY + s]);
+                            for (int j = 0; j < BK / 16; ++j)
+                                pair_mma_bf16(acc, sdesc(sa + j * astep, alead, 1024), sdesc(sb + j * bstep, B_MN ? OPERAND / 2 : 16, 1024), id,
+                                              k > 0 || j > 0);
+                            pair_commit(&bar[EMPTY + s]);
+                        }
+                        if (ok) pair_commit(&bar[TFULL + (n & 1)]);
                     }
-                    if (ok) pair_commit(&bar[TFULL + (n & 1)]);
                 }
             }
             // no MMA is in flight when TMEM is freed, also where a wait ran out
@@ -188,11 +254,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         uint32_t n = 0;
         bool ok = true;
-        for (int tile = pair; tile < tiles; tile += pairs) {
-            int m0, n0;
-            place(tile, m0, n0);
-            const int row = m0 + rank * HALF + quad * 32 + lane, c0 = n0 + half * HALF;
-            const bool in = row < p.M;
+        for (int i = 0; i < deal.count[0] + (EPI == OUT ? deal.count[1] : 0); ++i) {
+            const int o = EPI == OUT && i >= deal.count[0], j = o ? i - deal.count[0] : i;
+            const Product &pr = p.of[o];
+            const Unit u = unit(pr, deal.first[o] + j * deal.step[o]);
+            const int row = u.m + rank * HALF + quad * 32 + lane, c0 = u.n + half * HALF;
+            const bool in = row < pr.M;
             [[maybe_unused]] int target = -1;
             [[maybe_unused]] float lse = 0.f, g = 0.f, mx = kNone, sum = 0.f;
             if (EPI != OUT && in) {
@@ -203,7 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 }
             }
             auto finish = [&](int c, float (&v)[32]) {   // columns c0 + c .. + 31 of this thread's row
-                const int col = c0 + c, live = p.N - col;   // columns of this chunk that exist
+                const int col = c0 + c, live = pr.N - col;   // columns of this chunk that exist
                 if constexpr (EPI == STATS) {
                     if (live < 32) {
 #pragma unroll
@@ -253,28 +320,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                             }
                         }
                     }
-                } else {
-                    if (in) {
-                        if (p.add) {
-                            const float *a = p.add + (long long)row * p.N + col;
+                } else if (in && live > 0) {
+                    const bool whole = live >= 32 && pr.N % 4 == 0;   // columns and 16-byte rows of a float array
+                    const long long at = (long long)row * pr.N + col;
+                    if (pr.add && pr.cuts == 1) {
+                        if (whole) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i < live) v[i] += a[i];
-                        }
-                        if (p.sum) {
-                            float *o = p.sum + (long long)row * p.N + col;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i < live) o[i] = v[i];
-                        } else {
-                            const long long at = (long long)(row / p.T) * p.out_b + (long long)(row % p.T) * p.out_t + col;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                if (i < live) {
-                                    if (p.f32) ((float *)p.out)[at + i] = v[i];
-                                    else st_out((__nv_bfloat16 *)p.out + at + i, v[i]);
-                                }
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 f = reinterpret_cast<const float4 *>(pr.add + at)[i];
+                                v[4 * i] += f.x;
+                                v[4 * i + 1] += f.y;
+                                v[4 * i + 2] += f.z;
+                                v[4 * i + 3] += f.w;
                             }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i < live) v[i] += pr.add[at + i];
+                        }
+                    }
+                    const bool partial = pr.cuts > 1, sums = partial || pr.sum != nullptr;
+                    const long long place = sums ? at : (long long)(row / pr.T) * pr.out_b + (long long)(row % pr.T) * pr.out_t + col;
+                    if (sums || pr.f32) {
+                        float *to = (partial ? pr.part + (long long)u.cut * pr.M * pr.N : sums ? pr.sum : (float *)pr.out) + place;
+                        if (whole && (sums || pr.wide)) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) reinterpret_cast<float4 *>(to)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i < live) to[i] = v[i];
+                        }
+                    } else {
+                        __nv_bfloat16 *to = (__nv_bfloat16 *)pr.out + place;
+                        if (whole && pr.wide) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                reinterpret_cast<uint4 *>(to)[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                                                              pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i < live) st_out(to + i, v[i]);
                         }
                     }
                 }
@@ -294,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             };
             if constexpr (SEG) {
                 float all[HALF / 32][32] = {};
-                for (int seg = 0; seg < segs; ++seg) {
+                for (int seg = segments(u); seg > 0; --seg) {
                     if (!(ok = wait(TFULL + (n & 1), n >> 1))) break;
                     tc_fence_after();
 #pragma unroll
@@ -320,7 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 }
                 release();
             }
-            if (EPI == STATS && in) p.part[(long long)(2 * (n0 / TILE) + half) * p.M + row] = make_float2(mx, sum);
+            if (EPI == STATS && in) p.part[(long long)(2 * (u.n / TILE) + half) * pr.M + row] = make_float2(mx, sum);
         }
     }
     __syncwarp();
@@ -387,31 +474,80 @@ __global__ void __launch_bounds__(256) k_pack(lay::View<const T> v, int R, int T
     }
 }
 
+// Sums of a product's parts in a fixed order, and what OUT does with a whole one.  A thread has 4 columns of a row where `wide`.
+template <int V>
+__global__ void __launch_bounds__(256) k_join(const __grid_constant__ Product o)
+{
+    const long long all = (long long)o.M * o.N, step = (long long)gridDim.x * 256 * V;
+    for (long long i = (blockIdx.x * 256ll + threadIdx.x) * V; i < all; i += step) {
+        float v[V] = {};
+        for (int c = 0; c < o.cuts; ++c) {
+            lay::Vec<float, V> q;
+            float f[V];
+            q.load(o.part + c * all + i);
+            q.get(f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] += f[e];
+        }
+        const int row = (int)(i / o.N), col = (int)(i - (long long)row * o.N);
+        const long long place = o.sum ? i : (long long)(row / o.T) * o.out_b + (long long)(row % o.T) * o.out_t + col;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if (o.add) v[e] += o.add[i + e];
+            if (o.sum) o.sum[place + e] = v[e];
+            else if (o.f32) ((float *)o.out)[place + e] = v[e];
+            else st_out((__nv_bfloat16 *)o.out + place + e, v[e]);
+        }
+    }
+}
+
 // bf16 [planes][rows][cols], boxes of 64 columns x `high` rows
 bool make_map(CUtensorMap *m, const Operand &o, long long cols, long long rows, int planes, int high)
 {
     return lay::tensor_map(m, false, o.p, cols, rows, planes, o.pitch, o.plane, 64, high, true);
 }
 
-template <bool A_MN, bool B_MN, int EPI, bool SEG>
-cudaError_t launch_as(const CUtensorMap &a, const CUtensorMap &b, Gemm &p, int contraction, cudaStream_t st)
+void size(Product &o, int M, int N, int contraction)
 {
-    p.mt = tiles_of(p.M);
-    p.nt = tiles_of(p.N);
-    p.kb = (contraction + BK - 1) / BK;
-    p.seg = SEG ? kSegment : p.kb;
-    auto kernel = k_gemm<A_MN, B_MN, EPI, SEG>;
+    o.M = M;
+    o.N = N;
+    o.mt = tiles_of(M);
+    o.nt = tiles_of(N);
+    o.kb = o.len = (contraction + BK - 1) / BK;
+    o.cuts = 1;
+    o.T = 1;
+}
+
+int pairs_at_most() { return lay::sm_count() / 2; }
+
+template <int EPI, bool SEG>
+cudaError_t launch_as(const Maps &m, Gemm &p, cudaStream_t st)
+{
+    p.seg = kSegment;
+    auto kernel = k_gemm<EPI, SEG>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    const long long tiles = (long long)p.mt * p.nt, pairs = lay::sm_count() / 2;
-    kernel<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), THREADS, SMEM, st>>>(a, b, p);
+    long long units = 0, pairs = pairs_at_most();
+    for (const Product &o : p.of) units += (long long)o.mt * o.nt * o.cuts;
+    kernel<<<(unsigned)(2 * (units < pairs ? units : pairs)), THREADS, SMEM, st>>>(m, p);
     return cudaPeekAtLastError();
 }
 
-template <bool A_MN, bool B_MN, int EPI>
-cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, Gemm &p, int contraction, cudaStream_t st)
+template <int EPI>
+cudaError_t launch(const Maps &m, Gemm &p, cudaStream_t st)
 {
-    return p.np > 1 ? launch_as<A_MN, B_MN, EPI, true>(a, b, p, contraction, st) : launch_as<A_MN, B_MN, EPI, false>(a, b, p, contraction, st);
+    return p.np > 1 ? launch_as<EPI, true>(m, p, st) : launch_as<EPI, false>(m, p, st);
+}
+
+cudaError_t join(const Product &o, cudaStream_t st)
+{
+    if (o.cuts == 1) return cudaSuccess;
+    const bool four = o.N % 4 == 0;
+    const long long n = ((long long)o.M * o.N / (four ? 4 : 1) + 255) / 256, most = 16ll * lay::sm_count();
+    const unsigned blocks = (unsigned)(n < most ? n : most);
+    if (four) k_join<4><<<blocks, 256, 0, st>>>(o);
+    else k_join<1><<<blocks, 256, 0, st>>>(o);
+    return cudaPeekAtLastError();
 }
 
 Gemm common(const Call &c)
@@ -454,16 +590,27 @@ cudaError_t begin(const Call &c, bool bwd, cudaStream_t st)
 
 int tiles_of(int n) { return (int)(((long long)n + TILE - 1) / TILE); }
 
+// How the contractions of a piece's two products are cut: not longer than a pair's share of all steps, so that a few long tiles
+// do not keep the rest waiting, and 4 steps at least.
+void cuts_of(int M, int K, int n, int planes, int &dx, int &dw)
+{
+    const long long nk = tiles_of(K), a = ((long long)n + BK - 1) / BK, b = ((long long)M + BK - 1) / BK;
+    const long long all = nk * (tiles_of(M) * a + tiles_of(n) * b), least = planes == 1 ? 8 : 4;
+    long long share = (all + pairs_at_most() - 1) / pairs_at_most();
+    if (share < least) share = least;
+    dx = (int)((a + share - 1) / share);
+    dw = (int)((b + share - 1) / share);
+}
+
 cudaError_t forward(const Call &c, cudaStream_t st)
 {
     cudaError_t e = begin(c, false, st);
     if (e != cudaSuccess || c.M == 0) return e;
-    CUtensorMap mx, mw;
-    if (!make_map(&mx, c.xo, c.K, c.M, c.planes, HALF) || !make_map(&mw, c.wo, c.K, c.V, c.planes, HALF)) return cudaErrorInvalidValue;
+    Maps m = {};
+    if (!make_map(&m.a[0], c.xo, c.K, c.M, c.planes, HALF) || !make_map(&m.b[0], c.wo, c.K, c.V, c.planes, HALF)) return cudaErrorInvalidValue;
     Gemm p = common(c);
-    p.M = c.M;
-    p.N = c.V;
-    if ((e = launch<false, false, STATS>(mx, mw, p, c.K, st)) != cudaSuccess) return e;
+    size(p.of[0], c.M, c.V, c.K);
+    if ((e = launch<STATS>(m, p, st)) != cudaSuccess) return e;
     k_lse<<<(c.M + 31) / 32, 256, 0, st>>>(c.part, 2 * tiles_of(c.V), c.M, c.tgt, c.row, c.loss, c.lse);
     return cudaPeekAtLastError();
 }
@@ -475,44 +622,52 @@ cudaError_t backward(const Call &c, cudaStream_t st)
     const bool f32 = c.s->dtype == DN_F32;
     if (c.M == 0) return cudaMemsetAsync(c.dw, 0, (size_t)c.V * c.K * (f32 ? 4 : 2), st);
     const Operand d = {c.d, c.piece, (long long)c.M * c.piece};
-    CUtensorMap mx, mw, mxn, mwn;
-    if (!make_map(&mx, c.xo, c.K, c.M, c.planes, HALF) || !make_map(&mw, c.wo, c.K, c.V, c.planes, HALF) ||
-        !make_map(&mxn, c.xo, c.K, c.M, c.planes, BK) || !make_map(&mwn, c.wo, c.K, c.V, c.planes, BK))
+    Maps logits = {}, outs = {};
+    if (!make_map(&logits.a[0], c.xo, c.K, c.M, c.planes, HALF) || !make_map(&logits.b[0], c.wo, c.K, c.V, c.planes, HALF) ||
+        !make_map(&outs.b[1], c.xo, c.K, c.M, c.planes, BK) || !make_map(&outs.b[0], c.wo, c.K, c.V, c.planes, BK))
         return cudaErrorInvalidValue;
+    const size_t el = f32 ? 4 : 2;
     for (int v0 = 0; v0 < c.V; v0 += c.piece) {
         const int n = c.V - v0 < c.piece ? c.V - v0 : c.piece;
         const bool first = v0 == 0, last = v0 + n == c.V;
         // the maps end where this piece does: nothing behind it is read
-        CUtensorMap md, mdn;
-        if (!make_map(&md, d, n, c.M, c.planes, HALF) || !make_map(&mdn, d, n, c.M, c.planes, BK)) return cudaErrorInvalidValue;
+        if (!make_map(&outs.a[0], d, n, c.M, c.planes, HALF) || !make_map(&outs.a[1], d, n, c.M, c.planes, BK)) return cudaErrorInvalidValue;
         Gemm p = common(c);
-        p.M = c.M;
-        p.N = n;
-        p.b_row = p.v0 = v0;
+        size(p.of[0], c.M, n, c.K);
+        p.of[0].b_row = p.v0 = v0;
         p.d = (__nv_bfloat16 *)c.d;
         p.d_pitch = d.pitch;
         p.d_plane = d.plane;
-        if ((e = launch<false, false, GRAD>(mx, mw, p, c.K, st)) != cudaSuccess) return e;
+        if ((e = launch<GRAD>(logits, p, st)) != cudaSuccess) return e;
         p = common(c);
-        p.M = c.M;
-        p.N = c.K;
-        p.b_k = v0;
-        p.add = first ? nullptr : c.acc;
-        p.sum = last ? nullptr : c.acc;
-        p.out = c.dx->data;
-        p.out_b = c.dx->batch;
-        p.out_t = c.dx->time;
-        p.T = c.s->T;
-        p.f32 = f32;
-        if ((e = launch<false, true, OUT>(md, mwn, p, n, st)) != cudaSuccess) return e;
-        p = common(c);
-        p.M = n;
-        p.N = c.K;
-        p.out = (char *)c.dw + (size_t)v0 * c.K * (f32 ? 4 : 2);
-        p.out_t = c.K;
-        p.T = n;
-        p.f32 = f32;
-        if ((e = launch<true, true, OUT>(mdn, mxn, p, c.M, st)) != cudaSuccess) return e;
+        int dx_cuts, dw_cuts;
+        cuts_of(c.M, c.K, n, c.planes, dx_cuts, dw_cuts);
+        Product &dx = p.of[0], &dw = p.of[1];
+        size(dx, c.M, c.K, n);
+        size(dw, n, c.K, c.M);
+        auto cut = [](Product &o, int cuts) {
+            o.len = (o.kb + cuts - 1) / cuts;
+            o.cuts = (o.kb + o.len - 1) / o.len;
+        };
+        cut(dx, dx_cuts);
+        cut(dw, dw_cuts);
+        dx.b_k = v0;
+        dx.add = first ? nullptr : c.acc;
+        dx.sum = last ? nullptr : c.acc;
+        dx.part = c.cut;
+        dx.out = c.dx->data;
+        dx.out_b = c.dx->batch;
+        dx.out_t = c.dx->time;
+        dx.T = c.s->T;
+        dw.part = c.cut + (dx.cuts > 1 ? (size_t)dx.cuts * c.M * c.K : 0);
+        dw.out = (char *)c.dw + (size_t)v0 * c.K * el;
+        dw.out_t = c.K;
+        dw.T = n;
+        for (Product *o : {&dx, &dw}) {
+            o->f32 = f32;
+            o->wide = c.K % 8 == 0 && (uintptr_t)o->out % 16 == 0 && o->out_b * el % 16 == 0 && o->out_t * el % 16 == 0;
+        }
+        if ((e = launch<OUT>(outs, p, st)) != cudaSuccess || (e = join(dx, st)) != cudaSuccess || (e = join(dw, st)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

@@ -27,11 +27,13 @@ struct Call {
     float2 *part;                   // forward: [2 tiles][M] maximum and sum
     char *d;                        // backward: [planes][M][piece] bf16 gradients of the logits of a piece
     float *acc;                     // backward: [M][K] sums of dx over pieces (more than one)
+    float *cut;                     // backward: parts of dx and of a piece of dw whose contractions are cut
     float *loss, *lse;
     void *dw;
 };
 
 int tiles_of(int n);                // of 256
+void cuts_of(int M, int K, int n, int planes, int &dx, int &dw);   // parts that a piece's two contractions are cut into
 cudaError_t forward(const Call &c, cudaStream_t st);
 cudaError_t backward(const Call &c, cudaStream_t st);
 

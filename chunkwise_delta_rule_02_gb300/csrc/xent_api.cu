@@ -11,7 +11,10 @@ namespace {
 using lay::align256;
 
 // Most bytes of a piece's logit gradients: what the two products that read them find in the L2 cache.
-constexpr long long kPieceBytes = 128ll << 20;
+#ifndef PMB
+#define PMB 128ll
+#endif
+constexpr long long kPieceBytes = PMB << 20;
 
 bool aligned(const void *p, size_t n) { return ((uintptr_t)p % n) == 0; }
 bool has(const dn_view *v) { return v && v->data; }
@@ -81,6 +84,15 @@ size_t layout(Call &c, const dn_xent_shape *s, const dn_view *x, const dn_view *
         c.piece = (int)n;
         c.d = take((size_t)c.planes * c.M * n * 2);
         if (n < c.V) c.acc = (float *)take((size_t)c.M * c.K * 4);
+        // the last piece may be shorter, and cut otherwise
+        size_t cut = 0;
+        for (long long piece : {n, (c.V - 1) % n + 1}) {
+            int dx, dw;
+            cuts_of(c.M, c.K, (int)(piece < c.V ? piece : c.V), c.planes, dx, dw);
+            const size_t room = (dx > 1 ? (size_t)dx * c.M * c.K : 0) + (dw > 1 ? (size_t)dw * piece * c.K : 0);
+            if (room > cut) cut = room;
+        }
+        if (cut) c.cut = (float *)take(cut * 4);
     }
     return at;
 }
