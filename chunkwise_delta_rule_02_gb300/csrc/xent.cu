@@ -7,6 +7,7 @@
 // MN-major in memory, so that all four products run on x, w and D as they lie.  Warp 0 loads, warp 1 of the even CTA issues the
 // MMAs, eight warps take the finished tile from TMEM while the next one is computed in the other half of it.  What they do with it:
 //   STATS  maximum and sum of exponentials of a row over 128 columns, and the target's logit;
+//   SCORE  the same of few tokens, which are the columns then: the weight's rows are read once, in equal shares;
 //   GRAD   D, rounded to the operand's type for the two products that read it;
 //   OUT    the tile itself, added to what earlier pieces gave.
 // D in bf16 (2^-9 of each value) is what a bf16 input's gradient is computed from: the sums over the vocabulary and over the tokens
@@ -25,17 +26,18 @@ using lay::ex2;
 using lay::kLog2e;
 
 constexpr int TILE = 256, HALF = 128, BK = 64, STAGES = 6, THREADS = 320, EPI_WARPS = 8;
-constexpr int OPERAND = HALF * BK * 2, STAGE = 2 * OPERAND;          // bytes a CTA loads: of one operand, of both
-constexpr int SMEM = STAGES * STAGE + 1024 + 256;
+constexpr int OPERAND = HALF * BK * 2;                               // bytes of 128 rows of an operand
+constexpr int SMEM = 2 * STAGES * OPERAND + 1024 + 256;
 constexpr long long BUDGET = 4000000000LL;                           // clock cycles (about 2 s) for any one wait
 constexpr int GROUP = 16;                                            // row tiles that share the column tiles of a wave
 constexpr float kNone = -1e30f;                                      // maximum of no logits
+constexpr int kScore = 128;                                          // tokens up to which they are the columns
 
 // Steps after which float32 inputs' sums leave TMEM: the tensor core cuts what it adds off rather than rounding it, the same way each
 // time, which a contraction of 70001 tokens added up to 8e-5 of dw; segments of 256 are summed in registers, rounded.
 constexpr int kSegment = 4;
 
-enum { STATS, GRAD, OUT };
+enum { STATS, GRAD, OUT, SCORE };
 
 // One product C = A B^T and how its tiles are cut: units of a tile and a part of the contraction.
 struct Product {
@@ -58,15 +60,29 @@ struct Gemm {
     int np;                         // plane products: nibbles of pa, pb
     uint32_t pa, pb;
     uint32_t *status;
-    // STATS, GRAD
-    const int32_t *tgt;
-    const float *lse, *g;
-    float *row;
+    // STATS, GRAD, SCORE
+    const int64_t *tgt;             // of token (b, t) at b tgt_b + t tgt_t
+    const float *dloss;
+    long long tgt_b, tgt_t, g_b, g_t, ignore;
+    int T, V;
+    const float *lse;
+    float *row;                     // [M] the target's logit
     float2 *part;
+    int share;                      // SCORE: rows of w that a CTA has of a unit
     __nv_bfloat16 *d;
     long long d_pitch, d_plane;
     int v0, planes;
 };
+
+// A token's target, -1 for none: ignored, or (which the status word is told) outside the vocabulary.
+__device__ __forceinline__ int target_of(const Gemm &p, int row, bool tell)
+{
+    const long long v = p.tgt[(long long)(row / p.T) * p.tgt_b + (long long)(row % p.T) * p.tgt_t];
+    if (v == p.ignore) return -1;
+    if (v >= 0 && v < p.V) return (int)v;
+    if (tell) raise_status(p.status, kStatusBadOffsets);
+    return -1;
+}
 
 // Units of the two products for pair `p` of `n`: the first product's dealt in turn, the second's so that pairs with fewer of the
 // first have the more of the second that its length makes up for.
@@ -107,9 +123,11 @@ struct Maps {
 };
 
 // OUT: two products, D w and D^T x: B is MN-major in both, A in the second.  Otherwise one, both operands K-major.
-template <int EPI, bool SEG>
+// NT: columns of a tile (SCORE: 32, 64 or 128 tokens).
+template <int EPI, bool SEG, int NT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(const __grid_constant__ Maps maps, const __grid_constant__ Gemm p)
 {
+    constexpr int STAGE = OPERAND + NT / 2 * BK * 2;   // bytes a CTA loads of both operands
     extern __shared__ char raw[];
     char *sm = (char *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     uint64_t *bar = (uint64_t *)(sm + STAGES * STAGE);
@@ -155,6 +173,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
     };
     auto unit = [&](const Product &o, int u) {
         Unit r;
+        if (EPI == SCORE) return Unit{u * 2 * p.share, 0, 0, o.kb, 0};
         const int tiles = o.mt * o.nt;
         r.cut = u / tiles;
         const int tile = u - r.cut * tiles, per = GROUP * o.nt, grp = tile / per, in = tile - grp * per, gm = min(GROUP, o.mt - grp * GROUP);
@@ -178,7 +197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
                 constexpr bool B_MN = EPI == OUT;
                 for (int i = 0; ok && i < deal.count[o]; ++i) {
                     const Unit u = unit(pr, deal.first[o] + i * deal.step[o]);
-                    const int m = u.m + rank * HALF, n = u.n + rank * HALF, segs = segments(u);
+                    const int m = u.m + rank * (EPI == SCORE ? p.share : HALF), n = u.n + rank * (NT / 2), segs = segments(u);
                     for (int sq = 0; ok && sq < segs * p.np; ++sq) {
                         const int seg = sq / p.np, q = sq - seg * p.np;
                         const int a = p.pa >> 4 * q & 15, b = p.pb >> 4 * q & 15;
@@ -219,7 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
             bool ok = true;
             for (int o = 0; o < PRODUCTS; ++o) {
                 const bool a_mn = EPI == OUT && o == 1;
-                const uint32_t id = a_mn ? idesc(1, TILE, TILE, true, B_MN) : idesc(1, TILE, TILE, false, B_MN);
+                const uint32_t id = a_mn ? idesc(1, TILE, NT, true, B_MN) : idesc(1, TILE, NT, false, B_MN);
                 const uint32_t astep = a_mn ? 2048 : 32, alead = a_mn ? OPERAND / 2 : 16;
                 for (int i = 0; ok && i < deal.count[o]; ++i) {
                     const Unit u = unit(p.of[o], deal.first[o] + i * deal.step[o]);
@@ -249,6 +268,98 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
             pair_commit(&bar[DONE]);
             pair_wait(&bar[DONE], 0, BUDGET, &never);
         }
+    } else if constexpr (EPI == SCORE) {
+        // Rows are entries of the vocabulary, columns tokens, 32 a chunk and in turn a lane each; a warp joins its units' statistics.
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        constexpr int CHUNKS = NT / 32, MINE = (CHUNKS + 1) / 2;   // of this warp: half, half + 2
+        float mx[MINE], sum[MINE];
+        int target[MINE];
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+            const int token = 32 * (half + 2 * i) + lane;
+            mx[i] = kNone;
+            sum[i] = 0.f;
+            target[i] = half + 2 * i < CHUNKS && token < p.of[0].N ? target_of(p, token, blockIdx.x == 0 && quad == 2) : -1;
+        }
+        uint32_t n = 0;
+        bool ok = true;
+        for (int i = 0; i < deal.count[0]; ++i) {
+            const Unit u = unit(p.of[0], deal.first[0] + i * deal.step[0]);
+            const int in_cta = quad * 32 + lane, row = u.m + rank * p.share + in_cta;
+            const bool in = in_cta < p.share && row < p.of[0].M;
+            float all[MINE][32];
+#pragma unroll
+            for (int c = 0; c < MINE; ++c)
+#pragma unroll
+                for (int k = 0; k < 32; ++k) all[c][k] = 0.f;
+            for (int seg = segments(u); seg > 0; --seg) {
+                if (!(ok = wait(TFULL + (n & 1), n >> 1))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < MINE; ++c) {
+                    if (half + 2 * c < CHUNKS) {
+                        uint32_t r[32];
+                        tmem_ld32(tmem + (n & 1) * TILE + lanes + 32 * (half + 2 * c), r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) all[c][k] += __uint_as_float(r[k]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) peer_arrive(peer_addr(&bar[TEMPTY + (n & 1)], 0));
+                ++n;
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int c = 0; c < MINE; ++c) {
+                if (half + 2 * c >= CHUNKS) continue;
+                float(&v)[32] = all[c];
+                // targets among this warp's 32 entries
+                const int at = target[c] - (row - lane);
+                const bool mine = at >= 0 && at < 32 && quad * 32 + at < p.share;
+                for (uint32_t left = __ballot_sync(0xffffffffu, mine); left; left &= left - 1) {
+                    const int k = __ffs(left) - 1, who = __shfl_sync(0xffffffffu, at, k);
+                    float t = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) t = j == k ? v[j] : t;
+                    if (lane == who) p.row[32 * (half + 2 * c) + k] = t;
+                }
+                // each column's maximum, in the lane of its token, by halving; then its sum
+                float w[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) w[k] = v[k] = in ? v[k] : -INFINITY;
+#pragma unroll
+                for (int m = 16; m > 0; m >>= 1) {
+                    const bool up = lane & m;
+#pragma unroll
+                    for (int k = 0; k < m; ++k) {
+                        const float send = up ? w[k] : w[k + m], keep = up ? w[k + m] : w[k];
+                        w[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, m));
+                    }
+                }
+                const float top = fmaxf(mx[c], w[0]);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) w[k] = ex2((v[k] - __shfl_sync(0xffffffffu, top, k)) * kLog2e);
+#pragma unroll
+                for (int m = 16; m > 0; m >>= 1) {
+                    const bool up = lane & m;
+#pragma unroll
+                    for (int k = 0; k < m; ++k) {
+                        const float send = up ? w[k] : w[k + m], keep = up ? w[k + m] : w[k];
+                        w[k] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+                    }
+                }
+                sum[c] = fmaf(sum[c], ex2((mx[c] - top) * kLog2e), w[0]);
+                mx[c] = top;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < MINE; ++c) {
+            const int token = 32 * (half + 2 * c) + lane;
+            if (half + 2 * c < CHUNKS && token < p.of[0].N) p.part[(long long)(blockIdx.x * 4 + quad) * p.of[0].N + token] = make_float2(mx[c], sum[c]);
+        }
     } else {
         const int e = warp - 2, quad = warp & 3, half = e >> 2;   // TMEM lanes of this warp: 32 quad ..; columns: 128 half ..
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
@@ -262,11 +373,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
             const bool in = row < pr.M;
             [[maybe_unused]] int target = -1;
             [[maybe_unused]] float lse = 0.f, g = 0.f, mx = kNone, sum = 0.f;
-            if (EPI != OUT && in) {
-                target = p.tgt[row];
+            if ((EPI == STATS || EPI == GRAD) && in) {
+                target = target_of(p, row, p.v0 == 0 && u.n == 0 && half == 0);
                 if (EPI == GRAD) {
                     lse = p.lse[row];
-                    g = p.g[row];
+                    if (target >= 0) g = p.dloss[(long long)(row / p.T) * p.g_b + (long long)(row % p.T) * p.g_t];
                 }
             }
             auto finish = [&](int c, float (&v)[32]) {   // columns c0 + c .. + 31 of this thread's row
@@ -301,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const float prob = ex2((v[i] - lse) * kLog2e);
-                        v[i] = (i < live ? prob - (at + i == target ? 1.f : 0.f) : 0.f) * g;
+                        v[i] = i < live && target >= 0 ? (prob - (at + i == target ? 1.f : 0.f)) * g : 0.f;
                     }
                     if (in && col < p.d_pitch) {
                         for (int pl = 0; pl < p.planes; ++pl) {
@@ -417,24 +528,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
     if (warp == 1) pair_tmem_dealloc(tmem, 512);
 }
 
-// Targets as int32, -1 for none (ignored, or outside the vocabulary, which the status word says); backward: their dloss too.
-__global__ void __launch_bounds__(256) k_targets(lay::View<const int64_t> t, lay::View<const float> dloss, int M, int T, int V, int64_t ignore,
-                                                 int32_t *tgt, float *g, uint32_t *status)
+// One block: R rows, each 256 / R threads that take every so manieth of the row's pieces; then those in a fixed order.
+template <int R>
+__global__ void __launch_bounds__(256) k_lse(const __grid_constant__ Gemm p, const float2 *part, int P, int M, float *loss, float *lse)
 {
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= M) return;
-    const int64_t v = *t.at(i / T, 0, i % T);
-    const bool in = v != ignore && v >= 0 && v < V;
-    if (v != ignore && !in) raise_status(status, kStatusBadOffsets);
-    tgt[i] = in ? (int32_t)v : -1;
-    if (g) g[i] = in ? *dloss.at(i / T, 0, i % T) : 0.f;
-}
-
-// One block: 32 rows, a warp every 8th of a row's pieces; then the 8 in a fixed order.
-__global__ void __launch_bounds__(256) k_lse(const float2 *part, int P, int M, const int32_t *tgt, const float *row, float *loss, float *lse)
-{
-    __shared__ float2 sm[8][32];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, r = blockIdx.x * 32 + lane;
+    constexpr int S = 256 / R;
+    __shared__ float2 sm[S][R];
+    const int i = threadIdx.x % R, w = threadIdx.x / R, r = blockIdx.x * R + i;
     float mx = kNone, sum = 0.f;
     auto join = [&](float2 q) {
         const float top = fmaxf(mx, q.x);
@@ -443,33 +543,57 @@ __global__ void __launch_bounds__(256) k_lse(const float2 *part, int P, int M, c
     };
     if (r < M) {
 #pragma unroll 4
-        for (int j = w; j < P; j += 8) join(part[(long long)j * M + r]);
+        for (int j = w; j < P; j += S) join(part[(long long)j * M + r]);
     }
-    sm[w][lane] = make_float2(mx, sum);
-    __syncthreads();
+    sm[w][i] = make_float2(mx, sum);
+    for (int h = S / 2; h > 0; h >>= 1) {
+        __syncthreads();
+        if (w < h) {
+            mx = sm[w][i].x;
+            sum = sm[w][i].y;
+            join(sm[w + h][i]);
+            sm[w][i] = make_float2(mx, sum);
+        }
+    }
     if (w == 0 && r < M) {
-        for (int j = 1; j < 8; ++j) join(sm[j][lane]);
         const float l = mx + logf(sum);
         lse[r] = l;
-        loss[r] = tgt[r] < 0 ? 0.f : l - row[r];
+        loss[r] = target_of(p, r, false) < 0 ? 0.f : l - p.row[r];
     }
 }
 
-// Rows into [planes][rows][pitch] bf16: as they are, or as three planes, the largest first.  pitch is a multiple of 8.
+// x and w into [planes][rows][pitch] bf16: as they are, or as three planes, the largest first.  A thread has 8 columns of a row,
+// 2^shift threads a row at a time; the first blocks have x's rows.
+struct Packing {
+    const void *from[2];
+    long long b[2], t[2], pitch[2], plane[2];
+    __nv_bfloat16 *to[2];
+    int rows[2], T[2], blocks[2];
+    int K, shift;
+};
+
 template <class T>
-__global__ void __launch_bounds__(256) k_pack(lay::View<const T> v, int R, int T_, int K, __nv_bfloat16 *out, long long pitch, long long plane)
+__global__ void __launch_bounds__(256) k_pack(const __grid_constant__ Packing p)
 {
-    const long long all = (long long)R * pitch, step = (long long)gridDim.x * 256;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < all; i += step) {
-        const int r = (int)(i / pitch), k = (int)(i - r * pitch);
-        const float f = k < K ? ld_in(v.at(r / T_, 0, r % T_) + k) : 0.f;
-        const __nv_bfloat16 a = __float2bfloat16_rn(f);
-        out[i] = a;
-        if (sizeof(T) == 4) {
-            const float g = f - __bfloat162float(a);
-            const __nv_bfloat16 b = __float2bfloat16_rn(g);
-            out[i + plane] = b;
-            out[i + 2 * plane] = __float2bfloat16_rn(g - __bfloat162float(b));
+    const int o = blockIdx.x >= p.blocks[0], per = 256 >> p.shift;
+    const int r = (blockIdx.x - (o ? p.blocks[0] : 0)) * per + (threadIdx.x >> p.shift);
+    if (r >= p.rows[o]) return;
+    const T *from = (const T *)p.from[o] + (long long)(r / p.T[o]) * p.b[o] + (long long)(r % p.T[o]) * p.t[o];
+    __nv_bfloat16 *to = p.to[o] + r * p.pitch[o];
+    for (int c = (threadIdx.x & ((1 << p.shift) - 1)) * 8; c < p.pitch[o]; c += 8 << p.shift) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = c + e < p.K ? ld_in(from + c + e) : 0.f;
+#pragma unroll
+        for (int pl = 0; pl < (sizeof(T) == 4 ? 3 : 1); ++pl) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
+                f[2 * e] -= __uint_as_float(w[e] << 16);   // what the next plane holds
+                f[2 * e + 1] -= __uint_as_float(w[e] & 0xFFFF0000u);
+            }
+            *reinterpret_cast<uint4 *>(to + pl * p.plane[o] + c) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 }
@@ -520,11 +644,11 @@ void size(Product &o, int M, int N, int contraction)
 
 int pairs_at_most() { return lay::sm_count() / 2; }
 
-template <int EPI, bool SEG>
+template <int EPI, bool SEG, int NT = TILE>
 cudaError_t launch_as(const Maps &m, Gemm &p, cudaStream_t st)
 {
     p.seg = kSegment;
-    auto kernel = k_gemm<EPI, SEG>;
+    auto kernel = k_gemm<EPI, SEG, NT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     long long units = 0, pairs = pairs_at_most();
@@ -533,10 +657,10 @@ cudaError_t launch_as(const Maps &m, Gemm &p, cudaStream_t st)
     return cudaPeekAtLastError();
 }
 
-template <int EPI>
+template <int EPI, int NT = TILE>
 cudaError_t launch(const Maps &m, Gemm &p, cudaStream_t st)
 {
-    return p.np > 1 ? launch_as<EPI, true>(m, p, st) : launch_as<EPI, false>(m, p, st);
+    return p.np > 1 ? launch_as<EPI, true, NT>(m, p, st) : launch_as<EPI, false, NT>(m, p, st);
 }
 
 cudaError_t join(const Product &o, cudaStream_t st)
@@ -559,31 +683,59 @@ Gemm common(const Call &c)
     p.np = c.planes == 1 ? 1 : 6;
     p.pa = c.planes == 1 ? 0 : 0x001102;
     p.pb = c.planes == 1 ? 0 : 0x010120;
-    p.tgt = c.tgt;
+    p.tgt = (const int64_t *)c.targets->data;
+    p.tgt_b = c.targets->batch;
+    p.tgt_t = c.targets->time;
+    p.ignore = c.s->ignore_index;
+    p.T = c.s->T;
+    p.V = c.V;
+    if (c.dloss) {
+        p.dloss = (const float *)c.dloss->data;
+        p.g_b = c.dloss->batch;
+        p.g_t = c.dloss->time;
+    }
     p.lse = c.lse;
     p.row = c.row;
-    p.g = c.row;
     p.part = c.part;
     return p;
 }
 
-template <class T>
-void pack(const dn_view *v, int rows, int per, int K, const Operand &o, cudaStream_t st)
-{
-    const long long n = ((long long)rows * o.pitch + 255) / 256, most = 32ll * lay::sm_count();
-    k_pack<T><<<(unsigned)(n < most ? n : most), 256, 0, st>>>(lay::view_of<const T>(v), rows, per, K, (__nv_bfloat16 *)o.p, o.pitch, o.plane);
-}
-
-cudaError_t begin(const Call &c, bool bwd, cudaStream_t st)
+// Clears the status word; copies what the tensor maps cannot read in place.
+cudaError_t begin(const Call &c, cudaStream_t st)
 {
     cudaError_t e = cudaMemsetAsync(c.status, 0, sizeof(uint32_t), st);
-    if (e != cudaSuccess || c.M == 0) return e;
-    const bool f32 = c.s->dtype == DN_F32;
-    if (c.pack_x) f32 ? pack<float>(c.x, c.M, c.s->T, c.K, c.xo, st) : pack<__nv_bfloat16>(c.x, c.M, c.s->T, c.K, c.xo, st);
-    if (c.pack_w) f32 ? pack<float>(c.w, c.V, c.V, c.K, c.wo, st) : pack<__nv_bfloat16>(c.w, c.V, c.V, c.K, c.wo, st);
-    k_targets<<<(c.M + 255) / 256, 256, 0, st>>>(lay::view_of<const int64_t>(c.targets), lay::view_of<const float>(c.dloss), c.M, c.s->T, c.V,
-                                                 c.s->ignore_index, c.tgt, bwd ? c.row : nullptr, c.status);
+    if (e != cudaSuccess || c.M == 0 || !(c.pack_x || c.pack_w)) return e;
+    Packing p = {};
+    const dn_view *views[2] = {c.x, c.w};
+    const Operand *to[2] = {&c.xo, &c.wo};
+    const int rows[2] = {c.M, c.V}, per[2] = {c.s->T, c.V};
+    const bool packs[2] = {c.pack_x, c.pack_w};
+    p.K = c.K;
+    while (p.shift < 8 && 8 << p.shift < c.K) ++p.shift;
+    for (int o = 0; o < 2; ++o) {
+        p.T[o] = per[o];
+        if (!packs[o]) continue;
+        p.from[o] = views[o]->data;
+        p.b[o] = views[o]->batch;
+        p.t[o] = views[o]->time;
+        p.to[o] = (__nv_bfloat16 *)to[o]->p;
+        p.pitch[o] = to[o]->pitch;
+        p.plane[o] = to[o]->plane;
+        p.rows[o] = rows[o];
+        p.blocks[o] = (int)(((long long)rows[o] + (256 >> p.shift) - 1) / (256 >> p.shift));
+    }
+    const unsigned blocks = (unsigned)p.blocks[0] + (unsigned)p.blocks[1];
+    if (c.s->dtype == DN_F32) k_pack<float><<<blocks, 256, 0, st>>>(p);
+    else k_pack<__nv_bfloat16><<<blocks, 256, 0, st>>>(p);
     return cudaPeekAtLastError();
+}
+
+// SCORE: pairs take equal shares of the vocabulary, in as few rounds as tiles of 256 rows need
+int score_units(int V, int &share)
+{
+    const int pairs = pairs_at_most(), rounds = (tiles_of(V) + pairs - 1) / pairs;
+    share = (int)(((long long)V + 2ll * pairs * rounds - 1) / (2ll * pairs * rounds));
+    return (int)(((long long)V + 2 * share - 1) / (2 * share));
 }
 
 }  // namespace
@@ -602,22 +754,47 @@ void cuts_of(int M, int K, int n, int planes, int &dx, int &dw)
     dw = (int)((b + share - 1) / share);
 }
 
+// Pieces of a row that the forward pass leaves for k_lse
+int parts_of(int M, int V)
+{
+    if (M > kScore) return 2 * tiles_of(V);
+    int share;
+    const int units = score_units(V, share), pairs = pairs_at_most();
+    return 2 * 4 * (units < pairs ? units : pairs);
+}
+
 cudaError_t forward(const Call &c, cudaStream_t st)
 {
-    cudaError_t e = begin(c, false, st);
+    cudaError_t e = begin(c, st);
     if (e != cudaSuccess || c.M == 0) return e;
     Maps m = {};
-    if (!make_map(&m.a[0], c.xo, c.K, c.M, c.planes, HALF) || !make_map(&m.b[0], c.wo, c.K, c.V, c.planes, HALF)) return cudaErrorInvalidValue;
     Gemm p = common(c);
-    size(p.of[0], c.M, c.V, c.K);
-    if ((e = launch<STATS>(m, p, st)) != cudaSuccess) return e;
-    k_lse<<<(c.M + 31) / 32, 256, 0, st>>>(c.part, 2 * tiles_of(c.V), c.M, c.tgt, c.row, c.loss, c.lse);
+    if (c.M > kScore) {
+        if (!make_map(&m.a[0], c.xo, c.K, c.M, c.planes, HALF) || !make_map(&m.b[0], c.wo, c.K, c.V, c.planes, HALF)) return cudaErrorInvalidValue;
+        size(p.of[0], c.M, c.V, c.K);
+        e = launch<STATS>(m, p, st);
+    } else {
+        const int nt = c.M <= 32 ? 32 : c.M <= 64 ? 64 : 128;
+        if (!make_map(&m.a[0], c.wo, c.K, c.V, c.planes, HALF) || !make_map(&m.b[0], c.xo, c.K, c.M, c.planes, nt / 2)) return cudaErrorInvalidValue;
+        size(p.of[0], c.V, c.M, c.K);
+        p.of[0].mt = score_units(c.V, p.share);
+        p.of[0].nt = 1;
+        // the planes change places
+        const uint32_t pa = p.pa;
+        p.pa = p.pb;
+        p.pb = pa;
+        e = nt == 32 ? launch<SCORE, 32>(m, p, st) : nt == 64 ? launch<SCORE, 64>(m, p, st) : launch<SCORE, 128>(m, p, st);
+    }
+    if (e != cudaSuccess) return e;
+    const int P = parts_of(c.M, c.V);
+    if (c.M > 2048) k_lse<32><<<(c.M + 31) / 32, 256, 0, st>>>(p, c.part, P, c.M, c.loss, c.lse);
+    else k_lse<4><<<(c.M + 3) / 4, 256, 0, st>>>(p, c.part, P, c.M, c.loss, c.lse);
     return cudaPeekAtLastError();
 }
 
 cudaError_t backward(const Call &c, cudaStream_t st)
 {
-    cudaError_t e = begin(c, true, st);
+    cudaError_t e = begin(c, st);
     if (e != cudaSuccess) return e;
     const bool f32 = c.s->dtype == DN_F32;
     if (c.M == 0) return cudaMemsetAsync(c.dw, 0, (size_t)c.V * c.K * (f32 ? 4 : 2), st);

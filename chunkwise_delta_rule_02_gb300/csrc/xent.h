@@ -22,9 +22,8 @@ struct Call {
     Operand xo, wo;
     bool pack_x, pack_w;
     uint32_t *status;
-    int32_t *tgt;                   // [M] targets, -1: none
-    float *row;                     // [M] forward: the target's logit; backward: dloss, 0 without a target
-    float2 *part;                   // forward: [2 tiles][M] maximum and sum
+    float *row;                     // forward: [M] the target's logit
+    float2 *part;                   // forward: [parts_of][M] maximum and sum
     char *d;                        // backward: [planes][M][piece] bf16 gradients of the logits of a piece
     float *acc;                     // backward: [M][K] sums of dx over pieces (more than one)
     float *cut;                     // backward: parts of dx and of a piece of dw whose contractions are cut
@@ -33,6 +32,7 @@ struct Call {
 };
 
 int tiles_of(int n);                // of 256
+int parts_of(int M, int V);
 void cuts_of(int M, int K, int n, int planes, int &dx, int &dw);   // parts that a piece's two contractions are cut into
 cudaError_t forward(const Call &c, cudaStream_t st);
 cudaError_t backward(const Call &c, cudaStream_t st);

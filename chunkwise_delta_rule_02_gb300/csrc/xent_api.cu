@@ -11,10 +11,7 @@ namespace {
 using lay::align256;
 
 // Most bytes of a piece's logit gradients: what the two products that read them find in the L2 cache.
-#ifndef PMB
-#define PMB 128ll
-#endif
-constexpr long long kPieceBytes = PMB << 20;
+constexpr long long kPieceBytes = 128ll << 20;
 
 bool aligned(const void *p, size_t n) { return ((uintptr_t)p % n) == 0; }
 bool has(const dn_view *v) { return v && v->data; }
@@ -72,10 +69,9 @@ size_t layout(Call &c, const dn_xent_shape *s, const dn_view *x, const dn_view *
     if (c.M == 0) return at;
     operand(c.xo, c.pack_x, x, c.M, s->T);
     operand(c.wo, c.pack_w, w, c.V, c.V);
-    c.tgt = (int32_t *)take((size_t)c.M * 4);
-    c.row = (float *)take((size_t)c.M * 4);
     if (!bwd) {
-        c.part = (float2 *)take((size_t)c.M * 2 * tiles_of(c.V) * sizeof(float2));
+        c.row = (float *)take((size_t)c.M * 4);
+        c.part = (float2 *)take((size_t)c.M * parts_of(c.M, c.V) * sizeof(float2));
     } else {
         long long n = kPieceBytes / (2ll * c.planes * c.M) / 256 * 256;
         const long long whole = (c.V + 255ll) / 256 * 256;

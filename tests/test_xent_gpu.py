@@ -75,7 +75,7 @@ def check(gdn, x, w, t, dloss):
 
 
 SHAPES = [((1, 1), 1), ((1, 64), 5), ((3, 8), 300), ((7, 40), 257), ((128, 64), 256), ((129, 72), 512), ((257, 128), 1000), ((2, 100, 203), 777),
-          ((300, 1), 2), ((5, 515), 40), ((600, 320), 1300), ((4, 1, 16), 30), ((1, 9, 24), 70)]
+          ((300, 1), 2), ((5, 515), 40), ((32, 64), 3000), ((33, 48), 20000), ((64, 24), 40001), ((65, 136), 700), ((128, 200), 25000), ((1, 256), 50000), ((600, 320), 1300), ((4, 1, 16), 30), ((1, 9, 24), 70)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
