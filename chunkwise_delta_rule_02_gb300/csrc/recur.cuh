@@ -60,7 +60,7 @@ struct RecurIo {
 };
 
 struct RecurMaps {
-    CUtensorMap in[kArrays];
+    CUtensorMap in[kArrays], kept;   // kept: the kept states, backward
 };
 
 struct RecurCall {
@@ -209,14 +209,33 @@ __device__ __forceinline__ void cluster_barrier()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// 16 bytes into the shared memory of the cluster's block `rank`, at this block's address `dst`
-__device__ __forceinline__ void remote_store(const float4 *dst, int rank, float4 v)
+// 16 bytes into the shared memory of the cluster's block `rank`, at this block's address `dst`, counted by its barrier `bar`
+__device__ __forceinline__ void remote_store(const float4 *dst, const uint64_t *bar, int rank, float4 v)
 {
     asm volatile(
-        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
-        "st.shared::cluster.v4.f32 [a], {%2, %3, %4, %5};\n\t}" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
-        "r"(rank), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+        "{\n\t.reg .b32 a, b;\n\tmapa.shared::cluster.u32 a, %0, %2;\n\tmapa.shared::cluster.u32 b, %1, %2;\n\t"
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [a], {%3, %4, %5, %6}, [b];\n\t}" ::"r"(sm100::smem_u32(dst)),
+        "r"(sm100::smem_u32(bar)), "r"(rank), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
         : "memory");
+}
+
+// Bounded wait as sm100::mbar_wait, acquiring what the cluster's blocks stored
+__device__ __forceinline__ bool cluster_wait(uint64_t *bar, uint32_t parity, long long budget)
+{
+    long long t0 = 0;
+    for (int i = 0;; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(sm100::smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (i == 0) t0 = clock64();
+        else if (clock64() - t0 > budget) return false;
+    }
 }
 
 __device__ __forceinline__ void box_load(void *dst, const CUtensorMap *map, uint64_t *bar, int c, int t, int b)
@@ -234,18 +253,20 @@ template <int W, int Q>
 struct RecurShared {
     float4 warp[2][W][32 / Q];
     float2 carry[2][32 / Q];
-    uint64_t bar[2];
+    uint64_t bar[4];               // the inputs of a step are there; behind those: the cluster's maps are
 };
 
-// The maps of a step's runs, exchanged: (A, H) of this thread's run in, what enters it out (the state before it in the order
-// of the pass, BACK: from the last run to the first).  What entered the step is `carry` in a cluster, and becomes what leaves it;
-// a block alone has it in shared memory, where the step's last run leaves it (leave()).  `rank` is the block's place in the
-// cluster.  Maps of a step lie in buffer `par`, so that one barrier a level suffices; `block`: [2][CL][32 / Q] of the cluster's blocks.
-// `freed` is called behind the first barrier.
+// The maps of the runs of step `st`, exchanged: (A, H) of this thread's run in, what enters it out (the state before it in the
+// order of the pass, BACK: from the last run to the first).  What entered the step is `carry` in a cluster, and becomes what leaves
+// it; a block alone has it in shared memory, where the step's last run leaves it (leave()).  `rank` is the block's place in the
+// cluster.  Maps of two steps have places of their own, so that one barrier a step suffices: a block stores its map into the others
+// behind it, and they their next ones only when they have all of this step's, so that nobody overwrites what is still read.
+// `block`: [2][CL][32 / Q] of the cluster's blocks.  `freed` is called behind the barrier.
 template <int W, int Q, bool CUT, bool BACK, class F>
-__device__ __forceinline__ float2 exchange(RecurShared<W, Q> &sm, float4 *block, int par, int CL, int rank, float2 A, float2 H, float2 &carry,
-                                           F freed)
+__device__ __forceinline__ float2 exchange(RecurShared<W, Q> &sm, float4 *block, int st, int CL, int rank, float2 A, float2 H, float2 &carry,
+                                           bool &failed, uint32_t *status, F freed)
 {
+    const int par = st & 1;
     constexpr int L = 32 / Q;
     const int lane = threadIdx.x & 31, l = lane % L, warp = threadIdx.x >> 5;
     const int mine = BACK ? W - 1 - warp : warp, at = BACK ? CL - 1 - rank : rank, q = BACK ? Q - 1 - lane / L : lane / L;
@@ -274,7 +295,7 @@ __device__ __forceinline__ float2 exchange(RecurShared<W, Q> &sm, float4 *block,
     __syncthreads();
     freed();
     float2 h;
-    if (CL == 1) {
+    if (Q < 4 || CL == 1) {   // wider tiles are never shared (recur_plan)
         h = sm.carry[par][l];
 #pragma unroll 4
         for (int w = 0; w < mine; ++w) {
@@ -282,21 +303,25 @@ __device__ __forceinline__ float2 exchange(RecurShared<W, Q> &sm, float4 *block,
             h = pass<CUT>(make_float2(m.x, m.y), make_float2(m.z, m.w), h);
         }
     } else {
-        float2 wA = two(1.f), wH = two(0.f), oA = wA, oH = wH;   // of the warps before this one; of all
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            if (w == mine) {
-                wA = oA;
-                wH = oH;
-            }
+        if (threadIdx.x == 0) sm100::mbar_expect_tx(&sm.bar[2 + par], CL * L * 16);
+        float2 wA = two(1.f), wH = two(0.f);   // of the warps before this one
+#pragma unroll 4
+        for (int w = 0; w < mine; ++w) {
             const float4 m = sm.warp[par][w][l];
-            then<CUT>(oA, oH, make_float2(m.x, m.y), make_float2(m.z, m.w));
+            then<CUT>(wA, wH, make_float2(m.x, m.y), make_float2(m.z, m.w));
         }
-        // each warp tells some blocks
-        if (lane < L)
-            for (int k = warp; k < CL; k += W) remote_store(block + (par * CL + at) * L + l, k, make_float4(oA.x, oA.y, oH.x, oH.y));
-        __syncwarp();
-        cluster_barrier();
+        if (mine == W - 1) {   // the last one tells all blocks the whole
+            const float4 m = sm.warp[par][W - 1][l];
+            float2 oA = wA, oH = wH;
+            then<CUT>(oA, oH, make_float2(m.x, m.y), make_float2(m.z, m.w));
+            if (lane < L)
+                for (int k = 0; k < CL; ++k) remote_store(block + (par * CL + at) * L + l, &sm.bar[2 + par], k, make_float4(oA.x, oA.y, oH.x, oH.y));
+            __syncwarp();
+        }
+        if (!cluster_wait(&sm.bar[2 + par], (uint32_t)(st >> 1) & 1u, failed ? 1000 : kRecurBudget)) {
+            failed = true;
+            raise_status(status, kStatusTimeout);
+        }
         h = carry;
         for (int k = 0; k < CL; ++k) {
             if (k == at) h = carry;
@@ -358,12 +383,14 @@ __host__ __device__ constexpr int box_rows(int Q)
     return W * kRun * Q / ((W * kRun * Q + 255) / 256);
 }
 
-// The inputs of a block's two steps.  `sets`: bit mask of the arrays that a call has; their places follow each other.
-template <class T, int W, int Q, int MODE>
+// The inputs of a block's two steps.  `sets`: bit mask of the arrays that a call has; their places follow each other, and behind
+// them, KEPT (TMA only), the states that the block's runs start from.
+template <class T, int W, int Q, int MODE, bool KEPT>
 struct Inputs {
     static constexpr int C = 64 / Q, R = kRun * Q, kPlace = W * kRun * 64 * (int)sizeof(T);   // channels, tokens of a warp, bytes of an array's place
     static constexpr int kRows = box_rows<W>(Q), kBoxes = W * R / kRows;                         // of an array
     static_assert(kRows * kBoxes == W * R, "boxes share the rows evenly");
+    static constexpr int kKept = KEPT ? W * 64 * 4 : 0;
     char *base;
     uint64_t *bar;
     const RecurIo<T> *io;
@@ -372,7 +399,8 @@ struct Inputs {
     bool failed;
 
     __device__ __forceinline__ int place(int array) const { return __popc(sets & ((1 << array) - 1)); }
-    __device__ __forceinline__ char *slot(int st, int array) const { return base + ((st & 1) * count + place(array)) * kPlace; }
+    __device__ __forceinline__ char *slot(int st, int array) const { return base + (st & 1) * (count * kPlace + kKept) + place(array) * kPlace; }
+    __device__ __forceinline__ char *kept(int st) const { return base + (st & 1) * (count * kPlace + kKept) + count * kPlace; }
     // of a lane's two channels of its run's first token
     __device__ __forceinline__ const T *cells(int st, int array) const
     {
@@ -399,9 +427,8 @@ struct Inputs {
         count = __popc(sets);
         b = b_; c0 = c0_; D = D_;
         failed = false;
-        if (MODE == kTma && threadIdx.x == 0) {
-            sm100::mbar_init(&bar[0], 1);
-            sm100::mbar_init(&bar[1], 1);
+        if (threadIdx.x == 0) {   // the cluster's two as well
+            for (int i = 0; i < 4; ++i) sm100::mbar_init(&bar[i], 1);
             sm100::fence_barrier_init();
         }
     }
@@ -411,7 +438,8 @@ struct Inputs {
         if (MODE == kTma) {
             if (threadIdx.x == 0) {
                 uint64_t *full = &bar[st & 1];
-                sm100::mbar_expect_tx(full, count * kPlace);
+                sm100::mbar_expect_tx(full, count * kPlace + kKept);
+                if (KEPT) box_load(kept(st), &maps->kept, full, c0, t0 / kRun, b);
 #pragma unroll
                 for (int a = 0; a < kArrays; ++a)
                     if (sets >> a & 1)
@@ -514,11 +542,12 @@ __device__ __forceinline__ void put_two(T *p, float2 f, bool in0, bool in1)
     }
 }
 
-// How a call's inputs get to shared memory; TMA: their maps, in boxes of `rows` tokens.  `in`: bit mask of the arrays there.
+// How a call's inputs get to shared memory; TMA: their maps, in boxes of `rows` tokens (not without `maps`).  `in`: bit mask
+// of the arrays there.
 template <class T>
-int recur_mode(RecurMaps &m, const RecurIo<T> &io, int in, int rows, const RecurDims &g)
+int recur_mode(RecurMaps &m, const RecurIo<T> &io, int in, int rows, const RecurDims &g, bool maps = true)
 {
-    bool tma = g.T > 0 && g.D % 2 == 0, words = true;
+    bool tma = maps && g.T > 0 && g.D % 2 == 0, words = true;
     for (int a = 0; a < kArrays; ++a) {
         const View<const T> &i = io.in[a];
         if (in >> a & 1) {

@@ -25,18 +25,35 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
     float4 *block = reinterpret_cast<float4 *>(raw);   // maps of the cluster's blocks, then the inputs
     __shared__ RecurShared<W, Q> sm;
     __shared__ float2 red[3][W][L];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = g.CL > 1 ? cluster_rank() : 0;
-    const int id = blockIdx.x / g.CL, b = id / g.tiles, c0 = (id - b * g.tiles) * (64 / Q), c = c0 + 2 * (lane % L);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, CL = Q < 4 ? 1 : g.CL;   // wider tiles are never shared
+    const int rank = CL > 1 ? cluster_rank() : 0, id = blockIdx.x / CL, b = id / g.tiles, c0 = (id - b * g.tiles) * (64 / Q), c = c0 + 2 * (lane % L);
     const int q = warp * R + lane / L * kRun;     // of this lane's run, in a block's tokens
     const bool in0 = c < g.D, in1 = c + 1 < g.D;
     const bool gated = io.in[kZ].p != nullptr;
-    Inputs<T, W, Q, MODE> inputs;
-    inputs.init(raw + recur_block_bytes(g.CL, Q), sm.bar, &io, &maps, gated ? 31 : 23, b, c0, g.D);
+    constexpr bool KEPT = MODE != kElements;   // kept states come with the inputs
+    Inputs<T, W, Q, MODE, KEPT> inputs;
+    inputs.init(raw + recur_block_bytes(CL, Q), sm.bar, &io, &maps, gated ? 31 : 23, b, c0, g.D);
     const int te = PACKED ? g.cu[g.Nseq] : g.T;
-    const int span = W * R * g.CL, steps = (te + span - 1) / span;
+    const int span = W * R * CL, steps = (te + span - 1) / span;
     int t0 = (steps - 1) * span + rank * W * R;   // the block's first token of a step; step st handles the st-th span from the end
+    const float *keep = io.keep + (size_t)b * ((g.T + kRun - 1) / kRun) * g.D + c;
+    const int kept = ((q / kRun) * (64 / Q) + 2 * (lane % L)) * 4;   // of this lane's run, among a step's
+    auto ask = [&](int st, int first) {   // step st, the block's tokens from `first`
+        inputs.ask(st, first, te);
+        if (MODE == kWords) {
+            const int t = first + q;
+            const float *from = keep + (t < te ? (size_t)(t / kRun) * g.D : 0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool in = t < te && (i ? in1 : in0);
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sm100::smem_u32(inputs.kept(st) + kept + 4 * i)),
+                             "l"(in ? from + i : io.keep), "r"(in ? 4 : 0)
+                             : "memory");
+            }
+        }
+    };
     for (int st = 0; st < 2; ++st) {
-        if (st < steps) inputs.ask(st, t0 - st * span, te);
+        if (st < steps) ask(st, t0 - st * span);
         inputs.asked();
     }
     RecurParams par;
@@ -46,14 +63,15 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
     float2 carry = two(0.f);   // the gradient that reaches a token's state from behind it
     if (!PACKED && io.dhT) carry = load2(io.dhT + (size_t)b * g.D + c, in0, in1);
     if (warp == 0 && lane < L) sm.carry[0][lane] = carry;
-    const float *keep = io.keep + (size_t)b * ((g.T + kRun - 1) / kRun) * g.D + c;
+    // the state that enters a run: with the inputs, or, where these are loaded as elements, a step ahead in registers (which
+    // costs the waits of shared memory behind it: 41 of 290 us for 8 x 4096 tokens of 2048 channels when it was the only way)
     auto kept_at = [&](int t) { return t >= 0 && t < te ? load2(keep + (size_t)(t / kRun) * g.D, in0, in1) : two(0.f); };
-    float2 next = kept_at(t0 + q);   // the state that enters this lane's run
+    float2 next = KEPT ? two(0.f) : kept_at(t0 + q);
     float2 sq = two(0.f), sr = two(0.f), si = two(0.f);
     Edges edges = {};
     int seq = 0;
     if (MODE == kTma) __syncthreads();   // the barriers exist
-    if (g.CL > 1) cluster_barrier();     // all of the cluster's blocks run before one writes to another
+    if (CL > 1) cluster_barrier();     // all of the cluster's blocks run before one writes to another
 
     float2 back = carry;
     for (int st = 0; st < steps; ++st, t0 -= span) {
@@ -61,8 +79,9 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
         uint32_t starts = 0, ends = 0;
         if (PACKED) edges.find(g, t0 + warp * R, min(R, te - t0 - warp * R), t, min(kRun, n), starts, ends);
         float2 h = next;
-        next = kept_at(t - span);
+        if (!KEPT) next = kept_at(t - span);
         inputs.get(st, t0, te, g.status);
+        if (KEPT) h = *reinterpret_cast<const float2 *>(inputs.kept(st) + kept);
 
         // the run's states, and of each token what dh is multiplied with
         float2 a[kRun], gy[kRun], fq[kRun], f1[kRun], fx[kRun], fi[kRun];
@@ -124,8 +143,8 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
         }
         A = make_float2(fmaxf(A.x, kLeast), fmaxf(A.y, kLeast));
         if (PACKED && ends) A = two(-1.f);
-        back = exchange<W, Q, PACKED, true>(sm, block, st & 1, g.CL, rank, A, H, carry, [&] {
-            if (st + 2 < steps) inputs.ask(st + 2, t0 - 2 * span, te);
+        back = exchange<W, Q, PACKED, true>(sm, block, st, CL, rank, A, H, carry, inputs.failed, g.status, [&] {
+            if (st + 2 < steps) ask(st + 2, t0 - 2 * span);
             inputs.asked();
         });
         T *pdx = io.out[kX].at(b, 0, t + kRun - 1) + c, *pdr = io.out[kRg].at(b, 0, t + kRun - 1) + c, *pdi = io.out[kIg].at(b, 0, t + kRun - 1) + c;
@@ -158,10 +177,10 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
         };
         if (!kShort && whole) outputs(std::true_type{});
         else outputs(std::false_type{});
-        if (g.CL == 1) leave<W, Q, true>(sm, st & 1, back);
+        if (CL == 1) leave<W, Q, true>(sm, st & 1, back);
     }
     if (!PACKED && io.dh0) {
-        if (g.CL > 1 || steps == 0) {
+        if (CL > 1 || steps == 0) {
             if (rank == 0 && warp == 0 && lane < L) store2(io.dh0 + (size_t)b * g.D + c, carry, in0, in1);
         } else if (warp == 0 && lane < L) {
             store2(io.dh0 + (size_t)b * g.D + c, back, in0, in1);
@@ -184,7 +203,7 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
         float2 v = red[warp][0][lane];
 #pragma unroll
         for (int w = 1; w < W; ++w) v = add2(v, red[warp][w][lane]);
-        store2(io.part + (((size_t)b * g.CL + rank) * 3 + warp) * g.D + c, v, in0, in1);
+        store2(io.part + (((size_t)b * CL + rank) * 3 + warp) * g.D + c, v, in0, in1);
     }
 }
 
@@ -210,9 +229,11 @@ cudaError_t bwd(const RecurCall &c, cudaStream_t st)
     if (g.cu && io.dh0 && g.Nseq > 0) k_recur_empty_grad<<<g.Nseq, 256, 0, st>>>(g.cu, g.D, io.dhT, io.dh0);
     constexpr int W = bwd_warps(sizeof(T));
     const bool gated = io.in[kZ].p != nullptr;
-    const int smem = 2 * (gated ? 5 : 4) * W * kRun * 64 * (int)sizeof(T) + recur_block_bytes(g.CL, g.Q);
+    const int smem = 2 * W * 64 * ((gated ? 5 : 4) * kRun * (int)sizeof(T) + 4) + recur_block_bytes(g.CL, g.Q);
     RecurMaps m = {};
-    const int mode = recur_mode(m, io, gated ? 31 : 23, box_rows<W>(g.Q), g);
+    const bool maps = g.T > 0 && tensor_map(&m.kept, true, c.keep, g.D, (g.T + kRun - 1) / kRun, g.B, g.D, (long long)((g.T + kRun - 1) / kRun) * g.D,
+                                            64 / g.Q, W * g.Q, false);
+    const int mode = recur_mode(m, io, gated ? 31 : 23, box_rows<W>(g.Q), g, maps);
     const cudaError_t rc = recur_variant<T>(g, mode, [&](auto q, auto how, auto packed) {
         return recur_launch(k_recur_bwd<T, decltype(q)::value, decltype(how)::value, decltype(packed)::value>, g, 32 * W, smem, st, m, g, io);
     });

@@ -18,15 +18,15 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T)), kFwdResident) k_rec
     extern __shared__ __align__(128) char raw[];
     float4 *block = reinterpret_cast<float4 *>(raw);   // maps of the cluster's blocks, then the inputs
     __shared__ RecurShared<W, Q> sm;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = g.CL > 1 ? cluster_rank() : 0;
-    const int id = blockIdx.x / g.CL, b = id / g.tiles, c0 = (id - b * g.tiles) * (64 / Q), c = c0 + 2 * (lane % L);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, CL = Q < 4 ? 1 : g.CL;   // wider tiles are never shared
+    const int rank = CL > 1 ? cluster_rank() : 0, id = blockIdx.x / CL, b = id / g.tiles, c0 = (id - b * g.tiles) * (64 / Q), c = c0 + 2 * (lane % L);
     const int q = warp * R + lane / L * kRun;     // of this lane's run, in a block's tokens
     const bool in0 = c < g.D, in1 = c + 1 < g.D;
     const bool gated = io.in[kZ].p != nullptr;
-    Inputs<T, W, Q, MODE> inputs;
-    inputs.init(raw + recur_block_bytes(g.CL, Q), sm.bar, &io, &maps, gated ? 15 : 7, b, c0, g.D);
+    Inputs<T, W, Q, MODE, false> inputs;
+    inputs.init(raw + recur_block_bytes(CL, Q), sm.bar, &io, &maps, gated ? 15 : 7, b, c0, g.D);
     const int te = PACKED ? g.cu[g.Nseq] : g.T;   // malformed offsets: every sequence is empty
-    const int span = W * R * g.CL, steps = (te + span - 1) / span;
+    const int span = W * R * CL, steps = (te + span - 1) / span;
     int t0 = rank * W * R;                        // the block's first token of a step
     for (int st = 0; st < 2; ++st) {
         if (st < steps) inputs.ask(st, t0 + st * span, te);
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T)), kFwdResident) k_rec
     Edges edges = {};
     int seq = 0;
     if (MODE == kTma) __syncthreads();   // the barriers exist
-    if (g.CL > 1) cluster_barrier();     // all of the cluster's blocks run before one writes to another
+    if (CL > 1) cluster_barrier();     // all of the cluster's blocks run before one writes to another
 
     float2 h = carry;
     for (int st = 0; st < steps; ++st, t0 += span) {
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T)), kFwdResident) k_rec
         }
         A = make_float2(fmaxf(A.x, kLeast), fmaxf(A.y, kLeast));
         if (PACKED && starts) A = two(-1.f);
-        h = exchange<W, Q, PACKED, false>(sm, block, st & 1, g.CL, rank, A, H, carry, [&] {
+        h = exchange<W, Q, PACKED, false>(sm, block, st, CL, rank, A, H, carry, inputs.failed, g.status, [&] {
             if (st + 2 < steps) inputs.ask(st + 2, t0 + 2 * span, te);
             inputs.asked();
         });
@@ -125,11 +125,11 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T)), kFwdResident) k_rec
         if (!kShort && n >= kRun) outputs(std::true_type{});
         else outputs(std::false_type{});
         py += span * io.out[kX].t;
-        if (g.CL == 1) leave<W, Q, false>(sm, st & 1, h);
+        if (CL == 1) leave<W, Q, false>(sm, st & 1, h);
     }
     // what leaves the last run: a cluster's blocks all have it, a block alone its last warp
     if (!PACKED && io.hT) {
-        if (g.CL > 1 || steps == 0) {
+        if (CL > 1 || steps == 0) {
             if (rank == 0 && warp == 0 && lane < L) store2(io.hT + (size_t)b * g.D + c, carry, in0, in1);
         } else if (warp == W - 1 && lane >= 32 - L) {
             store2(io.hT + (size_t)b * g.D + c, h, in0, in1);
