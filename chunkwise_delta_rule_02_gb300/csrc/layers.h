@@ -11,9 +11,10 @@ namespace lay {
 // Whether tensor maps can be made at all (the driver has the entry point).
 bool has_tensor_maps();
 // Tensor map of a [planes][rows][cols] array of bf16 or float32, boxes of `wide` columns x `high` rows; pitches in elements.
-// Zero is read outside.  False where the array does not meet a map's rules.
+// `swizzle`: 0, 64 or
+// 128 bytes.  Zero is read outside.  False where the array does not meet a map's rules.
 bool tensor_map(CUtensorMap *m, bool f32, const void *p, long long cols, long long rows, long long planes, long long row_pitch,
-                long long plane_pitch, int wide, int high, bool swizzle);
+                long long plane_pitch, int wide, int high, int swizzle);
 
 struct ConvCall {
     const dn_conv_shape *s;

@@ -105,7 +105,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 bool has_tensor_maps() { return encode_fn() != nullptr; }
 
 bool tensor_map(CUtensorMap *m, bool f32, const void *p, long long cols, long long rows, long long planes, long long row_pitch,
-                long long plane_pitch, int wide, int high, bool swizzle)
+                long long plane_pitch, int wide, int high, int swizzle)
 {
     const long long e = f32 ? 4 : 2, row = row_pitch * e, plane = (planes > 1 ? plane_pitch : row_pitch) * e, most = 1ll << 40;
     if (!encode_fn() || (uintptr_t)p % 16 || row % 16 || plane % 16 || row < cols * e || plane <= 0 || row >= most || plane >= most ||
@@ -114,7 +114,7 @@ bool tensor_map(CUtensorMap *m, bool f32, const void *p, long long cols, long lo
     const cuuint64_t dim[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes}, stride[2] = {(cuuint64_t)row, (cuuint64_t)plane};
     const cuuint32_t box[3] = {(cuuint32_t)wide, (cuuint32_t)high, 1}, es[3] = {1, 1, 1};
     return encode_fn()(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dim, stride, box, es,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -551,7 +551,7 @@ int recur_mode(RecurMaps &m, const RecurIo<T> &io, int in, int rows, const Recur
     for (int a = 0; a < kArrays; ++a) {
         const View<const T> &i = io.in[a];
         if (in >> a & 1) {
-            tma = tma && tensor_map(&m.in[a], sizeof(T) == 4, i.p, g.D, g.T, g.B, i.t, i.b, 64 / g.Q, rows, false);
+            tma = tma && tensor_map(&m.in[a], sizeof(T) == 4, i.p, g.D, g.T, g.B, i.t, i.b, 64 / g.Q, rows, 0);
             words = words && (uintptr_t)i.p % 4 == 0 && (sizeof(T) == 4 || (i.t % 2 == 0 && i.b % 2 == 0));
         }
         if (a < 4 && io.out[a].p) {

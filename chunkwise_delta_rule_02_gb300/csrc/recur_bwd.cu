@@ -232,7 +232,7 @@ cudaError_t bwd(const RecurCall &c, cudaStream_t st)
     const int smem = 2 * W * 64 * ((gated ? 5 : 4) * kRun * (int)sizeof(T) + 4) + recur_block_bytes(g.CL, g.Q);
     RecurMaps m = {};
     const bool maps = g.T > 0 && tensor_map(&m.kept, true, c.keep, g.D, (g.T + kRun - 1) / kRun, g.B, g.D, (long long)((g.T + kRun - 1) / kRun) * g.D,
-                                            64 / g.Q, W * g.Q, false);
+                                            64 / g.Q, W * g.Q, 0);
     const int mode = recur_mode(m, io, gated ? 31 : 23, box_rows<W>(g.Q), g, maps);
     const cudaError_t rc = recur_variant<T>(g, mode, [&](auto q, auto how, auto packed) {
         return recur_launch(k_recur_bwd<T, decltype(q)::value, decltype(how)::value, decltype(packed)::value>, g, 32 * W, smem, st, m, g, io);

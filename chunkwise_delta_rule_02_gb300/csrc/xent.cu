@@ -27,7 +27,8 @@ using lay::kLog2e;
 
 constexpr int TILE = 256, HALF = 128, BK = 64, STAGES = 6, THREADS = 320, EPI_WARPS = 8;
 constexpr int OPERAND = HALF * BK * 2;                               // bytes of 128 rows of an operand
-constexpr int SMEM = 2 * STAGES * OPERAND + 1024 + 256;
+constexpr int BOX = 4096;                                            // bytes that an epilogue warp has for results on their way out
+constexpr int SMEM = 2 * STAGES * OPERAND + EPI_WARPS * BOX + 1024 + 256;
 constexpr long long BUDGET = 4000000000LL;                           // clock cycles (about 2 s) for any one wait
 constexpr int GROUP = 16;                                            // row tiles that share the column tiles of a wave
 constexpr float kNone = -1e30f;                                      // maximum of no logits
@@ -52,6 +53,7 @@ struct Product {
     void *out;
     long long out_b, out_t;         // row (b, t) of out at b out_b + t out_t
     int T, f32, wide;               // wide: out's rows start at 16 bytes, and N is a multiple of 8
+    int out_box, sum_box;           // by tensor maps: out (bf16); sum, 1 stored, 2 added to what is there
 };
 
 struct Gemm {
@@ -69,8 +71,6 @@ struct Gemm {
     float *row;                     // [M] the target's logit
     float2 *part;
     int share;                      // SCORE: rows of w that a CTA has of a unit
-    __nv_bfloat16 *d;
-    long long d_pitch, d_plane;
     int v0, planes;
 };
 
@@ -118,8 +118,23 @@ struct Deal {
 
 enum { FULL = 0, EMPTY = STAGES, TFULL = 2 * STAGES, TEMPTY = TFULL + 2, DONE = TEMPTY + 2, NBAR = DONE + 1 };
 
+__device__ __forceinline__ void store_box(const CUtensorMap *map, const void *src, int c0, int c1, int c2)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"((uint64_t)map), "r"(smem_u32(src)),
+                 "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
+__device__ __forceinline__ void add_box(const CUtensorMap *map, const void *src, int c0, int c1, int c2)
+{
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"((uint64_t)map),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
 struct Maps {
     CUtensorMap a[2], b[2];
+    CUtensorMap out[2], sum;        // boxes of 32 x 32: GRAD's D or OUT's results; OUT's sums of the first product
 };
 
 // OUT: two products, D w and D^T x: B is MN-major in both, A in the second.  Otherwise one, both operands K-major.
@@ -130,7 +145,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
     constexpr int STAGE = OPERAND + NT / 2 * BK * 2;   // bytes a CTA loads of both operands
     extern __shared__ char raw[];
     char *sm = (char *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    uint64_t *bar = (uint64_t *)(sm + STAGES * STAGE);
+    char *boxes = sm + STAGES * STAGE;
+    uint64_t *bar = (uint64_t *)(boxes + EPI_WARPS * BOX);
     uint32_t *s_tmem = (uint32_t *)(bar + NBAR);
     volatile int *s_abort = (volatile int *)(s_tmem + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -363,8 +379,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
     } else {
         const int e = warp - 2, quad = warp & 3, half = e >> 2;   // TMEM lanes of this warp: 32 quad ..; columns: 128 half ..
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        uint32_t n = 0;
-        bool ok = true;
+        uint32_t n = 0, flip = 0;
+        bool ok = true, whole_box = false;
+        // 32 columns of the warp's 32 rows to memory, through shared memory and a tensor map, which leaves out what lies behind the ends
+        auto box_bf16 = [&](const CUtensorMap *map, const uint32_t (&w)[16], int col, int row0, int plane) {
+            char *b = boxes + e * BOX + (flip ^= BOX / 2);
+            if (lane == 0) {   // the box before the last is read; the last one too, where it was a float one of twice the size
+                if (whole_box) bulk_wait_read();
+                else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            }
+            whole_box = false;
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4 *>(b + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                store_box(map, b, col, row0, plane);
+                bulk_commit();
+            }
+        };
+        auto box_f32 = [&](const CUtensorMap *map, const float (&v)[32], int col, int row0, bool add) {
+            char *b = boxes + e * BOX;
+            if (lane == 0) bulk_wait_read();
+            whole_box = true;
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<float4 *>(b + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (add) add_box(map, b, col, row0, 0);
+                else store_box(map, b, col, row0, 0);
+                bulk_commit();
+            }
+        };
         for (int i = 0; i < deal.count[0] + (EPI == OUT ? deal.count[1] : 0); ++i) {
             const int o = EPI == OUT && i >= deal.count[0], j = o ? i - deal.count[0] : i;
             const Product &pr = p.of[o];
@@ -407,34 +458,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
                     sum = fmaf(sum, ex2((mx - top) * kLog2e), s0 + s1);
                     mx = top;
                 } else if constexpr (EPI == GRAD) {
-                    // D: 0 behind the vocabulary's end, which the products read as well
                     const int at = p.v0 + col;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const float prob = ex2((v[i] - lse) * kLog2e);
                         v[i] = i < live && target >= 0 ? (prob - (at + i == target ? 1.f : 0.f)) * g : 0.f;
                     }
-                    if (in && col < p.d_pitch) {
-                        for (int pl = 0; pl < p.planes; ++pl) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(p.d + pl * p.d_plane + (long long)row * p.d_pitch + col);
+                    const int row0 = row - lane;
+                    for (int pl = 0; pl < p.planes; ++pl) {
+                        uint32_t w[16];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    w[j] = pack_bf16(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
-                                    // what the next plane holds
-                                    v[8 * i + 2 * j] -= __uint_as_float(w[j] << 16);
-                                    v[8 * i + 2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
-                                }
-                                dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
+                        for (int j = 0; j < 16; ++j) {
+                            w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+                            // what the next plane holds
+                            v[2 * j] -= __uint_as_float(w[j] << 16);
+                            v[2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
                         }
+                        if (live > 0 && row0 < pr.M) box_bf16(&maps.out[0], w, col, row0, pl);
                     }
-                } else if (in && live > 0) {
+                } else if (live > 0 && row - lane < pr.M && pr.cuts == 1 && pr.sum && pr.sum_box) {
+                    box_f32(&maps.sum, v, col, row - lane, pr.sum_box == 2);
+                } else if ((in || (pr.out_box && row - lane < pr.M)) && live > 0) {
                     const bool whole = live >= 32 && pr.N % 4 == 0;   // columns and 16-byte rows of a float array
                     const long long at = (long long)row * pr.N + col;
-                    if (pr.add && pr.cuts == 1) {
+                    if (in && pr.add && pr.cuts == 1) {
                         if (whole) {
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
@@ -451,6 +498,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
                         }
                     }
                     const bool partial = pr.cuts > 1, sums = partial || pr.sum != nullptr;
+                    if (!sums && pr.out_box) {   // with what lies in `add`, if anything, in it
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+                        box_bf16(&maps.out[o], w, col, row - lane, 0);
+                        return;
+                    }
                     const long long place = sums ? at : (long long)(row / pr.T) * pr.out_b + (long long)(row % pr.T) * pr.out_t + col;
                     if (sums || pr.f32) {
                         float *to = (partial ? pr.part + (long long)u.cut * pr.M * pr.N : sums ? pr.sum : (float *)pr.out) + place;
@@ -520,6 +574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
             }
             if (EPI == STATS && in) p.part[(long long)(2 * (u.n / TILE) + half) * pr.M + row] = make_float2(mx, sum);
         }
+        if (lane == 0) bulk_wait_all();
     }
     __syncwarp();
     __syncthreads();
@@ -628,7 +683,7 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Product o)
 // bf16 [planes][rows][cols], boxes of 64 columns x `high` rows
 bool make_map(CUtensorMap *m, const Operand &o, long long cols, long long rows, int planes, int high)
 {
-    return lay::tensor_map(m, false, o.p, cols, rows, planes, o.pitch, o.plane, 64, high, true);
+    return lay::tensor_map(m, false, o.p, cols, rows, planes, o.pitch, o.plane, 64, high, 128);
 }
 
 void size(Product &o, int M, int N, int contraction)
@@ -809,12 +864,10 @@ cudaError_t backward(const Call &c, cudaStream_t st)
         const bool first = v0 == 0, last = v0 + n == c.V;
         // the maps end where this piece does: nothing behind it is read
         if (!make_map(&outs.a[0], d, n, c.M, c.planes, HALF) || !make_map(&outs.a[1], d, n, c.M, c.planes, BK)) return cudaErrorInvalidValue;
+        if (!lay::tensor_map(&logits.out[0], false, c.d, n, c.M, c.planes, d.pitch, d.plane, 32, 32, 64)) return cudaErrorInvalidValue;
         Gemm p = common(c);
         size(p.of[0], c.M, n, c.K);
         p.of[0].b_row = p.v0 = v0;
-        p.d = (__nv_bfloat16 *)c.d;
-        p.d_pitch = d.pitch;
-        p.d_plane = d.plane;
         if ((e = launch<GRAD>(logits, p, st)) != cudaSuccess) return e;
         p = common(c);
         int dx_cuts, dw_cuts;
@@ -844,6 +897,11 @@ cudaError_t backward(const Call &c, cudaStream_t st)
             o->f32 = f32;
             o->wide = c.K % 8 == 0 && (uintptr_t)o->out % 16 == 0 && o->out_b * el % 16 == 0 && o->out_t * el % 16 == 0;
         }
+        // results that tensor maps can describe: dx of rows at one distance, dw, the sums of dx over pieces
+        const long long pitch = c.s->B == 1 || dx.out_b == dx.out_t * dx.T ? dx.out_t : c.s->T == 1 ? dx.out_b : 0;
+        dx.out_box = !f32 && last && dx.cuts == 1 && pitch > 0 && lay::tensor_map(&outs.out[0], false, dx.out, c.K, c.M, 1, pitch, 0, 32, 32, 64);
+        dw.out_box = !f32 && dw.cuts == 1 && lay::tensor_map(&outs.out[1], false, dw.out, c.K, n, 1, c.K, 0, 32, 32, 64);
+        dx.sum_box = !last && lay::tensor_map(&outs.sum, true, c.acc, c.K, c.M, 1, c.K, 0, 32, 32, 128) ? first ? 1 : 2 : 0;
         if ((e = launch<OUT>(outs, p, st)) != cudaSuccess || (e = join(dx, st)) != cudaSuccess || (e = join(dw, st)) != cudaSuccess) return e;
     }
     return cudaSuccess;
