@@ -181,7 +181,7 @@ def _same_device(first: torch.Tensor, *rest):
     for t in rest:
         if t is not None and t.get_device() != dev:
             raise ValueError("tensors on different devices: %s and %s" % (first.device, t.device))
-    if torch.cuda.current_device() != dev:
+    if torch._C._cuda_getDevice() != dev:
         raise ValueError("%s is not the current CUDA device: call under torch.cuda.device(%d)" % (first.device, dev))
 
 
@@ -191,7 +191,7 @@ def _p(t):
 
 def _stream(stream):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 

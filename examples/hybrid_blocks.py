@@ -1,11 +1,15 @@
-"""A small hybrid language model on the package's operators: gated delta rule blocks and selective state
-space blocks, trained on a synthetic copy task and then decoded token by token.
+"""A small hybrid language model on the package's operators: gated delta rule blocks, selective state
+space blocks and, where asked for, gated linear recurrence blocks, trained on a synthetic copy task and then decoded
+token by token.
 
 Each block is a residual norm (the sum of the stream and the block before it, its scale and the norm in one
 pass), projections, short causal convolutions, the delta rule or the scan, a gated norm (delta rule) or the
 scan's own gate, and an output projection.  The convolutions read the token-major projections and write what
 the delta rule reads; the gated norm reads that layout and writes the projection's: the forward pass has no
 transposition or copy in between (gradients come back in the axes' order, contiguous).  Decoding keeps, per block, the last taps of the convolutions and the recurrent states.
+
+With ``dropout`` a block's output goes through a generator's mask that is never stored: seed and call number lie
+on the device, and the gradient draws the mask again.  ``model.loss`` is the cross entropy of the last hidden states against the embedding, without the logits.
 
     python examples/hybrid_blocks.py
 """
@@ -59,6 +63,50 @@ class Scan(torch.autograd.Function):
         *args, saved = ctx.saved_tensors
         g = gdn.scan_backward(*args, dy=dy.contiguous(), saved=saved)
         return tuple(g[k] for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias"))
+
+
+class Recurrence(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, rg, ig, lam, rg_bias, ig_bias, z):
+        y, _, saved = gdn.recur_forward(x, rg, ig, lam, rg_bias, ig_bias, z, want_state=False, save=True)
+        ctx.save_for_backward(x, rg, ig, lam, rg_bias, ig_bias, z, saved)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        *args, saved = ctx.saved_tensors
+        g = gdn.recur_backward(*args, dy=dy.contiguous(), saved=saved)
+        return tuple(g[k] for k in ("dx", "drg", "dig", "dlam", "drg_bias", "dig_bias", "dz"))
+
+
+class Drop(torch.autograd.Function):
+    """Dropout; rng int64 [2] on the device, as it is now (the gradient draws the same mask)."""
+
+    @staticmethod
+    def forward(ctx, x, p, rng):
+        ctx.p = p
+        ctx.save_for_backward(rng.clone())
+        return gdn.dropout_forward(x, p, rng)
+
+    @staticmethod
+    def backward(ctx, dy):
+        return gdn.dropout_backward(dy.contiguous(), ctx.p, *ctx.saved_tensors), None, None
+
+
+class CrossEntropy(torch.autograd.Function):
+    """Loss of each token from hidden states and an output weight, without the logits."""
+
+    @staticmethod
+    def forward(ctx, x, w, targets):
+        loss, lse = gdn.xent_forward(x, w, targets, check_status=False)
+        ctx.save_for_backward(x, w, targets, lse)
+        return loss
+
+    @staticmethod
+    def backward(ctx, dloss):
+        x, w, targets, lse = ctx.saved_tensors
+        g = gdn.xent_backward(x, w, targets, lse, dloss, check_status=False)
+        return g["dx"], g["dw"], None
 
 
 class GatedNorm(torch.autograd.Function):
@@ -172,25 +220,76 @@ class ScanBlock(torch.nn.Module):
         return y @ self.out.to(BF)
 
 
-class HybridModel(torch.nn.Module):
-    def __init__(self, vocab=64, width=256, heads=2, d=128, channels=512, states=16, pairs=1):
+class RecurBlock(torch.nn.Module):
+    """Gated linear recurrence: one convolution, gates from its output, the output gate in the recurrence."""
+
+    def __init__(self, width, channels, taps=4):
         super().__init__()
+        self.channels = channels
+        p = lambda *s, scale: torch.nn.Parameter(torch.randn(*s) * scale)  # noqa: E731
+        self.proj = p(width, 2 * channels, scale=width ** -0.5)     # x, z
+        self.taps, self.tap_bias = p(channels, taps, scale=taps ** -0.5), torch.nn.Parameter(torch.zeros(channels))
+        self.gates = p(channels, 2 * channels, scale=channels ** -0.5)   # recurrence gate, input gate
+        self.gate_bias = torch.nn.ParameterList([torch.nn.Parameter(torch.zeros(channels)) for _ in range(2)])
+        # decays of 0.9 to 0.999 a token where the gate is open: 8 softplus(lam) = -log decay
+        m = -torch.log(0.9 + 0.099 * torch.rand(channels)) / 8
+        self.lam = torch.nn.Parameter(m + torch.log(-torch.expm1(-m)))
+        self.out = p(channels, width, scale=channels ** -0.5)
+
+    def _gated(self, x):
+        return (x @ self.gates.to(BF)).split(self.channels, -1)
+
+    def forward(self, u):
+        x, z = (u @ self.proj.to(BF)).split(self.channels, -1)
+        x = Conv.apply(x, self.taps, self.tap_bias)
+        rg, ig = self._gated(x)
+        return Recurrence.apply(x, rg, ig, self.lam, *self.gate_bias, z) @ self.out.to(BF)
+
+    def start(self, n, device):
+        return dict(taps=torch.zeros(n, self.taps.shape[1] - 1, self.channels, dtype=BF, device=device),
+                    state=torch.zeros(n, self.channels, device=device))
+
+    def step(self, u, s):
+        x, z = (u @ self.proj.to(BF)).split(self.channels, -1)
+        x, _ = gdn.conv_step(x, self.taps, self.tap_bias, s["taps"], out_state=s["taps"])
+        rg, ig = self._gated(x)
+        y, _ = gdn.recur_step(x, rg, ig, self.lam, *self.gate_bias, z, s["state"], out_state=s["state"])
+        return y @ self.out.to(BF)
+
+
+class HybridModel(torch.nn.Module):
+    def __init__(self, vocab=64, width=256, heads=2, d=128, channels=512, states=16, pairs=1, recurrent=0, dropout=0.0):
+        """pairs: of a delta rule and a scan block; recurrent: further blocks behind them; dropout: of what a block adds."""
+        super().__init__()
+        self.dropout = dropout
+        self.register_buffer("rng", torch.zeros(2, dtype=torch.int64), persistent=False)    # seed and call number of the dropout
         self.embed = torch.nn.Parameter(torch.randn(vocab, width) * 0.5)
         blocks = []
         for _ in range(pairs):
             blocks += [DeltaBlock(width, heads, d), ScanBlock(width, channels, states)]
+        blocks += [RecurBlock(width, channels) for _ in range(recurrent)]
         self.blocks = torch.nn.ModuleList(blocks)
         self.norms = torch.nn.ParameterList([torch.nn.Parameter(torch.ones(width)) for _ in range(len(blocks) + 1)])
         self.scales = torch.nn.ParameterList([torch.nn.Parameter(torch.ones(width)) for _ in range(len(blocks) + 1)])
 
-    def forward(self, tokens):
+    def hidden(self, tokens):
         r = self.embed[tokens].to(BF)
         x = torch.zeros_like(r)
         for i, block in enumerate(self.blocks):
             u, r = ResidualNorm.apply(x, r, self.norms[i], self.scales[i])
             x = block(u)
+            if self.dropout and self.training:
+                self.rng[1] += 1
+                x = Drop.apply(x, self.dropout, self.rng)
         u, _ = ResidualNorm.apply(x, r, self.norms[-1], self.scales[-1])
-        return u @ self.embed.t().to(BF)
+        return u
+
+    def forward(self, tokens):
+        return self.hidden(tokens) @ self.embed.t().to(BF)
+
+    def loss(self, tokens):
+        """Mean cross entropy of the tokens behind the first, without the logits."""
+        return CrossEntropy.apply(self.hidden(tokens[:, :-1]), self.embed.to(BF), tokens[:, 1:]).mean()
 
     def start(self, n):
         return [b.start(n, self.embed.device) for b in self.blocks]
@@ -213,15 +312,17 @@ def batch(n, T, vocab, gen):
     return torch.cat([span, span], 1).cuda()
 
 
-def train(model, steps=30, n=8, T=128, vocab=64, seed=0):
-    """The losses of `steps` training steps."""
+def train(model, steps=30, n=8, T=128, vocab=64, seed=0, logits=True):
+    """The losses of `steps` training steps; logits: through the logits, or without them (``model.loss``)."""
     gen = torch.Generator().manual_seed(seed)
     opt = torch.optim.Adam(model.parameters(), lr=3e-3)
     losses = []
     for _ in range(steps):
         tokens = batch(n, T, vocab, gen)
-        logits = model(tokens[:, :-1]).float()
-        loss = torch.nn.functional.cross_entropy(logits.flatten(0, 1), tokens[:, 1:].flatten())
+        if logits:
+            loss = torch.nn.functional.cross_entropy(model(tokens[:, :-1]).float().flatten(0, 1), tokens[:, 1:].flatten())
+        else:
+            loss = model.loss(tokens)
         opt.zero_grad(set_to_none=True)
         loss.backward()
         opt.step()
