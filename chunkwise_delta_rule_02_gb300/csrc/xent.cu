@@ -74,6 +74,11 @@ struct Gemm {
     int v0, planes;
 };
 
+// The kernels of a call are launched so that one may start while the one before it ends: each says so at once, and waits for the other's
+// results before it touches any memory.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // A token's target, -1 for none: ignored, or (which the status word is told) outside the vocabulary.
 __device__ __forceinline__ int target_of(const Gemm &p, int row, bool tell)
 {
@@ -149,6 +154,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
     uint64_t *bar = (uint64_t *)(boxes + EPI_WARPS * BOX);
     uint32_t *s_tmem = (uint32_t *)(bar + NBAR);
     volatile int *s_abort = (volatile int *)(s_tmem + 1);
+    let_next_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = pair_rank();
     const Deal deal(p, blockIdx.x >> 1, gridDim.x >> 1);
@@ -177,6 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
     pair_sync();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
+    wait_for_last();
     auto wait = [&](int b, uint32_t parity) -> bool {
         if (pair_wait(&bar[b], parity & 1u, BUDGET, s_abort)) return true;
         *s_abort = 1;
@@ -589,6 +596,8 @@ __global__ void __launch_bounds__(256) k_lse(const __grid_constant__ Gemm p, con
 {
     constexpr int S = 256 / R;
     __shared__ float2 sm[S][R];
+    let_next_start();
+    wait_for_last();
     const int i = threadIdx.x % R, w = threadIdx.x / R, r = blockIdx.x * R + i;
     float mx = kNone, sum = 0.f;
     auto join = [&](float2 q) {
@@ -630,6 +639,8 @@ struct Packing {
 template <class T>
 __global__ void __launch_bounds__(256) k_pack(const __grid_constant__ Packing p)
 {
+    let_next_start();
+    wait_for_last();
     const int o = blockIdx.x >= p.blocks[0], per = 256 >> p.shift;
     const int r = (blockIdx.x - (o ? p.blocks[0] : 0)) * per + (threadIdx.x >> p.shift);
     if (r >= p.rows[o]) return;
@@ -657,6 +668,8 @@ __global__ void __launch_bounds__(256) k_pack(const __grid_constant__ Packing p)
 template <int V>
 __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Product o)
 {
+    let_next_start();
+    wait_for_last();
     const long long all = (long long)o.M * o.N, step = (long long)gridDim.x * 256 * V;
     for (long long i = (blockIdx.x * 256ll + threadIdx.x) * V; i < all; i += step) {
         float v[V] = {};
@@ -686,6 +699,23 @@ bool make_map(CUtensorMap *m, const Operand &o, long long cols, long long rows, 
     return lay::tensor_map(m, false, o.p, cols, rows, planes, o.pitch, o.plane, 64, high, 128);
 }
 
+template <class K, class... A>
+cudaError_t start(K kernel, long long blocks, int threads, int smem, cudaStream_t st, const A &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e != cudaSuccess ? e : cudaPeekAtLastError();
+}
+
 void size(Product &o, int M, int N, int contraction)
 {
     o.M = M;
@@ -708,8 +738,7 @@ cudaError_t launch_as(const Maps &m, Gemm &p, cudaStream_t st)
     if (e != cudaSuccess) return e;
     long long units = 0, pairs = pairs_at_most();
     for (const Product &o : p.of) units += (long long)o.mt * o.nt * o.cuts;
-    kernel<<<(unsigned)(2 * (units < pairs ? units : pairs)), THREADS, SMEM, st>>>(m, p);
-    return cudaPeekAtLastError();
+    return start(kernel, 2 * (units < pairs ? units : pairs), THREADS, SMEM, st, m, p);
 }
 
 template <int EPI, int NT = TILE>
@@ -724,9 +753,7 @@ cudaError_t join(const Product &o, cudaStream_t st)
     const bool four = o.N % 4 == 0;
     const long long n = ((long long)o.M * o.N / (four ? 4 : 1) + 255) / 256, most = 16ll * lay::sm_count();
     const unsigned blocks = (unsigned)(n < most ? n : most);
-    if (four) k_join<4><<<blocks, 256, 0, st>>>(o);
-    else k_join<1><<<blocks, 256, 0, st>>>(o);
-    return cudaPeekAtLastError();
+    return start(four ? k_join<4> : k_join<1>, blocks, 256, 0, st, o);
 }
 
 Gemm common(const Call &c)
@@ -780,9 +807,7 @@ cudaError_t begin(const Call &c, cudaStream_t st)
         p.blocks[o] = (int)(((long long)rows[o] + (256 >> p.shift) - 1) / (256 >> p.shift));
     }
     const unsigned blocks = (unsigned)p.blocks[0] + (unsigned)p.blocks[1];
-    if (c.s->dtype == DN_F32) k_pack<float><<<blocks, 256, 0, st>>>(p);
-    else k_pack<__nv_bfloat16><<<blocks, 256, 0, st>>>(p);
-    return cudaPeekAtLastError();
+    return start(c.s->dtype == DN_F32 ? k_pack<float> : k_pack<__nv_bfloat16>, blocks, 256, 0, st, p);
 }
 
 // SCORE: pairs take equal shares of the vocabulary, in as few rounds as tiles of 256 rows need
@@ -842,9 +867,9 @@ cudaError_t forward(const Call &c, cudaStream_t st)
     }
     if (e != cudaSuccess) return e;
     const int P = parts_of(c.M, c.V);
-    if (c.M > 2048) k_lse<32><<<(c.M + 31) / 32, 256, 0, st>>>(p, c.part, P, c.M, c.loss, c.lse);
-    else k_lse<4><<<(c.M + 3) / 4, 256, 0, st>>>(p, c.part, P, c.M, c.loss, c.lse);
-    return cudaPeekAtLastError();
+    const float2 *part = c.part;
+    return c.M > 2048 ? start(k_lse<32>, (c.M + 31) / 32, 256, 0, st, p, part, P, c.M, c.loss, c.lse)
+                      : start(k_lse<4>, (c.M + 3) / 4, 256, 0, st, p, part, P, c.M, c.loss, c.lse);
 }
 
 cudaError_t backward(const Call &c, cudaStream_t st)

@@ -108,8 +108,8 @@ def test_the_loss_without_logits_is_the_loss(ex):
     tokens = ex.batch(4, 50, 64, torch.Generator().manual_seed(3))
     one = model.loss(tokens)
     two = torch.nn.functional.cross_entropy(model(tokens[:, :-1]).float().flatten(0, 1), tokens[:, 1:].flatten())
-    top = float(model(tokens[:, :-1]).float().abs().max())
-    assert abs(float(one) - float(two)) <= 2 * top * 2.0 ** -8
+    top = float(model(tokens[:, :-1]).detach().float().abs().max())
+    assert abs(float(one.detach()) - float(two.detach())) <= 2 * top * 2.0 ** -8
     ga, gb = (torch.autograd.grad(v, model.blocks[-1].lam)[0] for v in (one, two))
     assert float((ga - gb).norm()) <= 0.1 * float(gb.norm())
 
