@@ -52,7 +52,8 @@ struct Product {
     float *part;
     void *out;
     long long out_b, out_t;         // row (b, t) of out at b out_b + t out_t
-    int T, f32, wide;               // wide: out's rows start at 16 bytes, and N is a multiple of 8
+    long long pitch;                // the distance of rows where it is one, else 0
+    int T, f32, wide;               // wide: out's float rows start at 16 bytes
     int out_box, sum_box;           // by tensor maps: out (bf16); sum, 1 stored, 2 added to what is there
 };
 
@@ -67,12 +68,21 @@ struct Gemm {
     const float *dloss;
     long long tgt_b, tgt_t, g_b, g_t, ignore;
     int T, V;
+    const float *scale;             // the largest |dloss|, which D leaves out and the sums get back
     const float *lse;
     float *row;                     // [M] the target's logit
     float2 *part;
     int share;                      // SCORE: rows of w that a CTA has of a unit
     int v0, planes;
 };
+
+// A mean's dloss is one value for all tokens, whose rounding to bf16 would be off the same way in every row of D: up to 2^-8 of all
+// gradients.  So D holds (exp(l - lse) - onehot) times dloss over its largest magnitude, and the sums are multiplied with that.
+__device__ __forceinline__ float scale_of(const Gemm &p)
+{
+    const float s = *p.scale;
+    return s > 0.f ? s : 1.f;
+}
 
 // The kernels of a call are launched so that one may start while the one before it ends: each says so at once, and waits for the other's
 // results before it touches any memory.
@@ -89,8 +99,13 @@ __device__ __forceinline__ int target_of(const Gemm &p, int row, bool tell)
     return -1;
 }
 
+// What a unit costs, in stages of the ring: those of its contraction, and its way out of TMEM (2 tokens, 15733 entries of 474: 188 us
+// for the product when only the contraction counted, and pairs without a unit of dx got a hundred short units of dw)
+constexpr int kWayOut = 24;
+__host__ __device__ inline int cost_of(const Gemm &g, const Product &o) { return o.len * g.np + kWayOut; }
+
 // Units of the two products for pair `p` of `n`: the first product's dealt in turn, the second's so that pairs with fewer of the
-// first have the more of the second that its length makes up for.
+// first have the more of the second that its cost makes up for.
 struct Deal {
     int count[2], first[2], step[2];
     __host__ __device__ Deal(const Gemm &g, int p, int n)
@@ -100,7 +115,7 @@ struct Deal {
         count[0] = n0 / n + (p < r ? 1 : 0);
         first[0] = p;
         step[0] = n;
-        const int more = n1 > 0 ? (g.of[0].len + g.of[1].len / 2) / g.of[1].len : 0;
+        const int cost = n1 > 0 ? cost_of(g, g.of[1]) : 1, more = n1 > 0 ? (cost_of(g, g.of[0]) + cost / 2) / cost : 0;
         int base = n1 - (n - r) * more, low = 0, high;   // units a pair with more, with fewer of the first
         if (r == 0) {
             low = high = n1 / n;
@@ -388,6 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         uint32_t n = 0, flip = 0;
         bool ok = true, whole_box = false;
+        [[maybe_unused]] const float scale = EPI == STATS ? 1.f : scale_of(p);
         // 32 columns of the warp's 32 rows to memory, through shared memory and a tensor map, which leaves out what lies behind the ends
         auto box_bf16 = [&](const CUtensorMap *map, const uint32_t (&w)[16], int col, int row0, int plane) {
             char *b = boxes + e * BOX + (flip ^= BOX / 2);
@@ -435,11 +451,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
                 target = target_of(p, row, p.v0 == 0 && u.n == 0 && half == 0);
                 if (EPI == GRAD) {
                     lse = p.lse[row];
-                    if (target >= 0) g = p.dloss[(long long)(row / p.T) * p.g_b + (long long)(row % p.T) * p.g_t];
+                    if (target >= 0) g = p.dloss[(long long)(row / p.T) * p.g_b + (long long)(row % p.T) * p.g_t] / scale;
                 }
             }
             auto finish = [&](int c, float (&v)[32]) {   // columns c0 + c .. + 31 of this thread's row
                 const int col = c0 + c, live = pr.N - col;   // columns of this chunk that exist
+                if constexpr (EPI == OUT) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] *= scale;
+                }
                 if constexpr (EPI == STATS) {
                     if (live < 32) {
 #pragma unroll
@@ -485,57 +505,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
                     }
                 } else if (live > 0 && row - lane < pr.M && pr.cuts == 1 && pr.sum && pr.sum_box) {
                     box_f32(&maps.sum, v, col, row - lane, pr.sum_box == 2);
-                } else if ((in || (pr.out_box && row - lane < pr.M)) && live > 0) {
-                    const bool whole = live >= 32 && pr.N % 4 == 0;   // columns and 16-byte rows of a float array
+                } else if (live > 0 && row - lane < pr.M) {
+                    const bool partial = pr.cuts > 1, sums = partial || pr.sum != nullptr;
                     const long long at = (long long)row * pr.N + col;
-                    if (in && pr.add && pr.cuts == 1) {
-                        if (whole) {
+                    const float *add = partial ? nullptr : pr.add;
+                    const bool whole = live >= 32 && pr.N % 4 == 0;   // columns and 16-byte rows of a float array
+                    if (whole && add && in) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 f = reinterpret_cast<const float4 *>(pr.add + at)[i];
-                                v[4 * i] += f.x;
-                                v[4 * i + 1] += f.y;
-                                v[4 * i + 2] += f.z;
-                                v[4 * i + 3] += f.w;
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i < live) v[i] += pr.add[at + i];
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 f = reinterpret_cast<const float4 *>(add + at)[i];
+                            v[4 * i] += f.x;
+                            v[4 * i + 1] += f.y;
+                            v[4 * i + 2] += f.z;
+                            v[4 * i + 3] += f.w;
                         }
                     }
-                    const bool partial = pr.cuts > 1, sums = partial || pr.sum != nullptr;
-                    if (!sums && pr.out_box) {   // with what lies in `add`, if anything, in it
+                    if (!sums && pr.out_box && (whole || !add)) {
                         uint32_t w[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
                         box_bf16(&maps.out[o], w, col, row - lane, 0);
                         return;
                     }
-                    const long long place = sums ? at : (long long)(row / pr.T) * pr.out_b + (long long)(row % pr.T) * pr.out_t + col;
-                    if (sums || pr.f32) {
-                        float *to = (partial ? pr.part + (long long)u.cut * pr.M * pr.N : sums ? pr.sum : (float *)pr.out) + place;
-                        if (whole && (sums || pr.wide)) {
+                    float *to = partial ? pr.part + (long long)u.cut * pr.M * pr.N : pr.sum;
+                    if (whole && (sums || (pr.f32 && pr.wide))) {
+                        if (!sums) to = (float *)pr.out + (long long)(row / pr.T) * pr.out_b + (long long)(row % pr.T) * pr.out_t + col;
+                        else to += at;
+                        if (in) {
 #pragma unroll
                             for (int i = 0; i < 8; ++i) reinterpret_cast<float4 *>(to)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i < live) to[i] = v[i];
                         }
-                    } else {
-                        __nv_bfloat16 *to = (__nv_bfloat16 *)pr.out + place;
-                        if (whole && pr.wide) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                reinterpret_cast<uint4 *>(to)[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                                                                              pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i < live) st_out(to + i, v[i]);
-                        }
+                        return;
                     }
+                    // Rows of no particular alignment: turned in shared memory, so that a warp writes a row's 32 columns at a time
+                    float *turn = reinterpret_cast<float *>(boxes + e * BOX);
+                    if (lane == 0) bulk_wait_read();
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) turn[lane * 32 + (i ^ lane)] = v[i];
+                    __syncwarp();
+                    const int rows = min(32, pr.M - (row - lane)), row0 = row - lane;
+                    if (lane < live) {
+                        // one column a lane: pointers to the first row's, and the distance of rows
+                        const long long first = (long long)row0 * pr.N + col + lane, pitch = sums ? pr.N : pr.pitch;
+                        const float *more = add && !whole ? add + first : nullptr;
+                        auto put = [&](auto *dst) {
+#pragma unroll 4
+                            for (int r = 0; r < rows; ++r) {
+                                float f = turn[r * 32 + (lane ^ r)];
+                                if (more) f += more[r * (long long)pr.N];
+                                if (pitch) st_out(dst + r * pitch, f);
+                                else st_out(dst + (long long)((row0 + r) / pr.T) * pr.out_b + (long long)((row0 + r) % pr.T) * pr.out_t, f);
+                            }
+                        };
+                        const long long begin = sums ? first : (pitch ? row0 * pitch : 0) + col + lane;
+                        if (sums) put(to + begin);
+                        else if (pr.f32) put((float *)pr.out + begin);
+                        else put((__nv_bfloat16 *)pr.out + begin);
+                    }
+                    __syncwarp();
                 }
             };
             auto get = [&](int c, float (&v)[32]) {
@@ -624,6 +652,20 @@ __global__ void __launch_bounds__(256) k_lse(const __grid_constant__ Gemm p, con
         lse[r] = l;
         loss[r] = target_of(p, r, false) < 0 ? 0.f : l - p.row[r];
     }
+}
+
+// The largest finite |dloss| of the tokens that have a target, into a word that begin() cleared: magnitudes are ordered as their bits.
+__global__ void __launch_bounds__(256) k_scale(const __grid_constant__ Gemm p, int M, uint32_t *scale)
+{
+    let_next_start();
+    wait_for_last();
+    float top = 0.f;
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < M; i += gridDim.x * 256) {
+        const float g = fabsf(p.dloss[(long long)(i / p.T) * p.g_b + (long long)(i % p.T) * p.g_t]);
+        if (g > top && g <= 3.4e38f && target_of(p, i, false) >= 0) top = g;
+    }
+    const uint32_t v = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+    if ((threadIdx.x & 31) == 0 && v) atomicMax(scale, v);
 }
 
 // x and w into [planes][rows][pitch] bf16: as they are, or as three planes, the largest first.  A thread has 8 columns of a row,
@@ -776,16 +818,17 @@ Gemm common(const Call &c)
         p.g_b = c.dloss->batch;
         p.g_t = c.dloss->time;
     }
+    p.scale = (const float *)(c.status + 1);
     p.lse = c.lse;
     p.row = c.row;
     p.part = c.part;
     return p;
 }
 
-// Clears the status word; copies what the tensor maps cannot read in place.
+// Clears the status word and the scale; copies what the tensor maps cannot read in place.
 cudaError_t begin(const Call &c, cudaStream_t st)
 {
-    cudaError_t e = cudaMemsetAsync(c.status, 0, sizeof(uint32_t), st);
+    cudaError_t e = cudaMemsetAsync(c.status, 0, 2 * sizeof(uint32_t), st);   // and the scale behind it
     if (e != cudaSuccess || c.M == 0 || !(c.pack_x || c.pack_w)) return e;
     Packing p = {};
     const dn_view *views[2] = {c.x, c.w};
@@ -822,14 +865,14 @@ int score_units(int V, int &share)
 
 int tiles_of(int n) { return (int)(((long long)n + TILE - 1) / TILE); }
 
-// How the contractions of a piece's two products are cut: not longer than a pair's share of all steps, so that a few long tiles
-// do not keep the rest waiting, and 4 steps at least.
+// How the contractions of a piece's two products are cut: a unit not costlier than a pair's share of all, so that a few long
+// tiles do not keep the rest waiting, and not below 8 stages' worth.
 void cuts_of(int M, int K, int n, int planes, int &dx, int &dw)
 {
-    const long long nk = tiles_of(K), a = ((long long)n + BK - 1) / BK, b = ((long long)M + BK - 1) / BK;
-    const long long all = nk * (tiles_of(M) * a + tiles_of(n) * b), least = planes == 1 ? 8 : 4;
-    long long share = (all + pairs_at_most() - 1) / pairs_at_most();
-    if (share < least) share = least;
+    const long long np = planes == 1 ? 1 : 6, a = ((long long)n + BK - 1) / BK, b = ((long long)M + BK - 1) / BK;
+    const long long nx = (long long)tiles_of(K) * tiles_of(M), nw = (long long)tiles_of(K) * tiles_of(n), pairs = pairs_at_most();
+    long long share = (nx * (a * np + kWayOut) + nw * (b * np + kWayOut) + pairs - 1) / pairs / np;
+    if (share < 8) share = 8;
     dx = (int)((a + share - 1) / share);
     dw = (int)((b + share - 1) / share);
 }
@@ -884,6 +927,8 @@ cudaError_t backward(const Call &c, cudaStream_t st)
         !make_map(&outs.b[1], c.xo, c.K, c.M, c.planes, BK) || !make_map(&outs.b[0], c.wo, c.K, c.V, c.planes, BK))
         return cudaErrorInvalidValue;
     const size_t el = f32 ? 4 : 2;
+    const int groups = (c.M + 255) / 256;
+    if ((e = start(k_scale, groups < 128 ? groups : 128, 256, 0, st, common(c), c.M, c.status + 1)) != cudaSuccess) return e;
     for (int v0 = 0; v0 < c.V; v0 += c.piece) {
         const int n = c.V - v0 < c.piece ? c.V - v0 : c.piece;
         const bool first = v0 == 0, last = v0 + n == c.V;
@@ -920,11 +965,12 @@ cudaError_t backward(const Call &c, cudaStream_t st)
         dw.T = n;
         for (Product *o : {&dx, &dw}) {
             o->f32 = f32;
-            o->wide = c.K % 8 == 0 && (uintptr_t)o->out % 16 == 0 && o->out_b * el % 16 == 0 && o->out_t * el % 16 == 0;
+            o->wide = f32 && (uintptr_t)o->out % 16 == 0 && o->out_b % 4 == 0 && o->out_t % 4 == 0;
         }
         // results that tensor maps can describe: dx of rows at one distance, dw, the sums of dx over pieces
-        const long long pitch = c.s->B == 1 || dx.out_b == dx.out_t * dx.T ? dx.out_t : c.s->T == 1 ? dx.out_b : 0;
-        dx.out_box = !f32 && last && dx.cuts == 1 && pitch > 0 && lay::tensor_map(&outs.out[0], false, dx.out, c.K, c.M, 1, pitch, 0, 32, 32, 64);
+        dx.pitch = c.s->B == 1 || dx.out_b == dx.out_t * dx.T ? dx.out_t : c.s->T == 1 ? dx.out_b : 0;
+        dw.pitch = c.K;
+        dx.out_box = !f32 && last && dx.cuts == 1 && dx.pitch > 0 && lay::tensor_map(&outs.out[0], false, dx.out, c.K, c.M, 1, dx.pitch, 0, 32, 32, 64);
         dw.out_box = !f32 && dw.cuts == 1 && lay::tensor_map(&outs.out[1], false, dw.out, c.K, n, 1, c.K, 0, 32, 32, 64);
         dx.sum_box = !last && lay::tensor_map(&outs.sum, true, c.acc, c.K, c.M, 1, c.K, 0, 32, 32, 128) ? first ? 1 : 2 : 0;
         if ((e = launch<OUT>(outs, p, st)) != cudaSuccess || (e = join(dx, st)) != cudaSuccess || (e = join(dw, st)) != cudaSuccess) return e;
