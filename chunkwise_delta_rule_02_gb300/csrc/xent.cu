@@ -476,32 +476,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
 #pragma unroll
                     for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
                     // the difference first: exact where the exponential counts, whatever the logits' size
-                    float s0 = 0.f, s1 = 0.f;
+                    float2 s = lay::two(0.f);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        s0 += ex2((v[i] - top) * kLog2e);
-                        s1 += ex2((v[i + 1] - top) * kLog2e);
-                    }
-                    sum = fmaf(sum, ex2((mx - top) * kLog2e), s0 + s1);
+                    for (int i = 0; i < 32; i += 2)
+                        s = lay::add2(s, lay::ex2_2(lay::mul2(lay::add2(make_float2(v[i], v[i + 1]), lay::two(-top)), lay::two(kLog2e))));
+                    sum = fmaf(sum, ex2((mx - top) * kLog2e), s.x + s.y);
                     mx = top;
                 } else if constexpr (EPI == GRAD) {
-                    const int at = p.v0 + col;
+                    // two at a time: at 8 instructions an element a tile's way out took nearly as long as its products
+                    const float2 neg = lay::two(-lse), gg = lay::two(g);
+                    const int hit = target - p.v0 - col;   // this row's target among the columns
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float prob = ex2((v[i] - lse) * kLog2e);
-                        v[i] = i < live && target >= 0 ? (prob - (at + i == target ? 1.f : 0.f)) * g : 0.f;
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 q = lay::ex2_2(lay::mul2(lay::add2(make_float2(v[i], v[i + 1]), neg), lay::two(kLog2e)));
+                        v[i] = q.x;
+                        v[i + 1] = q.y;
                     }
-                    const int row0 = row - lane;
-                    for (int pl = 0; pl < p.planes; ++pl) {
-                        uint32_t w[16];
+                    if (__any_sync(0xffffffffu, hit >= 0 && hit < 32)) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-                            // what the next plane holds
-                            v[2 * j] -= __uint_as_float(w[j] << 16);
-                            v[2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
+                        for (int i = 0; i < 32; ++i) v[i] -= i == hit ? 1.f : 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 q = lay::mul2(make_float2(v[i], v[i + 1]), gg);
+                        v[i] = q.x;
+                        v[i + 1] = q.y;
+                    }
+                    // columns behind the vocabulary's end stay out of memory: the map ends there.  Rows without a target are 0 whatever they hold.
+                    const int row0 = row - lane;
+                    if (live > 0 && row0 < pr.M) {
+                        for (int pl = 0; pl < p.planes; ++pl) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) w[j] = target < 0 ? 0u : pack_bf16(v[2 * j], v[2 * j + 1]);
+                            box_bf16(&maps.out[0], w, col, row0, pl);
+                            if (pl + 1 < p.planes) {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) {   // what the next plane holds
+                                    v[2 * j] -= __uint_as_float(w[j] << 16);
+                                    v[2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
+                                }
+                            }
                         }
-                        if (live > 0 && row0 < pr.M) box_bf16(&maps.out[0], w, col, row0, pl);
                     }
                 } else if (live > 0 && row - lane < pr.M && pr.cuts == 1 && pr.sum && pr.sum_box) {
                     box_f32(&maps.sum, v, col, row - lane, pr.sum_box == 2);
