@@ -6,6 +6,9 @@
 // word(i), i the element's index in the [B][H][T][d] order whatever the strides, is word i mod 4 of
 // Philox 4x32 with 10 rounds (Salmon, Moraes, Dror, Shaw: Parallel random numbers: as easy as 1, 2, 3; 2011) of the counter
 // (i / 4, call number) under the key `seed`: no mask is stored, and none depends on how the work is split.
+//
+// With a residual bound by HBM (67 M bf16: 68 us, 89 % of a copy's rate), without one by the generator: 20 wide
+// multiplications and 20 logic operations for 4 elements (59 us; multiplications of the halves by two instructions: 69).
 #include <type_traits>
 
 #include "layers.h"

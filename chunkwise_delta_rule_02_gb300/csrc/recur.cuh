@@ -31,9 +31,9 @@ constexpr int kMaxCluster = 8;
 constexpr long long kRecurBudget = 4000000000LL;   // clock cycles (about 2 s) for any one wait
 
 // Warps of a block by the type's bytes, blocks that an SM holds.  bf16 forward: 12 warps twice, what 80 registers allow (4 x 8192
-// tokens of 2048 channels with the output gate: 148 us; 8 warps three times 157, 16 warps 186).  Backward: 6 warps
-// twice at 164 registers (training step of 8 x 4096 tokens: 437 us; 4 warps three times 459; runs of 4 tokens, 8
-// warps twice: 436, with twice the kept states).
+// tokens of 2048 channels with the output gate, measured side by side: 148 us; 8 warps three times 157, 16 warps 186).  Backward: 6
+// warps twice at 160 registers (training step of 8 x 4096 tokens, likewise: 437 us; 4 warps three times 459; runs of 4 tokens,
+// 8 warps twice: 436, with twice the kept states).
 __host__ __device__ constexpr int fwd_warps(int bytes) { return bytes == 2 ? 12 : 6; }
 __host__ __device__ constexpr int bwd_warps(int bytes) { return bytes == 2 ? 6 : 5; }
 constexpr int kFwdResident = 2, kBwdResident = 2;

@@ -13,6 +13,10 @@
 // D in bf16 (2^-9 of each value) is what a bf16 input's gradient is computed from: the sums over the vocabulary and over the tokens
 // are float32.  float32 inputs are split into three bf16 planes, 8 bits each, and six of their nine products kept: what is
 // left out is 2^-24 of the whole.
+//
+// Bound by the tensor cores, and in a loop by the power limit.  8192 tokens, 2048 features, 32768 entries, bf16: logits with
+// STATS 583 us alone (1.89 PFLOP/s, 83 % of the tensor cores' cycles; in a loop 655), both products of half the vocabulary 622 us
+// (88 % of the cycles); the training step 2740 us, 1.6 PFLOP/s of the 8 M V K operations that it does.
 #include "pair.cuh"
 #include "xent.h"
 

@@ -21,7 +21,8 @@ was written over them, refuse an ``out`` that does; the other calls do not look.
 Packed sequences: B = 1 and ``cu_seqlens``, int32 offsets on the device, as in
 ``binding.forward``.  The kernels check the offsets; with ``check_status`` (the
 default) a packed call reads the status word afterwards, which waits for the
-stream, and raises if they were malformed.  Other calls never wait.
+stream, and raises if they were malformed.  ``xent_*`` does so for its targets.  Other
+calls never wait.
 """
 from __future__ import annotations
 

@@ -1,8 +1,9 @@
 /*
  * gdn_layers.h — C ABI of the layer operators around the delta rule, in the same
  * library (libgdn_gb300.so, sm_103a): the short causal convolution ahead of
- * q, k, v, the selective state space scan of the layers that hybrid stacks mix
- * with the delta rule, and the RMS norm with its output gate or its residual sum.
+ * q, k, v, the selective state space scan and the gated linear recurrence of the
+ * layers that hybrid stacks mix with the delta rule, the RMS norm with its output
+ * gate or its residual sum, dropout, and the loss of the model that they make.
  *
  * Token arrays are passed as dn_view: a base pointer and element strides of the
  * batch, head and time axes; the feature axis is contiguous.  So the projection's
@@ -13,11 +14,13 @@
  * them (pointer and strides), else the kernels move one element at a time; 16-byte
  * alignment is always enough.  The norm and the single-token convolution move 16
  * bytes an access, the convolution over tokens 8, the scan 4 elements (one above
- * 32 states, and of x, dt, z and y for single tokens).
+ * 32 states, and of x, dt, z and y for single tokens).  The recurrence and the loss
+ * read through tensor maps where rows start at 16 bytes, else in words (the
+ * recurrence) or from a copy (the loss).
  *
- * Dtypes: shape->dtype (DN_F32 or DN_BF16) is that of every token array and of the
- * convolution's taps; parameters (weights, A, D, biases), scan states and their
- * gradients are float32.  Arithmetic is float32; a result is rounded once, when it
+ * Dtypes: shape->dtype (DN_F32 or DN_BF16) is that of every token array, of the
+ * convolution's taps and of the loss' weight; other parameters (weights, A, D, biases),
+ * recurrent states and their gradients are float32.  Arithmetic is float32; a result is rounded once, when it
  * is stored.
  *
  * Packed variable-length input, ownership, streams, errors: as in gdn.h.  B == 1,
