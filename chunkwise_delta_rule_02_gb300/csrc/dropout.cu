@@ -7,8 +7,8 @@
 // Philox 4x32 with 10 rounds (Salmon, Moraes, Dror, Shaw: Parallel random numbers: as easy as 1, 2, 3; 2011) of the counter
 // (i / 4, call number) under the key `seed`: no mask is stored, and none depends on how the work is split.
 //
-// With a residual bound by HBM (67 M bf16: 68 us, 89 % of a copy's rate), without one by the generator: 20 wide
-// multiplications and 20 logic operations for 4 elements (59 us; multiplications of the halves by two instructions: 69).
+// With a residual bound by HBM (67 M bf16: 65 us, 93 % of a copy's rate), without one by the generator: 18 wide
+// multiplications and 20 logic operations for 4 elements (57 us; multiplications of the halves by two instructions: 69).
 #include <type_traits>
 
 #include "layers.h"
@@ -18,9 +18,9 @@ namespace lay {
 
 namespace {
 
-// Threads of a block, blocks an SM, vectors a thread has in flight (256 x 8 x 2: 69 and 61 us for the two cases of 67 M elements;
-// 512 x 8 x 1: 72, 60; 1024 x 2 x 2: 78, 62).
-constexpr int kDropThreads = 512, kDropBlocks = 4, U = 2;
+// Threads of a block, blocks an SM, vectors a thread has in flight (67 M elements with the residual and without: 64.8 and 57.3 us;
+// 512 x 4 x 2: 65.2, 64.1; 512 x 8 x 1: 64.8, 57.4; 256 x 16 x 1: 67.7, 58.6).
+constexpr int kDropThreads = 256, kDropBlocks = 8, U = 2;
 
 struct DropDims {
     int H, T;
@@ -46,9 +46,12 @@ struct Philox {
             k1[r] = (uint32_t)(seed >> 32) + r * 0xBB67AE85u;
         }
     }
+    // BIG: counters may pass 32 bits.  Where they do not, one product of the first round and one of the second are the same for
+    // all elements, and are made once a thread.
+    template <bool BIG>
     __device__ __forceinline__ void words(uint64_t group, uint32_t (&w)[4]) const
     {
-        uint32_t a = (uint32_t)group, b = (uint32_t)(group >> 32), c = c2, d = c3;
+        uint32_t a = (uint32_t)group, b = BIG ? (uint32_t)(group >> 32) : 0u, c = c2, d = c3;
 #pragma unroll
         for (int r = 0; r < 10; ++r) {
             const uint64_t u = (uint64_t)a * 0xD2511F53u, v = (uint64_t)c * 0xCD9E8D57u;
@@ -63,7 +66,7 @@ struct Philox {
 
 // A thread takes V elements of a row at a time (V a multiple of 4: whole counters; what a flat row has beyond its vectors goes
 // one by one), or, V = 1, the up to 4 elements of one counter, each with a row of its own.
-template <class T, int V, bool RES>
+template <class T, int V, bool RES, bool BIG>
 __global__ void __launch_bounds__(kDropThreads) k_dropout(DropDims g, View<const T> x, View<const T> res, View<T> y)
 {
     Philox gen;
@@ -71,6 +74,13 @@ __global__ void __launch_bounds__(kDropThreads) k_dropout(DropDims g, View<const
     auto place = [&](long long i, int &b, int &h, int &t) -> long long {   // of element i: its row; the feature
         b = h = t = 0;
         if (g.flat) return i;
+        if (g.n < 1ll << 32) {   // divisions of 32 bits are a fifth of the others
+            const unsigned row = (unsigned)i / (unsigned)g.d, bh = row / (unsigned)g.T;
+            t = (int)(row - bh * (unsigned)g.T);
+            b = (int)(bh / (unsigned)g.H);
+            h = (int)(bh - (unsigned)b * (unsigned)g.H);
+            return (unsigned)i - row * (unsigned)g.d;
+        }
         const long long row = i / g.d, bh = row / g.T;
         t = (int)(row - bh * g.T);
         b = (int)(bh / g.H);
@@ -88,7 +98,7 @@ __global__ void __launch_bounds__(kDropThreads) k_dropout(DropDims g, View<const
     if constexpr (V == 1) {
         for (long long q = first; q * 4 < g.n; q += step) {
             uint32_t w[4];
-            gen.words((uint64_t)q, w);
+            gen.words<BIG>((uint64_t)q, w);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (q * 4 + e < g.n) single(q * 4 + e, w[e]);
@@ -119,7 +129,7 @@ __global__ void __launch_bounds__(kDropThreads) k_dropout(DropDims g, View<const
 #pragma unroll
                 for (int e = 0; e < V; e += 4) {
                     uint32_t w[4];
-                    gen.words((uint64_t)(q * (V / 4) + e / 4), w);
+                    gen.words<BIG>((uint64_t)(q * (V / 4) + e / 4), w);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         f[e + i] = w[i] >= g.threshold ? f[e + i] * g.scale : 0.f;
@@ -136,7 +146,7 @@ __global__ void __launch_bounds__(kDropThreads) k_dropout(DropDims g, View<const
         if (all * V + first < g.n) {   // at most V - 1, of the first threads
             const long long i = all * V + first;
             uint32_t w[4];
-            gen.words((uint64_t)i / 4, w);
+            gen.words<BIG>((uint64_t)i / 4, w);
             single(i, i % 4 == 0 ? w[0] : i % 4 == 1 ? w[1] : i % 4 == 2 ? w[2] : w[3]);
         }
     }
@@ -178,12 +188,13 @@ cudaError_t run(const DropCall &c, cudaStream_t st)
     const View<T> y = view_of<T>(views[2]);
     const long long per = wide ? V : 4, need = ((g.n + per - 1) / per + kDropThreads - 1) / kDropThreads;
     const unsigned blocks = (unsigned)(need < (long long)kDropBlocks * sm_count() ? need : (long long)kDropBlocks * sm_count());
-    if (wide) {
-        if (r.p) k_dropout<T, V, true><<<blocks, kDropThreads, 0, st>>>(g, x, r, y);
-        else k_dropout<T, V, false><<<blocks, kDropThreads, 0, st>>>(g, x, r, y);
+    auto go = [&](auto kernel) { kernel<<<blocks, kDropThreads, 0, st>>>(g, x, r, y); };
+    if (g.n > 1ll << 34) {
+        if (wide) r.p ? go(k_dropout<T, V, true, true>) : go(k_dropout<T, V, false, true>);
+        else r.p ? go(k_dropout<T, 1, true, true>) : go(k_dropout<T, 1, false, true>);
     } else {
-        if (r.p) k_dropout<T, 1, true><<<blocks, kDropThreads, 0, st>>>(g, x, r, y);
-        else k_dropout<T, 1, false><<<blocks, kDropThreads, 0, st>>>(g, x, r, y);
+        if (wide) r.p ? go(k_dropout<T, V, true, false>) : go(k_dropout<T, V, false, false>);
+        else r.p ? go(k_dropout<T, 1, true, false>) : go(k_dropout<T, 1, false, false>);
     }
     return cudaPeekAtLastError();
 }
