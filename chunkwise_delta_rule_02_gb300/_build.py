@@ -15,7 +15,7 @@ ROOT = os.path.dirname(PKG)
 SOURCES = ["api.cu", "general.cu", "fast.cu", "coop.cu", "decode.cu", "affine.cu", "bwd_tc.cu",
            "bscan_tc.cu", "layers_api.cu", "conv.cu", "norm.cu",
            "scan_fwd.cu", "scan_bwd.cu", "recur_fwd.cu", "recur_bwd.cu", "dropout.cu",
-           "xent.cu", "xent_api.cu"]
+           "xent.cu", "xent_few.cu", "xent_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-extended-lambda", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-Wall", "-I" + os.path.join(ROOT, "include")]

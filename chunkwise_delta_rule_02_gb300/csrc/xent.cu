@@ -18,7 +18,7 @@
 // STATS 583 us alone (1.89 PFLOP/s, 83 % of the tensor cores' cycles; in a loop 655), both products of half the vocabulary 622 us
 // (88 % of the cycles); the training step 2740 us, 1.6 PFLOP/s of the 8 M V K operations that it does.
 #include "pair.cuh"
-#include "xent.h"
+#include "xent.cuh"
 
 namespace gdn {
 namespace xent {
@@ -26,16 +26,12 @@ namespace xent {
 namespace {
 
 using namespace sm100;
-using lay::ex2;
-using lay::kLog2e;
-
 constexpr int TILE = 256, HALF = 128, BK = 64, STAGES = 6, THREADS = 320, EPI_WARPS = 8;
 constexpr int OPERAND = HALF * BK * 2;                               // bytes of 128 rows of an operand
 constexpr int BOX = 4096;                                            // bytes that an epilogue warp has for results on their way out
 constexpr int SMEM = 2 * STAGES * OPERAND + EPI_WARPS * BOX + 1024 + 256;
 constexpr long long BUDGET = 4000000000LL;                           // clock cycles (about 2 s) for any one wait
 constexpr int GROUP = 16;                                            // row tiles that share the column tiles of a wave
-constexpr float kNone = -1e30f;                                      // maximum of no logits
 constexpr int kScore = 128;                                          // tokens up to which they are the columns
 
 // Steps after which float32 inputs' sums leave TMEM: the tensor core cuts what it adds off rather than rounding it, the same way each
@@ -43,65 +39,6 @@ constexpr int kScore = 128;                                          // tokens u
 constexpr int kSegment = 4;
 
 enum { STATS, GRAD, OUT, SCORE };
-
-// One product C = A B^T and how its tiles are cut: units of a tile and a part of the contraction.
-struct Product {
-    int M, N;                       // rows and columns of C that exist
-    int mt, nt, kb;                 // tiles; 64-wide steps of the contraction
-    int cuts, len;                  // parts of the contraction and their steps
-    int b_row, b_k;                 // where B's rows and its contraction begin
-    // OUT: the sum, where cuts > 1 of one part, [cuts][M][N] in `part`
-    const float *add;               // [M][N] or null
-    float *sum;                     // [M][N], or null: out
-    float *part;
-    void *out;
-    long long out_b, out_t;         // row (b, t) of out at b out_b + t out_t
-    long long pitch;                // the distance of rows where it is one, else 0
-    int T, f32, wide;               // wide: out's float rows start at 16 bytes
-    int out_box, sum_box;           // by tensor maps: out (bf16); sum, 1 stored, 2 added to what is there
-};
-
-struct Gemm {
-    Product of[2];                  // the second of OUT only
-    int seg;                        // steps of a segment: all, or kSegment (SEG)
-    int np;                         // plane products: nibbles of pa, pb
-    uint32_t pa, pb;
-    uint32_t *status;
-    // STATS, GRAD, SCORE
-    const int64_t *tgt;             // of token (b, t) at b tgt_b + t tgt_t
-    const float *dloss;
-    long long tgt_b, tgt_t, g_b, g_t, ignore;
-    int T, V;
-    const float *scale;             // the largest |dloss|, which D leaves out and the sums get back
-    const float *lse;
-    float *row;                     // [M] the target's logit
-    float2 *part;
-    int share;                      // SCORE: rows of w that a CTA has of a unit
-    int v0, planes;
-};
-
-// A mean's dloss is one value for all tokens, whose rounding to bf16 would be off the same way in every row of D: up to 2^-8 of all
-// gradients.  So D holds (exp(l - lse) - onehot) times dloss over its largest magnitude, and the sums are multiplied with that.
-__device__ __forceinline__ float scale_of(const Gemm &p)
-{
-    const float s = *p.scale;
-    return s > 0.f ? s : 1.f;
-}
-
-// The kernels of a call are launched so that one may start while the one before it ends: each says so at once, and waits for the other's
-// results before it touches any memory.
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// A token's target, -1 for none: ignored, or (which the status word is told) outside the vocabulary.
-__device__ __forceinline__ int target_of(const Gemm &p, int row, bool tell)
-{
-    const long long v = p.tgt[(long long)(row / p.T) * p.tgt_b + (long long)(row % p.T) * p.tgt_t];
-    if (v == p.ignore) return -1;
-    if (v >= 0 && v < p.V) return (int)v;
-    if (tell) raise_status(p.status, kStatusBadOffsets);
-    return -1;
-}
 
 // What a unit costs, in stages of the ring: those of its contraction, and its way out of TMEM (2 tokens, 15733 entries of 474: 188 us
 // for the product when only the contraction counted, and pairs without a unit of dx got a hundred short units of dw)
@@ -726,6 +663,42 @@ __global__ void __launch_bounds__(256) k_pack(const __grid_constant__ Packing p)
     }
 }
 
+// bf16 rows of 16 bytes' multiples into dense ones of any width: a thread writes 8 elements, which it shifts out of the 16 that they lie
+// in, or, across rows, gathers.  (From the tiles such rows go 2 bytes a lane: 29 tokens, 69380 entries of 1591 features took 403 us for
+// the product alone, now 216 and this.)
+__global__ void __launch_bounds__(256) k_unpack(const __nv_bfloat16 *from, long long pitch, __nv_bfloat16 *to, int K, long long all)
+{
+    let_next_start();
+    wait_for_last();
+    const long long step = (long long)gridDim.x * 256 * 8;
+    for (long long i = (blockIdx.x * 256ll + threadIdx.x) * 8; i < all; i += step) {
+        const long long row = all < 1ll << 32 ? (unsigned)i / (unsigned)K : i / K;
+        int col = (int)(i - row * K);
+        const int n = (int)min(8ll, all - i);
+        const __nv_bfloat16 *line = from + row * pitch;
+        if (n == 8 && col + 8 <= K) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(line) + (col >> 3);
+            const uint4 lo = q[0], hi = col & 7 ? q[1] : make_uint4(0, 0, 0, 0);
+            uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+            for (int j = 0; j < 6; ++j) w[j] = col & 4 ? w[j + 2] : w[j];
+#pragma unroll
+            for (int j = 0; j < 5; ++j) w[j] = col & 2 ? w[j + 1] : w[j];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = col & 1 ? __funnelshift_r(w[j], w[j + 1], 16) : w[j];
+            *reinterpret_cast<uint4 *>(to + i) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            for (int j = 0; j < n; ++j) {
+                to[i + j] = line[col];
+                if (++col == K) {
+                    col = 0;
+                    line += pitch;
+                }
+            }
+        }
+    }
+}
+
 // Sums of a product's parts in a fixed order, and what OUT does with a whole one.  A thread has 4 columns of a row where `wide`.
 template <int V>
 __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Product o)
@@ -761,23 +734,6 @@ bool make_map(CUtensorMap *m, const Operand &o, long long cols, long long rows, 
     return lay::tensor_map(m, false, o.p, cols, rows, planes, o.pitch, o.plane, 64, high, 128);
 }
 
-template <class K, class... A>
-cudaError_t start(K kernel, long long blocks, int threads, int smem, cudaStream_t st, const A &...args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    return e != cudaSuccess ? e : cudaPeekAtLastError();
-}
-
 void size(Product &o, int M, int N, int contraction)
 {
     o.M = M;
@@ -807,42 +763,6 @@ template <int EPI, int NT = TILE>
 cudaError_t launch(const Maps &m, Gemm &p, cudaStream_t st)
 {
     return p.np > 1 ? launch_as<EPI, true, NT>(m, p, st) : launch_as<EPI, false, NT>(m, p, st);
-}
-
-cudaError_t join(const Product &o, cudaStream_t st)
-{
-    if (o.cuts == 1) return cudaSuccess;
-    const bool four = o.N % 4 == 0;
-    const long long n = ((long long)o.M * o.N / (four ? 4 : 1) + 255) / 256, most = 16ll * lay::sm_count();
-    const unsigned blocks = (unsigned)(n < most ? n : most);
-    return start(four ? k_join<4> : k_join<1>, blocks, 256, 0, st, o);
-}
-
-Gemm common(const Call &c)
-{
-    Gemm p = {};
-    p.status = c.status;
-    p.planes = c.planes;
-    // of three planes a side, the products from the smallest on
-    p.np = c.planes == 1 ? 1 : 6;
-    p.pa = c.planes == 1 ? 0 : 0x001102;
-    p.pb = c.planes == 1 ? 0 : 0x010120;
-    p.tgt = (const int64_t *)c.targets->data;
-    p.tgt_b = c.targets->batch;
-    p.tgt_t = c.targets->time;
-    p.ignore = c.s->ignore_index;
-    p.T = c.s->T;
-    p.V = c.V;
-    if (c.dloss) {
-        p.dloss = (const float *)c.dloss->data;
-        p.g_b = c.dloss->batch;
-        p.g_t = c.dloss->time;
-    }
-    p.scale = (const float *)(c.status + 1);
-    p.lse = c.lse;
-    p.row = c.row;
-    p.part = c.part;
-    return p;
 }
 
 // Clears the status word and the scale; copies what the tensor maps cannot read in place.
@@ -883,6 +803,66 @@ int score_units(int V, int &share)
 
 }  // namespace
 
+cudaError_t join_rows(const Gemm &p, const Call &c, int P, cudaStream_t st)
+{
+    const float2 *part = c.part;
+    return c.M > 2048 ? start(k_lse<32>, (c.M + 31) / 32, 256, 0, st, p, part, P, c.M, c.loss, c.lse)
+                      : start(k_lse<4>, (c.M + 3) / 4, 256, 0, st, p, part, P, c.M, c.loss, c.lse);
+}
+
+// Where a product's bf16 rows cannot leave by boxes: has them left in `at` instead, and says so
+static bool by_way_of(Product &o, CUtensorMap *map, void *at, int rows)
+{
+    const long long pitch = (o.N + 7ll) / 8 * 8;
+    if (!at || o.out_box || o.cuts > 1 || o.sum || o.f32 || o.pitch != o.N || (uintptr_t)o.out % 16 ||
+        !lay::tensor_map(map, false, at, o.N, rows, 1, pitch, 0, 32, 32, 64))
+        return false;
+    o.out_box = 1;
+    return true;
+}
+
+static cudaError_t unpack(const Product &o, const void *at, cudaStream_t st)
+{
+    const long long all = (long long)o.M * o.N, need = (all + 2047) / 2048, most = 16ll * lay::sm_count();
+    return start(k_unpack, need < most ? need : most, 256, 0, st, (const __nv_bfloat16 *)at, (o.N + 7ll) / 8 * 8, (__nv_bfloat16 *)o.out, o.N, all);
+}
+
+static cudaError_t join(const Product &o, cudaStream_t st)
+{
+    if (o.cuts == 1) return cudaSuccess;
+    const bool four = o.N % 4 == 0;
+    const long long n = ((long long)o.M * o.N / (four ? 4 : 1) + 255) / 256, most = 16ll * lay::sm_count();
+    const unsigned blocks = (unsigned)(n < most ? n : most);
+    return start(four ? k_join<4> : k_join<1>, blocks, 256, 0, st, o);
+}
+
+Gemm common(const Call &c)
+{
+    Gemm p = {};
+    p.status = c.status;
+    p.planes = c.planes;
+    // of three planes a side, the products from the smallest on
+    p.np = c.planes == 1 ? 1 : 6;
+    p.pa = c.planes == 1 ? 0 : 0x001102;
+    p.pb = c.planes == 1 ? 0 : 0x010120;
+    p.tgt = (const int64_t *)c.targets->data;
+    p.tgt_b = c.targets->batch;
+    p.tgt_t = c.targets->time;
+    p.ignore = c.s->ignore_index;
+    p.T = c.s->T;
+    p.V = c.V;
+    if (c.dloss) {
+        p.dloss = (const float *)c.dloss->data;
+        p.g_b = c.dloss->batch;
+        p.g_t = c.dloss->time;
+    }
+    p.scale = (const float *)(c.status + 1);
+    p.lse = c.lse;
+    p.row = c.row;
+    p.part = c.part;
+    return p;
+}
+
 int tiles_of(int n) { return (int)(((long long)n + TILE - 1) / TILE); }
 
 // How the contractions of a piece's two products are cut: a unit not costlier than a pair's share of all, so that a few long
@@ -910,6 +890,7 @@ cudaError_t forward(const Call &c, cudaStream_t st)
 {
     cudaError_t e = begin(c, st);
     if (e != cudaSuccess || c.M == 0) return e;
+    if (c.few) return few_forward(c, st);
     Maps m = {};
     Gemm p = common(c);
     if (c.M > kScore) {
@@ -929,10 +910,7 @@ cudaError_t forward(const Call &c, cudaStream_t st)
         e = nt == 32 ? launch<SCORE, 32>(m, p, st) : nt == 64 ? launch<SCORE, 64>(m, p, st) : launch<SCORE, 128>(m, p, st);
     }
     if (e != cudaSuccess) return e;
-    const int P = parts_of(c.M, c.V);
-    const float2 *part = c.part;
-    return c.M > 2048 ? start(k_lse<32>, (c.M + 31) / 32, 256, 0, st, p, part, P, c.M, c.loss, c.lse)
-                      : start(k_lse<4>, (c.M + 3) / 4, 256, 0, st, p, part, P, c.M, c.loss, c.lse);
+    return join_rows(p, c, parts_of(c.M, c.V), st);
 }
 
 cudaError_t backward(const Call &c, cudaStream_t st)
@@ -941,6 +919,7 @@ cudaError_t backward(const Call &c, cudaStream_t st)
     if (e != cudaSuccess) return e;
     const bool f32 = c.s->dtype == DN_F32;
     if (c.M == 0) return cudaMemsetAsync(c.dw, 0, (size_t)c.V * c.K * (f32 ? 4 : 2), st);
+    if (c.few) return few_backward(c, st);
     const Operand d = {c.d, c.piece, (long long)c.M * c.piece};
     Maps logits = {}, outs = {};
     if (!make_map(&logits.a[0], c.xo, c.K, c.M, c.planes, HALF) || !make_map(&logits.b[0], c.wo, c.K, c.V, c.planes, HALF) ||
@@ -993,7 +972,9 @@ cudaError_t backward(const Call &c, cudaStream_t st)
         dx.out_box = !f32 && last && dx.cuts == 1 && dx.pitch > 0 && lay::tensor_map(&outs.out[0], false, dx.out, c.K, c.M, 1, dx.pitch, 0, 32, 32, 64);
         dw.out_box = !f32 && dw.cuts == 1 && lay::tensor_map(&outs.out[1], false, dw.out, c.K, n, 1, c.K, 0, 32, 32, 64);
         dx.sum_box = !last && lay::tensor_map(&outs.sum, true, c.acc, c.K, c.M, 1, c.K, 0, 32, 32, 128) ? first ? 1 : 2 : 0;
+        const bool dx_later = last && by_way_of(dx, &outs.out[0], c.dx_rows, c.M), dw_later = by_way_of(dw, &outs.out[1], c.dw_rows, n);
         if ((e = launch<OUT>(outs, p, st)) != cudaSuccess || (e = join(dx, st)) != cudaSuccess || (e = join(dw, st)) != cudaSuccess) return e;
+        if ((dx_later && (e = unpack(dx, c.dx_rows, st)) != cudaSuccess) || (dw_later && (e = unpack(dw, c.dw_rows, st)) != cudaSuccess)) return e;
     }
     return cudaSuccess;
 }

@@ -69,6 +69,17 @@ size_t layout(Call &c, const dn_xent_shape *s, const dn_view *x, const dn_view *
         }
     };
     if (c.M == 0) return at;
+    c.few = few_tokens(c.M, c.K, c.planes == 3);
+    if (c.few) {
+        const int blocks = few_blocks(c.M, c.K, c.V, bwd);
+        if (bwd) {
+            c.cut = (float *)take((size_t)blocks * c.M * c.K * 4);
+        } else {
+            c.row = (float *)take((size_t)c.M * 4);
+            c.part = (float2 *)take((size_t)c.M * blocks * sizeof(float2));
+        }
+        return at;
+    }
     operand(c.xo, c.pack_x, x, c.M, s->T);
     operand(c.wo, c.pack_w, w, c.V, c.V);
     if (!bwd) {
@@ -91,6 +102,10 @@ size_t layout(Call &c, const dn_xent_shape *s, const dn_view *x, const dn_view *
             if (room > cut) cut = room;
         }
         if (cut) c.cut = (float *)take(cut * 4);
+        if (c.planes == 1 && c.K % 8) {
+            c.dx_rows = take((size_t)c.M * Kp * 2);
+            c.dw_rows = take((size_t)n * Kp * 2);
+        }
     }
     return at;
 }

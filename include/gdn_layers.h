@@ -216,7 +216,8 @@ dn_status dn_dropout(const dn_dropout_shape *shape, const dn_view *x, const dn_v
  * A token whose target is ignore_index has no loss (0) and no gradient; one whose target is outside
  * 0 .. V - 1 likewise, and the workspace's status word says so (dn_device_status: DN_ERR_INVALID_ARG).
  * Such tokens still take part in dw with weight 0: their x has to be finite.
- * Products are sums in float32 of bf16 operands, float32 ones as three bf16 planes; D is rounded to the dtype.
+ * Products are sums in float32 of bf16 operands, float32 ones as three bf16 planes; D, without dloss' largest
+ * magnitude, is rounded to the dtype.  (Up to 4 tokens, 16 in float32: all in float32.)
  * Memory: the backward pass holds D for a piece of the vocabulary at a time. */
 typedef struct {
     int32_t B, T, K, V;
