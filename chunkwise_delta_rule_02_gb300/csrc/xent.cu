@@ -467,7 +467,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
                     const long long at = (long long)row * pr.N + col;
                     const float *add = partial ? nullptr : pr.add;
                     const bool whole = live >= 32 && pr.N % 4 == 0;   // columns and 16-byte rows of a float array
-                    if (whole && add && in) {
+                    const bool boxed = !sums && pr.out_box;
+                    if (add && in && whole) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float4 f = reinterpret_cast<const float4 *>(add + at)[i];
@@ -476,8 +477,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
                             v[4 * i + 2] += f.z;
                             v[4 * i + 3] += f.w;
                         }
+                    } else if (add && in && boxed) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i < live) v[i] += add[at + i];
                     }
-                    if (!sums && pr.out_box && (whole || !add)) {
+                    if (boxed) {
                         uint32_t w[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);

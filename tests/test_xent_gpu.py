@@ -85,9 +85,11 @@ def test_values_and_gradients(gdn, shape, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_pieces_of_the_vocabulary(gdn, dtype):
-    """Tokens enough that the logits' gradients go by several pieces, the last one odd; row tiles of more than one group."""
-    check(gdn, *make((70001, 24), 3001 if dtype is BF else 1111, dtype))
+@pytest.mark.parametrize("K", [24, 21, 20, 36, 75])
+def test_pieces_of_the_vocabulary(gdn, dtype, K):
+    """Tokens enough that the logits' gradients go by several pieces, the last one odd; row tiles of more than one group; widths that
+    are a multiple of 8, of 4 and of nothing, with the sums of dx over pieces."""
+    check(gdn, *make((70001, K), 3001 if dtype is BF else 1111, dtype))
 
 
 def test_many_tiles_a_pair(gdn):
