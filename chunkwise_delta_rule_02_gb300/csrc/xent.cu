@@ -443,7 +443,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
                         v[i] = q.x;
                         v[i + 1] = q.y;
                     }
-                    // columns behind the vocabulary's end stay out of memory: the map ends there.  Rows without a target are 0 whatever they hold.
+                    // Columns behind the vocabulary's end: a box is cut off at 16 bytes, so that up to seven get into D's padding, and exp(-lse)
+                    // has no bound.  Rows without a target are 0 whatever they hold.
+                    if (live < 32) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = i < live ? v[i] : 0.f;
+                    }
                     const int row0 = row - lane;
                     if (live > 0 && row0 < pr.M) {
                         for (int pl = 0; pl < p.planes; ++pl) {
@@ -971,10 +976,11 @@ cudaError_t backward(const Call &c, cudaStream_t st)
             o->f32 = f32;
             o->wide = f32 && (uintptr_t)o->out % 16 == 0 && o->out_b % 4 == 0 && o->out_t % 4 == 0;
         }
-        // results that tensor maps can describe: dx of rows at one distance, dw, the sums of dx over pieces
+        // results that tensor maps can describe: dx of rows at one distance, dw, the sums of dx over pieces.  A box is cut off at
+        // 16 bytes, not at the element: a row has to end there.
         dx.pitch = c.s->B == 1 || dx.out_b == dx.out_t * dx.T ? dx.out_t : c.s->T == 1 ? dx.out_b : 0;
         dw.pitch = c.K;
-        dx.out_box = !f32 && last && dx.cuts == 1 && dx.pitch > 0 && lay::tensor_map(&outs.out[0], false, dx.out, c.K, c.M, 1, dx.pitch, 0, 32, 32, 64);
+        dx.out_box = !f32 && last && dx.cuts == 1 && dx.pitch > 0 && c.K % 8 == 0 && lay::tensor_map(&outs.out[0], false, dx.out, c.K, c.M, 1, dx.pitch, 0, 32, 32, 64);
         dw.out_box = !f32 && dw.cuts == 1 && lay::tensor_map(&outs.out[1], false, dw.out, c.K, n, 1, c.K, 0, 32, 32, 64);
         dx.sum_box = !last && lay::tensor_map(&outs.sum, true, c.acc, c.K, c.M, 1, c.K, 0, 32, 32, 128) ? first ? 1 : 2 : 0;
         const bool dx_later = last && by_way_of(dx, &outs.out[0], c.dx_rows, c.M), dw_later = by_way_of(dw, &outs.out[1], c.dw_rows, n);

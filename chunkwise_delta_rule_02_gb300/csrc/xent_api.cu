@@ -32,10 +32,11 @@ dn_status shape_ok(const dn_xent_shape *s)
     return DN_OK;
 }
 
-// Rows as one bf16 matrix that a tensor map can read: of 16-byte aligned rows at one distance
+// Rows as one bf16 matrix that a tensor map can read: of 16-byte aligned rows at one distance, and of whole 16 bytes, where a map's
+// boxes are cut off (what lies behind a shorter row might be read)
 bool direct(const dn_xent_shape *s, const dn_view *v, long long rows, long long per, long long &pitch)
 {
-    if (s->dtype != DN_BF16 || !aligned(v->data, 16)) return false;
+    if (s->dtype != DN_BF16 || s->K % 8 || !aligned(v->data, 16)) return false;
     if (rows > per && (per > 1 ? v->batch != v->time * per : false)) return false;
     pitch = per > 1 || rows <= 1 ? v->time : v->batch;
     if (rows <= 1) pitch = (s->K + 7) / 8 * 8;

@@ -146,6 +146,30 @@ def test_views_give_the_same(gdn, c):
             assert g[n] is None and g2[n] is None or torch.equal(g[n], g2[n]), n
 
 
+@pytest.mark.parametrize("dt,D", [(BF, 6), (BF, 70), (F32, 70), (F32, 66)])
+def test_rows_that_end_within_16_bytes(gdn, dt, D):
+    """Aligned rows of an even width in buffers of NaN: the dense call's values, and results leave what lies behind them."""
+    k = case((2, 40, D, dt, True, True, True, None), 16)
+    x, rg, ig, lam = k["args"]
+    wide = (D + 15) // 8 * 8
+
+    def aligned(t):
+        big = torch.full(t.shape[:2] + (wide,), float("nan"), dtype=dt, device=DEV)
+        big[..., :D] = t
+        return big[..., :D]
+
+    more = dict(k["more"], z=aligned(k["more"]["z"]))
+    big = torch.full((2, 40, wide), 7.0, dtype=dt, device=DEV)
+    y, hT, saved = gdn.recur_forward(aligned(x), aligned(rg), aligned(ig), lam, **more, out=big[..., :D], save=True)
+    ry, rh, want = want_of(k)
+    close(y, ry)
+    close(hT, rh)
+    assert bool((big[..., D:] == 7.0).all())
+    g = gdn.recur_backward(aligned(x), aligned(rg), aligned(ig), lam, **more, dy=aligned(k["dy"]), dhT=k["dhT"], saved=saved)
+    for n in GRADS:
+        assert ref.err(g[n], want[n]) <= TOL[g[n].dtype], n
+
+
 def test_a_result_leaves_what_lies_around_it(gdn):
     k = case((2, 21, 35, BF, True, False, False, None), 4)
     big = torch.full((4, 30, 50), 7.0, dtype=BF, device=DEV)

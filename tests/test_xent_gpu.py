@@ -92,6 +92,35 @@ def test_pieces_of_the_vocabulary(gdn, dtype, K):
     check(gdn, *make((70001, K), 3001 if dtype is BF else 1111, dtype))
 
 
+@pytest.mark.parametrize("M", [3, 50, 300])
+@pytest.mark.parametrize("K", [21, 4, 76])
+def test_rows_that_end_within_16_bytes(gdn, M, K):
+    """Aligned rows of a width that is no multiple of 8 in a buffer of NaN: what lies behind a row is not read."""
+    x, w, t, dloss = make((M, K), 500, BF, 17)
+    wide = (K + 15) // 8 * 8
+    bx, bw = (torch.full((n, wide), float("nan"), dtype=BF, device=DEV) for n in (M, 500))
+    bx[:, :K], bw[:, :K] = x, w
+    check(gdn, bx[:, :K], bw[:, :K], t, dloss)
+
+
+@pytest.mark.parametrize("T,B", [(7, 10001), (70001, 1)])
+def test_pieces_into_rows_of_other_strides(gdn, T, B):
+    """The library call with a dx whose rows lie apart: the same gradients, and nothing between them is touched."""
+    from chunkwise_delta_rule_02_gb300 import layers
+    for K in (24, 21):
+        x, w, t, dloss = make((B, T, K), 2500, BF, 16)
+        _, lse = gdn.xent_forward(x, w, t)
+        want = gdn.xent_backward(x, w, t, lse, dloss)
+        big = torch.full((B, T + 2, K + 11), 7.0, dtype=BF, device=DEV)
+        dx, dw = big[:, 1:T + 1, 8:K + 8], torch.empty_like(w)
+        shape = layers.xent_shape(x, w)
+        ws = torch.empty(layers.dn_xent_workspace_size(shape, x, w, True), dtype=torch.uint8, device=DEV)
+        layers.dn_xent_bwd(shape, x, w, t, lse, dloss, dx, dw, ws)
+        assert torch.equal(dx, want["dx"]) and torch.equal(dw, want["dw"])
+        big[:, 1:T + 1, 8:K + 8] = 7.0
+        assert bool((big == 7.0).all())
+
+
 def test_many_tiles_a_pair(gdn):
     check(gdn, *make((5000, 256), 9000, BF))
 
@@ -174,6 +203,28 @@ def test_large_logits(gdn):
     check(gdn, x, w, t, dloss)
     low = -x.abs() - 1                       # all logits far below 0
     check(gdn, low, w.abs() + 1, t, dloss)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_logits_far_below_zero(gdn, dtype):
+    """All logits near -400, an odd vocabulary: exp(-lse) is infinite, and nothing of it reaches a gradient.
+
+    The entries' common feature cancels in dx (the gradients of a token's logits sum to 0), their roundings do not, so what dx and dw may be
+    off is counted from the terms: D of a bf16 call is off by half a step 2^-8 of itself, of a float32 call by 2^-22; the probability by
+    4 |lse| 2^-24; the sums by their number of terms times 2^-24; and the result is rounded once."""
+    x, w, t, dloss = make((300, 64), 501, dtype, 18, scale=0.5)
+    x[:, 0], w[:, 0] = 20.0, -20.0
+    loss, lse = gdn.xent_forward(x, w, t)
+    g = gdn.xent_backward(x, w, t, lse, dloss)
+    rl, rs, rx, rw = plain(x, w, t, dloss)
+    room = 1e-5 * (1 + rs.abs())
+    assert bool(((lse - rs).abs() <= room).all()) and bool(((loss - rl).abs() <= 2 * room).all())
+    terms = torch.exp(x.double() @ w.double().t() - rs[:, None])
+    terms[torch.arange(300, device=DEV), t.clamp(min=0)] += 1
+    terms *= torch.where(t >= 0, dloss.double().abs(), 0.0)[:, None]
+    off = (2.0 ** -8 if dtype is BF else 2.0 ** -22) + (4 * float(rs.abs().max()) + 501) * 2.0 ** -24
+    for n, want, size in (("dx", rx, terms @ w.double().abs()), ("dw", rw, terms.t() @ x.double().abs())):
+        assert bool(((g[n].double() - want).abs() <= off * size + (2.0 ** -8 if dtype is BF else 2.0 ** -24) * want.abs()).all()), n
 
 
 def test_infinities_and_nan_stay_in_their_rows(gdn):
