@@ -636,13 +636,16 @@ __global__ void __launch_bounds__(256) k_scale(const __grid_constant__ Gemm p, i
 }
 
 // x and w into [planes][rows][pitch] bf16: as they are, or as three planes, the largest first.  A thread has 8 columns of a row,
-// 2^shift threads a row at a time; the first blocks have x's rows.
+// 2^shift threads a row at a time; the first blocks have x's rows.  Backward, rows of x without a target become 0: the products would
+// take 0 times what is not finite for NaN in all of dw.
 struct Packing {
+    Gemm g;
     const void *from[2];
     long long b[2], t[2], pitch[2], plane[2];
     __nv_bfloat16 *to[2];
     int rows[2], T[2], blocks[2];
-    int K, shift;
+    int K, shift, mask;
+    int whole[2];                   // rows of whole 16 bytes that start at 16 bytes (bf16)
 };
 
 template <class T>
@@ -655,10 +658,15 @@ __global__ void __launch_bounds__(256) k_pack(const __grid_constant__ Packing p)
     if (r >= p.rows[o]) return;
     const T *from = (const T *)p.from[o] + (long long)(r / p.T[o]) * p.b[o] + (long long)(r % p.T[o]) * p.t[o];
     __nv_bfloat16 *to = p.to[o] + r * p.pitch[o];
+    const bool none = p.mask && o == 0 && target_of(p.g, r, false) < 0;
     for (int c = (threadIdx.x & ((1 << p.shift) - 1)) * 8; c < p.pitch[o]; c += 8 << p.shift) {
+        if (sizeof(T) == 2 && (none || p.whole[o])) {
+            *reinterpret_cast<uint4 *>(to + c) = none ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(from + c);
+            continue;
+        }
         float f[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = c + e < p.K ? ld_in(from + c + e) : 0.f;
+        for (int e = 0; e < 8; ++e) f[e] = c + e < p.K && !none ? ld_in(from + c + e) : 0.f;
 #pragma unroll
         for (int pl = 0; pl < (sizeof(T) == 4 ? 3 : 1); ++pl) {
             uint32_t w[4];
@@ -776,7 +784,7 @@ cudaError_t launch(const Maps &m, Gemm &p, cudaStream_t st)
 }
 
 // Clears the status word and the scale; copies what the tensor maps cannot read in place.
-cudaError_t begin(const Call &c, cudaStream_t st)
+cudaError_t begin(const Call &c, bool bwd, cudaStream_t st)
 {
     cudaError_t e = cudaMemsetAsync(c.status, 0, 2 * sizeof(uint32_t), st);   // and the scale behind it
     if (e != cudaSuccess || c.M == 0 || !(c.pack_x || c.pack_w)) return e;
@@ -785,7 +793,9 @@ cudaError_t begin(const Call &c, cudaStream_t st)
     const Operand *to[2] = {&c.xo, &c.wo};
     const int rows[2] = {c.M, c.V}, per[2] = {c.s->T, c.V};
     const bool packs[2] = {c.pack_x, c.pack_w};
+    p.g = common(c);
     p.K = c.K;
+    p.mask = bwd;
     while (p.shift < 8 && 8 << p.shift < c.K) ++p.shift;
     for (int o = 0; o < 2; ++o) {
         p.T[o] = per[o];
@@ -793,6 +803,7 @@ cudaError_t begin(const Call &c, cudaStream_t st)
         p.from[o] = views[o]->data;
         p.b[o] = views[o]->batch;
         p.t[o] = views[o]->time;
+        p.whole[o] = c.K % 8 == 0 && (uintptr_t)p.from[o] % 16 == 0 && p.b[o] % 8 == 0 && p.t[o] % 8 == 0;
         p.to[o] = (__nv_bfloat16 *)to[o]->p;
         p.pitch[o] = to[o]->pitch;
         p.plane[o] = to[o]->plane;
@@ -898,7 +909,7 @@ int parts_of(int M, int V)
 
 cudaError_t forward(const Call &c, cudaStream_t st)
 {
-    cudaError_t e = begin(c, st);
+    cudaError_t e = begin(c, false, st);
     if (e != cudaSuccess || c.M == 0) return e;
     if (c.few) return few_forward(c, st);
     Maps m = {};
@@ -925,7 +936,7 @@ cudaError_t forward(const Call &c, cudaStream_t st)
 
 cudaError_t backward(const Call &c, cudaStream_t st)
 {
-    cudaError_t e = begin(c, st);
+    cudaError_t e = begin(c, true, st);
     if (e != cudaSuccess) return e;
     const bool f32 = c.s->dtype == DN_F32;
     if (c.M == 0) return cudaMemsetAsync(c.dw, 0, (size_t)c.V * c.K * (f32 ? 4 : 2), st);

@@ -60,7 +60,7 @@ size_t layout(Call &c, const dn_xent_shape *s, const dn_view *x, const dn_view *
     c.status = (uint32_t *)base;
     const long long Kp = (c.K + 7) / 8 * 8;
     auto operand = [&](Operand &o, bool &packed, const dn_view *v, long long rows, long long per) {
-        packed = !direct(s, v, rows, per, o.pitch);
+        packed = !v || !direct(s, v, rows, per, o.pitch);
         if (packed) {
             o.pitch = Kp;
             o.plane = rows * Kp;
@@ -70,7 +70,7 @@ size_t layout(Call &c, const dn_xent_shape *s, const dn_view *x, const dn_view *
         }
     };
     if (c.M == 0) return at;
-    c.few = few_tokens(c.M, c.K, c.planes == 3);
+    c.few = few_tokens(c.M, c.K, c.planes == 3, bwd);
     if (c.few) {
         const int blocks = few_blocks(c.M, c.K, c.V, bwd);
         if (bwd) {
@@ -81,7 +81,8 @@ size_t layout(Call &c, const dn_xent_shape *s, const dn_view *x, const dn_view *
         }
         return at;
     }
-    operand(c.xo, c.pack_x, x, c.M, s->T);
+    // backward, x is copied in any case: with 0 for tokens without a target, so that what they hold does not get into dw
+    operand(c.xo, c.pack_x, bwd ? nullptr : x, c.M, s->T);
     operand(c.wo, c.pack_w, w, c.V, c.V);
     if (!bwd) {
         c.row = (float *)take((size_t)c.M * 4);

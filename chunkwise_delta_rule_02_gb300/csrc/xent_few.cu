@@ -1,4 +1,5 @@
-// Linear softmax cross entropy of few tokens, on the CUDA cores: up to 16 in float32, up to 4 in bf16.
+// Linear softmax cross entropy of few tokens, on the CUDA cores: up to 16 in float32, up to 4 in bf16 (backward 16 of a width that is no
+// multiple of 8).
 //
 // Tiles of 256 tokens would be empty rows, and float32 operands three planes copied from a weight that is read once
 // anyway.  Here a block has a contiguous share of the vocabulary and x in shared memory; a warp takes 4 or 8 entries at
@@ -32,12 +33,13 @@ struct Few {
     float *dx;                      // [blocks][M][K]
 };
 
-template <class T, int MT>
+// MASK: 0 for a token without a target, whose weight is 0 in dw whatever it holds
+template <class T, int MT, bool MASK>
 __device__ __forceinline__ void load_x(const Few &p, float *xs)
 {
     for (int i = threadIdx.x; i < MT * p.K; i += blockDim.x) {
         const int m = i / p.K, k = i - m * p.K;
-        xs[i] = m < p.M ? ld_in((const T *)p.x + (long long)(m / p.g.T) * p.x_b + (long long)(m % p.g.T) * p.x_t + k) : 0.f;
+        xs[i] = m < p.M && (!MASK || target_of(p.g, m, false) >= 0) ? ld_in((const T *)p.x + (long long)(m / p.g.T) * p.x_b + (long long)(m % p.g.T) * p.x_t + k) : 0.f;
     }
 }
 
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_few_fwd(const __grid_constan
     wait_for_last();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, token = lane % MT;
     const int begin = blockIdx.x * p.share, end = min(p.V, begin + p.share);
-    load_x<T, MT>(p, xs);
+    load_x<T, MT, false>(p, xs);
     const int target = token < p.M ? target_of(p.g, token, blockIdx.x == 0 && threadIdx.x < MT) : -1;
     __syncthreads();
     float mx = kNone, sum = 0.f;
@@ -136,7 +138,7 @@ __global__ void __launch_bounds__(bwd_threads(MT), MT == 16 ? 1 : 2) k_few_bwd(c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, token = lane % MT;
     const int begin = blockIdx.x * p.share, end = min(p.V, begin + p.share);
     float *sums = xs + MT * p.K;
-    load_x<T, MT>(p, xs);
+    load_x<T, MT, true>(p, xs);
     for (int i = threadIdx.x; i < MT * p.K; i += kThreads) sums[i] = 0.f;
     int target = -1;
     float lse = 0.f, dl = 0.f;
@@ -235,15 +237,17 @@ template <class F>
 cudaError_t variant(const Call &c, F f)
 {
     const int mt = padded(c.M);
-    if (c.s->dtype != DN_F32) return f((__nv_bfloat16 *)nullptr, std::integral_constant<int, 4>{});
-    if (mt == 4) return f((float *)nullptr, std::integral_constant<int, 4>{});
-    if (mt == 8) return f((float *)nullptr, std::integral_constant<int, 8>{});
-    return f((float *)nullptr, std::integral_constant<int, 16>{});
+    auto of = [&](auto *t) {
+        return mt == 4 ? f(t, std::integral_constant<int, 4>{}) : mt == 8 ? f(t, std::integral_constant<int, 8>{}) : f(t, std::integral_constant<int, 16>{});
+    };
+    return c.s->dtype == DN_F32 ? of((float *)nullptr) : of((__nv_bfloat16 *)nullptr);
 }
 
 }  // namespace
 
-bool few_tokens(int M, int K, bool f32) { return M >= 1 && M <= (f32 ? 16 : 4) && shared_of(M, K, true) <= kFewShared; }
+// bf16: the tensor cores take 8 tokens of 50000 x 1024 through forward and backward in 30 and 125 us, this 74 and 146; where they need copies
+// of aligned rows, 69380 x 1591, in 136 and 440 us, this in 149 and 330.
+bool few_tokens(int M, int K, bool f32, bool bwd) { return M >= 1 && M <= (f32 || (bwd && K % 8) ? 16 : 4) && shared_of(M, K, true) <= kFewShared; }
 
 int few_blocks(int M, int K, int V, bool bwd)
 {

@@ -215,9 +215,10 @@ dn_status dn_dropout(const dn_dropout_shape *shape, const dn_view *x, const dn_v
  * b batch + t time (their feature axis is one element); loss, lse float32 [M].
  * A token whose target is ignore_index has no loss (0) and no gradient; one whose target is outside
  * 0 .. V - 1 likewise, and the workspace's status word says so (dn_device_status: DN_ERR_INVALID_ARG).
- * Such tokens still take part in dw with weight 0: their x has to be finite.
+ * What the hidden states of such tokens hold, NaN too, reaches no loss and no
+ * gradient.
  * Products are sums in float32 of bf16 operands, float32 ones as three bf16 planes; D, without dloss' largest
- * magnitude, is rounded to the dtype.  (Up to 4 tokens, 16 in float32: all in float32.)
+ * magnitude, is rounded to the dtype.  (Of few tokens all is in float32.)
  * Memory: the backward pass holds D for a piece of the vocabulary at a time. */
 typedef struct {
     int32_t B, T, K, V;
@@ -225,7 +226,8 @@ typedef struct {
     int64_t ignore_index;
 } dn_xent_shape;
 
-/* Goes by the views' alignment too: rows that start at 16 bytes are read in place, others from a copy. */
+/* Goes by the views' alignment too: rows that start at 16 bytes are read in place, others from a copy
+ * (backward, x always is). */
 size_t dn_xent_workspace_size(const dn_xent_shape *shape, const dn_view *x, const dn_view *w,
                               int for_backward);
 

@@ -28,7 +28,7 @@ def test_sizes(lay):
     M, V = 40, 30
     fwd = f(shape(lay))
     assert lay._XENT_SHAPE.size == 32 and fwd % 256 == 0 and fwd >= 256 + a256(M * 4) + a256(M * 8)
-    assert f(shape(lay), bwd=1) == 256 + a256(M * 256 * 2)
+    assert f(shape(lay), bwd=1) == 256 + a256(M * 16 * 2) + a256(M * 256 * 2)      # x is copied: without the tokens that have no target
     assert f(shape(lay, T=100), view(lay, b=1600)) == 256 + a256(200 * 4) + a256(200 * 2 * 8)    # two halves of one tile of the vocabulary
     # rows that do not start at 16 bytes, or at no one distance, are read from a copy
     assert f(shape(lay), view(lay, P + 2)) == fwd + a256(M * 16 * 2) == f(shape(lay), view(lay, b=400)) == f(shape(lay), view(lay, b=340, t=17))
@@ -38,7 +38,7 @@ def test_sizes(lay):
     assert f(shape(lay, B=0)) == 256 == f(shape(lay, T=0))
     # pieces of the vocabulary: the sums of dx are kept between them; dw's long contraction of few tiles is cut
     big = shape(lay, B=1, T=1 << 16, V=5000)
-    whole = 256 + (1024 * 2 << 16) + (16 * 4 << 16)
+    whole = 256 + (16 * 2 << 16) + (1024 * 2 << 16) + (16 * 4 << 16)
     assert f(big, view(lay, b=0), None, 1) > whole and (f(big, view(lay, b=0), None, 1) - whole) % (1024 * 16 * 4) == 0
     for bad in (dict(B=-1), dict(T=-1), dict(K=0), dict(V=0), dict(dtype=2), dict(B=1 << 20, T=1 << 20), dict(V=(1 << 30) + 1), dict(K=(1 << 24) + 1),
                 dict(B=1, T=1 << 30, V=1 << 30)):

@@ -241,6 +241,25 @@ def test_infinities_and_nan_stay_in_their_rows(gdn):
     assert not bool(torch.isfinite(loss2[~rest]).any())
 
 
+@pytest.mark.parametrize("dtype,M,K", [(BF, 3, 16), (BF, 12, 21), (BF, 300, 64), (BF, 300, 37), (BF, 70001, 8), (F32, 11, 20), (F32, 300, 37)])
+def test_padding_tokens_reach_nothing(gdn, dtype, M, K):
+    """Hidden states, dloss and lse of tokens without a target hold NaN and infinities: losses and gradients to the bit as with zeros there."""
+    x, w, t, dloss = make((M, K), 400, dtype, 19, ignored=0.4)
+    t[1], t[2] = -100, 5
+    pad = t < 0
+    x[pad] = 0
+    loss, lse = gdn.xent_forward(x, w, t)
+    want = gdn.xent_backward(x, w, t, lse, dloss)
+    x[pad] = float("nan")
+    x[1] = float("inf")
+    dloss[pad] = float("nan")
+    loss2, lse2 = gdn.xent_forward(x, w, t)
+    assert torch.equal(loss, loss2) and not bool(loss2[pad].any()) and torch.equal(lse[~pad], lse2[~pad])
+    lse2[pad] = float("-inf")
+    g = gdn.xent_backward(x, w, t, lse2, dloss)
+    assert torch.equal(g["dx"], want["dx"]) and torch.equal(g["dw"], want["dw"]) and not bool(g["dx"][pad].any())
+
+
 def test_gradients_against_differences(gdn):
     """Central differences along random directions, float32: the step 2^-5 leaves some 1e-3 of the derivative, the losses' rounding 1e-4."""
     x, w, t, dloss = make((60, 48), 130, F32, 10)
