@@ -40,10 +40,12 @@ constexpr int kSegment = 4;
 
 enum { STATS, GRAD, OUT, SCORE };
 
-// What a unit costs, in stages of the ring: those of its contraction, and its way out of TMEM (2 tokens, 15733 entries of 474: 188 us
-// for the product when only the contraction counted, and pairs without a unit of dx got a hundred short units of dw)
-constexpr int kWayOut = 24;
-__host__ __device__ inline int cost_of(const Gemm &g, const Product &o) { return o.len * g.np + kWayOut; }
+// What a unit costs, in stages of the ring: those of its contraction, and its way out of TMEM, which is longer for float32 (2 tokens,
+// 15733 entries of 474: 188 us for the product when only the contraction counted, and pairs without a unit of dx got a hundred
+// short units of dw).  bf16, 8 tokens of 50000 x 1024, backward with 4, 8, 12, 24 for it: 103, 93, 96, 127 us; 29 of 69380 x 1592 246, 223, 225, 281;
+// 1001 float32 of 5003 x 203 with 8, 12, 24: 131, 115, 115.
+__host__ __device__ constexpr int way_out(int np) { return np > 1 ? 24 : 8; }
+__host__ __device__ inline int cost_of(const Gemm &g, const Product &o) { return o.len * g.np + way_out(g.np); }
 
 // Units of the two products for pair `p` of `n`: the first product's dealt in turn, the second's so that pairs with fewer of the
 // first have the more of the second that its cost makes up for.
@@ -892,7 +894,7 @@ void cuts_of(int M, int K, int n, int planes, int &dx, int &dw)
 {
     const long long np = planes == 1 ? 1 : 6, a = ((long long)n + BK - 1) / BK, b = ((long long)M + BK - 1) / BK;
     const long long nx = (long long)tiles_of(K) * tiles_of(M), nw = (long long)tiles_of(K) * tiles_of(n), pairs = pairs_at_most();
-    long long share = (nx * (a * np + kWayOut) + nw * (b * np + kWayOut) + pairs - 1) / pairs / np;
+    long long share = (nx * (a * np + way_out(np)) + nw * (b * np + way_out(np)) + pairs - 1) / pairs / np;
     if (share < 8) share = 8;
     dx = (int)((a + share - 1) / share);
     dw = (int)((b + share - 1) / share);
