@@ -155,11 +155,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
     auto unit = [&](const Product &o, int u) {
         Unit r;
         if (EPI == SCORE) return Unit{u * 2 * p.share, 0, 0, o.kb, 0};
-        const int tiles = o.mt * o.nt;
-        r.cut = u / tiles;
-        const int tile = u - r.cut * tiles, per = GROUP * o.nt, grp = tile / per, in = tile - grp * per, gm = min(GROUP, o.mt - grp * GROUP);
-        r.m = (grp * GROUP + in % gm) * TILE;
-        r.n = in / gm * TILE;
+        // divisions only where they are needed: in the one thread that loads or issues, a tile's four took as long as a stage
+        const unsigned tiles = o.mt * o.nt, per = GROUP * o.nt;
+        r.cut = o.cuts == 1 ? 0 : u / tiles;
+        const unsigned tile = u - r.cut * tiles, grp = tile < per ? 0 : tile / per, in = tile - grp * per, gm = min(GROUP, o.mt - (int)grp * GROUP);
+        const unsigned col = gm == GROUP ? in / GROUP : in / gm;
+        r.m = (grp * GROUP + in - col * gm) * TILE;
+        r.n = col * TILE;
         r.k0 = r.cut * o.len;
         r.k1 = min(o.kb, r.k0 + o.len);
         return r;
@@ -180,7 +182,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
                     const Unit u = unit(pr, deal.first[o] + i * deal.step[o]);
                     const int m = u.m + rank * (EPI == SCORE ? p.share : HALF), n = u.n + rank * (NT / 2), segs = segments(u);
                     for (int sq = 0; ok && sq < segs * p.np; ++sq) {
-                        const int seg = sq / p.np, q = sq - seg * p.np;
+                        const int seg = SEG ? sq / p.np : 0, q = sq - seg * p.np;
                         const int a = p.pa >> 4 * q & 15, b = p.pb >> 4 * q & 15;
                         const int begin = SEG ? u.k0 + seg * p.seg : u.k0, end = SEG ? min(u.k1, begin + p.seg) : u.k1;
                         for (int k = begin; k < end; ++k, ++it) {
@@ -382,6 +384,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
                 bulk_commit();
             }
         };
+        // What belongs to this thread's row of a unit is asked for a unit ahead: of few features a tile's 4 chunks take as long as
+        // two or three trips to memory.
+        struct Row {
+            long long target;
+            float lse, g;
+        };
+        auto ask = [&](int i) {
+            Row r = {p.ignore, 0.f, 0.f};
+            if ((EPI == STATS || EPI == GRAD) && i < deal.count[0]) {
+                const int row = unit(p.of[0], deal.first[0] + i * deal.step[0]).m + rank * HALF + quad * 32 + lane;
+                if (row < p.of[0].M) {
+                    r.target = target_at(p, row);
+                    if (EPI == GRAD) {
+                        r.lse = p.lse[row];
+                        r.g = p.dloss[(long long)(row / p.T) * p.g_b + (long long)(row % p.T) * p.g_t];
+                    }
+                }
+            }
+            return r;
+        };
+        Row next = ask(0);
         for (int i = 0; i < deal.count[0] + (EPI == OUT ? deal.count[1] : 0); ++i) {
             const int o = EPI == OUT && i >= deal.count[0], j = o ? i - deal.count[0] : i;
             const Product &pr = p.of[o];
@@ -390,83 +413,97 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
             const bool in = row < pr.M;
             [[maybe_unused]] int target = -1;
             [[maybe_unused]] float lse = 0.f, g = 0.f, mx = kNone, sum = 0.f;
-            if ((EPI == STATS || EPI == GRAD) && in) {
-                target = target_of(p, row, p.v0 == 0 && u.n == 0 && half == 0);
-                if (EPI == GRAD) {
-                    lse = p.lse[row];
-                    if (target >= 0) g = p.dloss[(long long)(row / p.T) * p.g_b + (long long)(row % p.T) * p.g_t] / scale;
-                }
+            if constexpr (EPI == STATS || EPI == GRAD) {
+                const Row r = next;
+                next = ask(i + 1);
+                target = target_from(p, r.target, p.v0 == 0 && u.n == 0 && half == 0);
+                lse = r.lse;
+                if (EPI == GRAD && target >= 0) g = r.g / scale;
             }
-            auto finish = [&](int c, float (&v)[32]) {   // columns c0 + c .. + 31 of this thread's row
+            auto finish = [&](int c, auto &v) {   // columns c0 + c .. of this thread's row, 32 or 64
+                constexpr int W = sizeof(v) / sizeof(v[0]);
                 const int col = c0 + c, live = pr.N - col;   // columns of this chunk that exist
                 if constexpr (EPI == OUT) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= scale;
+                    for (int i = 0; i < W; ++i) v[i] *= scale;
                 }
                 if constexpr (EPI == STATS) {
-                    if (live < 32) {
+                    if (live < W) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = i < live ? v[i] : -INFINITY;
+                        for (int i = 0; i < W; ++i) v[i] = i < live ? v[i] : -INFINITY;
                     }
                     const int at = target - col;
-                    if (at >= 0 && at < 32) {
+                    if (at >= 0 && at < W) {
                         float t = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) t = i == at ? v[i] : t;
+                        for (int i = 0; i < W; ++i) t = i == at ? v[i] : t;
                         p.row[row] = t;
                     }
-                    float top = mx;
+                    float4 m = make_float4(mx, mx, mx, mx);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
+                    for (int i = 0; i < W; i += 4) {
+                        m.x = fmaxf(m.x, v[i]);
+                        m.y = fmaxf(m.y, v[i + 1]);
+                        m.z = fmaxf(m.z, v[i + 2]);
+                        m.w = fmaxf(m.w, v[i + 3]);
+                    }
+                    const float top = fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w));
                     // the difference first: exact where the exponential counts, whatever the logits' size
-                    float2 s = lay::two(0.f);
+                    float2 s[2] = {};
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        s = lay::add2(s, lay::ex2_2(lay::mul2(lay::add2(make_float2(v[i], v[i + 1]), lay::two(-top)), lay::two(kLog2e))));
-                    sum = fmaf(sum, ex2((mx - top) * kLog2e), s.x + s.y);
+                    for (int i = 0; i < W; i += 2)
+                        s[i >> 1 & 1] = lay::add2(s[i >> 1 & 1], lay::ex2_2(lay::mul2(lay::add2(make_float2(v[i], v[i + 1]), lay::two(-top)), lay::two(kLog2e))));
+                    s[0] = lay::add2(s[0], s[1]);
+                    sum = fmaf(sum, ex2((mx - top) * kLog2e), s[0].x + s[0].y);
                     mx = top;
                 } else if constexpr (EPI == GRAD) {
                     // two at a time: at 8 instructions an element a tile's way out took nearly as long as its products
                     const float2 neg = lay::two(-lse), gg = lay::two(g);
                     const int hit = target - p.v0 - col;   // this row's target among the columns
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
+                    for (int i = 0; i < W; i += 2) {
                         const float2 q = lay::ex2_2(lay::mul2(lay::add2(make_float2(v[i], v[i + 1]), neg), lay::two(kLog2e)));
                         v[i] = q.x;
                         v[i + 1] = q.y;
                     }
-                    if (__any_sync(0xffffffffu, hit >= 0 && hit < 32)) {
+                    if (__any_sync(0xffffffffu, hit >= 0 && hit < W)) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] -= i == hit ? 1.f : 0.f;
+                        for (int i = 0; i < W; ++i) v[i] -= i == hit ? 1.f : 0.f;
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
+                    for (int i = 0; i < W; i += 2) {
                         const float2 q = lay::mul2(make_float2(v[i], v[i + 1]), gg);
                         v[i] = q.x;
                         v[i + 1] = q.y;
                     }
                     // Columns behind the vocabulary's end: a box is cut off at 16 bytes, so that up to seven get into D's padding, and exp(-lse)
                     // has no bound.  Rows without a target are 0 whatever they hold.
-                    if (live < 32) {
+                    if (live < W) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = i < live ? v[i] : 0.f;
+                        for (int i = 0; i < W; ++i) v[i] = i < live ? v[i] : 0.f;
                     }
                     const int row0 = row - lane;
-                    if (live > 0 && row0 < pr.M) {
-                        for (int pl = 0; pl < p.planes; ++pl) {
-                            uint32_t w[16];
+                    if (row0 < pr.M) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) w[j] = target < 0 ? 0u : pack_bf16(v[2 * j], v[2 * j + 1]);
-                            box_bf16(&maps.out[0], w, col, row0, pl);
-                            if (pl + 1 < p.planes) {
+                        for (int h = 0; h < W; h += 32) {
+                            if (live <= h) break;
+                            for (int pl = 0; pl < p.planes; ++pl) {
+                                uint32_t w[16];
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) {   // what the next plane holds
-                                    v[2 * j] -= __uint_as_float(w[j] << 16);
-                                    v[2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
+                                for (int j = 0; j < 16; ++j) w[j] = target < 0 ? 0u : pack_bf16(v[h + 2 * j], v[h + 2 * j + 1]);
+                                box_bf16(&maps.out[0], w, col + h, row0, pl);
+                                if (pl + 1 < p.planes) {
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) {   // what the next plane holds
+                                        v[h + 2 * j] -= __uint_as_float(w[j] << 16);
+                                        v[h + 2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
+                                    }
                                 }
                             }
                         }
                     }
+                } else if constexpr (W > 32) {
+                    static_assert(EPI != OUT || W == 32, "OUT's boxes");
                 } else if (live > 0 && row - lane < pr.M && pr.cuts == 1 && pr.sum && pr.sum_box) {
                     box_f32(&maps.sum, v, col, row - lane, pr.sum_box == 2);
                 } else if (live > 0 && row - lane < pr.M) {
@@ -535,12 +572,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
                     __syncwarp();
                 }
             };
-            auto get = [&](int c, float (&v)[32]) {
-                uint32_t r[32];
-                tmem_ld32(tmem + (n & 1) * TILE + half * HALF + lanes + c, r);
+            auto get = [&](int c, auto &v) {
+                constexpr int W = sizeof(v) / sizeof(v[0]);
+                uint32_t r[W / 32][32];
+#pragma unroll
+                for (int h = 0; h < W / 32; ++h) tmem_ld32(tmem + (n & 1) * TILE + half * HALF + lanes + c + 32 * h, r[h]);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                for (int i = 0; i < W; ++i) v[i] = __uint_as_float(r[i / 32][i % 32]);
             };
             auto release = [&] {
                 tc_fence_before();
@@ -568,9 +607,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
             } else {
                 if (!(ok = wait(TFULL + (n & 1), n >> 1))) break;
                 tc_fence_after();
+                // columns at a time: with 64, maxima and exponentials have chains enough to hide their latency; OUT has nothing to hide
+                constexpr int WIDE = EPI == OUT ? 32 : 64;
 #pragma unroll 1
-                for (int c = 0; c < HALF; c += 32) {
-                    float v[32];
+                for (int c = 0; c < HALF; c += WIDE) {
+                    float v[WIDE];
                     get(c, v);
                     finish(c, v);
                 }
@@ -836,7 +877,7 @@ cudaError_t join_rows(const Gemm &p, const Call &c, int P, cudaStream_t st)
 // Where a product's bf16 rows cannot leave by boxes: has them left in `at` instead, and says so
 static bool by_way_of(Product &o, CUtensorMap *map, void *at, int rows)
 {
-    const long long pitch = (o.N + 7ll) / 8 * 8;
+    const long long pitch = copy_pitch(o.N);
     if (!at || o.out_box || o.cuts > 1 || o.sum || o.f32 || o.pitch != o.N || (uintptr_t)o.out % 16 ||
         !lay::tensor_map(map, false, at, o.N, rows, 1, pitch, 0, 32, 32, 64))
         return false;
@@ -847,7 +888,7 @@ static bool by_way_of(Product &o, CUtensorMap *map, void *at, int rows)
 static cudaError_t unpack(const Product &o, const void *at, cudaStream_t st)
 {
     const long long all = (long long)o.M * o.N, need = (all + 2047) / 2048, most = 16ll * lay::sm_count();
-    return start(k_unpack, need < most ? need : most, 256, 0, st, (const __nv_bfloat16 *)at, (o.N + 7ll) / 8 * 8, (__nv_bfloat16 *)o.out, o.N, all);
+    return start(k_unpack, need < most ? need : most, 256, 0, st, (const __nv_bfloat16 *)at, copy_pitch(o.N), (__nv_bfloat16 *)o.out, o.N, all);
 }
 
 static cudaError_t join(const Product &o, cudaStream_t st)

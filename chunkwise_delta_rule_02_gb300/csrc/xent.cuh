@@ -61,14 +61,20 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // A token's target, -1 for none: ignored, or (which the status word is told) outside the vocabulary.
-__device__ __forceinline__ int target_of(const Gemm &p, int row, bool tell)
+__device__ __forceinline__ long long target_at(const Gemm &p, int row)
 {
-    const long long v = p.tgt[(long long)(row / p.T) * p.tgt_b + (long long)(row % p.T) * p.tgt_t];
+    return p.tgt[(long long)(row / p.T) * p.tgt_b + (long long)(row % p.T) * p.tgt_t];
+}
+
+__device__ __forceinline__ int target_from(const Gemm &p, long long v, bool tell)
+{
     if (v == p.ignore) return -1;
     if (v >= 0 && v < p.V) return (int)v;
     if (tell) raise_status(p.status, kStatusBadOffsets);
     return -1;
 }
+
+__device__ __forceinline__ int target_of(const Gemm &p, int row, bool tell) { return target_from(p, target_at(p, row), tell); }
 
 template <class K, class... A>
 cudaError_t start(K kernel, long long blocks, int threads, int smem, cudaStream_t st, const A &...args)

@@ -58,7 +58,7 @@ size_t layout(Call &c, const dn_xent_shape *s, const dn_view *x, const dn_view *
         return p;
     };
     c.status = (uint32_t *)base;
-    const long long Kp = (c.K + 7) / 8 * 8;
+    const long long Kp = copy_pitch(c.K);
     auto operand = [&](Operand &o, bool &packed, const dn_view *v, long long rows, long long per) {
         packed = !v || !direct(s, v, rows, per, o.pitch);
         if (packed) {
