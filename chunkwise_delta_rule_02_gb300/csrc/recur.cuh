@@ -14,8 +14,9 @@
 //
 // The inputs of two steps lie in shared memory, filled by TMA (a box of 64 / Q channels and the block's tokens an
 // array): a step's are in registers when its maps are exchanged, and the barrier there frees their place for the
-// step after the next.  Arrays that a tensor map cannot describe (rows that do not start at 16 bytes) get there in
-// words of 4 bytes, or, bf16 that do not start at those, element by element in the step that needs them.
+// step after the next.  Of arrays that a tensor map cannot describe (rows that do not start at 16 bytes) every aligned 16 bytes that
+// hold an element of a row are copied asynchronously, and read from where the row begins in them (by single words and elements before:
+// 8 x 4096 tokens of 2047 channels, bf16 forward 591 us, backward 765, now 241 and 418; float32 527 and 839, now 271 and 469).
 #pragma once
 
 #include <type_traits>
@@ -30,15 +31,23 @@ constexpr int kRun = 8;                       // tokens of a lane and step (and 
 constexpr int kMaxCluster = 8;
 constexpr long long kRecurBudget = 4000000000LL;   // clock cycles (about 2 s) for any one wait
 
+enum { kTma, kChunks };                       // how inputs get to shared memory: boxes, or 16 bytes a lane
+
 // Warps of a block by the type's bytes, blocks that an SM holds.  bf16 forward: 12 warps twice, what 80 registers allow (4 x 8192
 // tokens of 2048 channels with the output gate, measured side by side: 148 us; 8 warps three times 157, 16 warps 186).  Backward: 6
 // warps twice at 160 registers (training step of 8 x 4096 tokens, likewise: 437 us; 4 warps three times 459; runs of 4 tokens,
-// 8 warps twice: 436, with twice the kept states).
-__host__ __device__ constexpr int fwd_warps(int bytes) { return bytes == 2 ? 12 : 6; }
-__host__ __device__ constexpr int bwd_warps(int bytes) { return bytes == 2 ? 6 : 5; }
+// 8 warps twice: 436, with twice the kept states).  float32 backward: 4 warps twice at 250 registers (4 x 4096 tokens of 1000 channels
+// 114 us, 5 warps 139).  Rows that come in whole 16 bytes (kChunks) leave room for fewer of them (bf16 forward, 2 x 4096 tokens of 1001
+// channels: 8 warps 54 us, 9, which is one block an SM, 72).
+__host__ __device__ constexpr int fwd_warps(int bytes, int Q, int mode)
+{
+    return mode == kTma ? (bytes == 2 ? 12 : 6) : bytes == 2 ? (Q == 4 ? 8 : 10) : Q == 4 ? 5 : 6;
+}
+__host__ __device__ constexpr int bwd_warps(int bytes) { return bytes == 2 ? 6 : 4; }
+// Bytes of an array's place: W warps' runs
+__host__ __device__ constexpr int place_bytes(int W, int Q, int mode, int bytes) { return W * kRun * (64 * bytes + (mode == kChunks ? 16 * Q : 0)); }
 constexpr int kFwdResident = 2, kBwdResident = 2;
 
-enum { kElements, kWords, kTma };             // how inputs get to shared memory
 
 struct RecurDims {
     int B, T, D, Nseq, tiles, CL, Q;   // tiles: channel tiles of a row; CL: blocks that share a row's tokens
@@ -384,12 +393,17 @@ __host__ __device__ constexpr int box_rows(int Q)
 }
 
 // The inputs of a block's two steps.  `sets`: bit mask of the arrays that a call has; their places follow each other, and behind
-// them, KEPT (TMA only), the states that the block's runs start from.
+// them, KEPT, the states that the block's runs start from.
 template <class T, int W, int Q, int MODE, bool KEPT>
 struct Inputs {
-    static constexpr int C = 64 / Q, R = kRun * Q, kPlace = W * kRun * 64 * (int)sizeof(T);   // channels, tokens of a warp, bytes of an array's place
+    static constexpr int C = 64 / Q, R = kRun * Q, kPlace = place_bytes(W, Q, MODE, sizeof(T));   // channels, tokens of a warp, bytes of an array's place
+    static constexpr int kPer = 16 / (int)sizeof(T), kPitch = MODE == kChunks ? C + kPer : C;          // elements of 16 bytes; of a row
+    struct Cells {
+        const T *p;
+        unsigned u, step;          // kChunks: where a row begins in its first 16 bytes, from token to token
+    };
     static constexpr int kRows = box_rows<W>(Q), kBoxes = W * R / kRows;                         // of an array
-    static_assert(kRows * kBoxes == W * R, "boxes share the rows evenly");
+    static_assert(MODE != kTma || kRows * kBoxes == W * R, "boxes share the rows evenly");
     static constexpr int kKept = KEPT ? W * 64 * 4 : 0;
     char *base;
     uint64_t *bar;
@@ -401,18 +415,34 @@ struct Inputs {
     __device__ __forceinline__ int place(int array) const { return __popc(sets & ((1 << array) - 1)); }
     __device__ __forceinline__ char *slot(int st, int array) const { return base + (st & 1) * (count * kPlace + kKept) + place(array) * kPlace; }
     __device__ __forceinline__ char *kept(int st) const { return base + (st & 1) * (count * kPlace + kKept) + count * kPlace; }
-    // of a lane's two channels of its run's first token
-    __device__ __forceinline__ const T *cells(int st, int array) const
+    // of a lane's two channels of its run, whose first token is t
+    __device__ __forceinline__ Cells cells(int st, int array, int t) const
     {
         const int lane = threadIdx.x & 31, l = lane % (32 / Q), q = lane / (32 / Q);
-        return (const T *)slot(st, array) + (((threadIdx.x >> 5) * Q + q) * kRun) * C + 2 * l;
+        Cells r = {(const T *)slot(st, array) + (((threadIdx.x >> 5) * Q + q) * kRun) * kPitch + 2 * l, 0, 0};
+        if (MODE == kChunks) {
+            const View<const T> &v = io->in[array];
+            r.u = (unsigned)((uintptr_t)v.p / sizeof(T)) + (unsigned)b * (unsigned)v.b + (unsigned)t * (unsigned)v.t + c0;
+            r.step = (unsigned)v.t;
+        }
+        return r;
     }
-    __device__ __forceinline__ static float2 at(const T *cells, int k)
+    __device__ __forceinline__ static Vec<T, 2> raw(const Cells &cells, int k)
     {
         Vec<T, 2> v;
+        if constexpr (MODE == kChunks) {
+            const T *p = cells.p + k * kPitch + (cells.u + k * cells.step) % kPer;
+            const T e[2] = {p[0], p[1]};
+            memcpy(&v.raw, e, sizeof(e));
+        } else {
+            v.load(cells.p + k * kPitch);
+        }
+        return v;
+    }
+    __device__ __forceinline__ static float2 at(const Cells &cells, int k)
+    {
         float f[2];
-        v.load(cells + k * C);
-        v.get(f);
+        raw(cells, k).get(f);
         return make_float2(f[0], f[1]);
     }
 
@@ -446,88 +476,53 @@ struct Inputs {
 #pragma unroll
                         for (int i = 0; i < kBoxes; ++i) box_load(slot(st, a) + i * (kPlace / kBoxes), &maps->in[a], full, c0, t0 + i * kRows, b);
             }
-        } else if (MODE == kWords) {
-            constexpr int P = 4 / sizeof(T), RW = C / P;           // elements of a word, words of a row
-            constexpr int H = RW > 32 ? RW / 32 : 1, V = RW > 32 ? 1 : 32 / RW;   // words of a row a lane, rows at a time
-            const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k0 = lane / RW, c = c0 + lane % RW * P;
-            const int t = t0 + warp * R + k0, n = te - t;
-            int bytes[H];
-            bool whole = n > R - V;
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                bytes[h] = max(0, min(4, (D - c - h * 32 * P) * (int)sizeof(T)));
-                whole = whole && bytes[h] == 4;
-            }
+        } else {
+            // every 16 bytes of memory that hold an element of a row, so that nothing outside of the pages of the array is touched; what else
+            // they hold is in channels that do not exist, or before the row
+            constexpr int N = C / kPer + 1;
+            const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = t0 + warp * R, n = te - t, live = min(C, D - c0);
 #pragma unroll
             for (int a = 0; a < kArrays; ++a) {
                 if (!(sets >> a & 1)) continue;
                 const View<const T> v = io->in[a];
-                const uint32_t to = sm100::smem_u32(slot(st, a)) + warp * (kPlace / W) + 4 * lane;
-                const T *from = v.at(b, 0, t) + c;
-                auto copy = [&](auto all) {
+                const T *from = v.at(b, 0, t) + c0;
+                const uint32_t to = sm100::smem_u32(slot(st, a)) + warp * (kPlace / W);
 #pragma unroll
-                    for (int k = 0; k < R; k += V) {
-#pragma unroll
-                        for (int h = 0; h < H; ++h) {
-                            const uint32_t dst = to + 4 * (k * RW + 32 * h);
-                            if constexpr (decltype(all)::value) {
-                                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(from + 32 * P * h) : "memory");
-                            } else {
-                                const int m = k < n ? bytes[h] : 0;
-                                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(m ? from + 32 * P * h : io->in[a].p), "r"(m)
-                                             : "memory");
-                            }
-                        }
-                        from += V * v.t;
-                    }
-                };
-                if (whole) copy(std::true_type{});
-                else copy(std::false_type{});
+                for (int i = lane; i < R * N; i += 32) {
+                    const int k = i / N, j = i % N;
+                    const uintptr_t row = (uintptr_t)(from + k * v.t);
+                    const int ahead = (int)(row % 16) / (int)sizeof(T);
+                    const bool some = k < n && j * kPer < ahead + live;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + (k * kPitch * (int)sizeof(T) + 16 * j)),
+                                 "l"((some ? row + 16 * j : (uintptr_t)v.p) & ~(uintptr_t)15), "r"(some ? 16 : 0)
+                                 : "memory");
+                }
             }
         }
     }
     // Every step asks or not, and closes what it asked for
     __device__ __forceinline__ void asked() const
     {
-        if (MODE == kWords) asm volatile("cp.async.commit_group;" ::: "memory");
+        if (MODE == kChunks) asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    // Waits for step st (or, elements, loads it): the block's tokens from t0
-    __device__ __forceinline__ void get(int st, int t0, int te, uint32_t *status)
+    // Waits for step st
+    __device__ __forceinline__ void get(int st, uint32_t *status)
     {
         if (MODE == kTma) {
             if (!sm100::mbar_wait(&bar[st & 1], (uint32_t)(st >> 1) & 1u, failed ? 1000 : kRecurBudget, nullptr)) {
                 failed = true;
                 raise_status(status, kStatusTimeout);
             }
-        } else if (MODE == kWords) {
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            __syncwarp();
         } else {
-            const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = t0 + warp * R, n = te - t;
-            T v[kArrays][2 * kRun];
-#pragma unroll
-            for (int a = 0; a < kArrays; ++a) {
-                if (!(sets >> a & 1)) continue;
-#pragma unroll
-                for (int j = 0; j < 2 * kRun; ++j) {
-                    const int i = j * 32 + lane, k = i / C, c = i % C;
-                    st_out(&v[a][j], 0.f);
-                    if (k < n && c0 + c < D) v[a][j] = io->in[a].at(b, 0, t + k)[c0 + c];
-                }
-            }
-            __syncwarp();
-#pragma unroll
-            for (int a = 0; a < kArrays; ++a) {
-                if (!(sets >> a & 1)) continue;
-#pragma unroll
-                for (int j = 0; j < 2 * kRun; ++j) ((T *)(slot(st, a) + warp * (kPlace / W)))[j * 32 + lane] = v[a][j];
-            }
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncwarp();
         }
     }
 };
 
-// Two channels of a token of a result.  Where the inputs come by TMA both exist (D is even) and lie in one word (of two).
+// Two channels of a token of a result.  Where the inputs come by TMA both exist (D is even) and lie in one word (of two).  (Otherwise
+// one store where they do, two where not, costs more instructions to fetch than it saves: 8 x 4096 tokens of 2047 channels, bf16
+// backward 417 -> 478 us.)
 template <int MODE, class T>
 __device__ __forceinline__ void put_two(T *p, float2 f, bool in0, bool in1)
 {
@@ -547,30 +542,27 @@ __device__ __forceinline__ void put_two(T *p, float2 f, bool in0, bool in1)
 template <class T>
 int recur_mode(RecurMaps &m, const RecurIo<T> &io, int in, int rows, const RecurDims &g, bool maps = true)
 {
-    bool tma = maps && g.T > 0 && g.D % 2 == 0, words = true;
+    bool tma = maps && g.T > 0 && g.D % 2 == 0;
     for (int a = 0; a < kArrays; ++a) {
         const View<const T> &i = io.in[a];
         if (in >> a & 1) {
             tma = tma && tensor_map(&m.in[a], sizeof(T) == 4, i.p, g.D, g.T, g.B, i.t, i.b, 64 / g.Q, rows, 0);
-            words = words && (uintptr_t)i.p % 4 == 0 && (sizeof(T) == 4 || (i.t % 2 == 0 && i.b % 2 == 0));
         }
         if (a < 4 && io.out[a].p) {
             const View<T> &o = io.out[a];
             tma = tma && (uintptr_t)o.p % (2 * sizeof(T)) == 0 && o.t % 2 == 0 && o.b % 2 == 0;
         }
     }
-    return tma ? kTma : words ? kWords : kElements;
+    return tma ? kTma : kChunks;
 }
 
-// Calls f(Q, mode, packed) with a call's variant as types; float32 that words serve always has no elements.
-template <class T, class F>
+// Calls f(Q, mode, packed) with a call's variant as types.
+template <class F>
 cudaError_t recur_variant(const RecurDims &g, int mode, F f)
 {
     auto with = [&](auto q) {
         auto how = [&](auto m) { return g.cu ? f(q, m, std::true_type{}) : f(q, m, std::false_type{}); };
-        if (mode == kTma) return how(std::integral_constant<int, kTma>{});
-        if (mode == kWords || sizeof(T) == 4) return how(std::integral_constant<int, kWords>{});
-        return how(std::integral_constant<int, sizeof(T) == 4 ? kWords : kElements>{});
+        return mode == kTma ? how(std::integral_constant<int, kTma>{}) : how(std::integral_constant<int, kChunks>{});
     };
     return g.Q == 4 ? with(std::integral_constant<int, 4>{}) : g.Q == 2 ? with(std::integral_constant<int, 2>{}) : with(std::integral_constant<int, 1>{});
 }

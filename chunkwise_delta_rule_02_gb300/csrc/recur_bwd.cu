@@ -33,8 +33,7 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
     const int q = warp * R + lane / L * kRun;     // of this lane's run, in a block's tokens
     const bool in0 = c < g.D, in1 = c + 1 < g.D;
     const bool gated = io.in[kZ].p != nullptr;
-    constexpr bool KEPT = MODE != kElements;   // kept states come with the inputs
-    Inputs<T, W, Q, MODE, KEPT> inputs;
+    Inputs<T, W, Q, MODE, true> inputs;
     inputs.init(raw + recur_block_bytes(CL, Q), sm.bar, &io, &maps, gated ? 31 : 23, b, c0, g.D);
     const int te = PACKED ? g.cu[g.Nseq] : g.T;
     const int span = W * R * CL, steps = (te + span - 1) / span;
@@ -43,7 +42,7 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
     const int kept = ((q / kRun) * (64 / Q) + 2 * (lane % L)) * 4;   // of this lane's run, among a step's
     auto ask = [&](int st, int first) {   // step st, the block's tokens from `first`
         inputs.ask(st, first, te);
-        if (MODE == kWords) {
+        if (MODE == kChunks) {
             const int t = first + q;
             const float *from = keep + (t < te ? (size_t)(t / kRun) * g.D : 0);
 #pragma unroll
@@ -66,10 +65,6 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
     float2 carry = two(0.f);   // the gradient that reaches a token's state from behind it
     if (!PACKED && io.dhT) carry = load2(io.dhT + (size_t)b * g.D + c, in0, in1);
     if (warp == 0 && lane < L) sm.carry[0][lane] = carry;
-    // the state that enters a run: with the inputs, or, where these are loaded as elements, a step ahead in registers (which
-    // costs the waits of shared memory behind it: 41 of 290 us for 8 x 4096 tokens of 2048 channels when it was the only way)
-    auto kept_at = [&](int t) { return t >= 0 && t < te ? load2(keep + (size_t)(t / kRun) * g.D, in0, in1) : two(0.f); };
-    float2 next = KEPT ? two(0.f) : kept_at(t0 + q);
     float2 sq = two(0.f), sr = two(0.f), si = two(0.f);
     Edges edges = {};
     int seq = 0;
@@ -81,15 +76,15 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
         const int t = t0 + q, n = te - t;   // tokens of the run that exist: 0 or less to kRun or more
         uint32_t starts = 0, ends = 0;
         if (PACKED) edges.find(g, t0 + warp * R, min(R, te - t0 - warp * R), t, min(kRun, n), starts, ends);
-        float2 h = next;
-        if (!KEPT) next = kept_at(t - span);
-        inputs.get(st, t0, te, g.status);
-        if (KEPT) h = *reinterpret_cast<const float2 *>(inputs.kept(st) + kept);
+        inputs.get(st, g.status);
+        // the state that enters the run, with the inputs (loaded a step ahead into registers it cost the waits of shared memory behind it:
+        // 41 of 290 us for 8 x 4096 tokens of 2048 channels)
+        float2 h = *reinterpret_cast<const float2 *>(inputs.kept(st) + kept);
 
         // the run's states, and of each token what dh is multiplied with
         float2 a[kRun], gy[kRun], fq[kRun], f1[kRun], fx[kRun], fi[kRun];
-        const T *px = inputs.cells(st, kX), *pr = inputs.cells(st, kRg), *pi = inputs.cells(st, kIg), *pz = inputs.cells(st, kZ);
-        const T *pd = inputs.cells(st, kDy);
+        const auto px = inputs.cells(st, kX, t), pr = inputs.cells(st, kRg, t), pi = inputs.cells(st, kIg, t), pz = inputs.cells(st, kZ, t);
+        const auto pd = inputs.cells(st, kDy, t);
         const bool whole = n >= kRun;
         seq = edges.first;
         auto states = [&](auto wide) {
@@ -232,13 +227,14 @@ cudaError_t bwd(const RecurCall &c, cudaStream_t st)
     if (g.cu && io.dh0 && g.Nseq > 0) k_recur_empty_grad<<<g.Nseq, 256, 0, st>>>(g.cu, g.D, io.dhT, io.dh0);
     constexpr int W = bwd_warps(sizeof(T));
     const bool gated = io.in[kZ].p != nullptr;
-    const int smem = 2 * W * 64 * ((gated ? 5 : 4) * kRun * (int)sizeof(T) + 4) + recur_block_bytes(g.CL, g.Q);
     RecurMaps m = {};
     const bool maps = g.T > 0 && tensor_map(&m.kept, true, c.keep, g.D, (g.T + kRun - 1) / kRun, g.B, g.D, (long long)((g.T + kRun - 1) / kRun) * g.D,
                                             64 / g.Q, W * g.Q, 0);
     const int mode = recur_mode(m, io, gated ? 31 : 23, box_rows<W>(g.Q), g, maps);
-    const cudaError_t rc = recur_variant<T>(g, mode, [&](auto q, auto how, auto packed) {
-        return recur_launch(k_recur_bwd<T, decltype(q)::value, decltype(how)::value, decltype(packed)::value>, g, 32 * W, smem, st, m, g, io);
+    const cudaError_t rc = recur_variant(g, mode, [&](auto q, auto how, auto packed) {
+        constexpr int Q = decltype(q)::value, M = decltype(how)::value, W = bwd_warps(sizeof(T));
+        const int smem = 2 * ((gated ? 5 : 4) * place_bytes(W, Q, M, sizeof(T)) + W * 64 * 4) + recur_block_bytes(g.CL, Q);
+        return recur_launch(k_recur_bwd<T, Q, M, decltype(packed)::value>, g, 32 * W, smem, st, m, g, io);
     });
     if (rc != cudaSuccess) return rc;
     const ColSum s = {c.part, (long long)g.B * g.CL, g.D, 3, {r->dlam, r->drg_bias, r->dig_bias}, {1, 1, 1}};

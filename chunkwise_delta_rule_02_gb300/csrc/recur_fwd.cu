@@ -17,10 +17,10 @@ namespace lay {
 namespace {
 
 template <class T, int Q, int MODE, bool PACKED>
-__global__ void __launch_bounds__(32 * fwd_warps(sizeof(T)), kFwdResident) k_recur_fwd(const __grid_constant__ RecurMaps maps, RecurDims g, RecurIo<T> io)
+__global__ void __launch_bounds__(32 * fwd_warps(sizeof(T), Q, MODE), kFwdResident) k_recur_fwd(const __grid_constant__ RecurMaps maps, RecurDims g, RecurIo<T> io)
 {
-    constexpr int W = fwd_warps(sizeof(T)), L = 32 / Q, R = kRun * Q;
-    constexpr bool kShort = MODE != kTma || PACKED;   // one copy of each loop: these run fewer steps, and wait for instructions
+    constexpr int W = fwd_warps(sizeof(T), Q, MODE), L = 32 / Q, R = kRun * Q;
+    constexpr bool kShort = PACKED;   // one copy of each loop: these run fewer steps, and wait for instructions
     extern __shared__ __align__(128) char raw[];
     float4 *block = reinterpret_cast<float4 *>(raw);   // maps of the cluster's blocks, then the inputs
     __shared__ RecurShared<W, Q> sm;
@@ -56,10 +56,10 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T)), kFwdResident) k_rec
         const int t = t0 + q, n = te - t;   // tokens of the run that exist: 0 or less to kRun or more
         uint32_t starts = 0, ends = 0;
         if (PACKED) edges.find(g, t0 + warp * R, min(R, te - t0 - warp * R), t, min(kRun, n), starts, ends);
-        inputs.get(st, t0, te, g.status);
+        inputs.get(st, g.status);
         float2 a[kRun], in[kRun], A = two(1.f), H = two(0.f);
         Vec<T, 2> z[kRun];
-        const T *px = inputs.cells(st, kX), *pr = inputs.cells(st, kRg), *pi = inputs.cells(st, kIg), *pz = inputs.cells(st, kZ);
+        const auto px = inputs.cells(st, kX, t), pr = inputs.cells(st, kRg, t), pi = inputs.cells(st, kIg, t), pz = inputs.cells(st, kZ, t);
         auto decays = [&](auto wide) {
 #pragma unroll
             for (int k = 0; k < kRun; ++k) {
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T)), kFwdResident) k_rec
         else decays(std::false_type{});
         if (gated) {
 #pragma unroll
-            for (int k = 0; k < kRun; ++k) z[k].load(pz + k * inputs.C);
+            for (int k = 0; k < kRun; ++k) z[k] = inputs.raw(pz, k);
         }
         if (n < kRun) {   // behind the end: nothing changes
 #pragma unroll
@@ -212,15 +212,17 @@ RecurIo<T> fwd_io(const RecurCall &c)
 template <class T>
 cudaError_t fwd(const RecurCall &c, cudaStream_t st)
 {
-    constexpr int W = fwd_warps(sizeof(T));
+    constexpr int W = fwd_warps(sizeof(T), 1, kTma);
     const RecurDims g = recur_dims(c, false);
     const RecurIo<T> io = fwd_io<T>(c);
     if (g.cu && io.hT && g.Nseq > 0) k_recur_empty<<<g.Nseq, 256, 0, st>>>(g.cu, g.D, g.h0, io.hT);
-    const int arrays = io.in[kZ].p ? 4 : 3, smem = 2 * arrays * W * kRun * 64 * (int)sizeof(T) + recur_block_bytes(g.CL, g.Q);
+    const int arrays = io.in[kZ].p ? 4 : 3;
     RecurMaps m = {};
     const int mode = recur_mode(m, io, (1 << arrays) - 1, box_rows<W>(g.Q), g);
-    return recur_variant<T>(g, mode, [&](auto q, auto how, auto packed) {
-        return recur_launch(k_recur_fwd<T, decltype(q)::value, decltype(how)::value, decltype(packed)::value>, g, 32 * W, smem, st, m, g, io);
+    return recur_variant(g, mode, [&](auto q, auto how, auto packed) {
+        constexpr int Q = decltype(q)::value, M = decltype(how)::value, W = fwd_warps(sizeof(T), Q, M);
+        const int smem = 2 * arrays * place_bytes(W, Q, M, sizeof(T)) + recur_block_bytes(g.CL, Q);
+        return recur_launch(k_recur_fwd<T, Q, M, decltype(packed)::value>, g, 32 * W, smem, st, m, g, io);
     });
 }
 
@@ -246,7 +248,7 @@ cudaError_t step(const RecurCall &c, cudaStream_t st)
 // are spans: runs that share a warp exchange their maps more cheaply than blocks do.
 RecurPlan recur_plan(const dn_recur_shape *s, bool bwd)
 {
-    const int e = s->dtype == DN_F32 ? 4 : 2, run = kRun * (bwd ? bwd_warps(e) : fwd_warps(e));
+    const int e = s->dtype == DN_F32 ? 4 : 2, run = kRun * (bwd ? bwd_warps(e) : fwd_warps(e, 1, kTma));
     const long long most = (long long)(bwd ? kBwdResident : kFwdResident) * sm_count();
     auto tiles = [&](int Q) { return (long long)s->B * ((s->D + 64 / Q - 1) / (64 / Q)); };
     RecurPlan p = {1, 1};

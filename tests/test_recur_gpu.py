@@ -170,6 +170,30 @@ def test_rows_that_end_within_16_bytes(gdn, dt, D):
         assert ref.err(g[n], want[n]) <= TOL[g[n].dtype], n
 
 
+@pytest.mark.parametrize("dt,D,pitch", [(BF, 37, 40), (BF, 67, 67), (BF, 130, 131), (F32, 37, 38), (F32, 67, 67), (F32, 130, 133)])
+@pytest.mark.parametrize("B,T", [(2, 90), (40, 33)])
+def test_rows_at_every_alignment(gdn, dt, D, pitch, B, T):
+    """Each array starts at another offset from 16 bytes in a buffer of NaN that ends with it; odd distances of rows; few rows and many."""
+    k = case((B, T, D, dt, True, True, True, None), 18)
+    x, rg, ig, lam = k["args"]
+
+    def at(t, o):
+        big = torch.full((o + B * T * pitch - (pitch - D),), float("nan"), dtype=dt, device=DEV)
+        v = big.as_strided((B, T, D), (T * pitch, pitch, 1), o)
+        v.copy_(t)
+        return v
+
+    for o in range(0, 8 if dt is BF else 4, 3):
+        a, more = (at(x, o), at(rg, o + 1), at(ig, o + 2), lam), dict(k["more"], z=at(k["more"]["z"], o + 5))
+        y, hT, saved = gdn.recur_forward(*a, **more, save=True)
+        ry, rh, want = want_of(k)
+        close(y, ry)
+        close(hT, rh)
+        g = gdn.recur_backward(*a, **more, dy=at(k["dy"], o + 3), dhT=k["dhT"], saved=saved)
+        for n in GRADS:
+            assert ref.err(g[n], want[n]) <= TOL[g[n].dtype], n
+
+
 def test_a_result_leaves_what_lies_around_it(gdn):
     k = case((2, 21, 35, BF, True, False, False, None), 4)
     big = torch.full((4, 30, 50), 7.0, dtype=BF, device=DEV)
