@@ -71,6 +71,11 @@ struct Vec {
     }
 };
 
+// Kernels of a call that are launched so that one may start while the one before it ends: each says so at once, and waits for the other's
+// results before it touches any memory.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2(float x)

@@ -17,6 +17,7 @@ namespace {
 // One block: copies the offsets, or zeros if they are malformed; sets the status word.
 __global__ void __launch_bounds__(256) k_offsets(const int32_t *cu, int N, int T, int32_t *out, uint32_t *status)
 {
+    let_next_start();
     int bad = 0;
     for (int i = threadIdx.x; i <= N; i += blockDim.x) {
         const int v = cu[i];

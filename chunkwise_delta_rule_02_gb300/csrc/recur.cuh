@@ -385,6 +385,22 @@ struct Edges {
     }
 };
 
+// Final states (initial states' gradients) of empty sequences: the initial ones (the final states' gradients).  A warp looks at 32
+// sequences at a time; a lane's channels are c and c + 1.
+template <int W, int L>
+__device__ __forceinline__ void pass_empty(const RecurDims &g, int rank, int CL, int c, bool in0, bool in1, const float *from, float *to)
+{
+    const int lane = threadIdx.x & 31;
+    if (!to) return;
+    for (int s0 = (rank * W + (threadIdx.x >> 5)) * 32; s0 < g.Nseq; s0 += CL * W * 32) {
+        const int s = s0 + lane;
+        for (uint32_t left = __ballot_sync(0xffffffffu, s < g.Nseq && g.cu[s] == g.cu[s + 1]); left; left &= left - 1) {
+            const size_t at = (size_t)(s0 + __ffs(left) - 1) * g.D + c;
+            if (lane < L) store2(to + at, from ? load2(from + at, in0, in1) : two(0.f), in0, in1);
+        }
+    }
+}
+
 // Tokens of a box: 256 at most
 template <int W>
 __host__ __device__ constexpr int box_rows(int Q)
@@ -578,12 +594,19 @@ cudaError_t recur_launch(K kernel, const RecurDims &g, int threads, int smem, cu
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)g.CL;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
     cfg.attrs = at;
-    cfg.numAttrs = g.CL > 1 ? 1 : 0;
+    if (g.CL > 1) {
+        at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        at[cfg.numAttrs].val.clusterDim.x = (unsigned)g.CL;
+        at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    if (g.cu) {   // behind the check of the offsets
+        at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
     e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }

@@ -35,6 +35,7 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
     const bool gated = io.in[kZ].p != nullptr;
     Inputs<T, W, Q, MODE, true> inputs;
     inputs.init(raw + recur_block_bytes(CL, Q), sm.bar, &io, &maps, gated ? 31 : 23, b, c0, g.D);
+    if (PACKED) wait_for_last();
     const int te = PACKED ? g.cu[g.Nseq] : g.T;
     const int span = W * R * CL, steps = (te + span - 1) / span;
     int t0 = (steps - 1) * span + rank * W * R;   // the block's first token of a step; step st handles the st-th span from the end
@@ -177,6 +178,7 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
         else outputs(std::false_type{});
         if (CL == 1) leave<W, Q, true>(sm, st & 1, back);
     }
+    if (PACKED) pass_empty<W, L>(g, rank, CL, c, in0, in1, io.dhT, io.dh0);
     if (!PACKED && io.dh0) {
         if (CL > 1 || steps == 0) {
             if (rank == 0 && warp == 0 && lane < L) store2(io.dh0 + (size_t)b * g.D + c, carry, in0, in1);
@@ -205,14 +207,6 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
     }
 }
 
-// Initial states' gradients of empty sequences: those of the final ones.
-__global__ void __launch_bounds__(256) k_recur_empty_grad(const int32_t *cu, int D, const float *from, float *to)
-{
-    const int s = blockIdx.x;
-    if (cu[s] != cu[s + 1]) return;
-    for (int c = threadIdx.x; c < D; c += 256) to[(size_t)s * D + c] = from ? from[(size_t)s * D + c] : 0.f;
-}
-
 template <class T>
 cudaError_t bwd(const RecurCall &c, cudaStream_t st)
 {
@@ -224,7 +218,6 @@ cudaError_t bwd(const RecurCall &c, cudaStream_t st)
     io.in[kZ] = view_of<const T>(&f->z); io.in[kDy] = view_of<const T>(&r->dy);
     io.out[kX] = view_of<T>(&r->dx); io.out[kRg] = view_of<T>(&r->drg); io.out[kIg] = view_of<T>(&r->dig); io.out[kZ] = view_of<T>(&r->dz);
     io.keep = c.keep; io.dhT = r->dhT; io.dh0 = r->dh0; io.part = c.part;
-    if (g.cu && io.dh0 && g.Nseq > 0) k_recur_empty_grad<<<g.Nseq, 256, 0, st>>>(g.cu, g.D, io.dhT, io.dh0);
     constexpr int W = bwd_warps(sizeof(T));
     const bool gated = io.in[kZ].p != nullptr;
     RecurMaps m = {};

@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T), Q, MODE), kFwdReside
     const bool gated = io.in[kZ].p != nullptr;
     Inputs<T, W, Q, MODE, false> inputs;
     inputs.init(raw + recur_block_bytes(CL, Q), sm.bar, &io, &maps, gated ? 15 : 7, b, c0, g.D);
+    if (PACKED) wait_for_last();
     const int te = PACKED ? g.cu[g.Nseq] : g.T;   // malformed offsets: every sequence is empty
     const int span = W * R * CL, steps = (te + span - 1) / span;
     int t0 = rank * W * R;                        // the block's first token of a step
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T), Q, MODE), kFwdReside
         py += span * io.out[kX].t;
         if (CL == 1) leave<W, Q, false>(sm, st & 1, h);
     }
+    if (PACKED) pass_empty<W, L>(g, rank, CL, c, in0, in1, g.h0, io.hT);
     // what leaves the last run: a cluster's blocks all have it, a block alone its last warp
     if (!PACKED && io.hT) {
         if (CL > 1 || steps == 0) {
@@ -141,14 +143,6 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T), Q, MODE), kFwdReside
             store2(io.hT + (size_t)b * g.D + c, h, in0, in1);
         }
     }
-}
-
-// Final states of empty sequences: the initial ones.
-__global__ void __launch_bounds__(256) k_recur_empty(const int32_t *cu, int D, const float *from, float *to)
-{
-    const int s = blockIdx.x;
-    if (cu[s] != cu[s + 1]) return;
-    for (int c = threadIdx.x; c < D; c += 256) to[(size_t)s * D + c] = from ? from[(size_t)s * D + c] : 0.f;
 }
 
 // Two neighbouring channels of a token, WIDE: one access, both channels exist.
@@ -215,7 +209,6 @@ cudaError_t fwd(const RecurCall &c, cudaStream_t st)
     constexpr int W = fwd_warps(sizeof(T), 1, kTma);
     const RecurDims g = recur_dims(c, false);
     const RecurIo<T> io = fwd_io<T>(c);
-    if (g.cu && io.hT && g.Nseq > 0) k_recur_empty<<<g.Nseq, 256, 0, st>>>(g.cu, g.D, g.h0, io.hT);
     const int arrays = io.in[kZ].p ? 4 : 3;
     RecurMaps m = {};
     const int mode = recur_mode(m, io, (1 << arrays) - 1, box_rows<W>(g.Q), g);

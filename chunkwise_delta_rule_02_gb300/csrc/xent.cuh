@@ -7,6 +7,8 @@ namespace gdn {
 namespace xent {
 
 using lay::ex2;
+using lay::let_next_start;
+using lay::wait_for_last;
 using lay::kLog2e;
 
 constexpr float kNone = -1e30f;   // maximum of no logits
@@ -54,11 +56,6 @@ __device__ __forceinline__ float scale_of(const Gemm &p)
     const float s = *p.scale;
     return s > 0.f ? s : 1.f;
 }
-
-// The kernels of a call are launched so that one may start while the one before it ends: each says so at once, and waits for the other's
-// results before it touches any memory.
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // A token's target, -1 for none: ignored, or (which the status word is told) outside the vocabulary.
 __device__ __forceinline__ long long target_at(const Gemm &p, int row)

@@ -15,8 +15,8 @@
  * alignment is always enough.  The norm and the single-token convolution move 16
  * bytes an access, the convolution over tokens 8, the scan 4 elements (one above
  * 32 states, and of x, dt, z and y for single tokens).  The recurrence and the loss
- * read through tensor maps where rows start at 16 bytes, else in words (the
- * recurrence) or from a copy (the loss).
+ * read through tensor maps where rows start at 16 bytes, else every aligned 16 bytes
+ * that hold an element of a row (the recurrence) or from a copy (the loss).
  *
  * Dtypes: shape->dtype (DN_F32 or DN_BF16) is that of every token array, of the
  * convolution's taps and of the loss' weight; other parameters (weights, A, D, biases),
