@@ -67,7 +67,8 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
     if (!PACKED && io.dhT) carry = load2(io.dhT + (size_t)b * g.D + c, in0, in1);
     if (warp == 0 && lane < L) sm.carry[0][lane] = carry;
     float2 sq = two(0.f), sr = two(0.f), si = two(0.f);
-    Edges edges = {};
+    Edges edges;
+    edges.init();
     int seq = 0;
     if (MODE == kTma) __syncthreads();   // the barriers exist
     if (CL > 1) cluster_barrier();     // all of the cluster's blocks run before one writes to another

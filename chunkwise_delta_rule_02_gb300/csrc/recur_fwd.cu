@@ -47,7 +47,8 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T), Q, MODE), kFwdReside
     if (warp == 0 && lane < L) sm.carry[0][lane] = carry;
     float *keep = io.keep ? io.keep + ((size_t)b * ((g.T + kRun - 1) / kRun) + (t0 + q) / kRun) * g.D + c : nullptr;
     T *py = io.out[kX].at(b, 0, t0 + q) + c;
-    Edges edges = {};
+    Edges edges;
+    edges.init();
     int seq = 0;
     if (MODE == kTma) __syncthreads();   // the barriers exist
     if (CL > 1) cluster_barrier();     // all of the cluster's blocks run before one writes to another

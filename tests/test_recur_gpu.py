@@ -170,6 +170,20 @@ def test_rows_that_end_within_16_bytes(gdn, dt, D):
         assert ref.err(g[n], want[n]) <= TOL[g[n].dtype], n
 
 
+@pytest.mark.parametrize("dt,D", [(BF, 64), (BF, 9), (F32, 40), (F32, 10000)])
+def test_many_short_sequences(gdn, dt, D):
+    """More sequences than a warp holds, many of them within a warp's tokens, empty ones in rows, between long ones."""
+    lens = [1] * 40 + [0] * 35 + [90] + [0, 0, 1, 2] * 12 + [20] * 3 + [0] * 33 + [130, 3] + [0] * 9 + [1] * 10
+    k = case((1, sum(lens), D, dt, True, True, True, lens), 19)
+    y, hT, saved = gdn.recur_forward(*k["args"], **k["more"], cu_seqlens=k["cu"], save=True)
+    ry, rh, want = want_of(k)
+    close(y, ry)
+    close(hT, rh)
+    g = gdn.recur_backward(*k["args"], **k["more"], dy=k["dy"], dhT=k["dhT"], saved=saved, cu_seqlens=k["cu"])
+    for n in GRADS:
+        assert ref.err(g[n], want[n]) <= TOL[g[n].dtype], n
+
+
 @pytest.mark.parametrize("dt,D,pitch", [(BF, 37, 40), (BF, 67, 67), (BF, 130, 131), (F32, 37, 38), (F32, 67, 67), (F32, 130, 133)])
 @pytest.mark.parametrize("B,T", [(2, 90), (40, 33)])
 def test_rows_at_every_alignment(gdn, dt, D, pitch, B, T):
