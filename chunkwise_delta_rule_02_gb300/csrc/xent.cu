@@ -37,6 +37,8 @@ constexpr int kScore = 128;                                          // tokens u
 // Steps after which float32 inputs' sums leave TMEM: the tensor core cuts what it adds off rather than rounding it, the same way each
 // time, which a contraction of 70001 tokens added up to 8e-5 of dw; segments of 256 are summed in registers, rounded.
 constexpr int kSegment = 4;
+// The same for bf16 logits of more than kLong steps, which came out 3e-6 low with 3289 features: segments of 1024.
+constexpr int kLong = 32, kLongSegment = 16;
 
 enum { STATS, GRAD, OUT, SCORE };
 
@@ -811,7 +813,7 @@ int pairs_at_most() { return lay::sm_count() / 2; }
 template <int EPI, bool SEG, int NT = TILE>
 cudaError_t launch_as(const Maps &m, Gemm &p, cudaStream_t st)
 {
-    p.seg = kSegment;
+    p.seg = p.np > 1 ? kSegment : kLongSegment;
     auto kernel = k_gemm<EPI, SEG, NT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
@@ -823,7 +825,8 @@ cudaError_t launch_as(const Maps &m, Gemm &p, cudaStream_t st)
 template <int EPI, int NT = TILE>
 cudaError_t launch(const Maps &m, Gemm &p, cudaStream_t st)
 {
-    return p.np > 1 ? launch_as<EPI, true, NT>(m, p, st) : launch_as<EPI, false, NT>(m, p, st);
+    const bool seg = p.np > 1 || ((EPI == STATS || EPI == SCORE) && p.of[0].kb > kLong);
+    return seg ? launch_as<EPI, true, NT>(m, p, st) : launch_as<EPI, false, NT>(m, p, st);
 }
 
 // Clears the status word and the scale; copies what the tensor maps cannot read in place.

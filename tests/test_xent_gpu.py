@@ -205,6 +205,16 @@ def test_large_logits(gdn):
     check(gdn, low, w.abs() + 1, t, dloss)
 
 
+@pytest.mark.parametrize("M", [40, 300])
+def test_losses_of_many_features(gdn, M):
+    """The sums of 9001 products are rounded, not cut off: a cut is a step of 2^-24 of the sum down each of 560 times, 1.7e-5 of the logit's own
+    size in the same direction, of which sums in segments of 1024 leave 64 steps a segment, 4e-6."""
+    x, w, t, _ = make((M, 9001), 200, BF, 20, ignored=0.0)
+    _, lse = gdn.xent_forward(x, w, t)
+    _, want = plain(x, w, t)
+    assert abs(float((lse.double() - want).mean())) <= 4e-6 * float((1 + want.abs()).mean())
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_logits_far_below_zero(gdn, dtype):
     """All logits near -400, an odd vocabulary: exp(-lse) is infinite, and nothing of it reaches a gradient.
