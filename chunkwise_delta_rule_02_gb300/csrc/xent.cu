@@ -625,6 +625,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_gemm(c
     }
     __syncwarp();
     __syncthreads();
+    // The last commit arrives on DONE of both blocks, and that the even one has seen its own says nothing about the other's: the odd
+    // block stays until its own has come too (every tile is out, so it is on its way), or the arrival might find the barriers of the next kernel.
+    if (warp == 1 && rank == 1) {
+        volatile int never = 0;
+        if (lane == 0) pair_wait(&bar[DONE], 0, BUDGET, &never);
+        __syncwarp();
+    }
     pair_sync();   // the other block's barriers are not touched any more
     tc_fence_after();
     if (warp == 1) pair_tmem_dealloc(tmem, 512);
