@@ -713,7 +713,8 @@ __global__ void __launch_bounds__(256) k_pack(const __grid_constant__ Packing p)
     const bool none = p.mask && o == 0 && target_of(p.g, r, false) < 0;
     for (int c = (threadIdx.x & ((1 << p.shift) - 1)) * 8; c < p.pitch[o]; c += 8 << p.shift) {
         if (sizeof(T) == 2 && (none || p.whole[o])) {
-            *reinterpret_cast<uint4 *>(to + c) = none ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(from + c);
+            // the copy's rows may be 8 columns longer than a row, and what lies behind the last one is not the caller's
+            *reinterpret_cast<uint4 *>(to + c) = none || c >= p.K ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(from + c);
             continue;
         }
         float f[8];
