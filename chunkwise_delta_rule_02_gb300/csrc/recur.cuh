@@ -19,6 +19,8 @@
 // 8 x 4096 tokens of 2047 channels, bf16 forward 591 us, backward 765, now 241 and 418; float32 527 and 839, now 271 and 469).
 #pragma once
 
+#include <stdlib.h>
+
 #include <type_traits>
 
 #include "layers.h"
@@ -29,7 +31,9 @@ namespace lay {
 
 constexpr int kRun = 8;                       // tokens of a lane and step (and between kept states)
 constexpr int kMaxCluster = 8;
+constexpr float kNan = __builtin_nanf("");
 constexpr long long kRecurBudget = 4000000000LL;   // clock cycles (about 2 s) for any one wait
+constexpr long long kHookBudget = 2000000LL;       // the same (about 1 ms) with a test hook set (recur_dims)
 
 enum { kTma, kChunks };                       // how inputs get to shared memory: boxes, or 16 bytes a lane
 
@@ -55,6 +59,8 @@ struct RecurDims {
     const int32_t *cu;             // checked offsets, or null
     const float *lam, *rbias, *ibias, *h0;
     uint32_t *status;
+    long long budget;              // of a wait
+    int short_in, short_map;       // test hooks: steps from which on 16 bytes too many are waited for, of inputs, of maps
 };
 
 enum { kX, kRg, kIg, kZ, kDy, kArrays };
@@ -101,6 +107,15 @@ inline RecurDims recur_dims(const RecurCall &c, bool bwd)
     g.cu = c.cu;
     g.lam = c.io->lam; g.rbias = c.io->rg_bias; g.ibias = c.io->ig_bias; g.h0 = c.io->h0;
     g.status = c.status;
+    // Test hooks (failure detection): with GDN_DEBUG_WITHHOLD_INPUTS=n, GDN_DEBUG_WITHHOLD_MAP=n a block waits from step n on for 16 bytes
+    // of inputs (where they come by TMA), of its cluster's maps, that nobody sends; the wait runs out after about 1 ms.
+    auto hook = [](const char *name) {
+        const char *v = getenv(name);
+        return v && v[0] ? atoi(v) : 0x7fffffff;
+    };
+    g.short_in = hook("GDN_DEBUG_WITHHOLD_INPUTS");
+    g.short_map = hook("GDN_DEBUG_WITHHOLD_MAP");
+    g.budget = g.short_in != 0x7fffffff || g.short_map != 0x7fffffff ? kHookBudget : kRecurBudget;
     return g;
 }
 
@@ -213,6 +228,16 @@ __device__ __forceinline__ int cluster_rank()
     return (int)r;
 }
 
+// The end of a cluster's block: it leaves when all of them have stopped storing.  Whoever has all maps knows that nothing is on its way
+// to it; one that gave up waiting for them (`lost`) leaves a store in flight a thousand times the time that it takes.
+__device__ __forceinline__ void leave_cluster(bool lost)
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (lost)
+        for (const long long t0 = clock64(); clock64() - t0 < 1000000;) {}
+}
+
 __device__ __forceinline__ void cluster_barrier()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -271,9 +296,11 @@ struct RecurShared {
 // cluster.  Maps of two steps have places of their own, so that one barrier a step suffices: a block stores its map into the others
 // behind it, and they their next ones only when they have all of this step's, so that nobody overwrites what is still read.
 // `block`: [2][CL][32 / Q] of the cluster's blocks.  `freed` is called behind the barrier.
+// lost: the wait for the maps ran out, now or before.  The barrier that counts them is in the middle of its phase then, and neither
+// it nor another block's is touched again; what enters the run and leaves the step is NaN.
 template <int W, int Q, bool CUT, bool BACK, class F>
 __device__ __forceinline__ float2 exchange(RecurShared<W, Q> &sm, float4 *block, int st, int CL, int rank, float2 A, float2 H, float2 &carry,
-                                           bool &failed, uint32_t *status, F freed)
+                                           bool &lost, const RecurDims &g, F freed)
 {
     const int par = st & 1;
     constexpr int L = 32 / Q;
@@ -312,7 +339,7 @@ __device__ __forceinline__ float2 exchange(RecurShared<W, Q> &sm, float4 *block,
             h = pass<CUT>(make_float2(m.x, m.y), make_float2(m.z, m.w), h);
         }
     } else {
-        if (threadIdx.x == 0) sm100::mbar_expect_tx(&sm.bar[2 + par], CL * L * 16);
+        if (threadIdx.x == 0 && !lost) sm100::mbar_expect_tx(&sm.bar[2 + par], (CL * L + (st >= g.short_map)) * 16);
         float2 wA = two(1.f), wH = two(0.f);   // of the warps before this one
 #pragma unroll 4
         for (int w = 0; w < mine; ++w) {
@@ -323,13 +350,13 @@ __device__ __forceinline__ float2 exchange(RecurShared<W, Q> &sm, float4 *block,
             const float4 m = sm.warp[par][W - 1][l];
             float2 oA = wA, oH = wH;
             then<CUT>(oA, oH, make_float2(m.x, m.y), make_float2(m.z, m.w));
-            if (lane < L)
+            if (lane < L && !lost)
                 for (int k = 0; k < CL; ++k) remote_store(block + (par * CL + at) * L + l, &sm.bar[2 + par], k, make_float4(oA.x, oA.y, oH.x, oH.y));
             __syncwarp();
         }
-        if (!cluster_wait(&sm.bar[2 + par], (uint32_t)(st >> 1) & 1u, failed ? 1000 : kRecurBudget)) {
-            failed = true;
-            raise_status(status, kStatusTimeout);
+        if (lost || !cluster_wait(&sm.bar[2 + par], (uint32_t)(st >> 1) & 1u, g.budget)) {
+            if (!lost) raise_status(g.status, kStatusTimeout);
+            lost = true;
         }
         h = carry;
         for (int k = 0; k < CL; ++k) {
@@ -338,6 +365,7 @@ __device__ __forceinline__ float2 exchange(RecurShared<W, Q> &sm, float4 *block,
             carry = pass<CUT>(make_float2(m.x, m.y), make_float2(m.z, m.w), carry);
         }
         h = pass<CUT>(wA, wH, h);
+        if (lost) h = carry = two(kNan);
     }
     return Q > 1 ? pass<CUT>(pA, pH, h) : h;
 }
@@ -447,7 +475,8 @@ struct Inputs {
     const RecurIo<T> *io;
     const RecurMaps *maps;
     int sets, count, b, c0, D;     // arrays and their number; row; first channel
-    bool failed;
+    int top;                       // steps asked for, of the thread that asks
+    bool failed;                   // a wait ran out: nothing is asked for any more, what the places hold is not used
 
     __device__ __forceinline__ int place(int array) const { return __popc(sets & ((1 << array) - 1)); }
     __device__ __forceinline__ char *slot(int st, int array) const { return base + (st & 1) * (count * kPlace + kKept) + place(array) * kPlace; }
@@ -494,18 +523,20 @@ struct Inputs {
         count = __popc(sets);
         b = b_; c0 = c0_; D = D_;
         failed = false;
+        top = 0;
         if (threadIdx.x == 0) {   // the cluster's two as well
             for (int i = 0; i < 4; ++i) sm100::mbar_init(&bar[i], 1);
             sm100::fence_barrier_init();
         }
     }
     // Asks for step `st`, the block's tokens t0 .. te - 1 at most; nobody reads what it overwrites any more.
-    __device__ __forceinline__ void ask(int st, int t0, int te) const
+    __device__ __forceinline__ void ask(int st, int t0, int te, int short_in)
     {
         if (MODE == kTma) {
-            if (threadIdx.x == 0) {
+            if (threadIdx.x == 0 && !failed) {
+                top = st + 1;
                 uint64_t *full = &bar[st & 1];
-                sm100::mbar_expect_tx(full, count * kPlace + kKept);
+                sm100::mbar_expect_tx(full, count * kPlace + kKept + (st >= short_in ? 16 : 0));
                 if (KEPT) box_load(kept(st), &maps->kept, full, c0, t0 / kRun, b);
 #pragma unroll
                 for (int a = 0; a < kArrays; ++a)
@@ -542,17 +573,45 @@ struct Inputs {
     {
         if (MODE == kChunks) asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    // Waits for step st
-    __device__ __forceinline__ void get(int st, uint32_t *status)
+    __device__ __forceinline__ bool arrived(int st, long long budget) const
+    {
+        return sm100::mbar_wait(&bar[st & 1], (uint32_t)(st >> 1) & 1u, budget, nullptr);
+    }
+    // Waits for step st.  Where that runs out, the thread's results from there on are NaN, and by the maps those behind it: forward by
+    // the decays' parameter, backward by its x and dy (the one costs the backward 2 of 395 us for 8 x 4096 tokens of 2048 channels, the
+    // other the forward 3 of 141 for 4 x 8192).
+    __device__ __forceinline__ void get(int st, const RecurDims &g, RecurParams &par)
     {
         if (MODE == kTma) {
-            if (!sm100::mbar_wait(&bar[st & 1], (uint32_t)(st >> 1) & 1u, failed ? 1000 : kRecurBudget, nullptr)) {
+            if constexpr (!KEPT) {
+                if (!failed && !arrived(st, g.budget)) {
+                    failed = true;
+                    par.km = two(kNan);
+                    raise_status(g.status, kStatusTimeout);
+                }
+            } else if (failed || !arrived(st, g.budget)) {
+                if (!failed) raise_status(g.status, kStatusTimeout);
                 failed = true;
-                raise_status(status, kStatusTimeout);
+#pragma unroll 1
+                for (int a = kX; a <= kDy; a += kDy - kX) {
+                    Vec<T, 2> v;
+                    const float none[2] = {kNan, kNan};
+                    v.set(none);
+                    T *p = const_cast<T *>(cells(st, a, 0).p);
+#pragma unroll 1
+                    for (int k = 0; k < kRun; ++k, p += kPitch) v.store(p);
+                }
             }
         } else {
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncwarp();
+        }
+    }
+    // At a block's end: what was asked for before a wait ran out, of two steps at most, lands before the shared memory goes away.
+    __device__ __forceinline__ void drain(long long budget) const
+    {
+        if (MODE == kTma && failed && threadIdx.x == 0) {
+            for (int st = max(0, top - 2); st < top; ++st) arrived(st, budget);
         }
     }
 };

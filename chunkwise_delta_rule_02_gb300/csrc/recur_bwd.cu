@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
     const float *keep = io.keep + (size_t)b * ((g.T + kRun - 1) / kRun) * g.D + c;
     const int kept = ((q / kRun) * (64 / Q) + 2 * (lane % L)) * 4;   // of this lane's run, among a step's
     auto ask = [&](int st, int first) {   // step st, the block's tokens from `first`
-        inputs.ask(st, first, te);
+        inputs.ask(st, first, te, g.short_in);
         if (MODE == kChunks) {
             const int t = first + q;
             const float *from = keep + (t < te ? (size_t)(t / kRun) * g.D : 0);
@@ -74,11 +74,12 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
     if (CL > 1) cluster_barrier();     // all of the cluster's blocks run before one writes to another
 
     float2 back = carry;
+    bool lost = false;
     for (int st = 0; st < steps; ++st, t0 -= span) {
         const int t = t0 + q, n = te - t;   // tokens of the run that exist: 0 or less to kRun or more
         uint32_t starts = 0, ends = 0;
         if (PACKED) edges.find(g, t0 + warp * R, min(R, te - t0 - warp * R), t, min(kRun, n), starts, ends);
-        inputs.get(st, g.status);
+        inputs.get(st, g, par);
         // the state that enters the run, with the inputs (loaded a step ahead into registers it cost the waits of shared memory behind it:
         // 41 of 290 us for 8 x 4096 tokens of 2048 channels)
         float2 h = *reinterpret_cast<const float2 *>(inputs.kept(st) + kept);
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
         }
         A = make_float2(fmaxf(A.x, kLeast), fmaxf(A.y, kLeast));
         if (PACKED && ends) A = two(-1.f);
-        back = exchange<W, Q, PACKED, true>(sm, block, st, CL, rank, A, H, carry, inputs.failed, g.status, [&] {
+        back = exchange<W, Q, PACKED, true>(sm, block, st, CL, rank, A, H, carry, lost, g, [&] {
             if (st + 2 < steps) ask(st + 2, t0 - 2 * span);
             inputs.asked();
         });
@@ -206,6 +207,8 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T)), kBwdResident) k_rec
         for (int w = 1; w < W; ++w) v = add2(v, red[warp][w][lane]);
         store2(io.part + (((size_t)b * CL + rank) * 3 + warp) * g.D + c, v, in0, in1);
     }
+    inputs.drain(g.budget);
+    if (CL > 1) leave_cluster(lost);
 }
 
 template <class T>

@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T), Q, MODE), kFwdReside
     const int span = W * R * CL, steps = (te + span - 1) / span;
     int t0 = rank * W * R;                        // the block's first token of a step
     for (int st = 0; st < 2; ++st) {
-        if (st < steps) inputs.ask(st, t0 + st * span, te);
+        if (st < steps) inputs.ask(st, t0 + st * span, te, g.short_in);
         inputs.asked();
     }
     RecurParams par;
@@ -54,11 +54,12 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T), Q, MODE), kFwdReside
     if (CL > 1) cluster_barrier();     // all of the cluster's blocks run before one writes to another
 
     float2 h = carry;
+    bool lost = false;
     for (int st = 0; st < steps; ++st, t0 += span) {
         const int t = t0 + q, n = te - t;   // tokens of the run that exist: 0 or less to kRun or more
         uint32_t starts = 0, ends = 0;
         if (PACKED) edges.find(g, t0 + warp * R, min(R, te - t0 - warp * R), t, min(kRun, n), starts, ends);
-        inputs.get(st, g.status);
+        inputs.get(st, g, par);
         float2 a[kRun], in[kRun], A = two(1.f), H = two(0.f);
         Vec<T, 2> z[kRun];
         const auto px = inputs.cells(st, kX, t), pr = inputs.cells(st, kRg, t), pi = inputs.cells(st, kIg, t), pz = inputs.cells(st, kZ, t);
@@ -101,8 +102,8 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T), Q, MODE), kFwdReside
         }
         A = make_float2(fmaxf(A.x, kLeast), fmaxf(A.y, kLeast));
         if (PACKED && starts) A = two(-1.f);
-        h = exchange<W, Q, PACKED, false>(sm, block, st, CL, rank, A, H, carry, inputs.failed, g.status, [&] {
-            if (st + 2 < steps) inputs.ask(st + 2, t0 + 2 * span, te);
+        h = exchange<W, Q, PACKED, false>(sm, block, st, CL, rank, A, H, carry, lost, g, [&] {
+            if (st + 2 < steps) inputs.ask(st + 2, t0 + 2 * span, te, g.short_in);
             inputs.asked();
         });
         if (keep) {
@@ -144,6 +145,8 @@ __global__ void __launch_bounds__(32 * fwd_warps(sizeof(T), Q, MODE), kFwdReside
             store2(io.hT + (size_t)b * g.D + c, h, in0, in1);
         }
     }
+    inputs.drain(g.budget);
+    if (CL > 1) leave_cluster(lost);
 }
 
 // Two neighbouring channels of a token, WIDE: one access, both channels exist.
