@@ -298,7 +298,8 @@ dn_status recur_begin(RecurCall &c, const dn_recur_shape *s, const dn_recur_io *
         c.cu = cu;
         return status_of(check_offsets(s->cu_seqlens, s->num_seqs, s->T, cu, (uint32_t *)ws, st));
     }
-    return DN_OK;
+    // no kernel goes through the offsets and clears the word: a wait that runs out is to be found in it, and nothing else
+    return status_of(cudaMemsetAsync(ws, 0, sizeof(uint32_t), st));
 }
 
 }  // namespace

@@ -22,7 +22,9 @@ Packed sequences: B = 1 and ``cu_seqlens``, int32 offsets on the device, as in
 ``binding.forward``.  The kernels check the offsets; with ``check_status`` (the
 default) a packed call reads the status word afterwards, which waits for the
 stream, and raises if they were malformed.  ``xent_*`` does so for its targets.  Other
-calls never wait.
+calls never wait.  The waits inside the recurrence's kernels are bounded; should one run out,
+the results behind it are NaN, and ``dn_device_status(ws)`` of the ``ws`` that was passed to the
+call, packed or not, says DN_ERR_TIMEOUT.
 """
 from __future__ import annotations
 
@@ -249,9 +251,9 @@ def _size(what: str, shape: bytes, for_backward: int, device: int) -> int:
     return int(f(shape, for_backward)) if for_backward >= 0 else int(f(shape))
 
 
-def _ws(what: str, shape: bytes, for_backward: int, like: torch.Tensor, packed: bool, where: str) -> torch.Tensor:
-    """Workspace, or (for_backward -1) saved buffer.  Calls that are not packed leave the status word alone:
-    where they need nothing else, all of a device share one buffer that nothing is written to."""
+def _ws(what: str, shape: bytes, for_backward: int, like: torch.Tensor, packed: bool, where: str, waits: bool = False) -> torch.Tensor:
+    """Workspace, or (for_backward -1) saved buffer.  Calls that are neither packed nor wait on the device (the recurrence does) leave the
+    status word alone: where they need nothing else, all of a device share one buffer that nothing is written to."""
     dev = like.get_device()
     if packed:          # the record holds an address: nothing to remember
         f = getattr(_L(), what)
@@ -260,7 +262,7 @@ def _ws(what: str, shape: bytes, for_backward: int, like: torch.Tensor, packed: 
         n = _size(what, shape, for_backward, dev)
     if n == 0:
         raise GdnError(DN_ERR_INVALID_ARG, where)
-    if n == _STATUS_ONLY and not packed and for_backward >= 0:
+    if n == _STATUS_ONLY and not packed and not waits and for_backward >= 0:
         ws = _status_only.get(dev)
         if ws is None:
             ws = _status_only[dev] = torch.zeros(_STATUS_ONLY, dtype=torch.uint8, device=like.device)
@@ -610,7 +612,7 @@ def recur_forward(x, rg, ig, lam, rg_bias=None, ig_bias=None, z=None, h0=None, c
     hT = torch.empty((n, x.shape[2]), dtype=torch.float32, device=x.device) if want_state else None
     shape = recur_shape(x, c, cu_seqlens)
     packed = cu_seqlens is not None
-    ws = _ws("dn_recur_workspace_size", shape, 0, x, packed, "dn_recur_fwd") if ws is None else _buffer(ws, "ws", x)
+    ws = _ws("dn_recur_workspace_size", shape, 0, x, packed, "dn_recur_fwd", True) if ws is None else _buffer(ws, "ws", x)
     saved = _ws("dn_recur_saved_size", shape, -1, x, packed, "dn_recur_fwd") if save else None
     dn_recur_fwd(shape, recur_io(x, rg, ig, lam, rg_bias, ig_bias, z, h0, y, hT), saved, ws)
     if check_status and packed:
@@ -633,7 +635,7 @@ def recur_backward(x, rg, ig, lam, rg_bias=None, ig_bias=None, z=None, h0=None, 
     g = dict(dx=new(x), drg=new(rg), dig=new(ig), dz=new(z), dlam=new(lam), drg_bias=new(rg_bias), dig_bias=new(ig_bias), dh0=new(h0))
     shape = recur_shape(x, c, cu_seqlens)
     packed = cu_seqlens is not None
-    ws = _ws("dn_recur_workspace_size", shape, 1, x, packed, "dn_recur_bwd") if ws is None else _buffer(ws, "ws", x)
+    ws = _ws("dn_recur_workspace_size", shape, 1, x, packed, "dn_recur_bwd", True) if ws is None else _buffer(ws, "ws", x)
     dn_recur_bwd(shape, recur_io(x, rg, ig, lam, rg_bias, ig_bias, z, h0, None, None),
                  recur_grads(dy, g["dx"], g["drg"], g["dig"], g["dz"], dhT, g["dlam"], g["drg_bias"], g["dig_bias"], g["dh0"]), saved, ws)
     if check_status and packed:

@@ -27,7 +27,10 @@
  * T = total tokens, cu_seqlens = device int32 offsets [num_seqs + 1]; nothing
  * crosses a sequence boundary and empty sequences are allowed.  Malformed offsets
  * are found on the device: the call then treats every sequence as empty and sets
- * the status word of the workspace (dn_device_status: DN_ERR_INVALID_ARG).
+ * the status word of the workspace (dn_device_status: DN_ERR_INVALID_ARG).  The word
+ * belongs to calls with packed offsets and to every call of the recurrence (but the
+ * single token's) and of the loss, which wait on the device; other calls leave it alone.
+ * Results behind a wait of the recurrence that ran out are NaN.
  * Pointers need the alignment of their element type; workspaces and saved
  * buffers 16 bytes.
  */
