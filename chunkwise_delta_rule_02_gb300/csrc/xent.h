@@ -38,7 +38,7 @@ int tiles_of(int n);                // of 256
 inline long long copy_pitch(long long K) { return (K + 15) / 16 * 16; }
 int parts_of(int M, int V);
 // Whether a call goes without the tensor cores, and its blocks (rows of `part`, parts of dx)
-bool few_tokens(int M, int K, bool f32, bool bwd);
+bool few_tokens(int M, int K, bool f32);
 int few_blocks(int M, int K, int V, bool bwd);
 void cuts_of(int M, int K, int n, int planes, int &dx, int &dw);   // parts that a piece's two contractions are cut into
 cudaError_t few_forward(const Call &c, cudaStream_t st);

@@ -70,7 +70,7 @@ size_t layout(Call &c, const dn_xent_shape *s, const dn_view *x, const dn_view *
         }
     };
     if (c.M == 0) return at;
-    c.few = few_tokens(c.M, c.K, c.planes == 3, bwd);
+    c.few = few_tokens(c.M, c.K, c.planes == 3);
     if (c.few) {
         const int blocks = few_blocks(c.M, c.K, c.V, bwd);
         if (bwd) {

@@ -1,5 +1,5 @@
-// Linear softmax cross entropy of few tokens, on the CUDA cores: up to 16 in float32, up to 4 in bf16 (backward 16 of a width that is no
-// multiple of 8).
+// Linear softmax cross entropy of few tokens, on the CUDA cores: up to 16 in float32, up to 4 in bf16 where the width is no multiple of 8
+// (16 below 512) or small.
 //
 // Tiles of 256 tokens would be empty rows, and float32 operands three planes copied from a weight that is read once
 // anyway.  Here a block has a contiguous share of the vocabulary and x in shared memory; a warp takes 4 or 8 entries at
@@ -245,9 +245,17 @@ cudaError_t variant(const Call &c, F f)
 
 }  // namespace
 
-// bf16: the tensor cores take 8 tokens of 50000 x 1024 through forward and backward in 30 and 125 us, this 74 and 146; where they need copies
-// of aligned rows, 69380 x 1591, in 136 and 440 us, this in 149 and 330.
-bool few_tokens(int M, int K, bool f32, bool bwd) { return M >= 1 && M <= (f32 || (bwd && K % 8) ? 16 : 4) && shared_of(M, K, true) <= kFewShared; }
+// bf16, us forward and backward with the tensor cores and so, measured side by side:
+//   widths that they read in place, 4 tokens of 131072 x 4096: 170, 686 and 356, 2129; 50000 x 1024: 28, 95 and 52, 116;
+//     32000 x 512: 18, 45 and 18, 42; 1000 x 64: 17, 29 and 12, 14 (launches);
+//   widths that they need copies for, 69380 x 1591: of 4 tokens 136, 342 and 94, 278, of 5 136, 342 and 140, 334, of 16 137, 348 and 183, 405;
+//     5003 x 203: of 5 tokens 21, 33 and 14, 16, of 16 21, 35 and 16, 20.
+// The same for both directions: a logit's sum is what the backward's has to repeat, and the tensor cores round otherwise.
+bool few_tokens(int M, int K, bool f32)
+{
+    const int most = f32 ? 16 : K % 8 ? (K <= 512 ? 16 : 4) : K <= 512 ? 4 : 0;
+    return M >= 1 && M <= most && shared_of(M, K, true) <= kFewShared;
+}
 
 int few_blocks(int M, int K, int V, bool bwd)
 {

@@ -1,0 +1,57 @@
+"""GPU tests of the loss where all products of a logit have one sign: x and w around 1, so that a logit of K features is about K and what
+its sum loses shows.  Forward and backward have to lose the same: a probability is exp of the difference of the backward's logit and the
+forward's lse.
+
+What a sum loses.  The tensor core cuts what it adds off: a step of 16 products loses up to 2^-23 of the sum so far (one unit u of its
+last place), half of that on average, and what differs from logit to logit is a random walk of n steps of u / sqrt(12).  n = K / 16; the
+sum so far is at most S = K up to 2048 features, and 1024 in segments above.  On the CUDA cores it is rounded, far less."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture()
+def gdn():
+    import __graft_entry__
+    __graft_entry__.build()
+    import chunkwise_delta_rule_02_gb300 as g
+    return g
+
+
+def make(M, K, V, dtype, seed=1):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(M, K, generator=g) * 0.5 + 1).to(dtype).to(DEV)
+    w = (torch.randn(V, K, generator=g) * 2 * K ** -0.5 + 1).to(dtype).to(DEV)
+    return x, w, torch.randint(0, V, (M,), generator=g).to(DEV), torch.randn(M, generator=g).to(DEV)
+
+
+#: tokens, features, entries, type, whether the call goes without the tensor cores
+CASES = [(300, 2048, 500, BF, False), (12, 1591, 500, BF, False), (7, 2047, 300, BF, False), (12, 2048, 300, BF, False), (4, 2048, 300, BF, False),
+         (4, 2047, 300, BF, True), (12, 501, 300, BF, True), (300, 4001, 200, F32, False), (12, 1500, 300, F32, True)]
+
+
+@pytest.mark.parametrize("M,K,V,dtype,few", CASES)
+def test_gradients_of_logits_with_a_common_part(gdn, M, K, V, dtype, few):
+    """By element.  D is off by the result's half step (bf16; not where the call goes without the tensor cores) and by the probability's error: 5
+    times the random walk above, and 4 |lse| 2^-24 for lse, its two terms and the logit, all float32 numbers.  Then sums of at most max(M, V) terms in
+    float32, cut off or rounded, 2^-23 of the terms' size a step, and the result's rounding."""
+    x, w, t, dloss = make(M, K, V, dtype)
+    _, lse = gdn.xent_forward(x, w, t)
+    g = gdn.xent_backward(x, w, t, lse, dloss)
+    logits = x.double() @ w.double().t()
+    want = torch.logsumexp(logits, 1)
+    d = torch.exp(logits - want[:, None])
+    terms = d.clone()
+    d[torch.arange(M, device=DEV), t] -= 1
+    terms[torch.arange(M, device=DEV), t] += 1
+    d, terms = d * dloss.double()[:, None], terms * dloss.double().abs()[:, None]
+    n, S = K / 16, min(K, 1024 if K > 2048 or dtype is F32 else 2048)
+    walk = 0.0 if few else 5 * n ** 0.5 * 2.0 ** -23 * 1.5 * S / 12 ** 0.5
+    off = (2.0 ** -9 if dtype is BF and not few else 0.0) + walk + (4 * float(want.abs().max()) + 2 * max(M, V)) * 2.0 ** -24
+    step = torch.finfo(dtype).eps / 2
+    for n, ref, size in (("dx", d @ w.double(), terms @ w.double().abs()), ("dw", d.t() @ x.double(), terms.t() @ x.double().abs())):
+        worst = float(((g[n].double() - ref).abs() / (off * size + step * ref.abs())).max())
+        assert worst <= 1, (n, worst)
