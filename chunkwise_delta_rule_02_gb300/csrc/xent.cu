@@ -37,7 +37,8 @@ constexpr int kScore = 128;                                          // tokens u
 // Steps after which float32 inputs' sums leave TMEM: the tensor core cuts what it adds off rather than rounding it, the same way each
 // time, which a contraction of 70001 tokens added up to 8e-5 of dw; segments of 256 are summed in registers, rounded.
 constexpr int kSegment = 4;
-// The same for bf16 logits of more than kLong steps, which came out 3e-6 low with 3289 features: segments of 1024.
+// The same for bf16 logits of more than kLong steps, which came out 3e-6 low with 3289 features: segments of 1024.  In both passes: what both lose
+// cancels in a probability, and only that (300 tokens of 9001 features around 1: with segments in the forward alone dw was 7.8e-2 off).
 constexpr int kLong = 32, kLongSegment = 16;
 
 enum { STATS, GRAD, OUT, SCORE };
@@ -833,7 +834,7 @@ cudaError_t launch_as(const Maps &m, Gemm &p, cudaStream_t st)
 template <int EPI, int NT = TILE>
 cudaError_t launch(const Maps &m, Gemm &p, cudaStream_t st)
 {
-    const bool seg = p.np > 1 || ((EPI == STATS || EPI == SCORE) && p.of[0].kb > kLong);
+    const bool seg = p.np > 1 || (EPI != OUT && p.of[0].kb > kLong);
     return seg ? launch_as<EPI, true, NT>(m, p, st) : launch_as<EPI, false, NT>(m, p, st);
 }
 

@@ -32,7 +32,7 @@ struct Product {
 
 struct Gemm {
     Product of[2];                  // the second of OUT only
-    int seg;                        // steps of a segment: all, or kSegment (SEG)
+    int seg;                        // SEG: steps of a segment, kSegment or kLongSegment
     int np;                         // plane products: nibbles of pa, pb
     uint32_t pa, pb;
     uint32_t *status;
