@@ -65,8 +65,9 @@ struct Philox {
 };
 
 // A thread takes V elements of a row at a time (V a multiple of 4: whole counters; what a flat row has beyond its vectors goes
-// one by one), or, V = 1, the up to 4 elements of one counter, each with a row of its own.
-template <class T, int V, bool RES, bool BIG>
+// one by one), or, V = 1, the up to 4 elements of one counter, each with a row of its own.  NONE: the threshold is 2^32, above every
+// word (a kernel of its own: as a second condition in the comparison it cost 3 of 57 us).
+template <class T, int V, bool RES, bool BIG, bool NONE = false>
 __global__ void __launch_bounds__(kDropThreads) k_dropout(DropDims g, View<const T> x, View<const T> res, View<T> y)
 {
     Philox gen;
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kDropThreads) k_dropout(DropDims g, View<const
     auto single = [&](long long i, uint32_t w) {
         int b, h, t;
         const long long j = place(i, b, h, t);
-        float f = w >= g.threshold ? ld_in(x.at(b, h, t) + j) * g.scale : 0.f;
+        float f = !NONE && w >= g.threshold ? ld_in(x.at(b, h, t) + j) * g.scale : 0.f;
         if (RES) f += ld_in(res.at(b, h, t) + j);
         st_out(y.at(b, h, t) + j, f);
     };
@@ -170,7 +171,8 @@ cudaError_t run(const DropCall &c, cudaStream_t st)
     g.n = (long long)s->B * s->H * s->T * s->d;
     g.rng = c.rng;
     const double th = s->p * 4294967296.0 + 0.5;
-    g.threshold = th >= 4294967295.0 ? 4294967295u : (uint32_t)th;
+    const bool none = th >= 4294967296.0;
+    g.threshold = none ? 0u : (uint32_t)th;
     g.scale = (float)(1.0 / (1.0 - s->p));
     if (g.n == 0) return cudaSuccess;
     dn_view at[3] = {};
@@ -182,14 +184,16 @@ cudaError_t run(const DropCall &c, cudaStream_t st)
             views[i] = &at[i];
         }
     }
-    const bool wide = (g.flat || s->d % V == 0) && can_vector(views[0], sizeof(T), 16) && can_vector(views[1], sizeof(T), 16) &&
+    const bool wide = !none && (g.flat || s->d % V == 0) && can_vector(views[0], sizeof(T), 16) && can_vector(views[1], sizeof(T), 16) &&
                       can_vector(views[2], sizeof(T), 16);
     const View<const T> x = view_of<const T>(views[0]), r = view_of<const T>(views[1]);
     const View<T> y = view_of<T>(views[2]);
     const long long per = wide ? V : 4, need = ((g.n + per - 1) / per + kDropThreads - 1) / kDropThreads;
     const unsigned blocks = (unsigned)(need < (long long)kDropBlocks * sm_count() ? need : (long long)kDropBlocks * sm_count());
     auto go = [&](auto kernel) { kernel<<<blocks, kDropThreads, 0, st>>>(g, x, r, y); };
-    if (g.n > 1ll << 34) {
+    if (none) {
+        r.p ? go(k_dropout<T, 1, true, true, true>) : go(k_dropout<T, 1, false, true, true>);
+    } else if (g.n > 1ll << 34) {
         if (wide) r.p ? go(k_dropout<T, V, true, true>) : go(k_dropout<T, V, false, true>);
         else r.p ? go(k_dropout<T, 1, true, true>) : go(k_dropout<T, 1, false, true>);
     } else {
