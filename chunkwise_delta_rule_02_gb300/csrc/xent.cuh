@@ -11,7 +11,7 @@ using lay::let_next_start;
 using lay::wait_for_last;
 using lay::kLog2e;
 
-constexpr float kNone = -1e30f;   // maximum of no logits
+constexpr float kNone = -3.402823466e38f;   // maximum of no logits: the lowest number, so that differences to it are numbers or -infinity
 
 // One product C = A B^T and how its tiles are cut: units of a tile and a part of the contraction.
 struct Product {
