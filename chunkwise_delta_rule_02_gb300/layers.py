@@ -543,7 +543,11 @@ def recur_shape(x: torch.Tensor, c: float = 8.0, cu_seqlens=None) -> bytes:
     """dn_recur_shape record of x [B,T,D] (x [n,D]: single tokens)."""
     xs = x.shape
     cu, n = _cu(cu_seqlens, xs[0])
-    return _RECUR_SHAPE.pack(xs[0], xs[1] if len(xs) == 3 else 1, xs[-1], _dtype_code(x, "x"), c, n, cu)
+    code = _dtype_code(x, "x")
+    try:
+        return _RECUR_SHAPE.pack(xs[0], xs[1] if len(xs) == 3 else 1, xs[-1], code, c, n, cu)
+    except struct.error:
+        raise ValueError("c must be a number and the sizes 32-bit ones, got c = %r, x %s" % (c, tuple(xs))) from None
 
 
 def recur_io(x, rg, ig, lam, rg_bias, ig_bias, z, h0, y, hT) -> bytes:
@@ -661,8 +665,12 @@ def recur_step(x, rg, ig, lam, rg_bias=None, ig_bias=None, z=None, state=None, o
 
 def dn_dropout(x, p, rng, residual, y, stream=None):
     B, H, T, d = _dims(x)
-    _check(_L().dn_dropout(_DROPOUT_SHAPE.pack(B, H, T, d, _dtype_code(x, "x"), 0, p), _view(x), _view(residual), _p(rng), _view(y),
-                           _stream(stream)), "dn_dropout")
+    code = _dtype_code(x, "x")
+    try:
+        shape = _DROPOUT_SHAPE.pack(B, H, T, d, code, 0, p)
+    except struct.error:
+        raise ValueError("p must be a number and the sizes 32-bit ones, got p = %r, x %s" % (p, tuple(x.shape))) from None
+    _check(_L().dn_dropout(shape, _view(x), _view(residual), _p(rng), _view(y), _stream(stream)), "dn_dropout")
 
 
 def _dropout(x, p, rng, residual, out, name):
@@ -769,7 +777,12 @@ def norm_backward(x, w, dy, z=None, sum=None, dsum=None, res_scale=None, eps=1e-
 def xent_shape(x: torch.Tensor, w: torch.Tensor, ignore_index: int = -100) -> bytes:
     """dn_xent_shape record of x [R,K] or [B,T,K] and w [V,K]."""
     B, _, T, K = _dims(x)
-    return _XENT_SHAPE.pack(B, T, K, w.shape[0], _dtype_code(x, "x"), 0, ignore_index)
+    code = _dtype_code(x, "x")
+    try:
+        return _XENT_SHAPE.pack(B, T, K, w.shape[0], code, 0, ignore_index)
+    except struct.error:
+        raise ValueError("ignore_index must be a 64-bit integer and the sizes 32-bit ones, got %r, x %s, w %s"
+                         % (ignore_index, tuple(x.shape), tuple(w.shape))) from None
 
 
 def _weight_view(w: torch.Tensor) -> bytes:
