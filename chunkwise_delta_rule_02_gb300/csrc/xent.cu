@@ -40,6 +40,10 @@ constexpr int kSegment = 4;
 // The same for bf16 logits of more than kLong steps, which came out 3e-6 low with 3289 features: segments of 1024.  In both passes: what both lose
 // cancels in a probability, and only that (300 tokens of 9001 features around 1: with segments in the forward alone dw was 7.8e-2 off).
 constexpr int kLong = 32, kLongSegment = 16;
+// bf16 contractions over the vocabulary or the tokens have no segments (the products of a training step would pay for them); they are cut
+// into parts of 16384, whose sums are joined in float32 and rounded.  A part's sum comes out up to 6e-5 of its terms low (dx of 1024 tokens of
+// 131072 x 1024, terms of one sign: 2.0e-4 in parts of 65536).
+constexpr int kPart = 256;
 
 enum { STATS, GRAD, OUT, SCORE };
 
@@ -942,13 +946,14 @@ Gemm common(const Call &c)
 int tiles_of(int n) { return (int)(((long long)n + TILE - 1) / TILE); }
 
 // How the contractions of a piece's two products are cut: a unit not costlier than a pair's share of all, so that a few long
-// tiles do not keep the rest waiting, and not below 8 stages' worth.
+// tiles do not keep the rest waiting, and not below 8 stages' worth; bf16: nor above kPart.
 void cuts_of(int M, int K, int n, int planes, int &dx, int &dw)
 {
     const long long np = planes == 1 ? 1 : 6, a = ((long long)n + BK - 1) / BK, b = ((long long)M + BK - 1) / BK;
     const long long nx = (long long)tiles_of(K) * tiles_of(M), nw = (long long)tiles_of(K) * tiles_of(n), pairs = pairs_at_most();
     long long share = (nx * (a * np + way_out(np)) + nw * (b * np + way_out(np)) + pairs - 1) / pairs / np;
     if (share < 8) share = 8;
+    if (planes == 1 && share > kPart) share = kPart;
     dx = (int)((a + share - 1) / share);
     dw = (int)((b + share - 1) / share);
 }

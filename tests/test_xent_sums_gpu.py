@@ -68,3 +68,23 @@ def test_losses_of_many_features_of_one_sign(gdn, M):
     _, lse = gdn.xent_forward(x, w, t)
     want = torch.logsumexp(x.double() @ w.double().t(), 1)
     assert abs(float((lse.double() - want).mean())) <= 1.5 * 1.2e-2 + 10 * 2.0 ** -11
+
+
+def test_a_long_sum_over_the_vocabulary(gdn):
+    """dx of 131072 entries whose weights are around 1 / 4: the positive terms, D w of all entries but the target's, grow to a sum that the tensor
+    core cuts off, which the target's term then takes away.  Each of n products loses what lies 2 bits below u, 2^-27 of the sum so far on
+    average, in all n 2^-28 of the terms (9001 features of one sign, one sum: 3.1e-5 against 3.4e-5): in parts of 16384 that is 6.1e-5 of the
+    terms, and 1.5 times that the bound; in one of 65536 it would be 2.4e-4 (measured 2.0e-4).  D's rounding, 2^-9 each, is a random one: 1e-6."""
+    M, K, V = 1024, 1024, 131072
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = (torch.randn(M, K, generator=g, device=DEV) * 0.3 + 1).to(BF)
+    w = (torch.randn(V, K, generator=g, device=DEV) * 0.3 * K ** -0.5 + 0.25).to(BF)
+    t = torch.randint(0, V, (M,), generator=g, device=DEV)
+    _, lse = gdn.xent_forward(x, w, t)
+    dx = gdn.xent_backward(x, w, t, lse, torch.ones((), device=DEV).expand(M))["dx"]
+    d = x.double() @ w.double().t()
+    d = torch.exp(d - torch.logsumexp(d, 1, keepdim=True))
+    d[torch.arange(M, device=DEV), t] -= 1
+    off = dx.double() - d @ w.double()
+    terms = float((d.abs() @ w.double().abs()).mean())
+    assert abs(float(off.mean())) <= 1.5 * 16384 * 2.0 ** -28 * terms
