@@ -40,8 +40,8 @@ enum { kTma, kChunks };                       // how inputs get to shared memory
 // Warps of a block by the type's bytes, blocks that an SM holds.  bf16 forward: 12 warps twice, what 80 registers allow (4 x 8192
 // tokens of 2048 channels with the output gate, measured side by side: 148 us; 8 warps three times 157, 16 warps 186).  Backward: 6
 // warps twice at 160 registers (training step of 8 x 4096 tokens, likewise: 437 us; 4 warps three times 459; runs of 4 tokens,
-// 8 warps twice: 436, with twice the kept states).  float32 backward: 4 warps twice at 250 registers (4 x 4096 tokens of 1000 channels
-// 114 us, 5 warps 139).  Rows that come in whole 16 bytes (kChunks) leave room for fewer of them (bf16 forward, 2 x 4096 tokens of 1001
+// 8 warps twice: 436, with twice the kept states).  float32 backward: 4 warps twice, at 160 registers where rows come by boxes (4 x 4096 tokens
+// of 1000 channels 114 us, 5 warps 139) and 250 where they come in pieces.  Rows that come in whole 16 bytes (kChunks) leave room for fewer of them (bf16 forward, 2 x 4096 tokens of 1001
 // channels: 8 warps 54 us, 9, which is one block an SM, 72).
 __host__ __device__ constexpr int fwd_warps(int bytes, int Q, int mode)
 {

@@ -10,8 +10,8 @@
 // the forward pass kept at the run's start, so that nothing of the forward recurrence has to be exchanged; what
 // dh is multiplied with is in registers before the exchange.
 //
-// Bound by latency at 12 warps an SM: six factors of 16 elements a thread are 96 of its 156 registers.  8 x 4096 tokens of
-// 2048 channels, bf16 with output gate: 248 us, 18 bytes an element at 4.8 TB/s, 65 instructions an element at 1.9 a cycle and SM.
+// Bound by latency at 12 warps an SM: six factors of 16 elements a thread are 96 of its 158 registers.  8 x 4096 tokens of
+// 2048 channels, bf16 with output gate: 250 us, 18 bytes an element at 4.8 TB/s, 65 instructions an element at 1.9 a cycle and SM.
 #include "recur.cuh"
 
 namespace gdn {

@@ -7,7 +7,7 @@
 // Bound by instruction issue: 43 instructions an element (three sigmoids, the series of the decay and the
 // root are half of them) against 10 bytes of bf16 with the output gate.  8 x 4096 tokens of 2048 channels:
 // 142 us, 4.8 TB/s of a copy's 6.7, 2.4 instructions a cycle and SM; 256 blocks on 152 SMs leave 15 % of
-// the SMs' time empty.  4 x 8192 tokens: 141 us; one row of 16384 tokens, 1024 channels: 51 us, 11 steps of a
+// the SMs' time empty.  4 x 8192 tokens: 143 us with the status word's clearing; one row of 16384 tokens, 1024 channels: 52 us, 11 steps of a
 // barrier and an exchange each.
 #include "recur.cuh"
 

@@ -21,7 +21,7 @@ constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32, kFewRows = 64;
 __host__ __device__ constexpr int bwd_threads(int MT) { return MT == 16 ? 512 : 256; }
 // entries that a warp takes at a time, and steps along the features whose loads are in flight together
 __host__ __device__ constexpr int at_once(int MT) { return MT == 16 ? 4 : 8; }
-__host__ __device__ constexpr int steps_at_once(int) { return 4; }
+constexpr int kStepsAtOnce = 4;
 constexpr int kFewShared = 200 << 10;   // bytes
 
 struct Few {
@@ -54,7 +54,7 @@ __device__ __forceinline__ void logits(const Few &p, const float *xs, int row, i
 #pragma unroll
     for (int r = 0; r < kAtOnce; ++r) w[r] = (const T *)p.w + (long long)min(row + r, end - 1) * p.w_t;
     float acc[G * 32] = {};
-#pragma unroll steps_at_once(MT)
+#pragma unroll kStepsAtOnce
     for (int k = lane; k < p.K; k += 32) {
         float f[kAtOnce];
 #pragma unroll

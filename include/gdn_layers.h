@@ -221,8 +221,9 @@ dn_status dn_dropout(const dn_dropout_shape *shape, const dn_view *x, const dn_v
  * What the hidden states of such tokens hold, NaN too, reaches no loss and no
  * gradient.
  * Products are sums in float32 of bf16 operands, float32 ones as three bf16 planes; D, without dloss' largest
- * magnitude, is rounded to the dtype.  (Of up to 16 float32 tokens, and up to 4 bf16 ones of a width that is
- * up to 512 or no multiple of 8, all is in float32.)  Both passes sum a token's logits in the same way.
+ * magnitude, is rounded to the dtype.  (Of few tokens, 16 at most, where the tensor cores would not pay, all is in
+ * float32.)  The tensor core cuts sums off: of n terms of one sign about 2^-28 n of their size, n at most 256 (float32),
+ * 2048 (bf16 logits) and 16384 (bf16 gradients).  Both passes sum a token's logits in the same way.
  * Memory: the backward pass holds D for a piece of the vocabulary at a time. */
 typedef struct {
     int32_t B, T, K, V;
