@@ -1,5 +1,5 @@
 // Linear softmax cross entropy of few tokens, on the CUDA cores: up to 16 in float32, up to 4 in bf16 where the width is no multiple of 8
-// (16 below 512) or small.
+// (16 up to 512 features) or at most 512.
 //
 // Tiles of 256 tokens would be empty rows, and float32 operands three planes copied from a weight that is read once
 // anyway.  Here a block has a contiguous share of the vocabulary and x in shared memory; a warp takes 4 or 8 entries at

@@ -88,3 +88,26 @@ def test_a_long_sum_over_the_vocabulary(gdn):
     off = dx.double() - d @ w.double()
     terms = float((d.abs() @ w.double().abs()).mean())
     assert abs(float(off.mean())) <= 1.5 * 16384 * 2.0 ** -28 * terms
+
+
+@pytest.mark.parametrize("M,K,V,dtype", [(4096, 24, 70001, BF), (4096, 21, 70001, BF), (2048, 520, 90000, BF), (40000, 72, 5000, BF), (700, 40, 70001, F32)])
+def test_pieces_whose_products_are_cut(gdn, M, K, V, dtype):
+    """Several pieces of the vocabulary (or one), each product's contraction in several parts: relative Frobenius, D and the result rounded to bf16
+    once each, 2^-8 at most; float32 1e-5; and 4 max |lse| 2^-24 for the probabilities."""
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x = torch.randn(M, K, generator=g, device=DEV).to(dtype)
+    w = (torch.randn(V, K, generator=g, device=DEV) * 2 * K ** -0.5).to(dtype)
+    t = torch.randint(0, V, (M,), generator=g, device=DEV)
+    dloss = torch.randn(M, generator=g, device=DEV)
+    _, lse = gdn.xent_forward(x, w, t)
+    got = gdn.xent_backward(x, w, t, lse, dloss)
+    d = x.double() @ w.double().t()
+    want = torch.logsumexp(d, 1)
+    d = d.sub_(want[:, None]).exp_()
+    d[torch.arange(M, device=DEV), t] -= 1
+    d *= dloss.double()[:, None]
+    tol = (2.0 ** -8 if dtype is BF else 1e-5) + 4 * float(want.abs().max()) * 2.0 ** -24
+    for n, ref in (("dx", d @ w.double()), ("dw", d.t() @ x.double())):
+        assert float((got[n].double() - ref).norm() / ref.norm()) <= tol, n
+    again = gdn.xent_backward(x, w, t, lse, dloss)
+    assert torch.equal(got["dx"], again["dx"]) and torch.equal(got["dw"], again["dw"])
